@@ -217,6 +217,76 @@ kvq_status kvq_append(const kvq_cache_desc* cache, const void* k_new, const void
                       const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq,
                       uint32_t* err_word, void* stream);
 
+/* kvq_rope_table: how the pair frequencies are stretched for contexts longer
+ * than the one a model was trained on. */
+#define KVQ_ROPE_PLAIN 0  /* f_j = base^(-2j/R)                                              */
+#define KVQ_ROPE_LINEAR 1 /* f_j / factor: all positions compressed                          */
+#define KVQ_ROPE_NTK 2    /* base * factor^(R/(R-2)): the slowest pair stretched by factor,  */
+                          /* the fastest left as it is                                       */
+#define KVQ_ROPE_BANDS 3  /* by the turns t_j = original_len f_j / 2 pi of a pair over the   */
+                          /* trained length: f_j if t_j >= high_turns, f_j / factor if       */
+                          /* t_j <= low_turns, a blend linear in t_j between                 */
+
+typedef struct {
+  double base;              /* > 1, 10000 for example                                        */
+  int32_t scaling;          /* KVQ_ROPE_*                                                    */
+  double factor;            /* >= 1; not read by KVQ_ROPE_PLAIN                              */
+  double original_len;      /* > 0; KVQ_ROPE_BANDS only                                      */
+  double low_turns;         /* >= 0; KVQ_ROPE_BANDS only                                     */
+  double high_turns;        /* > low_turns; KVQ_ROPE_BANDS only                              */
+  double amplitude;         /* multiplies every cosine and sine (0 stands for 1)             */
+} kvq_rope_freqs;
+
+/* Rotary positions of one model: a table that kvq_rope_table filled (or the
+ * caller, by the same layout) and how pairs lie in a head. */
+typedef struct {
+  int32_t rotary_dim;       /* R: the first R dims of a head turn, the others pass through;  */
+                            /* 8..128 in steps of 8                                          */
+  int32_t interleaved;      /* 0: pairs (j, j + R/2); 1: pairs (2j, 2j + 1)                  */
+  int32_t max_pos;          /* positions in the table                                        */
+  const float* table;       /* device float [max_pos][R/2][2]: cosine, sine; 16-byte aligned */
+} kvq_rope_desc;
+
+/*
+ * kvq_rope_table -- fill a table of cosines and sines.  The pages store keys as
+ * the model computes them and do not name rotary positions: this and
+ * kvq_rope_append serve models whose keys are turned before they are cached.
+ * Angles p * f_j, cosines and sines are computed in double and rounded once to
+ * float32.  Made once per model, kept by the caller.
+ *   table : device float [max_pos][rotary_dim / 2][2], 16-byte aligned
+ */
+kvq_status kvq_rope_table(const kvq_rope_freqs* freqs, int32_t rotary_dim, int32_t max_pos, float* table,
+                          void* stream);
+
+/*
+ * kvq_rope_append -- turn queries and keys by their positions and write keys
+ * and values into the cache, one call for the new tokens of a step or a chunk.
+ * Of every pair (x0, x1) of a head at position p: y0 = x0 c - x1 s, y1 = x0 s +
+ * x1 c with c, s = the table's row p, computed as the exact value rounded to
+ * float32 and then to bf16.  Rotated queries go to q_out; keys and values are
+ * then written exactly as kvq_append writes the bf16 vectors (all modes and
+ * formats), so codes and scales are the same whether a key is turned here or
+ * beforehand.
+ *   q            : device bf16, row r head i at q + r * q_stride + i * 128, or NULL
+ *                  with q_heads = 0 (keys and values only)
+ *   q_out        : device bf16 [n][q_heads][128]; may be q itself if q_stride =
+ *                  q_heads * 128
+ *   k_new, v_new : device bf16, row r head h at k_new + r * k_stride + h * 128, or
+ *                  both NULL (queries only: seq_idx, pos, block_table are not read)
+ *   *_stride     : elements between rows, a multiple of 4, at least heads * 128 (slices
+ *                  of one fused projection); 0 stands for heads * 128
+ *   rope_pos     : device int32 [n] positions in the table, or NULL to use pos (the
+ *                  cache slot; the two differ once a cache has been through kvq_evict)
+ *   seq_idx, pos, mode, block_table, batch, max_blocks_per_seq: as kvq_append
+ * A row whose rope position is outside [0, max_pos) sets KVQ_DEVERR_POSITION and
+ * is skipped whole (its q_out row and its cache slot stay as they were).
+ */
+kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const void* q, int32_t q_heads,
+                           int64_t q_stride, void* q_out, const void* k_new, int64_t k_stride, const void* v_new,
+                           int64_t v_stride, int32_t n, const int32_t* rope_pos, const int32_t* seq_idx,
+                           const int32_t* pos, int32_t mode, const int32_t* block_table, int32_t batch,
+                           int32_t max_blocks_per_seq, uint32_t* err_word, void* stream);
+
 /* Work decomposition of kvq_decode (host-only arithmetic, no CUDA calls). */
 typedef struct {
   int32_t stream_ctas;    /* CTAs sharing the token blocks of all (seq, kv_head) units */

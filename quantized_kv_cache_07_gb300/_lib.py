@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkvq.so")
@@ -31,6 +31,10 @@ APPEND_QUANT = 0
 APPEND_RING = 1
 APPEND_STEP = 2
 PREFILL_TILES = -1  # kvq_prefill stream_ctas: the query-tile path
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_NTK = 2
+ROPE_BANDS = 3
 DECODE_GEOMETRY_READY = 1  # kvq_decode_ex flag: lengths and block table final before the previous kernel ends
 
 
@@ -53,6 +57,17 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
+class RopeFreqs(ctypes.Structure):
+    """Mirror of kvq_rope_freqs."""
+    _fields_ = [("base", c_double), ("scaling", c_int32), ("factor", c_double), ("original_len", c_double),
+                ("low_turns", c_double), ("high_turns", c_double), ("amplitude", c_double)]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of kvq_rope_desc."""
+    _fields_ = [("rotary_dim", c_int32), ("interleaved", c_int32), ("max_pos", c_int32), ("table", c_void_p)]
+
+
 class DecodePlan(ctypes.Structure):
     """Mirror of kvq_decode_plan."""
     _fields_ = [("stream_ctas", c_int32), ("window_ctas", c_int32), ("units", c_int32),
@@ -67,6 +82,10 @@ SIGNATURES = {
     "kvq_block_bytes": (c_int32, [c_int32, POINTER(c_size_t)]),
     "kvq_append": (c_int32, [POINTER(CacheDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
                              c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "kvq_rope_table": (c_int32, [POINTER(RopeFreqs), c_int32, c_int32, c_void_p, c_void_p]),
+    "kvq_rope_append": (c_int32, [POINTER(CacheDesc), POINTER(RopeDesc), c_void_p, c_int32, c_int64, c_void_p,
+                                  c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
+                                  c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
     "kvq_make_decode_plan": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
                                        POINTER(DecodePlan)]),
     "kvq_decode_device_plan": (c_int32, [POINTER(CacheDesc), c_int32, c_int32, c_int32, POINTER(DecodePlan)]),
@@ -142,6 +161,54 @@ def kvq_append(desc: CacheDesc, k_new, v_new, seq_idx, pos, mode: int, block_tab
     _check(load().kvq_append(ctypes.byref(desc), _ptr(k_new), _ptr(v_new), n, _ptr(seq_idx), _ptr(pos), mode,
                              _ptr(block_table), batch, max_blocks_per_seq, _ptr(err_word),
                              _stream(stream) if n else None), "kvq_append")
+
+
+def _tensor(t, dtype, where: str, shape=None, strided: bool = False):
+    """Pointer of a tensor argument of a newer entry point, None or a raw pointer
+    passed through.  The library cannot see a tensor's type, layout or device:
+    they are checked here, and a mismatch is an invalid argument."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if (t.dtype is not getattr(torch, dtype) or not t.is_cuda or t.device.index != torch.cuda.current_device()
+            or not (strided or t.is_contiguous()) or (shape is not None and tuple(t.shape) != tuple(shape))):
+        raise KvqError(KVQ_ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+def _rows(t, heads: int, n: int, where: str):
+    """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    ptr = _tensor(t, "bfloat16", where, strided=True)
+    inner = t.stride()[1:] if n else ()
+    if (tuple(t.shape) not in ((n, heads * 128), (n, heads, 128)) or
+            (n and inner != ((1,) if t.dim() == 2 else (128, 1)))):
+        raise KvqError(KVQ_ERR_INVALID_ARG, where)
+    return ptr, t.stride(0) if n > 1 else 0
+
+
+def kvq_rope_table(freqs: RopeFreqs, rotary_dim: int, max_pos: int, table, stream=None):
+    _check(load().kvq_rope_table(ctypes.byref(freqs), rotary_dim, max_pos,
+                                 _tensor(table, "float32", "kvq_rope_table"), _stream(stream)), "kvq_rope_table")
+
+
+def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_new, v_new, pos, seq_idx, slot,
+                    mode: int, block_table, batch: int, max_blocks_per_seq: int, err_word=None, stream=None):
+    """kvq_rope_append: ``pos`` are the rope positions (int32 [n], None to use ``slot``) and ``slot`` the cache
+    positions (the C argument pos).  q, k_new and v_new may be slices of one projection [n, heads * 128]: their row
+    strides are taken from the tensors.  q and q_out, or k_new and v_new, may be None."""
+    where = "kvq_rope_append"
+    ref = pos if pos is not None else slot
+    n = int(ref.shape[0])
+    qp, qs = _rows(q, q_heads, n, where)
+    kp, ks = _rows(k_new, desc.num_kv_heads, n, where)
+    vp, vs = _rows(v_new, desc.num_kv_heads, n, where)
+    _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
+                                  _tensor(q_out, "bfloat16", where), kp, ks, vp, vs, n,
+                                  _tensor(pos, "int32", where), _tensor(seq_idx, "int32", where),
+                                  _tensor(slot, "int32", where), mode, _tensor(block_table, "int32", where), batch,
+                                  max_blocks_per_seq, _ptr(err_word), _stream(stream) if n else None), where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,

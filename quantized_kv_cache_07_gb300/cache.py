@@ -84,6 +84,31 @@ class KVCache:
         return sum(t.numel() * t.element_size() for t in ts if t is not None)
 
 
+class RopeTable:
+    """Cosines and sines of one model's rotary positions (kvq_rope_table), made once.
+
+    ``scaling`` is "plain", "linear", "ntk" or "bands" (include/kvq.h, KVQ_ROPE_*);
+    ``desc`` goes to _lib.kvq_rope_append.
+    """
+
+    SCALINGS = {"plain": _lib.ROPE_PLAIN, "linear": _lib.ROPE_LINEAR, "ntk": _lib.ROPE_NTK, "bands": _lib.ROPE_BANDS}
+
+    def __init__(self, max_pos: int, rotary_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "plain", factor: float = 1.0, original_len: float = 0.0, low_turns: float = 0.0,
+                 high_turns: float = 0.0, amplitude: float = 1.0, device="cuda"):
+        _require_cuda()
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling {scaling!r} is none of {', '.join(self.SCALINGS)}")
+        if max_pos < 1 or rotary_dim < 2:
+            raise ValueError("a rotary table needs positions and pairs")
+        self.table = torch.empty(max_pos, rotary_dim // 2, 2, dtype=torch.float32, device=device)
+        freqs = _lib.RopeFreqs(base=base, scaling=self.SCALINGS[scaling], factor=factor, original_len=original_len,
+                               low_turns=low_turns, high_turns=high_turns, amplitude=amplitude)
+        _lib.kvq_rope_table(freqs, rotary_dim, max_pos, self.table)
+        self.desc = _lib.RopeDesc(rotary_dim=rotary_dim, interleaved=int(interleaved), max_pos=max_pos,
+                                  table=self.table.data_ptr())
+
+
 class DecodeWorkspace:
     """Scratch for the split-attention partials and merge counters of kvq_decode."""
 

@@ -2,6 +2,7 @@
 // Declarations and the contract of every entry point are in include/kvq.h.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/kvq.h"
@@ -16,6 +17,10 @@ constexpr int kMaxBatch = 4096;  // sequence geometry is staged in shared memory
 constexpr int kMaxWindow = 128;  // window ring: at most 8 bf16 blocks per (sequence, kv head)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+bool rotary_dim_ok(int R) { return R >= 8 && R <= kHeadDim && R % 8 == 0; }
 
 bool format_supported(int kb, int vb) {
   return (kb == 8 && vb == 8) || (kb == 4 && vb == 4) || (kb == 4 && vb == 8) || (kb == 8 && vb == 4) ||
@@ -421,6 +426,106 @@ kvq_status kvq_dequant(const kvq_cache_desc* cache, const int32_t* slots, int32_
   a.k_out = k_out;
   a.v_out = v_out;
   if (kvq::launch_dequant(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+kvq_status kvq_rope_table(const kvq_rope_freqs* freqs, int32_t rotary_dim, int32_t max_pos, float* table,
+                          void* stream) {
+  if (!freqs || !table || max_pos < 1) return KVQ_ERR_INVALID_ARG;
+  if (!rotary_dim_ok(rotary_dim)) return KVQ_ERR_UNSUPPORTED;
+  if (!aligned16(table)) return KVQ_ERR_ALIGNMENT;
+  if (!(freqs->base > 1.0) || !std::isfinite(freqs->base) || !std::isfinite(freqs->amplitude) || freqs->amplitude < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (freqs->scaling < KVQ_ROPE_PLAIN || freqs->scaling > KVQ_ROPE_BANDS) return KVQ_ERR_INVALID_ARG;
+  if (freqs->scaling != KVQ_ROPE_PLAIN && (!(freqs->factor >= 1.0) || !std::isfinite(freqs->factor)))
+    return KVQ_ERR_INVALID_ARG;
+  const bool bands = freqs->scaling == KVQ_ROPE_BANDS;
+  if (bands && (!(freqs->original_len > 0) || !std::isfinite(freqs->original_len) || !(freqs->low_turns >= 0) ||
+                !(freqs->high_turns > freqs->low_turns) || !std::isfinite(freqs->high_turns)))
+    return KVQ_ERR_INVALID_ARG;
+  const double R = rotary_dim;
+  const double base =
+      freqs->scaling == KVQ_ROPE_NTK ? freqs->base * std::pow(freqs->factor, R / (R - 2.0)) : freqs->base;
+  kvq::RopeFreqs f{};
+  f.amplitude = freqs->amplitude == 0.0 ? 1.0 : freqs->amplitude;
+  for (int j = 0; j < rotary_dim / 2; ++j) {
+    double w = std::pow(base, -2.0 * j / R);
+    if (freqs->scaling == KVQ_ROPE_LINEAR) w /= freqs->factor;
+    if (bands) {
+      const double turns = freqs->original_len * w / 6.283185307179586476925;
+      double keep = (turns - freqs->low_turns) / (freqs->high_turns - freqs->low_turns);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      w = keep * w + (1.0 - keep) * w / freqs->factor;
+    }
+    f.f[j] = w;
+  }
+  if (kvq::launch_rope_table(f, rotary_dim / 2, max_pos, table, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const void* q, int32_t q_heads,
+                           int64_t q_stride, void* q_out, const void* k_new, int64_t k_stride, const void* v_new,
+                           int64_t v_stride, int32_t n, const int32_t* rope_pos, const int32_t* seq_idx,
+                           const int32_t* pos, int32_t mode, const int32_t* block_table, int32_t batch,
+                           int32_t max_blocks_per_seq, uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!rope || n < 0 || q_heads < 0 || rope->max_pos < 1) return KVQ_ERR_INVALID_ARG;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return KVQ_ERR_INVALID_ARG;
+  if (!rotary_dim_ok(rope->rotary_dim)) return KVQ_ERR_UNSUPPORTED;
+  if (mode != KVQ_APPEND_QUANT && mode != KVQ_APPEND_RING && mode != KVQ_APPEND_STEP) return KVQ_ERR_INVALID_ARG;
+  const int64_t q_row = int64_t(q_heads) * kHeadDim, kv_row = int64_t(cache->num_kv_heads) * kHeadDim;
+  if (q_stride == 0) q_stride = q_row;
+  if (k_stride == 0) k_stride = kv_row;
+  if (v_stride == 0) v_stride = kv_row;
+  if (n == 0) return KVQ_OK;
+  if (!rope->table) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(rope->table)) return KVQ_ERR_ALIGNMENT;
+  const bool write = k_new != nullptr;
+  if (write != (v_new != nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (!write && q_heads == 0) return KVQ_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_heads > 0) || (q_out != nullptr) != (q_heads > 0)) return KVQ_ERR_INVALID_ARG;
+  if (q_heads > 0) {
+    if (q_stride < q_row) return KVQ_ERR_INVALID_ARG;
+    if (q == q_out && q_stride != q_row) return KVQ_ERR_INVALID_ARG;
+    if (!aligned8(q) || !aligned8(q_out) || q_stride % 4) return KVQ_ERR_ALIGNMENT;
+  }
+  if (write) {
+    if (!seq_idx || !pos || batch < 1) return KVQ_ERR_INVALID_ARG;
+    if (k_stride < kv_row || v_stride < kv_row) return KVQ_ERR_INVALID_ARG;
+    if (!aligned8(k_new) || !aligned8(v_new) || k_stride % 4 || v_stride % 4) return KVQ_ERR_ALIGNMENT;
+    if (mode != KVQ_APPEND_QUANT && cache->window == 0) return KVQ_ERR_INVALID_ARG;
+    if (mode == KVQ_APPEND_STEP && cache->k_bits == 2) return KVQ_ERR_UNSUPPORTED;
+    if (mode != KVQ_APPEND_RING && (!block_table || max_blocks_per_seq < 1)) return KVQ_ERR_INVALID_ARG;
+  }
+  if (!rope_pos && !pos) return KVQ_ERR_INVALID_ARG;
+  if (n * (int64_t(q_heads) + 2ll * cache->num_kv_heads) > (1ll << 33)) return KVQ_ERR_UNSUPPORTED;  // grid limit
+  kvq::RopeArgs a;
+  a.ap.c = view(cache);
+  a.ap.k_new = static_cast<const uint16_t*>(k_new);
+  a.ap.v_new = static_cast<const uint16_t*>(v_new);
+  a.ap.n = n;
+  a.ap.seq_idx = seq_idx;
+  a.ap.pos = pos;
+  a.ap.mode = mode;
+  a.ap.table = block_table;
+  a.ap.batch = batch;
+  a.ap.mbps = max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
+  a.ap.err = err_word;
+  a.write = write;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.Hq = q_heads;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.table = rope->table;
+  a.R = rope->rotary_dim;
+  a.max_pos = rope->max_pos;
+  a.interleaved = rope->interleaved != 0;
+  a.rope_pos = rope_pos ? rope_pos : pos;
+  if (kvq::launch_rope_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
 

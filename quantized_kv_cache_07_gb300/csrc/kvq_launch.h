@@ -39,6 +39,26 @@ struct AppendArgs {
   uint32_t* err;
 };
 
+// Rotary write: the append arguments (k_new, v_new with row strides in elements)
+// plus queries and the table of cosines and sines.
+struct RopeArgs {
+  AppendArgs ap;
+  bool write;  // keys and values given
+  const uint16_t* q;
+  uint16_t* q_out;
+  int Hq;  // query heads to turn (0: none)
+  long long q_stride, k_stride, v_stride;
+  const float* table;  // [max_pos][R / 2][2]
+  int R, max_pos;
+  bool interleaved;
+  const int* rope_pos;
+};
+
+struct RopeFreqs {
+  double f[64];
+  double amplitude;
+};
+
 struct DequantArgs {
   CacheView c;
   const int* slots;
@@ -88,6 +108,8 @@ int switch_blocks_for(int k_bits);
 DecodeLayout decode_layout(int B, int Hq, int H, int window, int stream_ctas, int switch_cost);
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float* table, cudaStream_t s);
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s);
 // Resident decode CTAs per SM for this cache format and batch (occupancy
 // query on the current device, cached); 0 for an unsupported format.

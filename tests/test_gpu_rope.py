@@ -1,0 +1,247 @@
+"""Rotary positions with the cache write (kvq_rope_table, kvq_rope_append).
+
+The rotation's definition is checked in float64: rotated values are the exact
+ones rounded to float32 and then to bf16, so queries are compared bit for bit,
+and the stored cache is compared, bit for bit, with kvq_append of the rotated keys.
+"""
+import numpy as np
+import pytest
+
+from oracle import kvq_oracle as O
+from synth import f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+FORMATS = {
+    "int8": dict(k_bits=8, v_bits=8), "int4_factor": dict(k_bits=4, v_bits=4, factor=True),
+    "asym_k4v8": dict(k_bits=4, v_bits=8, asym=True), "k8v4_chan": dict(k_bits=8, v_bits=4, factor=True,
+                                                                       k_per_channel=True),
+    "int2": dict(k_bits=2, v_bits=2), "asym_int2": dict(k_bits=2, v_bits=2, asym=True),
+    "bf16": dict(k_bits=16, v_bits=16),
+}
+
+
+def _t(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def _i(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
+
+
+def rotate(bits, cs, interleaved):
+    """bf16 bits [n, heads, 128] turned by cs [n, pairs, 2] (float64 of the table): bf16 bits."""
+    x = O.bf16_to_f64(bits)
+    pairs = cs.shape[1]
+    j = np.arange(pairs)
+    a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + pairs)
+    c, s = cs[:, None, :, 0], cs[:, None, :, 1]
+    y = x.copy()
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., a] * s + x[..., b] * c
+    return f32_to_bf16_bits(y.astype(np.float32))
+
+
+def _cache(fmt, H, blocks, rng, **kw):
+    from quantized_kv_cache_07_gb300.cache import KVCache
+    f = dict(FORMATS[fmt])
+    factor = (0.5 + rng.random((H, 128))).astype(np.float32) if f.pop("factor", False) else None
+    if f.get("k_per_channel"):
+        factor /= 40.0
+    return KVCache(blocks, H, channel_factor=factor, **f, **kw)
+
+
+def _pools(c):
+    return [None if t is None else t.view(torch.uint8).cpu().numpy()
+            for t in (c.k_codes, c.v_codes, c.meta, c.k_window, c.v_window)]
+
+
+def _same(a, b):
+    for x, y in zip(_pools(a), _pools(b)):
+        assert (x is None) == (y is None)
+        if x is not None:
+            np.testing.assert_array_equal(x, y)
+
+
+@pytest.mark.parametrize("scaling,kw", [
+    ("plain", {}), ("plain", dict(base=500000.0, rotary_dim=64, amplitude=1.25)), ("linear", dict(factor=4.0)),
+    ("ntk", dict(factor=8.0, rotary_dim=96)),
+    ("bands", dict(base=500000.0, factor=8.0, original_len=8192, low_turns=1.0, high_turns=4.0)),
+])
+def test_table_against_float64(scaling, kw):
+    from quantized_kv_cache_07_gb300.cache import RopeTable
+    n = 131072 if scaling == "plain" else 4099
+    t = RopeTable(n, scaling=scaling, **kw)
+    R, base, f = kw.get("rotary_dim", 128), kw.get("base", 10000.0), kw.get("factor", 1.0)
+    if scaling == "ntk":
+        base = base * f ** (R / (R - 2))
+    w = base ** (-2.0 * np.arange(R // 2) / R)
+    if scaling == "linear":
+        w = w / f
+    if scaling == "bands":
+        turns = kw["original_len"] * w / (2 * np.pi)
+        keep = np.clip((turns - kw["low_turns"]) / (kw["high_turns"] - kw["low_turns"]), 0, 1)
+        assert 0 < np.sum((keep > 0) & (keep < 1)) and keep[0] == 1 and keep[-1] == 0
+        w = keep * w + (1 - keep) * w / f
+    at = np.unique(np.concatenate([np.arange(40), np.random.default_rng(1).integers(0, n, 500), [n - 1]]))
+    angle = at[:, None] * w
+    ref = kw.get("amplitude", 1.0) * np.stack([np.cos(angle), np.sin(angle)], -1)
+    got = t.table.cpu().numpy()[at]
+    # half a step of float32 below 2, and 1e-10 for the angle's own rounding (131071 times 2^-53 and a few operations)
+    np.testing.assert_allclose(got, ref, rtol=2.0 ** -24, atol=1e-10)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("interleaved,R", [(False, 128), (True, 128), (False, 64), (True, 96), (False, 8)])
+def test_rotated_queries_and_stored_keys_bit_for_bit(fmt, interleaved, R):
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import RopeTable
+    rng = np.random.default_rng(3)
+    Hq, H, lens = 6, 2, (37, 1, 50)
+    n = sum(lens)
+    seq = np.repeat(np.arange(3), lens)
+    slot = np.concatenate([np.arange(l) for l in lens])
+    pos = slot + np.repeat([1000, 7, 4000], lens)           # positions far from the slots
+    table = _i(rng.permutation(12).reshape(3, 4))
+    qkv = f32_to_bf16_bits(rng.standard_normal((n, (Hq + 2 * H) * 128)).astype(np.float32))
+    qkv[5] = 0                                              # a zero row
+    rope = RopeTable(4096, rotary_dim=R, interleaved=interleaved)
+    x = _t(qkv)
+    q, k, v = x[:, :Hq * 128], x[:, Hq * 128:(Hq + H) * 128], x[:, (Hq + H) * 128:]
+    q_out = torch.full((n, Hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    state = rng.bit_generator.state
+    c = _cache(fmt, H, 12, rng)
+    _lib.kvq_rope_append(c.desc, rope.desc, q, Hq, q_out, k, v, _i(pos), _i(seq), _i(slot), _lib.APPEND_QUANT, table,
+                         3, 4, err_word=err)
+    cs = rope.table.cpu().numpy().astype(np.float64)[pos]
+    heads = qkv.reshape(n, -1, 128)
+    np.testing.assert_array_equal(q_out.view(torch.int16).cpu().numpy().view(np.uint16),
+                                  rotate(heads[:, :Hq], cs, interleaved))
+    rng.bit_generator.state = state
+    ref = _cache(fmt, H, 12, rng)
+    _lib.kvq_append(ref.desc, _t(rotate(heads[:, Hq:Hq + H], cs, interleaved)), _t(heads[:, Hq + H:]), _i(seq),
+                    _i(slot), _lib.APPEND_QUANT, table, 3, 4, err_word=err)
+    _same(c, ref)
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "int4_factor", "asym_k4v8"])
+def test_steps_through_the_window(fmt):
+    """Token by token through the bf16 window (KVQ_APPEND_STEP), every step with its own positions."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import RopeTable
+    rng = np.random.default_rng(4)
+    B, H, W, steps = 3, 2, 16, 41
+    rope = RopeTable(512, rotary_dim=64)
+    table = _i(rng.permutation(9).reshape(3, 3))
+    state = rng.bit_generator.state
+    a = _cache(fmt, H, 9, rng, window=W, window_batch=B)
+    rng.bit_generator.state = state
+    b = _cache(fmt, H, 9, rng, window=W, window_batch=B)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tab = rope.table.cpu().numpy().astype(np.float64)
+    for p in range(steps):
+        k = f32_to_bf16_bits(rng.standard_normal((B, H, 128)).astype(np.float32))
+        v = f32_to_bf16_bits(rng.standard_normal((B, H, 128)).astype(np.float32))
+        slot, pos = np.full(B, p), p + np.array([0, 100, 400])
+        _lib.kvq_rope_append(a.desc, rope.desc, None, 0, None, _t(k), _t(v), _i(pos), _i(np.arange(B)), _i(slot),
+                             _lib.APPEND_STEP, table, B, 3, err_word=err)
+        _lib.kvq_append(b.desc, _t(rotate(k, tab[pos], False)), _t(v), _i(np.arange(B)), _i(slot), _lib.APPEND_STEP,
+                        table, B, 3, err_word=err)
+    _same(a, b)
+    assert int(err.item()) == 0
+
+
+def test_bad_positions_are_flagged_and_their_rows_left_alone():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(5)
+    rope = RopeTable(64)
+    x = _t(f32_to_bf16_bits(rng.standard_normal((5, 2, 128)).astype(np.float32)))
+    for fmt in (dict(k_bits=8, v_bits=8), dict(k_bits=2, v_bits=2)):
+        c = KVCache(4, 2, **fmt)
+        c.k_codes.fill_(9)
+        q_out = torch.full((5, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        # every row at the start of a block of its own; rows 1 and 3 have no such position
+        _lib.kvq_rope_append(c.desc, rope.desc, x, 2, q_out, x, x, _i([0, -1, 63, 64, 5]), _i([0, 0, 0, 0, 9]),
+                             _i([0, 16, 32, 48, 0]), _lib.APPEND_QUANT, _i([[0, 1, 2, 3]]), 1, 4, err_word=err)
+        assert int(err.item()) == _lib.KVQ_DEVERR_POSITION
+        assert torch.all(q_out[[1, 3]] == 7) and not torch.any(torch.all((q_out[[0, 2, 4]] == 7).flatten(1), 1))
+        blocks = c.k_codes.view(2, 4, -1)
+        assert torch.all(blocks[:, [1, 3]] == 9) and torch.any(blocks[:, 0] != 9) and torch.any(blocks[:, 2] != 9)
+
+
+def test_queries_alone_in_place_and_keys_alone():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(6)
+    rope = RopeTable(300, interleaved=True)
+    bits = f32_to_bf16_bits(rng.standard_normal((9, 5, 128)).astype(np.float32))
+    pos = rng.integers(0, 300, 9)
+    want = rotate(bits, rope.table.cpu().numpy().astype(np.float64)[pos], True)
+    c = KVCache(1, 5, 8, 8)
+    q = _t(bits)
+    _lib.kvq_rope_append(c.desc, rope.desc, q, 5, q, None, None, _i(pos), None, None, _lib.APPEND_QUANT, None, 0, 0)
+    np.testing.assert_array_equal(q.view(torch.int16).cpu().numpy().view(np.uint16), want)
+    assert not torch.any(c.k_codes)
+    # keys alone, the cache slot standing for the position
+    slot = np.arange(9)
+    cs = rope.table.cpu().numpy().astype(np.float64)[slot]
+    _lib.kvq_rope_append(c.desc, rope.desc, None, 0, None, _t(bits), _t(bits), None, _i(slot * 0), _i(slot),
+                         _lib.APPEND_QUANT, _i([[0]]), 1, 1)
+    ref = KVCache(1, 5, 8, 8)
+    _lib.kvq_append(ref.desc, _t(rotate(bits, cs, True)), _t(bits), _i(slot * 0), _i(slot), _lib.APPEND_QUANT,
+                    _i([[0]]), 1, 1)
+    _same(c, ref)
+    # no rows
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    z = torch.empty(0, 5, 128, dtype=torch.bfloat16, device="cuda")
+    _lib.kvq_rope_append(c.desc, rope.desc, z, 5, z, z, z, e, e, e, _lib.APPEND_QUANT, _i([[0]]), 1, 1)
+
+
+def test_the_binding_refuses_what_the_library_cannot_see():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rope, c = RopeTable(64), KVCache(1, 2, 8, 8)
+    x = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda")
+    i = _i([0, 1, 2])
+
+    def call(q=x, q_out=x, k=x, v=x, pos=i, slot=i):
+        _lib.kvq_rope_append(c.desc, rope.desc, q, 2, q_out, k, v, pos, i * 0, slot, _lib.APPEND_QUANT, _i([[0]]), 1, 1)
+
+    call(q_out=torch.empty_like(x))
+    for kw in (dict(q=x.float()), dict(k=x.cpu()), dict(v=x[:, :1]), dict(q=x.transpose(1, 2)), dict(pos=i.long()),
+               dict(q_out=x.half()), dict(slot=i.repeat(2)[::2])):
+        with pytest.raises(_lib.KvqError) as e:
+            call(**kw)
+        assert e.value.status == _lib.KVQ_ERR_INVALID_ARG
+
+
+def test_captured_and_replayed_on_a_side_stream():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(8)
+    rope, c = RopeTable(200), KVCache(2, 2, 8, 8)
+    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    out, pos, slot = torch.zeros_like(x), _i([0, 0, 0, 0]), _i([0, 1, 0, 1])
+    seq, table = _i([0, 0, 1, 1]), _i([[0], [1]])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        _lib.kvq_rope_append(c.desc, rope.desc, x, 2, out, x, x, pos, seq, slot, _lib.APPEND_QUANT, table, 2, 1)
+    for _ in range(2):
+        bits = f32_to_bf16_bits(rng.standard_normal((4, 2, 128)).astype(np.float32))
+        p = rng.integers(0, 200, 4)
+        x.copy_(_t(bits))
+        pos.copy_(_i(p))
+        g.replay()
+        torch.cuda.synchronize()
+        want = rotate(bits, rope.table.cpu().numpy().astype(np.float64)[p], False)
+        np.testing.assert_array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), want)

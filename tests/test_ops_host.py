@@ -1,0 +1,83 @@
+"""Argument checks of the rotary write without a GPU: every refusal is a
+status, given before anything is launched."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.build import build
+    build()
+    return _lib
+
+
+def _desc(lib, **kw):
+    d = dict(num_kv_heads=8, head_dim=128, block_size=16, num_blocks=4, k_bits=8, v_bits=8,
+             k_codes=0x1000, v_codes=0x2000, meta=0x3000)
+    d.update(kw)
+    return lib.CacheDesc(**d)
+
+
+WINDOW = dict(window=16, window_batch=1, k_window=0xD000, v_window=0xE000)
+
+
+@pytest.mark.parametrize("cache,rope,kw,status", [
+    (dict(head_dim=64), {}, {}, 2),
+    ({}, dict(rotary_dim=0), {}, 2), ({}, dict(rotary_dim=12), {}, 2), ({}, dict(rotary_dim=136), {}, 2),
+    ({}, dict(interleaved=2), {}, 1), ({}, dict(max_pos=0), {}, 1), ({}, dict(table=None), {}, 1),
+    ({}, dict(table=0x4008), {}, 3),
+    ({}, {}, dict(n=-1), 1), ({}, {}, dict(q_heads=-1), 1), ({}, {}, dict(mode=3), 1),
+    # queries need an output and heads; keys need values; something has to be given
+    ({}, {}, dict(q_out=None), 1), ({}, {}, dict(q_heads=0), 1), ({}, {}, dict(v_new=None), 1),
+    ({}, {}, dict(q=None, q_out=None, q_heads=0, k_new=None, v_new=None), 1),
+    # row strides: a multiple of 4, not shorter than a row; in place only for contiguous rows
+    ({}, {}, dict(q_stride=32 * 128 - 4), 1), ({}, {}, dict(q_stride=32 * 128 + 2), 3),
+    ({}, {}, dict(k_stride=8 * 128 - 4), 1), ({}, {}, dict(v_stride=8 * 128 + 1), 3),
+    ({}, {}, dict(q_out=0x5000, q_stride=48 * 128), 1),
+    ({}, {}, dict(q=0x5004), 3), ({}, {}, dict(k_new=0x7004), 3), ({}, {}, dict(q_out=0x6002), 3),
+    # the write's own arguments, as kvq_append has them
+    ({}, {}, dict(seq_idx=None), 1), ({}, {}, dict(pos=None), 1), ({}, {}, dict(block_table=None), 1),
+    ({}, {}, dict(batch=0), 1), ({}, {}, dict(mbps=0), 1), ({}, {}, dict(mode=1), 1), ({}, {}, dict(mode=2), 1),
+    (dict(k_bits=2, v_bits=2, **WINDOW), {}, dict(mode=2), 2),
+    # queries only still need positions
+    ({}, {}, dict(k_new=None, v_new=None, rope_pos=None, pos=None), 1),
+    # more vectors than a grid holds
+    ({}, {}, dict(n=2 ** 30), 2),
+    # no rows: nothing to do, nothing read
+    ({}, dict(table=None), dict(n=0, q=None, k_new=None), 0),
+])
+def test_rope_append_refusals(lib, cache, rope, kw, status):
+    r = dict(rotary_dim=128, interleaved=0, max_pos=64, table=0x4000)
+    r.update(rope)
+    a = dict(q=0x5000, q_heads=32, q_stride=0, q_out=0x6000, k_new=0x7000, k_stride=0, v_new=0x8000, v_stride=0, n=1,
+             rope_pos=0x9000, seq_idx=0xA000, pos=0xB000, mode=0, block_table=0xC000, batch=1, mbps=1)
+    a.update(kw)
+    st = lib.load().kvq_rope_append(ctypes.byref(_desc(lib, **cache)), ctypes.byref(lib.RopeDesc(**r)), a["q"],
+                                    a["q_heads"], a["q_stride"], a["q_out"], a["k_new"], a["k_stride"], a["v_new"],
+                                    a["v_stride"], a["n"], a["rope_pos"], a["seq_idx"], a["pos"], a["mode"],
+                                    a["block_table"], a["batch"], a["mbps"], None, None)
+    assert st == status
+
+
+@pytest.mark.parametrize("freqs,rotary,max_pos,table,status", [
+    (dict(base=1.0), 128, 8, 0x4000, 1), (dict(base=float("nan")), 128, 8, 0x4000, 1),
+    (dict(base=float("inf")), 128, 8, 0x4000, 1), (dict(scaling=4), 128, 8, 0x4000, 1),
+    (dict(scaling=1, factor=0.5), 128, 8, 0x4000, 1), (dict(scaling=2, factor=float("nan")), 128, 8, 0x4000, 1),
+    (dict(scaling=3, factor=8.0), 128, 8, 0x4000, 1),
+    (dict(scaling=3, factor=8.0, original_len=8192, low_turns=4, high_turns=4), 128, 8, 0x4000, 1),
+    (dict(amplitude=-1.0), 128, 8, 0x4000, 1), ({}, 10, 8, 0x4000, 2), ({}, 128, 0, 0x4000, 1),
+    ({}, 128, 8, None, 1), ({}, 128, 8, 0x4004, 3),
+])
+def test_rope_table_refusals(lib, freqs, rotary, max_pos, table, status):
+    f = dict(base=10000.0, scaling=0, factor=1.0, amplitude=1.0)
+    f.update(freqs)
+    assert lib.load().kvq_rope_table(ctypes.byref(lib.RopeFreqs(**f)), rotary, max_pos, table, None) == status
+
+
+def test_null_descriptors_are_refused(lib):
+    so = lib.load()
+    assert so.kvq_rope_table(None, 128, 8, 0x4000, None) == lib.KVQ_ERR_INVALID_ARG
+    assert so.kvq_rope_append(ctypes.byref(_desc(lib)), None, 0x5000, 32, 0, 0x6000, 0x7000, 0, 0x8000, 0, 1, 0x9000,
+                              0xA000, 0xB000, 0, 0xC000, 1, 1, None, None) == lib.KVQ_ERR_INVALID_ARG
