@@ -466,6 +466,71 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, in
                                       size_t* bytes);
 
 /*
+ * kvq_attn_mass -- add the attention weight that every cached token received in
+ * a decode step to its running sum, for an eviction by that sum (kvq_evict).
+ * The pages name eviction beside quantization ([P3] "Precision floors and mixed
+ * cache formats") without a rule; this is the sum of the softmax weights:
+ *   mass[b][h][i] = decay * mass[b][h][i] + sum over the query heads g of KV head h of
+ *                   exp(q_g . k_hat_i / sqrt(D) - lse[b][g]),   i < seq_lens[b]
+ * with k_hat as kvq_decode reads it (all formats; tokens of the bf16 window, by
+ * their positions, included) and lse as kvq_decode or kvq_decode_shared wrote it for the same
+ * queries.  A query whose lse is -inf (it attended to nothing) adds nothing.
+ *   q, seq_lens, block_table : as kvq_decode
+ *   lse         : device float [batch][q_heads]
+ *   mass        : device float [batch][num_kv_heads][mass_stride], 16-byte aligned;
+ *                 entries at and behind seq_lens[b] are left as they are
+ *   mass_stride : a multiple of 4; a sequence longer than it sets KVQ_DEVERR_SEQ_LEN
+ *                 and is cut
+ *   decay       : finite; 1 keeps the whole history, less forgets it
+ * A block whose table entry is out of range sets KVQ_DEVERR_BLOCK_ID and its
+ * tokens' sums stay as they are.
+ */
+kvq_status kvq_attn_mass(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads, const float* lse,
+                         const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq, float* mass,
+                         int32_t mass_stride, float decay, uint32_t* err_word, void* stream);
+
+/*
+ * kvq_evict -- keep each sequence's heaviest tokens, in place ([P3] "Precision
+ * floors and mixed cache formats" names eviction beside quantization).  Every KV
+ * head chooses for itself.  Of the seq_lens[b] tokens of a sequence keep[b] stay
+ * (all of them if it holds no more): the protected ones first, then those
+ * of the largest mass, of equal ones the lowest slot (NaN counts as the least).  Their tokens then
+ * fill slots 0..new_lens[b]-1: a kept token in one of those slots stays there, and
+ * the i-th slot that lost its token takes the i-th kept token from behind.  Codes,
+ * scales and zero points move as they are stored; nothing is requantized.  Slots
+ * are no longer positions afterwards: the next token is appended at slot
+ * new_lens[b] and turned (kvq_rope_append) by its true position.
+ *   mass          : device float [batch][num_kv_heads][mass_stride] (kvq_attn_mass)
+ *   mass_out      : the kept tokens' sums by their new slots; may be mass itself, or NULL
+ *   keep          : device int32 [batch], >= 0
+ *   protect_first : tokens in the first slots that always stay where they are (attention
+ *                   sinks, a prefix shared with other sequences), >= 0
+ *   protect_recent: tokens whose position is among the last so many before next_pos[b] always
+ *                   stay, >= 0.  (Where more are protected than kept, the lowest slots stay.)
+ *   token_pos     : device int32 [batch][num_kv_heads][mass_stride], each token's position, or
+ *                   NULL: the slot (a sequence that was never evicted from)
+ *   token_pos_out : positions by new slots; may be token_pos itself, or NULL
+ *   next_pos      : device int32 [batch], the position of each sequence's next token; NULL
+ *                   (without token_pos only): seq_lens.  token_pos needs token_pos_out too.
+ *   new_lens      : device int32 [batch], not seq_lens itself (KVQ_ERR_INVALID_ARG)
+ *   source        : device int32 [batch][num_kv_heads][mass_stride]: the slot that each new
+ *                   slot's token came from
+ *   mass_stride   : entries of a row of mass, token_pos and source
+ * Entries at and behind new_lens[b] are left as they are, in every output and in the cache.
+ * Caches with a bf16 window: ring tokens are kept, and the number evicted is rounded down to a
+ * multiple of window, so that ring tokens keep their slots.  Their rows' entries move down with
+ * the length.  2-bit caches: KVQ_ERR_UNSUPPORTED (a token cannot leave its block's scale).
+ * Blocks of the evicted sequences must not be shared with other sequences, except those below
+ * protect_first.  Errors: SEQ_LEN (a length or keep < 0, or beyond the table or the row: cut),
+ * BLOCK_ID (the move of a token is skipped).
+ */
+kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass_out, int32_t mass_stride,
+                     const int32_t* seq_lens, const int32_t* keep, int32_t protect_first, int32_t protect_recent,
+                     const int32_t* token_pos, int32_t* token_pos_out, const int32_t* next_pos,
+                     const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, int32_t* new_lens,
+                     int32_t* source, uint32_t* err_word, void* stream);
+
+/*
  * kvq_dequant -- read the block store back: x_hat = RN32(code * s)
  * ([P2] "Quantization needs a scale convention"), without the per-channel key
  * factor; in the asymmetric format x_hat = RN32(u * s + m) (one fused

@@ -86,6 +86,11 @@ SIGNATURES = {
     "kvq_rope_append": (c_int32, [POINTER(CacheDesc), POINTER(RopeDesc), c_void_p, c_int32, c_int64, c_void_p,
                                   c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "kvq_attn_mass": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
+                                c_void_p, c_int32, c_float, c_void_p, c_void_p]),
+    "kvq_evict": (c_int32, [POINTER(CacheDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                            c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                            c_void_p]),
     "kvq_make_decode_plan": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
                                        POINTER(DecodePlan)]),
     "kvq_decode_device_plan": (c_int32, [POINTER(CacheDesc), c_int32, c_int32, c_int32, POINTER(DecodePlan)]),
@@ -209,6 +214,37 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
                                   _tensor(pos, "int32", where), _tensor(seq_idx, "int32", where),
                                   _tensor(slot, "int32", where), mode, _tensor(block_table, "int32", where), batch,
                                   max_blocks_per_seq, _ptr(err_word), _stream(stream) if n else None), where)
+
+
+def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,
+                  mass, decay: float = 1.0, err_word=None, stream=None, mass_stride: int | None = None):
+    """kvq_attn_mass; ``mass`` is float32 [batch, kv_heads, mass_stride]."""
+    where = "kvq_attn_mass"
+    if mass_stride is None:
+        mass_stride = int(mass.shape[-1])
+    _check(load().kvq_attn_mass(ctypes.byref(desc), _tensor(q, "bfloat16", where), batch, q_heads,
+                                _tensor(lse, "float32", where), _tensor(seq_lens, "int32", where),
+                                _tensor(block_table, "int32", where), max_blocks_per_seq,
+                                _tensor(mass, "float32", where, (batch, desc.num_kv_heads, mass_stride)), mass_stride,
+                                decay, _ptr(err_word), _stream(stream)), where)
+
+
+def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batch: int, max_blocks_per_seq: int,
+              source, new_lens, protect_first: int = 0, protect_recent: int = 0, token_pos=None, token_pos_out=None,
+              next_pos=None, err_word=None, stream=None, mass_stride: int | None = None):
+    """kvq_evict; mass, mass_out, source, token_pos and token_pos_out are [batch, kv_heads, mass_stride]."""
+    where = "kvq_evict"
+    if mass_stride is None:
+        mass_stride = int(mass.shape[-1])
+    rows = (batch, desc.num_kv_heads, mass_stride)
+    _check(load().kvq_evict(ctypes.byref(desc), _tensor(mass, "float32", where, rows),
+                            _tensor(mass_out, "float32", where, rows), mass_stride,
+                            _tensor(seq_lens, "int32", where, (batch,)), _tensor(keep, "int32", where, (batch,)),
+                            protect_first, protect_recent, _tensor(token_pos, "int32", where, rows),
+                            _tensor(token_pos_out, "int32", where, rows), _tensor(next_pos, "int32", where, (batch,)),
+                            _tensor(block_table, "int32", where), batch, max_blocks_per_seq,
+                            _tensor(new_lens, "int32", where, (batch,)), _tensor(source, "int32", where, rows),
+                            _ptr(err_word), _stream(stream)), where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,

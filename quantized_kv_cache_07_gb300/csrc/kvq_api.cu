@@ -529,4 +529,72 @@ kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rop
   return KVQ_OK;
 }
 
+kvq_status kvq_attn_mass(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads, const float* lse,
+                         const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq, float* mass,
+                         int32_t mass_stride, float decay, uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_decode_shape(cache, batch, q_heads);
+  if (st != KVQ_OK) return st;
+  if (batch == 0) return KVQ_OK;
+  if (!q || !lse || !seq_lens || !block_table || !mass || max_blocks_per_seq < 1 || mass_stride < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if (!std::isfinite(decay)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(mass) || mass_stride % 4) return KVQ_ERR_ALIGNMENT;
+  kvq::MassArgs a;
+  a.c = view(cache);
+  a.q = static_cast<const uint16_t*>(q);
+  a.B = batch;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->num_kv_heads;
+  a.lse = lse;
+  a.seq_lens = seq_lens;
+  a.table = block_table;
+  a.mbps = max_blocks_per_seq;
+  a.mass = mass;
+  a.stride = mass_stride;
+  a.decay = decay;
+  a.err = err_word;
+  if (kvq::launch_mass(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass_out, int32_t mass_stride,
+                     const int32_t* seq_lens, const int32_t* keep, int32_t protect_first, int32_t protect_recent,
+                     const int32_t* token_pos, int32_t* token_pos_out, const int32_t* next_pos,
+                     const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, int32_t* new_lens,
+                     int32_t* source, uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (cache->k_bits == 2) return KVQ_ERR_UNSUPPORTED;
+  st = check_decode_shape(cache, batch, cache->num_kv_heads);
+  if (st != KVQ_OK) return st;
+  if (protect_first < 0 || protect_recent < 0) return KVQ_ERR_INVALID_ARG;
+  if (batch == 0) return KVQ_OK;
+  if (!mass || !seq_lens || !keep || !block_table || !new_lens || !source || max_blocks_per_seq < 1 ||
+      mass_stride < 1 || new_lens == seq_lens || new_lens == keep)
+    return KVQ_ERR_INVALID_ARG;
+  if (token_pos && (!token_pos_out || !next_pos)) return KVQ_ERR_INVALID_ARG;  // positions would be lost, or misread
+  kvq::EvictArgs a;
+  a.c = view(cache);
+  a.mass = mass;
+  a.mass_out = mass_out;
+  a.token_pos = token_pos;
+  a.pos_out = token_pos_out;
+  a.next_pos = next_pos;
+  a.source = source;
+  a.new_lens = new_lens;
+  a.seq_lens = seq_lens;
+  a.keep = keep;
+  a.stride = mass_stride;
+  a.protect_first = protect_first;
+  a.protect_recent = protect_recent;
+  a.table = block_table;
+  a.B = batch;
+  a.mbps = max_blocks_per_seq;
+  a.err = err_word;
+  if (kvq::launch_evict(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
 }  // extern "C"

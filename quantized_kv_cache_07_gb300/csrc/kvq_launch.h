@@ -59,6 +59,37 @@ struct RopeFreqs {
   double amplitude;
 };
 
+struct MassArgs {
+  CacheView c;
+  const uint16_t* q;  // bf16 [B][Hq][128]
+  int B, Hq, G;
+  const float* lse;  // [B][Hq]
+  const int* seq_lens;
+  const int* table;
+  int mbps;
+  float* mass;  // [B][H][stride]
+  int stride;
+  float decay;
+  uint32_t* err;
+};
+
+struct EvictArgs {
+  CacheView c;
+  const float* mass;  // [B][H][stride], as all per-token rows
+  float* mass_out;    // or null
+  const int* token_pos;  // or null: the slot
+  int* pos_out;          // or null
+  const int* next_pos;   // [B] or null: the length
+  int* source;
+  int* new_lens;  // [B]
+  const int* seq_lens;
+  const int* keep;  // [B]
+  int stride, protect_first, protect_recent;
+  const int* table;
+  int B, mbps;
+  uint32_t* err;
+};
+
 struct DequantArgs {
   CacheView c;
   const int* slots;
@@ -110,6 +141,8 @@ DecodeLayout decode_layout(int B, int Hq, int H, int window, int stream_ctas, in
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float* table, cudaStream_t s);
+cudaError_t launch_mass(const MassArgs& a, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s);
 // Resident decode CTAs per SM for this cache format and batch (occupancy
 // query on the current device, cached); 0 for an unsupported format.

@@ -1,5 +1,5 @@
-"""Argument checks of the rotary write without a GPU: every refusal is a
-status, given before anything is launched."""
+"""Argument checks of the cache operators beside decode, without a GPU: every
+refusal is a status, given before anything is launched."""
 import ctypes
 
 import pytest
@@ -81,3 +81,42 @@ def test_null_descriptors_are_refused(lib):
     assert so.kvq_rope_table(None, 128, 8, 0x4000, None) == lib.KVQ_ERR_INVALID_ARG
     assert so.kvq_rope_append(ctypes.byref(_desc(lib)), None, 0x5000, 32, 0, 0x6000, 0x7000, 0, 0x8000, 0, 1, 0x9000,
                               0xA000, 0xB000, 0, 0xC000, 1, 1, None, None) == lib.KVQ_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("cache,kw,status", [
+    (dict(block_size=32), {}, 2), ({}, dict(batch=-1), 1), ({}, dict(batch=5000), 2), ({}, dict(q_heads=12), 1),
+    ({}, dict(q_heads=128), 2), ({}, dict(q=None), 1), ({}, dict(lse=None), 1), ({}, dict(lens=None), 1),
+    ({}, dict(table=None), 1), ({}, dict(mass=None), 1), ({}, dict(mbps=0), 1), ({}, dict(stride=0), 1),
+    ({}, dict(stride=18), 3), ({}, dict(mass=0x9004), 3), ({}, dict(q=0x5008), 3), ({}, dict(decay=float("nan")), 1),
+    ({}, dict(decay=float("inf")), 1), ({}, dict(batch=0, q=None), 0),
+    (dict(window=16, window_batch=1, k_window=0xD000, v_window=0xE000), dict(batch=2), 1),
+])
+def test_attn_mass_refusals(lib, cache, kw, status):
+    a = dict(q=0x5000, batch=1, q_heads=8, lse=0x6000, lens=0x7000, table=0x8000, mbps=1, mass=0x9000, stride=16,
+             decay=1.0)
+    a.update(kw)
+    st = lib.load().kvq_attn_mass(ctypes.byref(_desc(lib, **cache)), a["q"], a["batch"], a["q_heads"], a["lse"],
+                                  a["lens"], a["table"], a["mbps"], a["mass"], a["stride"], a["decay"], None, None)
+    assert st == status
+
+
+@pytest.mark.parametrize("cache,kw,status", [
+    # a token cannot leave a 2-bit block's scale
+    (dict(k_bits=2, v_bits=2), {}, 2), (dict(k_codes=None), {}, 1),
+    ({}, dict(batch=-1), 1), ({}, dict(batch=5000), 2), ({}, dict(mass=None), 1), ({}, dict(lens=None), 1),
+    ({}, dict(keep=None), 1), ({}, dict(table=None), 1), ({}, dict(new_lens=None), 1), ({}, dict(source=None), 1),
+    ({}, dict(stride=0), 1), ({}, dict(mbps=0), 1), ({}, dict(first=-1), 1), ({}, dict(recent=-1), 1),
+    # the lengths are read by both launches
+    ({}, dict(new_lens=0x6000), 1), ({}, dict(new_lens=0x7000), 1),
+    # positions in need positions out and the next position
+    ({}, dict(pos=0xA000), 1), ({}, dict(pos=0xA000, pos_out=0xA000), 1), ({}, dict(pos=0xA000, next=0xB000), 1),
+    ({}, dict(batch=0, mass=None), 0),
+])
+def test_evict_refusals(lib, cache, kw, status):
+    a = dict(mass=0x5000, mass_out=None, stride=16, lens=0x6000, keep=0x7000, first=0, recent=0, pos=None,
+             pos_out=None, next=None, table=0x8000, batch=1, mbps=1, new_lens=0x9000, source=0xC000)
+    a.update(kw)
+    st = lib.load().kvq_evict(ctypes.byref(_desc(lib, **cache)), a["mass"], a["mass_out"], a["stride"], a["lens"],
+                              a["keep"], a["first"], a["recent"], a["pos"], a["pos_out"], a["next"], a["table"],
+                              a["batch"], a["mbps"], a["new_lens"], a["source"], None, None)
+    assert st == status
