@@ -376,6 +376,39 @@ kvq_status kvq_decode_ex(const kvq_cache_desc* cache, const void* q, int32_t bat
                          void* out, int32_t out_fp32, float* lse, void* workspace, size_t workspace_bytes,
                          int32_t stream_ctas, uint32_t flags, uint32_t* err_word, void* stream);
 
+/*
+ * kvq_decode_shared -- kvq_decode for a batch whose sequences share prefixes (a
+ * system prompt, a document that many requests ask about, samples of one
+ * prompt).  "The cache is written incrementally and read repeatedly" ([P3], opening
+ * section): a prefix that several sequences hold in the same blocks is read once
+ * for all of them.  The result is kvq_decode's on the same arguments, within the
+ * output tolerance:
+ *   out[b] = sum_i softmax(q[b] . k_hat_i / sqrt(D)) v_hat_i,  i < seq_lens[b].
+ * Group i is sequences group_start[i] .. group_start[i+1] - 1 of the batch; the first
+ * prefix_blocks[i] entries of their block-table rows are the same blocks (read from
+ * the row of the group's first sequence, whatever its own length).  A sequence
+ * may be shorter than the prefix: it attends to its own seq_lens[b] tokens of
+ * it.  Sequences outside every group share nothing.
+ *   group_start  : device int32 [num_groups + 1], not falling, within [0, batch];
+ *                  otherwise KVQ_DEVERR_POSITION (and the next valid start is used)
+ *   prefix_blocks: device int32 [num_groups], 16-token blocks, within [0, max_blocks_per_seq];
+ *                  otherwise KVQ_DEVERR_SEQ_LEN (and the nearest is used)
+ *   num_groups   : 1..256 (more: KVQ_ERR_UNSUPPORTED)
+ *   workspace    : >= kvq_decode_shared_workspace_size bytes, zeroed once by kvq_workspace_init;
+ *                  one per concurrently running call
+ * Everything else as kvq_decode, every cache format and query mode, the bf16
+ * window (which holds each sequence's own last tokens) included.
+ */
+kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
+                             const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                             int32_t num_groups, const int32_t* group_start, const int32_t* prefix_blocks, void* out,
+                             int32_t out_fp32, float* lse, void* workspace, size_t workspace_bytes,
+                             uint32_t* err_word, void* stream);
+
+/* Workspace bytes kvq_decode_shared needs on the current device. */
+kvq_status kvq_decode_shared_workspace_size(const kvq_cache_desc* cache, int32_t batch, int32_t q_heads,
+                                            int32_t num_groups, size_t* bytes);
+
 /* Size of the fixed device scratch behind kvq_decode_static_scratch (bytes). */
 #define KVQ_STATIC_SCRATCH_BYTES (8u << 20)
 

@@ -86,6 +86,10 @@ SIGNATURES = {
     "kvq_rope_append": (c_int32, [POINTER(CacheDesc), POINTER(RopeDesc), c_void_p, c_int32, c_int64, c_void_p,
                                   c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "kvq_decode_shared": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                                    c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p,
+                                    c_void_p]),
+    "kvq_decode_shared_workspace_size": (c_int32, [POINTER(CacheDesc), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
     "kvq_attn_mass": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
                                 c_void_p, c_int32, c_float, c_void_p, c_void_p]),
     "kvq_evict": (c_int32, [POINTER(CacheDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
@@ -214,6 +218,30 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
                                   _tensor(pos, "int32", where), _tensor(seq_idx, "int32", where),
                                   _tensor(slot, "int32", where), mode, _tensor(block_table, "int32", where), batch,
                                   max_blocks_per_seq, _ptr(err_word), _stream(stream) if n else None), where)
+
+
+def kvq_decode_shared_workspace_size(desc: CacheDesc, batch: int, q_heads: int, num_groups: int) -> int:
+    out = c_size_t(0)
+    _check(load().kvq_decode_shared_workspace_size(ctypes.byref(desc), batch, q_heads, num_groups, ctypes.byref(out)),
+           "kvq_decode_shared_workspace_size")
+    return out.value
+
+
+def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, block_table, max_blocks_per_seq: int,
+                      num_groups: int, group_start, prefix_blocks, out, lse=None, workspace=None,
+                      workspace_bytes: int = 0, err_word=None, stream=None, out_fp32: bool | None = None):
+    where = "kvq_decode_shared"
+    if out_fp32 is None:
+        import torch
+        out_fp32 = out.dtype == torch.float32
+    _check(load().kvq_decode_shared(ctypes.byref(desc), _tensor(q, "bfloat16", where), batch, q_heads,
+                                    _tensor(seq_lens, "int32", where), _tensor(block_table, "int32", where),
+                                    max_blocks_per_seq, num_groups,
+                                    _tensor(group_start, "int32", where, (num_groups + 1,)),
+                                    _tensor(prefix_blocks, "int32", where, (num_groups,)),
+                                    _tensor(out, "float32" if out_fp32 else "bfloat16", where), int(bool(out_fp32)),
+                                    _tensor(lse, "float32", where), _tensor(workspace, "uint8", where),
+                                    workspace_bytes, _ptr(err_word), _stream(stream)), where)
 
 
 def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,

@@ -119,6 +119,15 @@ class DecodeWorkspace:
         _lib.kvq_workspace_init(self.buf, self.nbytes)
 
 
+class SharedWorkspace:
+    """Scratch of kvq_decode_shared, zeroed once."""
+
+    def __init__(self, cache: KVCache, batch: int, q_heads: int, num_groups: int):
+        self.nbytes = _lib.kvq_decode_shared_workspace_size(cache.desc, batch, q_heads, num_groups)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=cache.device)
+        _lib.kvq_workspace_init(self.buf, self.nbytes)
+
+
 def _bits_tensor(bits: np.ndarray, device) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).to(device).view(torch.bfloat16)
 

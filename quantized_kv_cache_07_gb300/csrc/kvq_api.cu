@@ -120,6 +120,44 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
   return (long long)((n + TR - 1) / TR) * kv_heads;
 }
 
+// Workspace of kvq_decode_shared: the suffix decode's, its result, and the prefix records.
+kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::DecodeLayout* dl,
+                         kvq::SharedLayout* sl) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  const kvq::CacheView v = view(c);
+  const int H = c->num_kv_heads, G = q_heads / H;
+  const int per = kvq::suffix_ctas_per_sm_for(c->k_bits, c->v_bits, c->asym != 0, v.q_bits, batch);
+  const int P = stream_ctas_for(sms * per, c->window > 0 ? batch * H : 0, batch * H);
+  sl->ctas = kvq::shared_tiles_ctas(v);
+  if (P <= 0 || sl->ctas <= 0) return KVQ_ERR_CUDA;
+  *dl = kvq::decode_layout(batch, q_heads, H, c->window, P, kvq::switch_blocks_for(c->k_bits));
+  sl->tile = 16;
+  // every group adds at most one tile that is not full
+  const long long units = ((long long)batch * G / sl->tile + num_groups) * H;
+  sl->slots = sl->ctas + int(units);
+  size_t o = dl->total;
+  sl->off_o = o;
+  o = round_up(o + size_t(batch) * q_heads * kHeadDim * 4, 256);
+  sl->off_lse = o;
+  o = round_up(o + size_t(batch) * q_heads * 4, 256);
+  sl->off_m = o;
+  o = round_up(o + size_t(sl->slots) * sl->tile * 4, 256);
+  sl->off_l = o;
+  o = round_up(o + size_t(sl->slots) * sl->tile * 4, 256);
+  sl->off_rec = o;
+  o = round_up(o + size_t(sl->slots) * sl->tile * kHeadDim * 4, 256);
+  sl->total = o;
+  return KVQ_OK;
+}
+
+kvq_status check_groups(int num_groups) {
+  if (num_groups < 1) return KVQ_ERR_INVALID_ARG;
+  return num_groups > kvq::kMaxGroups ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+}
+
 }  // namespace
 
 namespace kvq {
@@ -526,6 +564,69 @@ kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rop
   a.interleaved = rope->interleaved != 0;
   a.rope_pos = rope_pos ? rope_pos : pos;
   if (kvq::launch_rope_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+kvq_status kvq_decode_shared_workspace_size(const kvq_cache_desc* cache, int32_t batch, int32_t q_heads,
+                                            int32_t num_groups, size_t* bytes) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (!bytes) return KVQ_ERR_INVALID_ARG;
+  if ((st = check_decode_shape(cache, batch, q_heads)) != KVQ_OK) return st;
+  if ((st = check_groups(num_groups)) != KVQ_OK) return st;
+  kvq::DecodeLayout dl;
+  kvq::SharedLayout sl;
+  if ((st = shared_layout(cache, batch, q_heads, num_groups, &dl, &sl)) != KVQ_OK) return st;
+  *bytes = sl.total;
+  return KVQ_OK;
+}
+
+kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
+                             const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                             int32_t num_groups, const int32_t* group_start, const int32_t* prefix_blocks, void* out,
+                             int32_t out_fp32, float* lse, void* workspace, size_t workspace_bytes,
+                             uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if ((st = check_decode_shape(cache, batch, q_heads)) != KVQ_OK) return st;
+  if ((st = check_groups(num_groups)) != KVQ_OK) return st;
+  if (batch == 0) return KVQ_OK;
+  if (!q || !seq_lens || !block_table || !out || max_blocks_per_seq < 1 || !group_start || !prefix_blocks)
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
+  if (!workspace) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  kvq::SharedArgs s;
+  if ((st = shared_layout(cache, batch, q_heads, num_groups, &s.d.lay, &s.sl)) != KVQ_OK) return st;
+  if (workspace_bytes < s.sl.total) return KVQ_ERR_WORKSPACE;
+  kvq::DecodeArgs& a = s.d;
+  a.c = view(cache);
+  a.q = static_cast<const uint16_t*>(q);
+  a.B = batch;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->num_kv_heads;
+  a.seq_lens = seq_lens;
+  a.pos = nullptr;
+  a.seq_of = nullptr;
+  a.nseq = batch;
+  a.table = block_table;
+  a.mbps = max_blocks_per_seq;
+  a.out = out;
+  a.out_fp32 = out_fp32 ? 1 : 0;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.err = err_word;
+  a.group_start = group_start;
+  a.prefix_blocks = prefix_blocks;
+  a.num_groups = num_groups;
+  kvq::DecodeArgs suffix = a;  // its result goes to the workspace
+  suffix.out = a.ws + s.sl.off_o;
+  suffix.out_fp32 = 1;
+  suffix.lse = reinterpret_cast<float*>(a.ws + s.sl.off_lse);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (kvq::launch_suffix(suffix, cs) != cudaSuccess || kvq::launch_shared_tiles(s, cs) != cudaSuccess ||
+      kvq::launch_shared_merge(s, cs) != cudaSuccess)
+    return KVQ_ERR_CUDA;
   return KVQ_OK;
 }
 

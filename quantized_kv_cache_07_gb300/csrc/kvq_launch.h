@@ -127,6 +127,27 @@ struct DecodeArgs {
   // 1: seq_lens and the block table are final before the preceding kernel on
   // the stream ends (KVQ_DECODE_GEOMETRY_READY): read them before the wait
   int ahead = 0;
+  // kvq_decode_shared: groups of sequences with a common prefix
+  const int* group_start = nullptr;    // [num_groups + 1]
+  const int* prefix_blocks = nullptr;  // [num_groups]
+  int num_groups = 0;
+};
+
+constexpr int kMaxGroups = 256;
+
+// Workspace of kvq_decode_shared behind the suffix decode's own (byte offsets).
+// The prefix is split over `ctas` CTAs; a unit is a tile of `tile` query vectors of
+// one group and KV head; CTA c's share of unit u is record c + u.
+struct SharedLayout {
+  int ctas, tile, slots;
+  size_t off_o, off_lse;             // suffix result: float [B][Hq][128], [B][Hq]
+  size_t off_m, off_l, off_rec;      // records: float [slots][tile], twice, and [slots][tile][128]
+  size_t total;
+};
+
+struct SharedArgs {
+  DecodeArgs d;  // out, lse: the caller's
+  SharedLayout sl;
 };
 
 // The largest GQA group (query heads per KV head) the decode kernel takes: one
@@ -154,6 +175,15 @@ cudaError_t launch_decode_asym(const DecodeArgs& a, cudaStream_t s);
 // The two-part fp16 query instantiations (kvq_decode_q32.cu).
 int decode_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch, bool rows);
 cudaError_t launch_decode_q32(const DecodeArgs& a, cudaStream_t s);
+// kvq_decode_shared: the suffix decode (kvq_decode_suffix*.cu), the prefix on query tiles
+// (kvq_shared_tiles.cu) and the merge of both (kvq_shared.cu).
+int suffix_ctas_per_sm_for(int k_bits, int v_bits, bool asym, int q_bits, int batch);
+cudaError_t launch_suffix(const DecodeArgs& a, cudaStream_t s);
+int suffix_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch);
+cudaError_t launch_suffix_q32(const DecodeArgs& a, cudaStream_t s);
+int shared_tiles_ctas(const CacheView& c);  // one wave on the current device, 0: failure
+cudaError_t launch_shared_tiles(const SharedArgs& a, cudaStream_t s);
+cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s);
 // Prefill on 16-vector query tiles (kvq_prefill_tiles.cu): quantized blocks
 // (8-, 4- or 2-bit, symmetric or asymmetric), any query format, no window.
 // Needs no workspace.

@@ -1,0 +1,106 @@
+// The merge of kvq_decode_shared: each query's prefix records and the result of
+// the suffix decode, by log-sum-exp.
+//
+// One warp per query vector; lane l holds dims 4l..4l+3.  The vector's unit and the
+// CTAs that own its steps follow from the same arithmetic as in the prefix
+// kernel, so nothing is counted and no order depends on the scheduling.
+#include "kvq_shared.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kMergeThreads = 256;
+
+__global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const SharedArgs sa, int step) {
+  __shared__ SharedGeo geo;
+  const DecodeArgs& a = sa.d;
+  const int tid = threadIdx.x, lane = tid & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
+  const long long q = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
+  if (q >= (long long)a.B * a.Hq) return;
+  const int b = int(q / a.Hq), hq = int(q % a.Hq), h = hq / a.G, hj = hq % a.G;
+  const float4 so = reinterpret_cast<const float4*>(a.ws + sa.sl.off_o)[q * (kHeadDim / 4) + lane];
+  const float sl = reinterpret_cast<const float*>(a.ws + sa.sl.off_lse)[q];
+  // the suffix is a record with l = 1
+  float M = sl == kNegInf ? kNegInf : sl * kLog2e;
+  float l = sl == kNegInf ? 0.f : 1.f;
+  float4 o = sl == kNegInf ? make_float4(0.f, 0.f, 0.f, 0.f) : so;
+  const int g = group_of(&geo.g, a.num_groups, b);
+  if (g >= 0 && geo.g.blocks[g] > 0) {
+    const int v = (b - geo.g.start[g]) * a.G + hj, tile = v / sa.sl.tile, steps = steps_of(geo.g.blocks[g], step);
+    const int i = tile * a.c.H + h, u = geo.unit0[g] + i;
+    const long long x = geo.x0[g] + (long long)i * steps;
+    const int Pe = shared_ctas(&geo, sa.sl.ctas);
+    const long long c0 = cta_of(x, geo.T, Pe), c1 = cta_of(x + steps - 1, geo.T, Pe);
+    const float* pm = reinterpret_cast<const float*>(a.ws + sa.sl.off_m);
+    const float* pl = reinterpret_cast<const float*>(a.ws + sa.sl.off_l);
+    const float* po = reinterpret_cast<const float*>(a.ws + sa.sl.off_rec);
+    constexpr int kR = 8;  // records in flight
+    for (long long c = c0; c <= c1; c += kR) {
+      float mr[kR], lr[kR];
+      float4 orr[kR];
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        mr[r] = kNegInf;
+        lr[r] = 0.f;
+        orr[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + r <= c1) {
+          const size_t at = size_t(c + r + u) * sa.sl.tile + v % sa.sl.tile;
+          mr[r] = pm[at];
+          lr[r] = pl[at];
+          orr[r] = reinterpret_cast<const float4*>(po + at * kHeadDim)[lane];
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) Mn = fmaxf(Mn, mr[r]);
+      const float rs = M == kNegInf ? 0.f : exp2f(M - Mn);
+      l *= rs;
+      o.x *= rs;
+      o.y *= rs;
+      o.z *= rs;
+      o.w *= rs;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const float w = mr[r] == kNegInf ? 0.f : exp2f(mr[r] - Mn);
+        l = fmaf(w, lr[r], l);
+        o.x = fmaf(w, orr[r].x, o.x);
+        o.y = fmaf(w, orr[r].y, o.y);
+        o.z = fmaf(w, orr[r].z, o.z);
+        o.w = fmaf(w, orr[r].w, o.w);
+      }
+      M = Mn;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;  // nothing attended: out = 0
+  if (a.out_fp32) {
+    reinterpret_cast<float4*>(a.out)[q * (kHeadDim / 4) + lane] =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  } else {
+    reinterpret_cast<uint2*>(a.out)[q * (kHeadDim / 4) + lane] =
+        make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[q] = l > 0.f ? (M + log2f(l)) * kLn2 : kNegInf;
+}
+
+}  // namespace
+
+cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s) {
+  const long long warps = (long long)a.d.B * a.d.Hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((warps + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_merge_kernel, a, kConsumerWarps);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace kvq

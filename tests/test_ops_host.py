@@ -120,3 +120,25 @@ def test_evict_refusals(lib, cache, kw, status):
                               a["keep"], a["first"], a["recent"], a["pos"], a["pos_out"], a["next"], a["table"],
                               a["batch"], a["mbps"], a["new_lens"], a["source"], None, None)
     assert st == status
+
+
+@pytest.mark.parametrize("cache,kw,status", [
+    (dict(head_dim=64), {}, 2), ({}, dict(batch=-1), 1), ({}, dict(batch=5000), 2), ({}, dict(q_heads=12), 1),
+    ({}, dict(q_heads=128), 2), ({}, dict(groups=0), 1), ({}, dict(groups=257), 2), ({}, dict(q=None), 1),
+    ({}, dict(lens=None), 1), ({}, dict(table=None), 1), ({}, dict(mbps=0), 1), ({}, dict(start=None), 1),
+    ({}, dict(blocks=None), 1), ({}, dict(out=None), 1), ({}, dict(q=0x5008), 3), ({}, dict(out=0xA008), 3),
+    ({}, dict(ws=None), 4), ({}, dict(ws=0xB008), 3), ({}, dict(batch=0, q=None, ws=None), 0),
+])
+def test_decode_shared_refusals(lib, cache, kw, status):
+    a = dict(q=0x5000, batch=2, q_heads=8, lens=0x6000, table=0x7000, mbps=4, groups=1, start=0x8000, blocks=0x9000,
+             out=0xA000, ws=0xB000, nbytes=1 << 30)
+    a.update(kw)
+    st = lib.load().kvq_decode_shared(ctypes.byref(_desc(lib, **cache)), a["q"], a["batch"], a["q_heads"], a["lens"],
+                                      a["table"], a["mbps"], a["groups"], a["start"], a["blocks"], a["out"], 0, None,
+                                      a["ws"], a["nbytes"], None, None)
+    assert st == status
+    import ctypes as c
+    size = c.c_size_t(0)
+    if "groups" in kw or "batch" in kw and kw["batch"] != 0:
+        assert lib.load().kvq_decode_shared_workspace_size(ctypes.byref(_desc(lib)), a["batch"], a["q_heads"],
+                                                           a["groups"], c.byref(size)) == status
