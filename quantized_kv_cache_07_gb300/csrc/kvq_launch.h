@@ -140,6 +140,7 @@ constexpr int kMaxGroups = 256;
 // one group and KV head; CTA c's share of unit u is record c + u.
 struct SharedLayout {
   int ctas, tile, slots;
+  bool tc;  // tcgen05 path (tile 128), else mma.sync (tile 16)
   size_t off_o, off_lse;             // suffix result: float [B][Hq][128], [B][Hq]
   size_t off_m, off_l, off_rec;      // records: float [slots][tile], twice, and [slots][tile][128]
   size_t total;
@@ -176,13 +177,15 @@ cudaError_t launch_decode_asym(const DecodeArgs& a, cudaStream_t s);
 int decode_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch, bool rows);
 cudaError_t launch_decode_q32(const DecodeArgs& a, cudaStream_t s);
 // kvq_decode_shared: the suffix decode (kvq_decode_suffix*.cu), the prefix on query tiles
-// (kvq_shared_tiles.cu) and the merge of both (kvq_shared.cu).
+// (kvq_shared_tiles.cu: mma.sync, kvq_shared_tc.cu: tcgen05) and the merge (kvq_shared.cu).
 int suffix_ctas_per_sm_for(int k_bits, int v_bits, bool asym, int q_bits, int batch);
 cudaError_t launch_suffix(const DecodeArgs& a, cudaStream_t s);
 int suffix_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch);
 cudaError_t launch_suffix_q32(const DecodeArgs& a, cudaStream_t s);
 int shared_tiles_ctas(const CacheView& c);  // one wave on the current device, 0: failure
 cudaError_t launch_shared_tiles(const SharedArgs& a, cudaStream_t s);
+int shared_tc_ctas(const CacheView& c);
+cudaError_t launch_shared_tc(const SharedArgs& a, cudaStream_t s);
 cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s);
 // Prefill on 16-vector query tiles (kvq_prefill_tiles.cu): quantized blocks
 // (8-, 4- or 2-bit, symmetric or asymmetric), any query format, no window.

@@ -109,6 +109,32 @@ def test_sequences_shorter_than_their_prefix(fmt):
     assert run.err_bits() == 0
 
 
+@pytest.mark.parametrize("fmt", ["int8_g4", "int4_factor_g8", "k4v8_g3_t3", "k8v4_g5", "window32_int8",
+                                 "window16_asym_k4v8", "asym_int8", "kchan_int8", "qint8_asym_k8v4", "int2",
+                                 "asym_int2_g8"])
+def test_full_tiles_of_every_format(fmt):
+    """Groups of enough vectors for the 128-vector tiles, over more than one unit per CTA, with rows that end before,
+    inside and behind the prefix."""
+    w = small_workload(fmt, **dict(dict(batch=50, len_range=(500, 640), paged=True), **FORMATS[fmt]))
+    groups = [(0, 41, 29), (41, 50, 9)]
+    inp = shared_inputs(w, groups)
+    run = DeviceRun(inp)
+    lens = np.array(inp.lengths)
+    if not w.window:
+        lens[[3, 8, 20, 33, 42, 45]] = [0, 1, 463, 464, 143, 200]
+    lens[7] = 0
+    lens_t = torch.from_numpy(lens.astype(np.int32)).cuda()
+    out, lse = decode_shared(run, groups, lens=lens_t)
+    o, l = run.decode(lens=lens_t)
+    empty = lens == 0
+    assert np.all(out[empty] == 0) and np.all(np.isneginf(lse[empty]))
+    np.testing.assert_allclose(out[~empty], o[~empty], rtol=0, atol=2e-3)
+    np.testing.assert_allclose(lse[~empty], l[~empty], rtol=0, atol=2e-3)
+    whole = {(b, h) for b in range(0, 50, 6) if lens[b] == inp.lengths[b] for h in range(w.kv_heads)}
+    assert compare_outputs(inp, out, lse, oracle_decode(inp, whole), False) <= 1.0
+    assert run.err_bits() == 0
+
+
 @pytest.mark.parametrize("kw,groups", [
     (dict(batch=40, q_heads=32, kv_heads=8, len_range=(2100, 2300)), [(0, 40, 130)]),       # 160 vectors, long
     (dict(batch=3, q_heads=4, kv_heads=4, len_range=(9000, 9100), k_bits=4), [(0, 3, 560)]),  # few vectors, many CTAs
@@ -138,6 +164,25 @@ def test_many_vectors_and_long_prefixes(kw, groups):
         np.testing.assert_array_equal(again[0], out)
         np.testing.assert_array_equal(again[1], lse)
     assert run.err_bits() == 0
+
+
+@pytest.mark.parametrize("kw", [dict(k_bits=4, v_bits=4, asym=True), dict(k_bits=2, v_bits=2), dict()])
+@pytest.mark.parametrize("P", [1, 4, 7, 12, 23])
+def test_short_prefixes_again_and_again(kw, P):
+    """A few tiles per CTA, where the conversion runs furthest ahead of the softmax: the same bits every time."""
+    w = small_workload("shared_again", **dict(dict(batch=8, len_range=(400, 420), paged=True), **kw))
+    groups = [(0, 8, P)]
+    inp = shared_inputs(w, groups)
+    run = DeviceRun(inp)
+    ref, ref_lse = run.decode()
+    first = decode_shared(run, groups)
+    np.testing.assert_allclose(first[0], ref, rtol=0, atol=2e-3)
+    np.testing.assert_allclose(first[1], ref_lse, rtol=0, atol=2e-3)
+    for _ in range(25):
+        out, lse = decode_shared(run, groups)
+        assert run.err_bits() == 0
+        np.testing.assert_array_equal(out, first[0])
+        np.testing.assert_array_equal(lse, first[1])
 
 
 def test_large_scores_and_extreme_value_scales():
