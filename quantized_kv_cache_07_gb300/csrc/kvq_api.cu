@@ -131,10 +131,10 @@ kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int nu
   const int H = c->num_kv_heads, G = q_heads / H;
   const int per = kvq::suffix_ctas_per_sm_for(c->k_bits, c->v_bits, c->asym != 0, v.q_bits, batch);
   const int P = stream_ctas_for(sms * per, c->window > 0 ? batch * H : 0, batch * H);
-  // 128-vector tiles on tcgen05 where the groups fill them, 16-vector tiles
+  // 256-vector units on tcgen05 where the groups fill them, 16-vector tiles
   // otherwise, for bf16 blocks and for the two-part mode.
   sl->tc = c->k_bits != 16 && v.q_bits != 32 && batch * G >= 32 * num_groups;
-  sl->tile = sl->tc ? 128 : 16;
+  sl->tile = sl->tc ? 256 : 16;
   sl->ctas = sl->tc ? kvq::shared_tc_ctas(v) : kvq::shared_tiles_ctas(v);
   if (P <= 0 || sl->ctas <= 0) return KVQ_ERR_CUDA;
   *dl = kvq::decode_layout(batch, q_heads, H, c->window, P, kvq::switch_blocks_for(c->k_bits));

@@ -140,7 +140,7 @@ constexpr int kMaxGroups = 256;
 // one group and KV head; CTA c's share of unit u is record c + u.
 struct SharedLayout {
   int ctas, tile, slots;
-  bool tc;  // tcgen05 path (tile 128), else mma.sync (tile 16)
+  bool tc;  // tcgen05 path (tile 256), else mma.sync (tile 16)
   size_t off_o, off_lse;             // suffix result: float [B][Hq][128], [B][Hq]
   size_t off_m, off_l, off_rec;      // records: float [slots][tile], twice, and [slots][tile][128]
   size_t total;

@@ -37,8 +37,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
     const float* pm = reinterpret_cast<const float*>(a.ws + sa.sl.off_m);
     const float* pl = reinterpret_cast<const float*>(a.ws + sa.sl.off_l);
     const float* po = reinterpret_cast<const float*>(a.ws + sa.sl.off_rec);
+    // On tcgen05 a unit of at most 128 vectors has two records per CTA, the second one's rows behind the first's;
+    // a record without a token (m = -inf) may hold anything.
+    const int nv = min((geo.g.start[g + 1] - geo.g.start[g]) * a.G - tile * sa.sl.tile, sa.sl.tile);
+    const int two = sa.sl.tc && nv <= sa.sl.tile / 2 ? 1 : 0;
+    const long long n = (c1 - c0 + 1) << two;
     constexpr int kR = 8;  // records in flight
-    for (long long c = c0; c <= c1; c += kR) {
+    for (long long i0 = 0; i0 < n; i0 += kR) {
       float mr[kR], lr[kR];
       float4 orr[kR];
 #pragma unroll
@@ -46,11 +51,13 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
         mr[r] = kNegInf;
         lr[r] = 0.f;
         orr[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c + r <= c1) {
-          const size_t at = size_t(c + r + u) * sa.sl.tile + v % sa.sl.tile;
+        if (i0 + r < n) {
+          const size_t at = size_t(c0 + ((i0 + r) >> two) + u) * sa.sl.tile + v % sa.sl.tile +
+                            (two && ((i0 + r) & 1) ? sa.sl.tile / 2 : 0);
           mr[r] = pm[at];
           lr[r] = pl[at];
           orr[r] = reinterpret_cast<const float4*>(po + at * kHeadDim)[lane];
+          if (mr[r] == kNegInf) orr[r] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       }
       float Mn = M;

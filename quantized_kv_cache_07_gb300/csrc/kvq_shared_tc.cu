@@ -8,11 +8,18 @@
 // Each block is converted once for 128 vectors; on mma.sync every 16 vectors
 // convert it again, and that conversion is what bounds the 16-vector tiles.
 //
-// Roles: warps 0-3 softmax (thread v = vector v = tensor-memory lane v), warps
-// 4-7 conversion (warp w = block w of the 64 tokens, the next tile's codes already in
-// registers).  Threads of warps 0 and 1 issue the products between their own steps (a ninth
-// warp would cost every thread 32 of its 128 registers).  K, V and S are double-buffered; P overwrites its S.  256 columns of tensor memory
-// and about 105 KB of shared memory: two CTAs share an SM and fill each other's waits.
+// A unit is up to 256 query vectors of a group and KV head.  With more than 128 of
+// them two softmax warpgroups take 128 each and meet every tile; with fewer both
+// hold the same vectors and take the tiles in turn, each with its own running maximum,
+// sum and O, and leave two records.
+//
+// Roles (512 threads, one CTA per SM): warpgroups 0 and 1 softmax (thread v = vector v =
+// tensor-memory lane v), warpgroup 2 converts (warp w = block w of the 64 tokens, the next tile's codes
+// already in registers), warp 12 issues the products.  Tiles pass through a ring of 4
+// stages (codes as fp16, scales); S is double-buffered per softmax warpgroup and P overwrites its S.
+// The registers go where the scores are: 160 a softmax thread, 112 a converting one, 80 the rest.
+// (Measured before: the same products issued by softmax threads between their steps, two CTAs of
+// 256 threads per SM: 75 us for 64 sequences on 32768 tokens, each issue holding its warp for 1000 cycles.)
 //
 // Orders inside a tile.  The tokens and dims of a block are permuted so that a lane's codes
 // (fragment-native order, include/kvq.h) go to shared memory as 16-byte (K) and
@@ -31,25 +38,29 @@
 namespace kvq {
 namespace {
 
-constexpr int kQ = 128;            // query vectors of a unit
-constexpr int kTok = 64;           // tokens of a tile
-constexpr int kTcThreads = 256;
-constexpr int kTmemCols = 256;     // O: 0..127, S buffers: 128.., 192..
-constexpr int kScaleRing = 4;      // a tile's scales are written two tiles ahead of its predecessor's last reader
+constexpr int kQ = 128;         // query vectors of a softmax warpgroup
+constexpr int kTok = 64;        // tokens of a tile
+constexpr int kTcThreads = 512;
+constexpr int kTmemCols = 512;  // O of warpgroup j: 128 j; its S buffers: 256 + 128 j, + 64
+constexpr int kRing = 4;        // stages of converted tiles
+
+struct TcStage {
+  uint8_t k[2][kTok * 128];  // two halves of 64 dims
+  uint8_t v[kHeadDim * 128];
+};
 
 struct TcSmem {
-  alignas(1024) uint8_t q[2][kQ * 128];      // two halves of 64 dims
-  alignas(1024) uint8_t k[2][2][kTok * 128];  // [buffer][half]
-  alignas(1024) uint8_t v[2][kHeadDim * 128];
-  float sk[kScaleRing][kTok], sv[kScaleRing][kTok], mk[kScaleRing][kTok], mv[kScaleRing][kTok];
-  float svmax[kScaleRing][4];
-  float qs[kQ], qz[kQ];
-  int qlen[kQ];
-  uint64_t k_full[4];  // by tile & 3: a softmax warp may look after the conversion has run two tiles ahead
-  uint64_t v_full[2], qk_done[2], p_full[2], pv_done[2];
+  alignas(1024) uint8_t q[2][2][kQ * 128];  // [warpgroup][half]
+  alignas(1024) TcStage st[kRing];
+  float sk[kRing][kTok], sv[kRing][kTok], mk[kRing][kTok], mv[kRing][kTok];
+  float svmax[kRing][4];
+  float qs[2 * kQ], qz[2 * kQ];
+  int qlen[2 * kQ];
+  // full: a stage's 128 converting threads; empty: its products are done; q_full: the softmax threads have
+  // staged a segment's queries; s_full, p_full, o_done [warpgroup][S buffer]: scores, weights, P . V done
+  uint64_t full[kRing], empty[kRing], q_full, seg_done, s_full[2][2], p_full[2][2], o_done[2][2];
   uint32_t tmem;
-  int dead;
-  int maxlen, minlen;
+  int minlen[2];
   SharedGeo geo;
 };
 
@@ -192,147 +203,230 @@ __device__ __forceinline__ void put_values(const Raw<VB>& raw, uint8_t* const ti
   }
 }
 
-// Query vector v (this lane's four bf16 values in raw) into the swizzled Q tile by one warp; returns its score scale.
+// A query vector into the swizzled Q tile by 8 lanes: lane `sub` holds dims 16 sub .. + 15 (raw: their bf16 bits,
+// f: their key factors, if the cache has them).  The vector's score scale and sum (as the product sees it) come back.
+// Four vectors a step in a loop, not unrolled: code that runs once is fetched at memory speed (unrolled over the
+// 32 vectors of a warp the staging took 13 us).
 template <bool ASYM>
-__device__ __forceinline__ float put_query(const DecodeArgs& a, uint2 raw, float4 c, int v, TcSmem* sm, int lane) {
-  float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
-                __uint_as_float(raw.y & 0xFFFF0000u)};
-  if (a.c.factor) {
-    x[0] *= c.x;
-    x[1] *= c.y;
-    x[2] *= c.z;
-    x[3] *= c.w;
-  }
-  // non-negative floats order as their bits: one warp reduction
-  const float am = __uint_as_float(__reduce_max_sync(
-      kFull, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
-  float scale = kLog2e * kInvSqrtD;
-  if (a.c.q_bits == 8) {
-    float q[4];
-    scale *= quantize_int8_row(x, am, q);
+__device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw)[2], const float (&f)[16], uint8_t* half,
+                                          int row, int sub, float& scale, float& sum) {
+  float x[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = q[j];
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+      x[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+  }
+  if (a.c.factor) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= f[k];
+  }
+  float am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) am = fmaxf(am, fabsf(x[k]));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
+  scale = kLog2e * kInvSqrtD;
+  if (a.c.q_bits == 8) {
+    float s = 1.f;
+#pragma unroll
+    for (int k = 0; k < 16; k += 4) {
+      const float y[4] = {x[k], x[k + 1], x[k + 2], x[k + 3]};
+      float c[4];
+      s = quantize_int8_row(y, am, c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[k + e] = c[e];
+    }
+    scale *= s;
   } else {
     // exact powers of two: am * 2^(14 - e) in [2^14, 2^15); below 2^-112 the scores are zero to any precision
     const uint32_t e = max(__float_as_uint(am) >> 23, 15u);
-    const float f = __uint_as_float((268u - e) << 23);
+    const float f2 = __uint_as_float((268u - e) << 23);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= f;
+    for (int k = 0; k < 16; ++k) x[k] *= f2;
     scale *= __uint_as_float((e - 14u) << 23);
   }
-  const uint2 y = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-  if constexpr (ASYM) {  // the vector's sum as the product sees it
-    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&y.x));
-    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&y.y));
-    float z = (f0.x + f0.y) + (f1.x + f1.y);
+  scale = fmaxf(scale, 1.17549435e-38f);  // positive, so that a masked score stays -inf
+  sum = 0.f;
+  const int t = sub >> 1;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFull, z, o);
-    if (lane == 0) sm->qz[v] = z;
+  for (int i = 0; i < 2; ++i) {  // dims 32 t + 8 (2 (sub & 1) + i) ..: chunk i of this half
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = pack_half2(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
+      if constexpr (ASYM) {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&y[k]));
+        sum += h.x + h.y;
+      }
+    }
+    *reinterpret_cast<uint4*>(half + row * 128 + ((dim_chunk(t, i) ^ (row & 7)) * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
   }
-  const int t = lane >> 3, i = (lane & 7) >> 1;
-  *reinterpret_cast<uint2*>(sm->q[i >> 1] + v * 128 + ((dim_chunk(t, i) ^ (v & 7)) * 16) + 8 * (lane & 1)) = y;
-  return fmaxf(scale, 1.17549435e-38f);  // positive, so that a masked score stays -inf
+  if constexpr (ASYM) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  }
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// The segments of a CTA, walked alike by every role: tiles t0 .. t0 + nt - 1 of a unit.
+struct Segment {
+  SharedUnit un;
+  int nt, t0, nblk, first, rows;
+  int nv;     // query vectors of the unit's tile
+  bool both;  // more than 128: both warpgroups meet every tile
+};
+__device__ __forceinline__ Segment segment_at(const SharedGeo* geo, const DecodeArgs& a, long long x, long long x1) {
+  Segment g;
+  g.un = unit_at(geo, a.num_groups, a.c.H, kTok / kBlock, x);
+  g.nt = int(min(x1, g.un.start + g.un.steps) - x);
+  g.t0 = int(x - g.un.start);
+  g.nblk = geo->g.blocks[g.un.group];
+  g.first = geo->g.start[g.un.group];
+  g.rows = geo->g.start[g.un.group + 1] - g.first;
+  g.nv = min(g.rows * a.G - g.un.tile * 2 * kQ, 2 * kQ);
+  g.both = g.nv > kQ;
+  return g;
+}
+// Tiles of a segment that warpgroup j takes.
+__device__ __forceinline__ int jobs_of(const Segment& g, int j) { return g.both ? g.nt : (g.nt + 1 - j) / 2; }
+
 template <int KB, int VB, bool ASYM>
-__global__ void __launch_bounds__(kTcThreads, 2) shared_tc_kernel(const SharedArgs sa) {
+__global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedArgs sa) {
   using F = Fmt<KB, VB, ASYM>;
   constexpr int kStep = kTok / kBlock;
   constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f), kVC = VB == 8 ? 128.f : (VB == 4 ? 8.f : 2.f);
   const DecodeArgs& a = sa.d;
   extern __shared__ uint8_t raw_smem[];
   TcSmem* sm = reinterpret_cast<TcSmem*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
-  const int G = a.G, H = a.c.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) mbar_init(&sm->k_full[i], 128);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm->v_full[i], 128);
-      mbar_init(&sm->qk_done[i], 1);
-      mbar_init(&sm->p_full[i], 128);
-      mbar_init(&sm->pv_done[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sm->full[i], 128);
+      mbar_init(&sm->empty[i], 1);
     }
-    sm->dead = 0;
+    mbar_init(&sm->q_full, 2 * kQ);
+    mbar_init(&sm->seg_done, 2 * kQ);
+    for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sm->s_full[j][i], 1);
+        mbar_init(&sm->p_full[j][i], kQ);
+        mbar_init(&sm->o_done[j][i], 1);
+      }
     fence_mbar_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  shared_geometry(&sm->geo, a, kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix decode
+  shared_geometry(&sm->geo, a, 2 * kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix decode
   const SharedGeo* geo = &sm->geo;
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
   if (ci >= Pe) return;
   const long long x0 = (long long)ci * geo->T / Pe, x1 = (long long)(ci + 1) * geo->T / Pe;
   if (x0 >= x1) return;
-  if (warp == 4) tmem_alloc(&sm->tmem, kTmemCols);
+  if (warp == 12) tmem_alloc(&sm->tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm->tmem;
-  const uint32_t km = magic_f16x2(a.B);
-  const uint32_t c64 = 0x64646464u | (uint32_t(a.B) >> 16);  // a.B <= 4096: the constant itself
+  const uint32_t tmem = __shfl_sync(kFull, sm->tmem, 0);
+  // Every wait is bounded; a role that gives up leaves its loop, the others follow when their own waits run out.
+  bool ok = true;
+  auto ring_wait = [&](uint64_t* bars, int n) { return mbar_wait(&bars[n & (kRing - 1)], uint32_t(n / kRing) & 1u); };
+  auto pair_wait = [&](uint64_t* bars, int c) { return mbar_wait(&bars[c & 1], uint32_t(c >> 1) & 1u); };
 
-  int it = 0;  // tiles of the CTA so far: buffer it & 1, phase (it >> 1) & 1
-  auto wait = [&](uint64_t* bars, int i) { return mbar_wait(&bars[i & 1], uint32_t(i >> 1) & 1u); };
-  auto wait_k = [&](int i) { return mbar_wait(&sm->k_full[i & 3], uint32_t(i >> 2) & 1u); };
-  auto give_up = [&]() {
-    flag(a.err, KVQ_DEVERR_TIMEOUT);
-    sm->dead = 1;
-  };
-  for (long long x = x0; x < x1;) {
-    const SharedUnit un = unit_at(geo, a.num_groups, H, kStep, x);
-    const int nt = int(min(x1, un.start + un.steps) - x);  // tiles of this segment
-    const int t0 = int(x - un.start);                      // the first one's number in the unit
-    x += nt;
-    const int nblk = geo->g.blocks[un.group], first = geo->g.start[un.group];
-    const int rows = geo->g.start[un.group + 1] - first;
-    if (tid == 0) {
-      sm->maxlen = 0;
-      sm->minlen = 0x7fffffff;
-    }
-    __syncthreads();
-    {
-      // all of this warp's 16 vectors are loaded before the first is converted: one memory latency, not 16
-      constexpr int kPer = kQ / (kTcThreads / 32);
-      const uint16_t* q0 = a.q + (size_t(first) * a.Hq + un.h * G) * kHeadDim + 4 * lane;
-      uint2 raw[kPer];
-      int mylen = 0;  // lane i < 16: vector i's prefix length
-      float4 c = make_float4(1.f, 1.f, 1.f, 1.f);
-      if (a.c.factor) c = *reinterpret_cast<const float4*>(a.c.factor + un.h * kHeadDim + 4 * lane);
-      const int gv0 = un.tile * kQ + warp * kPer;
-      {
-        const int rr = (gv0 + (lane & (kPer - 1))) / G;
-        if (rr < rows) mylen = prefix_len(a, first + rr, nblk);
-        if (lane < kPer) {
-          sm->qlen[warp * kPer + lane] = mylen;
-          atomicMax(&sm->maxlen, mylen);
-          if (rr < rows) atomicMin(&sm->minlen, mylen);
+  if (warp >= 12) {
+    // ---------------------------------------------------------------- products
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 12) {
+      const bool leader = elect_one();
+      const uint32_t q_addr = smem_u32(sm->q), st_addr = smem_u32(sm->st);
+      int n0 = 0, c0 = 0, c1 = 0, seg = 0;  // tiles and jobs before this segment
+      for (long long x = x0; x < x1 && ok; ++seg) {
+        const Segment g = segment_at(geo, a, x, x1);
+        x += g.nt;
+        ok = mbar_wait(&sm->q_full, uint32_t(seg) & 1u);
+        // P . V runs one tile behind the scores, two where the warpgroups take turns
+        const int lag = g.both ? 1 : 2;
+        for (int i = 0; i < g.nt + lag && ok; ++i) {
+          if (i < g.nt) {
+            const int n = n0 + i;
+            ok = ring_wait(sm->full, n);
+            tc_fence_after();
+            const uint64_t kd = tile_desc(st_addr + uint32_t(n & (kRing - 1)) * uint32_t(sizeof(TcStage)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (!g.both && (i & 1) != j) continue;
+              const int c = (j ? c1 : c0) + (g.both ? i : i >> 1);
+              if (c >= 2) ok = ok && pair_wait(sm->o_done[j], c - 2);  // S's buffer: its weights have been read
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t qd = tile_desc(q_addr + (g.both ? j : 0) * uint32_t(sizeof(sm->q[0])));
+              const uint32_t d = tmem + 256 + 128 * j + 64 * (c & 1);
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < kHeadDim / 16; ++k)
+                  tc_mma_ss(d, qd + (k >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (k & 3),
+                            kd + (k >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (k & 3), f16_idesc(kQ, kTok), k > 0);
+                tc_commit(&sm->s_full[j][c & 1]);
+              }
+              __syncwarp();
+            }
+          }
+          const int p = i - lag;
+          if (p >= 0 && ok) {
+            const int n = n0 + p, s = n & (kRing - 1);
+            const uint64_t vd = tile_desc(st_addr + uint32_t(s) * uint32_t(sizeof(TcStage)) + uint32_t(sizeof(sm->st[0].k)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (!g.both && (p & 1) != j) continue;
+              const int job = g.both ? p : p >> 1, c = (j ? c1 : c0) + job;
+              ok = ok && pair_wait(sm->p_full[j], c);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t d = tmem + 128 * j, w = tmem + 256 + 128 * j + 64 * (c & 1);
+              if (leader) {
+#pragma unroll
+                for (int k = 0; k < kTok / 16; ++k)
+                  tc_mma_ts(d, w + 8 * k, vd + 2 * k, f16_idesc(kQ, kHeadDim), job > 0 || k > 0);
+                tc_commit(&sm->o_done[j][c & 1]);
+                if (j == 1 || !g.both) tc_commit(&sm->empty[s]);
+              }
+              __syncwarp();
+            }
+          }
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int rr = (gv0 + i) / G, hj = (gv0 + i) % G;
-        raw[i] = make_uint2(0u, 0u);
-        if (rr < rows) raw[i] = *reinterpret_cast<const uint2*>(q0 + (size_t(rr) * a.Hq + hj) * kHeadDim);
-      }
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float qs = put_query<ASYM>(a, raw[i], c, warp * kPer + i, sm, lane);
-        if (lane == 0) sm->qs[warp * kPer + i] = qs;
+        n0 += g.nt;
+        c0 += jobs_of(g, 0);
+        c1 += jobs_of(g, 1);
       }
     }
-    fence_async_smem();
-    __syncthreads();
-
-    if (warp >= 4) {
-      // -------------------------------------------------------------- conversion
-      const int w = warp - 4;
-      const int* table = a.table + size_t(first) * a.mbps;
-      const int maxlen = sm->maxlen;
+  } else if (warp >= 8) {
+    // ---------------------------------------------------------------- conversion
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    const int w = warp - 8;
+    const uint32_t km = magic_f16x2(a.B);
+    const uint32_t c64 = 0x64646464u | (uint32_t(a.B) >> 16);  // a.B <= 4096: the constant itself
+    int n = 0;
+    for (long long x = x0; x < x1 && ok;) {
+      const Segment g = segment_at(geo, a, x, x1);
+      x += g.nt;
+      const int* table = a.table + size_t(g.first) * a.mbps;
+      int maxlen = 0;  // of the unit's rows: scales of slots behind it are not data
+      for (int r = g.un.tile * 2 * kQ / a.G + lane; r <= (g.un.tile * 2 * kQ + g.nv - 1) / a.G; r += 32)
+        maxlen = max(maxlen, prefix_len(a, g.first + r, g.nblk));
+      maxlen = __reduce_max_sync(kFull, maxlen);
       int ids = -1, ids_next = -1;  // this warp's table entries of 32 tiles, and of the next 32
       auto load_ids = [&](int i) {
-        const int blk = (t0 + i + lane) * kStep + w;
+        const int blk = (g.t0 + i + lane) * kStep + w;
         int id = -1;
-        if (i + lane < nt && blk < nblk) {
+        if (i + lane < g.nt && blk < g.nblk) {
           id = table[blk];
           if (id < 0 || id >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
@@ -351,13 +445,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) shared_tc_kernel(const SharedAr
           ids = ids_next;
           ids_next = load_ids(i + 32);
         }
-        return i < nt ? __shfl_sync(kFull, ids, i & 31) : -1;
+        return i < g.nt ? __shfl_sync(kFull, ids, i & 31) : -1;
       };
       auto fetch_keys = [&](int phys) {
         ks = vs = ko = vo = 0.f;
         rk.clear();
         if (phys < 0) return;
-        const size_t hb = size_t(un.h) * a.c.num_blocks + phys;
+        const size_t hb = size_t(g.un.h) * a.c.num_blocks + phys;
         rk.load(a.c.k_codes + hb * F::kKBB, lane);
         const float* rec = a.c.meta + hb * F::kMF + (F::kGroup ? 0 : (lane & 15));
         ks = a.c.k_chan ? 1.f : __ldcg(rec + F::kKS);
@@ -369,164 +463,156 @@ __global__ void __launch_bounds__(kTcThreads, 2) shared_tc_kernel(const SharedAr
       };
       auto fetch_values = [&](int phys) {
         rv.clear();
-        if (phys >= 0) rv.load(a.c.v_codes + (size_t(un.h) * a.c.num_blocks + phys) * F::kVBB, lane);
+        if (phys >= 0) rv.load(a.c.v_codes + (size_t(g.un.h) * a.c.num_blocks + phys) * F::kVBB, lane);
       };
-      bool ok = true;
       {
         const int phys = block_of(0);
         fetch_keys(phys);
         fetch_values(phys);
       }
 #pragma unroll 1
-      for (int i = 0; i < nt; ++i) {
-        const int n = it + i, b = n & 1, sc = n & (kScaleRing - 1);
-        if (n >= 2 && !__all_sync(kFull, wait(sm->qk_done, n - 2))) {
-          ok = false;
-          break;
-        }
-        put_keys<KB>(rk, sm->k[b][0], sm->k[b][1], w, lane, km, c64);
-        // scales of slots behind the longest row are not data
-        const bool data = ((t0 + i) * kStep + w) * kBlock + lane < maxlen;
+      for (int i = 0; i < g.nt; ++i, ++n) {
+        const int s = n & (kRing - 1);
+        ok = __all_sync(kFull, n < kRing || ring_wait(sm->empty, n - kRing));
+        if (!ok) break;
+        put_keys<KB>(rk, sm->st[s].k[0], sm->st[s].k[1], w, lane, km, c64);
+        const bool data = ((g.t0 + i) * kStep + w) * kBlock + lane < maxlen;
         if (!data) vs = 0.f;
         if (lane < kBlock) {
           const int col = tile_col(w, lane);
-          sm->sk[sc][col] = ks;
-          sm->sv[sc][col] = vs;
+          sm->sk[s][col] = ks;
+          sm->sv[s][col] = vs;
           if constexpr (ASYM) {
-            sm->mk[sc][col] = fmaf(kKC, ks, ko);
-            sm->mv[sc][col] = data ? fmaf(kVC, vs, vo) : 0.f;
+            sm->mk[s][col] = fmaf(kKC, ks, ko);
+            sm->mv[s][col] = data ? fmaf(kVC, vs, vo) : 0.f;
           }
         }
         // value scales are positive: they order as their bits
         const uint32_t vm = __reduce_max_sync(kFull, lane < kBlock ? __float_as_uint(vs) : 0u);
-        if (lane == 0) sm->svmax[sc][w] = __uint_as_float(vm);
-        fence_async_smem();
-        mbar_arrive(&sm->k_full[n & 3]);
+        if (lane == 0) sm->svmax[s][w] = __uint_as_float(vm);
         const int phys = block_of(i + 1);
         fetch_keys(phys);
-        if (n >= 2 && !__all_sync(kFull, wait(sm->pv_done, n - 2))) {
-          ok = false;
-          break;
-        }
-        put_values<VB>(rv, sm->v[b], w, lane, km, c64);
-        fence_async_smem();
-        mbar_arrive(&sm->v_full[b]);
+        put_values<VB>(rv, sm->st[s].v, w, lane, km, c64);
         fetch_values(phys);
+        fence_async_smem();
+        mbar_arrive(&sm->full[s]);
       }
-      if (!ok) give_up();
-    } else {
-      // -------------------------------------------------------------- softmax
-      const int v = tid;
-      const uint32_t lanes = tmem + (uint32_t(warp * 32) << 16);
-      const float qs = sm->qs[v], qz = ASYM ? sm->qz[v] : 0.f;
-      const int len = sm->qlen[v], minlen = sm->minlen;
-      float m = kNegInf, l = 0.f, z = 0.f, sg = float(kSigma0);
-      float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
-      bool ok = true;
-      // S of tile i (issued by warp 1), and P . V of tile i (issued by warp 0): one thread each.  S's buffer is
-      // free once P . V of tile i - 2 has read its weights.
-      auto issue_qk = [&](int i) {
-        if (warp != 1 || i >= nt) return;
-        if (lane == 0) {
-          const int n = it + i, b = n & 1;
-          if (wait_k(n) && (n < 2 || wait(sm->pv_done, n - 2))) {
-            tc_fence_after();
-            const uint64_t qd = tile_desc(smem_u32(sm->q[0])), kd = tile_desc(smem_u32(sm->k[b][0]));
-#pragma unroll
-            for (int k = 0; k < kHeadDim / 16; ++k)
-              tc_mma_ss(tmem + 128 + 64 * b, qd + (k >> 2) * (sizeof(sm->q[0]) >> 4) + 2 * (k & 3),
-                        kd + (k >> 2) * (sizeof(sm->k[0][0]) >> 4) + 2 * (k & 3), f16_idesc(kQ, kTok), k > 0);
-            tc_commit(&sm->qk_done[b]);
-          } else {
-            ok = false;
-          }
-        }
-        __syncwarp();
-      };
-      auto issue_pv = [&](int i) {
-        if (warp != 0) return;
-        if (lane == 0) {
-          const int n = it + i, b = n & 1;
-          if (wait(sm->p_full, n) && wait(sm->v_full, n)) {
-            tc_fence_after();
-            const uint64_t vd = tile_desc(smem_u32(sm->v[b]));
-#pragma unroll
-            for (int k = 0; k < kTok / 16; ++k)
-              tc_mma_ts(tmem, tmem + 128 + 64 * b + 8 * k, vd + 2 * k, f16_idesc(kQ, kHeadDim), i > 0 || k > 0);
-            tc_commit(&sm->pv_done[b]);
-          } else {
-            ok = false;
-          }
-        }
-        __syncwarp();
-      };
-      issue_qk(0);
-      issue_qk(1);
-      // O *= f, this thread's row; the products before tile i have to be complete
-      auto rescale = [&](int i, float f) {
-        if (i == 0) return true;
-        if (!__all_sync(kFull, wait(sm->pv_done, it + i - 1))) return false;
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(lanes + c, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-          tmem_st32(lanes + c, o);
-        }
-        tc_wait_st();
-        return true;
-      };
-      for (int i = 0; i < nt; ++i) {
-        const int n = it + i, b = n & 1, sc = n & (kScaleRing - 1);
-        ok = __all_sync(kFull, ok && wait_k(n) && wait(sm->qk_done, n));  // the scales, the scores
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    const int j = warp >> 2, v = tid & (kQ - 1);  // warpgroup, its vector
+    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t o_cols = lanes + 128 * j, s_cols = lanes + 256 + 128 * j;
+    int n0 = 0, c = 0, seg = 0;  // tiles before this segment; this warpgroup's jobs so far
+    for (long long x = x0; x < x1 && ok; ++seg) {
+      const Segment g = segment_at(geo, a, x, x1);
+      x += g.nt;
+      if (seg > 0) {  // both warpgroups are done with the previous segment's queries
+        mbar_arrive(&sm->seg_done);
+        ok = __all_sync(kFull, mbar_wait(&sm->seg_done, uint32_t(seg - 1) & 1u));
         if (!ok) break;
-        tc_fence_after();
-        const int tok0 = (t0 + i) * kTok;
-        const uint32_t st = lanes + 128 + 64 * b;
-        // 32 columns of S times their key scales (the zero-point terms added), masked
-        auto scores = [&](int half, uint32_t (&r)[32]) {
-          tmem_ld32(st + half, r);
-          tc_wait_ld();
+      }
+      {
+        // this warp's 32 vectors (16 of the shared 128), 4 a step, the next step's loads ahead
+        const int per = g.both ? 32 : 16, v0 = (g.both ? warp : 2 * (warp & 3) + j) * per, sub = lane & 7;
+        const int G = a.G, gv0 = g.un.tile * 2 * kQ + v0;
+        const uint16_t* src = a.q + (size_t(g.first) * a.Hq + g.un.h * G) * kHeadDim + 16 * sub;
+        float f[16];
+        if (a.c.factor) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&sm->sk[sc][half + c]);
-            if constexpr (ASYM) {
-              const float4 ko = *reinterpret_cast<const float4*>(&sm->mk[sc][half + c]);
-              fma2(r[c], r[c + 1], ks.x, ks.y, ko.x * qz, ko.y * qz);
-              fma2(r[c + 2], r[c + 3], ks.z, ks.w, ko.z * qz, ko.w * qz);
-            } else {
-              mul2(r[c], r[c + 1], ks.x, ks.y);
-              mul2(r[c + 2], r[c + 3], ks.z, ks.w);
-            }
+          for (int k = 0; k < 16; k += 4)
+            *reinterpret_cast<float4*>(f + k) =
+                *reinterpret_cast<const float4*>(a.c.factor + g.un.h * kHeadDim + 16 * sub + k);
+        }
+        if (lane < per) {
+          const int r = (gv0 + lane) / G;
+          sm->qlen[v0 + lane] = r < g.rows ? prefix_len(a, g.first + r, g.nblk) : 0;
+        }
+        uint8_t* half = sm->q[g.both ? j : 0][sub & 1];
+        int r = (gv0 + (lane >> 3)) / G, hj = (gv0 + (lane >> 3)) % G;
+        uint4 raw[2];
+        auto load = [&]() {
+          raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < g.rows) {
+            const uint4* p = reinterpret_cast<const uint4*>(src + (size_t(r) * a.Hq + hj) * kHeadDim);
+            raw[0] = p[0];
+            raw[1] = p[1];
           }
-          if (tok0 + kTok > minlen) {  // a row of the unit ends inside this tile or before it
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (tok0 + tile_token(c) + half / 8 >= len) r[c] = __float_as_uint(kNegInf);
+          hj += 4;
+          while (hj >= G) {
+            hj -= G;
+            ++r;
           }
         };
-        float mx = kNegInf;
+        load();
 #pragma unroll 1
-        for (int half = 0; half < kTok; half += 32) {
-          uint32_t r[32];
-          scores(half, r);
-          float m2 = kNegInf;
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            mx = fmaxf(mx, fmaxf(__uint_as_float(r[c]), __uint_as_float(r[c + 1])));
-            m2 = fmaxf(m2, fmaxf(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3])));
+        for (int b = 0; b < per; b += 4) {
+          const uint4 cur[2] = {raw[0], raw[1]};
+          load();
+          const int at = v0 + b + (lane >> 3);
+          float qs, sum;
+          put_query<ASYM>(a, cur, f, half, at & (kQ - 1), sub, qs, sum);
+          if (sub == 0) {
+            sm->qs[at] = qs;
+            sm->qz[at] = sum;
           }
-          mx = fmaxf(mx, m2);
         }
-        mx *= qs;
+      }
+      fence_async_smem();
+      mbar_arrive(&sm->q_full);
+      ok = __all_sync(kFull, mbar_wait(&sm->q_full, uint32_t(seg) & 1u));
+      if (!ok) break;
+      const int at = g.both ? tid : v;
+      const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] : 0.f;
+      const int len = sm->qlen[at];
+      // the warp's shortest row decides whether a tile needs the mask at all (unused vectors do not count)
+      const int minlen = __reduce_min_sync(kFull, at < g.nv ? len : 0x7fffffff);
+      float m = kNegInf, l = 0.f, z = 0.f, sg = float(kSigma0);
+      float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
+      const int jobs = jobs_of(g, j);
+#pragma unroll 1
+      for (int i = 0; i < jobs; ++i, ++c) {
+        const int tile = g.both ? i : 2 * i + j, sc = (n0 + tile) & (kRing - 1);
+        ok = __all_sync(kFull, ring_wait(sm->full, n0 + tile) && pair_wait(sm->s_full[j], c));  // scales, scores
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = s_cols + 64 * (c & 1);
+        uint32_t r[kTok];
+        tmem_ld32(st, r);
+        tmem_ld32(st + 32, r + 32);
+        tc_wait_ld();
+        const int tok0 = (g.t0 + tile) * kTok;
+#pragma unroll
+        for (int k = 0; k < kTok; k += 4) {
+          const float4 ks = *reinterpret_cast<const float4*>(&sm->sk[sc][k]);
+          if constexpr (ASYM) {
+            const float4 ko = *reinterpret_cast<const float4*>(&sm->mk[sc][k]);
+            fma2(r[k], r[k + 1], ks.x, ks.y, ko.x * qz, ko.y * qz);
+            fma2(r[k + 2], r[k + 3], ks.z, ks.w, ko.z * qz, ko.w * qz);
+          } else {
+            mul2(r[k], r[k + 1], ks.x, ks.y);
+            mul2(r[k + 2], r[k + 3], ks.z, ks.w);
+          }
+        }
+        if (tok0 + kTok > minlen) {  // a row of the warp ends inside this tile or before it
+#pragma unroll
+          for (int k = 0; k < kTok; ++k)
+            if (tok0 + tile_token(k) >= len) r[k] = __float_as_uint(kNegInf);
+        }
+        float x4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+        for (int k = 0; k < kTok; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x4[e] = fmaxf(x4[e], fmaxf(__uint_as_float(r[k + 2 * e]), __uint_as_float(r[k + 2 * e + 1])));
+        const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * qs;
         const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
         const float svm = fmaxf(fmaxf(sm4.x, sm4.y), fmaxf(sm4.z, sm4.w));
-        if (__any_sync(kFull, mx > m + kMaxSlack) || svm > svlim) {  // svm is the same in every thread
+        const bool up = __any_sync(kFull, mx > m + kMaxSlack);
+        if (up || svm > svlim) {  // svm is the same in every thread
           float f = 1.f;
-          if (__any_sync(kFull, mx > m + kMaxSlack)) {
+          if (up) {
             const float mn = fmaxf(m, mx);
             f = mn == kNegInf ? 1.f : ex2(m - mn);
             m = mn;
@@ -541,74 +627,101 @@ __global__ void __launch_bounds__(kTcThreads, 2) shared_tc_kernel(const SharedAr
           }
           l *= f;
           z *= f;
-          ok = rescale(i, f);
-          if (!ok) break;
+          if (i > 0) {  // O too, once the products so far are complete
+            ok = __all_sync(kFull, pair_wait(sm->o_done[j], c - 1));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < kHeadDim; k += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_cols + k, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_cols + k, o);
+            }
+            tc_wait_st();
+          }
         }
-        if (i > 0) issue_qk(i + 1);  // by now P . V of tile i - 1 has most likely finished
         const float base = m == kNegInf ? 0.f : m - sg;
         uint32_t la[4] = {0u, 0u, 0u, 0u};  // four partial sums of the weights
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < kTok; half += 32) {
-          uint32_t r[32], p[16];
-          scores(half, r);
+          uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 vs = *reinterpret_cast<const float4*>(&sm->sv[sc][half + c]);
-            fma2(r[c], r[c + 1], qs, qs, -base, -base);
-            fma2(r[c + 2], r[c + 3], qs, qs, -base, -base);
+          for (int k = half; k < half + 32; k += 4) {
+            const float4 vs = *reinterpret_cast<const float4*>(&sm->sv[sc][k]);
+            fma2(r[k], r[k + 1], qs, qs, -base, -base);
+            fma2(r[k + 2], r[k + 3], qs, qs, -base, -base);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[c + j] = __float_as_uint(ex2(__uint_as_float(r[c + j])));
-            add2(la[0], la[1], r[c], r[c + 1]);
-            add2(la[2], la[3], r[c + 2], r[c + 3]);
+            for (int e = 0; e < 4; ++e) r[k + e] = __float_as_uint(ex2(__uint_as_float(r[k + e])));
+            add2(la[0], la[1], r[k], r[k + 1]);
+            add2(la[2], la[3], r[k + 2], r[k + 3]);
             if constexpr (ASYM) {
-              const float4 vo = *reinterpret_cast<const float4*>(&sm->mv[sc][half + c]);
-              z = fmaf(__uint_as_float(r[c]), vo.x, fmaf(__uint_as_float(r[c + 1]), vo.y, z));
-              z = fmaf(__uint_as_float(r[c + 2]), vo.z, fmaf(__uint_as_float(r[c + 3]), vo.w, z));
+              const float4 vo = *reinterpret_cast<const float4*>(&sm->mv[sc][k]);
+              z = fmaf(__uint_as_float(r[k]), vo.x, fmaf(__uint_as_float(r[k + 1]), vo.y, z));
+              z = fmaf(__uint_as_float(r[k + 2]), vo.z, fmaf(__uint_as_float(r[k + 3]), vo.w, z));
             }
-            mul2(r[c], r[c + 1], vs.x, vs.y);
-            mul2(r[c + 2], r[c + 3], vs.z, vs.w);
-            p[c / 2] = pack_half2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-            p[c / 2 + 1] = pack_half2(__uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
+            mul2(r[k], r[k + 1], vs.x, vs.y);
+            mul2(r[k + 2], r[k + 3], vs.z, vs.w);
+            p[(k - half) / 2] = pack_half2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+            p[(k - half) / 2 + 1] = pack_half2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3]));
           }
-          tmem_st16(st + half / 2, p);  // over columns that have been read
+          tmem_st16(st + half / 2, p);  // over S, which has been read
         }
         l += (__uint_as_float(la[0]) + __uint_as_float(la[1])) + (__uint_as_float(la[2]) + __uint_as_float(la[3]));
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&sm->p_full[b]);
-        issue_pv(i);
+        mbar_arrive(&sm->p_full[j][c & 1]);
       }
-      // ---- this segment's record
-      ok = __all_sync(kFull, ok && wait(sm->pv_done, it + nt - 1));
-      if (ok) {
+      if (!ok) break;
+      // ---- this segment's record: vectors 128 j .. of the unit, or the second record of its 128 vectors
+      if (jobs > 0) {
+        ok = __all_sync(kFull, pair_wait(sm->o_done[j], c - 1));
+        if (!ok) break;
         tc_fence_after();
-        const size_t slot = size_t(ci + un.u);
-        float4* rec = reinterpret_cast<float4*>(a.ws + sa.sl.off_rec) + (slot * kQ + v) * (kHeadDim / 4);
+      }
+      if (g.both ? tid < g.nv : v < g.nv) {
+        const size_t slot = size_t(ci + g.un.u) * 2 * kQ + tid;
+        reinterpret_cast<float*>(a.ws + sa.sl.off_m)[slot] = m == kNegInf ? kNegInf : m - sg;
+        reinterpret_cast<float*>(a.ws + sa.sl.off_l)[slot] = l;
+      }
+      const int used = min(32, (g.both ? g.nv - j * kQ : g.nv) - (warp & 3) * 32);  // this warp's vectors in use
+      if (jobs > 0 && used > 0) {
+        // O's rows to global memory as whole 128-byte lines, by way of 4 KB of this warp's in a part of Q
+        // that no product reads any more (its own Q; the unused second one where both share the first)
+        float4* buf = reinterpret_cast<float4*>(g.both ? sm->q[j][0] : sm->q[1][j]) + (warp & 3) * 256;
+        float4* rec = reinterpret_cast<float4*>(a.ws + sa.sl.off_rec) +
+                      (size_t(ci + g.un.u) * 2 * kQ + warp * 32) * (kHeadDim / 4);
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 32) {
+        for (int k = 0; k < kHeadDim; k += 32) {
           uint32_t o[32];
-          tmem_ld32(lanes + c, o);
+          tmem_ld32(o_cols + k, o);
           tc_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            rec[(c + j) / 4] = make_float4(__uint_as_float(o[j]) + z, __uint_as_float(o[j + 1]) + z,
-                                           __uint_as_float(o[j + 2]) + z, __uint_as_float(o[j + 3]) + z);
+          for (int e = 0; e < 8; ++e)
+            buf[lane * 8 + (e ^ (lane & 7))] =
+                make_float4(__uint_as_float(o[4 * e]) + z, __uint_as_float(o[4 * e + 1]) + z,
+                            __uint_as_float(o[4 * e + 2]) + z, __uint_as_float(o[4 * e + 3]) + z);
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int row = 4 * e + (lane >> 3);
+            if (row < used) rec[size_t(row) * (kHeadDim / 4) + k / 4 + (lane & 7)] = buf[row * 8 + ((lane & 7) ^ (row & 7))];
+          }
+          __syncwarp();
         }
-        reinterpret_cast<float*>(a.ws + sa.sl.off_m)[slot * kQ + v] = m == kNegInf ? kNegInf : m - sg;
-        reinterpret_cast<float*>(a.ws + sa.sl.off_l)[slot * kQ + v] = l;
         tc_fence_before();
-      } else {
-        give_up();
       }
+      n0 += g.nt;
     }
-    it += nt;
-    __syncthreads();  // Q, the lengths and O are free for the next segment
-    if (sm->dead) break;
   }
+  if (!ok) flag(a.err, KVQ_DEVERR_TIMEOUT);
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_free(tmem, kTmemCols);
+  if (warp == 12) tmem_free(tmem, kTmemCols);
 }
 
 template <int KB, int VB, bool ASYM>
@@ -623,17 +736,14 @@ struct SharedTcKernel {
     std::lock_guard<std::mutex> lk(mu);
     auto it = done.find(dev);
     if (it != done.end()) return it->second;
-    int sms = 0, room = 0;
+    int sms = 0;
     const auto k = shared_tc_kernel<KB, VB, ASYM>;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&room, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev) != cudaSuccess ||
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
             cudaSuccess)
       return 0;
-    // two CTAs fit an SM: 128 registers a thread, 256 of 512 tensor-memory columns and the shared memory
-    // (the occupancy query answers one for a kernel that uses tensor memory)
-    return done[dev] = sms * (2 * (smem_bytes() + 1024) <= room ? 2 : 1);
+    return done[dev] = sms;  // one CTA per SM: its shared memory and all of its tensor memory
   }
   static cudaError_t launch(const SharedArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
