@@ -18,9 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_decode_asym.cu", "kvq_decode_q32.cu",
-           "kvq_decode_suffix.cu", "kvq_decode_suffix_q32.cu", "kvq_evict.cu", "kvq_mass.cu", "kvq_noalloc.cu",
+           "kvq_evict.cu", "kvq_mass.cu", "kvq_noalloc.cu",
            "kvq_prefill_tiles.cu", "kvq_rope.cu", "kvq_shared.cu", "kvq_shared_tc.cu",
-           "kvq_shared_tiles.cu"]
+           "kvq_shared_tiles.cu", "kvq_suffix.cu", "kvq_suffix_q32.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I" + INCLUDE]

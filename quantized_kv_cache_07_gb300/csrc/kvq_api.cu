@@ -120,38 +120,34 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
   return (long long)((n + TR - 1) / TR) * kv_heads;
 }
 
-// Workspace of kvq_decode_shared: the suffix decode's, its result, and the prefix records.
-kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::DecodeLayout* dl,
-                         kvq::SharedLayout* sl) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return KVQ_ERR_CUDA;
+// Workspace of kvq_decode_shared: the records of the prefix and of the suffixes.
+kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::SharedLayout* sl) {
   const kvq::CacheView v = view(c);
   const int H = c->num_kv_heads, G = q_heads / H;
-  const int per = kvq::suffix_ctas_per_sm_for(c->k_bits, c->v_bits, c->asym != 0, v.q_bits, batch);
-  const int P = stream_ctas_for(sms * per, c->window > 0 ? batch * H : 0, batch * H);
   // 256-vector units on tcgen05 where the groups fill them, 16-vector tiles
   // otherwise, for bf16 blocks and for the two-part mode.
   sl->tc = c->k_bits != 16 && v.q_bits != 32 && batch * G >= 32 * num_groups;
   sl->tile = sl->tc ? 256 : 16;
   sl->ctas = sl->tc ? kvq::shared_tc_ctas(v) : kvq::shared_tiles_ctas(v);
-  if (P <= 0 || sl->ctas <= 0) return KVQ_ERR_CUDA;
-  *dl = kvq::decode_layout(batch, q_heads, H, c->window, P, kvq::switch_blocks_for(c->k_bits));
-  // every group adds at most one tile that is not full
+  sl->suf_ctas = kvq::suffix_ctas(v, batch);
+  if (sl->ctas <= 0 || sl->suf_ctas <= 0) return KVQ_ERR_CUDA;
+  // every group adds at most one tile that is not full; every unit at most one chunk that is not
   const long long units = ((long long)batch * G / sl->tile + num_groups) * H;
   sl->slots = sl->ctas + int(units);
-  size_t o = dl->total;
-  sl->off_o = o;
-  o = round_up(o + size_t(batch) * q_heads * kHeadDim * 4, 256);
-  sl->off_lse = o;
-  o = round_up(o + size_t(batch) * q_heads * 4, 256);
-  sl->off_m = o;
-  o = round_up(o + size_t(sl->slots) * sl->tile * 4, 256);
-  sl->off_l = o;
-  o = round_up(o + size_t(sl->slots) * sl->tile * 4, 256);
-  sl->off_rec = o;
-  o = round_up(o + size_t(sl->slots) * sl->tile * kHeadDim * 4, 256);
+  sl->suf_slots = 2 * sl->suf_ctas + (c->window > 0 ? 2 : 1) * batch * H;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = round_up(o + bytes, 256);
+    return at;
+  };
+  sl->off_m = take(size_t(sl->slots) * sl->tile * 4);
+  sl->off_l = take(size_t(sl->slots) * sl->tile * 4);
+  sl->off_rec = take(size_t(sl->slots) * sl->tile * kHeadDim * 4);
+  sl->off_sm = take(size_t(sl->suf_slots) * G * 4);
+  sl->off_sl = take(size_t(sl->suf_slots) * G * 4);
+  sl->off_so = take(size_t(sl->suf_slots) * G * kHeadDim * 4);
+  sl->off_chunks = take(size_t(batch) * 8);
   sl->total = o;
   return KVQ_OK;
 }
@@ -577,9 +573,8 @@ kvq_status kvq_decode_shared_workspace_size(const kvq_cache_desc* cache, int32_t
   if (!bytes) return KVQ_ERR_INVALID_ARG;
   if ((st = check_decode_shape(cache, batch, q_heads)) != KVQ_OK) return st;
   if ((st = check_groups(num_groups)) != KVQ_OK) return st;
-  kvq::DecodeLayout dl;
   kvq::SharedLayout sl;
-  if ((st = shared_layout(cache, batch, q_heads, num_groups, &dl, &sl)) != KVQ_OK) return st;
+  if ((st = shared_layout(cache, batch, q_heads, num_groups, &sl)) != KVQ_OK) return st;
   *bytes = sl.total;
   return KVQ_OK;
 }
@@ -600,7 +595,7 @@ kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t
   if (!workspace) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
   kvq::SharedArgs s;
-  if ((st = shared_layout(cache, batch, q_heads, num_groups, &s.d.lay, &s.sl)) != KVQ_OK) return st;
+  if ((st = shared_layout(cache, batch, q_heads, num_groups, &s.sl)) != KVQ_OK) return st;
   if (workspace_bytes < s.sl.total) return KVQ_ERR_WORKSPACE;
   kvq::DecodeArgs& a = s.d;
   a.c = view(cache);
@@ -622,12 +617,8 @@ kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t
   a.group_start = group_start;
   a.prefix_blocks = prefix_blocks;
   a.num_groups = num_groups;
-  kvq::DecodeArgs suffix = a;  // its result goes to the workspace
-  suffix.out = a.ws + s.sl.off_o;
-  suffix.out_fp32 = 1;
-  suffix.lse = reinterpret_cast<float*>(a.ws + s.sl.off_lse);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (kvq::launch_suffix(suffix, cs) != cudaSuccess || (s.sl.tc ? kvq::launch_shared_tc(s, cs) : kvq::launch_shared_tiles(s, cs)) != cudaSuccess ||
+  if (kvq::launch_suffix(s, cs) != cudaSuccess || (s.sl.tc ? kvq::launch_shared_tc(s, cs) : kvq::launch_shared_tiles(s, cs)) != cudaSuccess ||
       kvq::launch_shared_merge(s, cs) != cudaSuccess)
     return KVQ_ERR_CUDA;
   return KVQ_OK;

@@ -109,58 +109,6 @@ struct Fmt {
   static constexpr int kVO = kGroup ? 3 : kMF / 2 + kBlock;
 };
 
-// Groups of sequences that share a prefix, in shared memory: group i holds
-// sequences start[i]..start[i + 1] - 1, which share their first blocks[i] blocks.
-struct GroupGeo {
-  int start[kMaxGroups + 4];
-  int blocks[kMaxGroups];
-};
-
-// Read and clean the caller's arrays (all threads of the CTA; ends with a
-// barrier): starts within [0, B] and not falling, prefixes within the table.
-// Returns (in every thread) the error bits of what had to be cleaned.
-__device__ __forceinline__ unsigned load_groups(GroupGeo* geo, const int* start, const int* blocks, int n, int B,
-                                                int mbps, int tid, int threads) {
-  unsigned bad = 0u;
-  for (int i = tid; i < n; i += threads) {
-    const int p = blocks[i];
-    if (p < 0 || p > mbps) bad |= KVQ_DEVERR_SEQ_LEN;
-    geo->blocks[i] = min(max(p, 0), mbps);
-  }
-  if (tid < 32) {
-    int top = 0;
-    for (int base = 0; base <= n; base += 32) {
-      const int i = base + tid;
-      const int raw = i <= n ? start[i] : 0;
-      int v = max(i <= n ? min(raw, B) : 0, 0);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int m = __shfl_up_sync(0xffffffffu, v, o);
-        if (tid >= o) v = max(v, m);
-      }
-      v = max(v, top);
-      if (i <= n) {
-        if (v != raw) bad |= KVQ_DEVERR_POSITION;
-        geo->start[i] = v;
-      }
-      top = __shfl_sync(0xffffffffu, v, 31);
-    }
-  }
-  unsigned all = __syncthreads_or(bad & KVQ_DEVERR_SEQ_LEN) ? KVQ_DEVERR_SEQ_LEN : 0u;
-  return all | (__syncthreads_or(bad & KVQ_DEVERR_POSITION) ? KVQ_DEVERR_POSITION : 0u);
-}
-
-// The group of sequence b, or -1: the last group that starts at or before b and holds it.
-__device__ __forceinline__ int group_of(const GroupGeo* geo, int n, int b) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (geo->start[mid] <= b) lo = mid;
-    else hi = mid - 1;
-  }
-  return b >= geo->start[lo] && b < geo->start[lo + 1] ? lo : -1;
-}
-
 // Shared-memory map after the stage ring (all offsets 16-byte aligned).
 struct SmemMap {
   int merge_o;   // float [4 warps][4 q][128] (combine, four queries per pass)
@@ -176,13 +124,11 @@ struct SmemMap {
   int len;       // int [B]
   int pre;       // int [B+1]
   int vpre;      // int [B+1]
-  int rows;      // int [B]: sequence of each row (prefill), or first block of each sequence (suffix decode)
-  int groups;    // GroupGeo (suffix decode only)
+  int rows;      // int [B]: sequence of each row (prefill only)
   int total;
 };
 
-__host__ __device__ inline SmemMap smem_map(int stage_bytes_total, int stages, int B, bool loq, bool rows,
-                                            bool groups = false) {
+__host__ __device__ inline SmemMap smem_map(int stage_bytes_total, int stages, int B, bool loq, bool rows) {
   SmemMap m;
   int o = stage_bytes_total;
   m.merge_o = o;  o += kConsumerWarps * 4 * kHeadDim * 4;
@@ -199,7 +145,6 @@ __host__ __device__ inline SmemMap smem_map(int stage_bytes_total, int stages, i
   m.pre = o;      o += (((B + 1) * 4 + 15) / 16) * 16;
   m.vpre = o;     o += (((B + 1) * 4 + 15) / 16) * 16;
   m.rows = o;     o += rows ? ((B * 4 + 15) / 16) * 16 : 0;
-  m.groups = o;   o += groups ? int(sizeof(GroupGeo)) : 0;
   m.total = o;
   return m;
 }
@@ -1152,8 +1097,7 @@ __device__ __forceinline__ bool scan_geometry(const DecodeArgs& a, int B, int W,
 
 // LOQ: the two-part mode (q_bits 32) of code blocks: the query and the value
 // weights p * s_v each carried as fp16 high + low parts.
-// SUF: the tokens behind each sequence's shared prefix only (kvq_decode_shared).
-template <int KB, int VB, bool ASYM, bool LOQ, bool SUF>
+template <int KB, int VB, bool ASYM, bool LOQ>
 __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   using F = Fmt<KB, VB, ASYM>;
   constexpr int S = F::kStages;
@@ -1162,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   const int P = prm.P, Uw = prm.Uw;
   const int H = a.c.H, G = a.G, B = a.B;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const SmemMap mp = smem_map(S * F::kStageBytes, S, B, LOQ, SUF || a.pos != nullptr, SUF);
+  const SmemMap mp = smem_map(S * F::kStageBytes, S, B, LOQ, a.pos != nullptr);
   Scratch sc;
   sc.merge_o = reinterpret_cast<float*>(smem + mp.merge_o);
   sc.merge_m = reinterpret_cast<float*>(smem + mp.merge_ml);
@@ -1208,17 +1152,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   // early in turn, then wait until the previous kernel has completed (its
   // writes visible) before reading memory it may write.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  GroupGeo* const groups = reinterpret_cast<GroupGeo*>(smem + mp.groups);
   auto load_len = [&](int b) {
-    if constexpr (SUF) {
-      const int g = group_of(groups, a.num_groups, b);
-      const int L = a.seq_lens[b], cap = a.mbps * kBlock + W;
-      if ((L < 0 || L > cap) && blockIdx.x == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
-      const int Lc = min(max(L, 0), cap);
-      const int skip = min(g < 0 ? 0 : groups->blocks[g] * kBlock, max(Lc - W, 0));
-      rows_s[b] = g < 0 ? 0 : groups->blocks[g];  // read only where the suffix holds blocks: skip is the whole prefix
-      return Lc - skip;
-    }
     if (!a.pos) return a.seq_lens[b];
     // prefill: row b is position pos[b] of sequence seq_of[b] and attends to 0..pos[b]
     const int sb = a.seq_of[b];
@@ -1240,10 +1174,6 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   if (a.ahead) len_bad = scan_geometry(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if constexpr (SUF) {
-    const unsigned bad = load_groups(groups, a.group_start, a.prefix_blocks, a.num_groups, B, a.mbps, tid, kThreads);
-    if (bad && blockIdx.x == 0 && tid == 0) flag(a.err, bad);
-  }
   // ---- sequence geometry: clamped lengths and block prefix sums
   if (!a.ahead) len_bad = scan_geometry(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
   if (len_bad && blockIdx.x == 0 && tid == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
@@ -1343,8 +1273,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
         const int idx = local + lane;
         int v = 0;
         if (idx < nblk) {
-          if constexpr (SUF) v = a.table[size_t(b) * a.mbps + rows_s[b] + idx];
-          else v = a.table[size_t(a.pos ? rows_s[b] : b) * a.mbps + idx];
+          v = a.table[size_t(a.pos ? rows_s[b] : b) * a.mbps + idx];
           if (v < 0 || v >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
             v = 0;
@@ -1541,11 +1470,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
 }
 
 // ------------------------------------------------------------------ host side
-template <int KB, int VB, bool ASYM, bool LOQ, bool SUF = false>
+template <int KB, int VB, bool ASYM, bool LOQ>
 struct Kernel {
   using F = Fmt<KB, VB, ASYM>;
   static int smem_bytes(int B, bool rows) {
-    return smem_map(F::kStages * F::kStageBytes, F::kStages, B, LOQ, rows, SUF).total;
+    return smem_map(F::kStages * F::kStageBytes, F::kStages, B, LOQ, rows).total;
   }
   // Allow the largest opt-in dynamic shared memory once per device; the
   // per-launch size (which depends on the batch) then always fits.
@@ -1556,11 +1485,11 @@ struct Kernel {
     if (done.count(dev)) return;
     int optin = 0;
     cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ, SUF>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
     // Ask for the largest shared-memory carveout: the occupancy used to size
     // the single wave assumes it, and a smaller split (chosen by default)
     // would fit one CTA fewer per SM and turn the wave into 1.5 waves.
-    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ, SUF>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ>, cudaFuncAttributePreferredSharedMemoryCarveout,
                          cudaSharedmemCarveoutMaxShared);
     done[dev] = true;
   }
@@ -1576,14 +1505,14 @@ struct Kernel {
     auto itc = cache.find(key);
     if (itc != cache.end()) return itc->second;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<KB, VB, ASYM, LOQ, SUF>, kThreads, smem) != cudaSuccess)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<KB, VB, ASYM, LOQ>, kThreads, smem) != cudaSuccess)
       n = 1;
     n = n < 1 ? 1 : n;
     cache[key] = n;
     return n;
   }
   static cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
-    const int smem = smem_bytes(a.B, SUF || a.pos != nullptr);
+    const int smem = smem_bytes(a.B, a.pos != nullptr);
     int dev = 0;
     cudaGetDevice(&dev);
     ensure_attribute(dev);
@@ -1599,7 +1528,7 @@ struct Kernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ, SUF>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ>, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
   }

@@ -135,14 +135,17 @@ struct DecodeArgs {
 
 constexpr int kMaxGroups = 256;
 
-// Workspace of kvq_decode_shared behind the suffix decode's own (byte offsets).
-// The prefix is split over `ctas` CTAs; a unit is a tile of `tile` query vectors of
-// one group and KV head; CTA c's share of unit u is record c + u.
+// Workspace of kvq_decode_shared (byte offsets).  The prefix is split over `ctas` CTAs; a unit is
+// a tile of `tile` query vectors of one group and KV head; CTA c's share of unit u is record c + u.
+// The suffixes are split into chunks over `suf_ctas` CTAs, one record each, and one per unit for a
+// bf16 window behind them.
 struct SharedLayout {
   int ctas, tile, slots;
   bool tc;  // tcgen05 path (tile 256), else mma.sync (tile 16)
-  size_t off_o, off_lse;             // suffix result: float [B][Hq][128], [B][Hq]
-  size_t off_m, off_l, off_rec;      // records: float [slots][tile], twice, and [slots][tile][128]
+  int suf_ctas, suf_slots;
+  size_t off_m, off_l, off_rec;     // prefix records: float [slots][tile], twice, and [slots][tile][128]
+  size_t off_sm, off_sl, off_so;    // suffix records: float [suf_slots][G], twice, and [suf_slots][G][128]
+  size_t off_chunks;                // int2 [B]: first chunk of a sequence, chunks of each of its heads
   size_t total;
 };
 
@@ -176,13 +179,14 @@ cudaError_t launch_decode_asym(const DecodeArgs& a, cudaStream_t s);
 // The two-part fp16 query instantiations (kvq_decode_q32.cu).
 int decode_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch, bool rows);
 cudaError_t launch_decode_q32(const DecodeArgs& a, cudaStream_t s);
-// kvq_decode_shared: the suffix decode (kvq_decode_suffix*.cu), the prefix on query tiles
+// kvq_decode_shared: the suffixes (kvq_suffix*.cu), the prefix on query tiles
 // (kvq_shared_tiles.cu: mma.sync, kvq_shared_tc.cu: tcgen05) and the merge (kvq_shared.cu).
-int suffix_ctas_per_sm_for(int k_bits, int v_bits, bool asym, int q_bits, int batch);
-cudaError_t launch_suffix(const DecodeArgs& a, cudaStream_t s);
-int suffix_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch);
-cudaError_t launch_suffix_q32(const DecodeArgs& a, cudaStream_t s);
-int shared_tiles_ctas(const CacheView& c);  // one wave on the current device, 0: failure
+// The *_ctas functions give one wave on the current device, 0 on failure.
+int suffix_ctas(const CacheView& c, int batch);
+cudaError_t launch_suffix(const SharedArgs& a, cudaStream_t s);
+int suffix_ctas_q32(const CacheView& c, int batch);
+cudaError_t launch_suffix_q32(const SharedArgs& a, cudaStream_t s);
+int shared_tiles_ctas(const CacheView& c);
 cudaError_t launch_shared_tiles(const SharedArgs& a, cudaStream_t s);
 int shared_tc_ctas(const CacheView& c);
 cudaError_t launch_shared_tc(const SharedArgs& a, cudaStream_t s);

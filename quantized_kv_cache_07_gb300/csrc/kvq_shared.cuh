@@ -12,6 +12,58 @@
 namespace kvq {
 namespace {
 
+// Groups of sequences that share a prefix, in shared memory: group i holds
+// sequences start[i]..start[i + 1] - 1, which share their first blocks[i] blocks.
+struct GroupGeo {
+  int start[kMaxGroups + 4];
+  int blocks[kMaxGroups];
+};
+
+// Read and clean the caller's arrays (all threads of the CTA; ends with a
+// barrier): starts within [0, B] and not falling, prefixes within the table.
+// Returns (in every thread) the error bits of what had to be cleaned.
+__device__ __forceinline__ unsigned load_groups(GroupGeo* geo, const int* start, const int* blocks, int n, int B,
+                                                int mbps, int tid, int threads) {
+  unsigned bad = 0u;
+  for (int i = tid; i < n; i += threads) {
+    const int p = blocks[i];
+    if (p < 0 || p > mbps) bad |= KVQ_DEVERR_SEQ_LEN;
+    geo->blocks[i] = min(max(p, 0), mbps);
+  }
+  if (tid < 32) {
+    int top = 0;
+    for (int base = 0; base <= n; base += 32) {
+      const int i = base + tid;
+      const int raw = i <= n ? start[i] : 0;
+      int v = max(i <= n ? min(raw, B) : 0, 0);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int m = __shfl_up_sync(kFull, v, o);
+        if (tid >= o) v = max(v, m);
+      }
+      v = max(v, top);
+      if (i <= n) {
+        if (v != raw) bad |= KVQ_DEVERR_POSITION;
+        geo->start[i] = v;
+      }
+      top = __shfl_sync(kFull, v, 31);
+    }
+  }
+  unsigned all = __syncthreads_or(bad & KVQ_DEVERR_SEQ_LEN) ? KVQ_DEVERR_SEQ_LEN : 0u;
+  return all | (__syncthreads_or(bad & KVQ_DEVERR_POSITION) ? KVQ_DEVERR_POSITION : 0u);
+}
+
+// The group of sequence b, or -1: the last group that starts at or before b and holds it.
+__device__ __forceinline__ int group_of(const GroupGeo* geo, int n, int b) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (geo->start[mid] <= b) lo = mid;
+    else hi = mid - 1;
+  }
+  return b >= geo->start[lo] && b < geo->start[lo + 1] ? lo : -1;
+}
+
 struct SharedGeo {
   GroupGeo g;
   int unit0[kMaxGroups + 4];       // units of the groups before group i

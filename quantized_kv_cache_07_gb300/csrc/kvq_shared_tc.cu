@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  shared_geometry(&sm->geo, a, 2 * kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix decode
+  shared_geometry(&sm->geo, a, 2 * kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix kernel
   const SharedGeo* geo = &sm->geo;
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
   if (ci >= Pe) return;

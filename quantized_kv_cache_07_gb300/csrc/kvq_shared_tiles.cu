@@ -5,7 +5,7 @@
 // CTA streams its share of the prefix once for the tile, as the chunked prefill
 // does (kvq_tiles.cuh).  The prefix of a unit is cut over several CTAs; each
 // writes one record (m, l, o) per vector, and kvq_shared.cu merges the records
-// with the result of the suffix decode.  Every cache format and query mode.
+// with those of the suffixes.  Every cache format and query mode.
 #include "kvq_shared.cuh"
 #include "kvq_tiles.cuh"
 
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
   if (!F::kBf16 && a.c.k_chan) unit_key_scales(tid, kThreads);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  shared_geometry(geo, a, kTileQ, kStep, tid, kThreads, false);  // errors are reported by the suffix decode
+  shared_geometry(geo, a, kTileQ, kStep, tid, kThreads, false);  // errors are reported by the suffix kernel
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
   if (ci >= Pe) return;
   const long long x0 = (long long)ci * geo->T / Pe, x1 = (long long)(ci + 1) * geo->T / Pe;
