@@ -16,15 +16,16 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   const int tid = threadIdx.x, lane = tid & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
   const long long q = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
-  if (q >= (long long)a.B * a.Hq) return;
-  const int b = int(q / a.Hq), hq = int(q % a.Hq), h = hq / a.G, hj = hq % a.G;
+  const bool any = q < (long long)a.B * a.Hq;
+  const int b = any ? int(q / a.Hq) : 0, hq = any ? int(q % a.Hq) : 0, h = hq / a.G, hj = hq % a.G;
   // ---- where the records are: prefix ones (np), the suffix's chunks (ns), the window's
   const int2 ch = reinterpret_cast<const int2*>(a.ws + sa.sl.off_chunks)[b];
+  const int2 last = reinterpret_cast<const int2*>(a.ws + sa.sl.off_chunks)[a.B - 1];
+  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
+  if (!any) return;
   const int H = a.c.H, ns = ch.y;
   const size_t first_s = size_t(ch.x) + size_t(h) * ns;  // suffix record of chunk 0 of this unit
-  const int2 last = reinterpret_cast<const int2*>(a.ws + sa.sl.off_chunks)[a.B - 1];
   const size_t win = size_t(last.x) + size_t(last.y) * H + size_t(b) * H + h;
   int np = 0, two = 0, v = 0;
   size_t first_p = 0;

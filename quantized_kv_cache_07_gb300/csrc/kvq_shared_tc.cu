@@ -232,13 +232,15 @@ __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw
   scale = kLog2e * kInvSqrtD;
   if (a.c.q_bits == 8) {
     float s = 1.f;
-#pragma unroll
-    for (int k = 0; k < 16; k += 4) {
-      const float y[4] = {x[k], x[k + 1], x[k + 2], x[k + 3]};
+#pragma unroll 1
+    for (int k = 0; k < 16; k += 4) {  // a loop: the rounding with its exact ties is long code
+      const float y[4] = {x[0], x[1], x[2], x[3]};
       float c[4];
       s = quantize_int8_row(y, am, c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[k + e] = c[e];
+      for (int e = 0; e < 12; ++e) x[e] = x[e + 4];  // rotate, so that every index is known
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[12 + e] = c[e];
     }
     scale *= s;
   } else {
@@ -418,10 +420,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
       const Segment g = segment_at(geo, a, x, x1);
       x += g.nt;
       const int* table = a.table + size_t(g.first) * a.mbps;
-      int maxlen = 0;  // of the unit's rows: scales of slots behind it are not data
-      for (int r = g.un.tile * 2 * kQ / a.G + lane; r <= (g.un.tile * 2 * kQ + g.nv - 1) / a.G; r += 32)
-        maxlen = max(maxlen, prefix_len(a, g.first + r, g.nblk));
-      maxlen = __reduce_max_sync(kFull, maxlen);
       int ids = -1, ids_next = -1;  // this warp's table entries of 32 tiles, and of the next 32
       auto load_ids = [&](int i) {
         const int blk = (g.t0 + i + lane) * kStep + w;
@@ -436,6 +434,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
         return id;
       };
       ids_next = load_ids(0);
+      int maxlen = 0;  // of the unit's rows: scales of slots behind it are not data
+      for (int r = g.un.tile * 2 * kQ / a.G + lane; r <= (g.un.tile * 2 * kQ + g.nv - 1) / a.G; r += 32)
+        maxlen = max(maxlen, prefix_len(a, g.first + r, g.nblk));
+      maxlen = __reduce_max_sync(kFull, maxlen);
       // this warp's block of the tile: codes, and the record entries of token `lane` (lanes 0..15)
       Raw<KB> rk;
       Raw<VB> rv;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
         if (!ok) break;
       }
       {
-        // this warp's 32 vectors (16 of the shared 128), 4 a step, the next step's loads ahead
+        // this warp's 32 vectors (16 of the shared 128), 4 a step
         const int per = g.both ? 32 : 16, v0 = (g.both ? warp : 2 * (warp & 3) + j) * per, sub = lane & 7;
         const int G = a.G, gv0 = g.un.tile * 2 * kQ + v0;
         const uint16_t* src = a.q + (size_t(g.first) * a.Hq + g.un.h * G) * kHeadDim + 16 * sub;
@@ -525,31 +527,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
             *reinterpret_cast<float4*>(f + k) =
                 *reinterpret_cast<const float4*>(a.c.factor + g.un.h * kHeadDim + 16 * sub + k);
         }
-        if (lane < per) {
-          const int r = (gv0 + lane) / G;
-          sm->qlen[v0 + lane] = r < g.rows ? prefix_len(a, g.first + r, g.nblk) : 0;
-        }
         uint8_t* half = sm->q[g.both ? j : 0][sub & 1];
         int r = (gv0 + (lane >> 3)) / G, hj = (gv0 + (lane >> 3)) % G;
-        uint4 raw[2];
-        auto load = [&]() {
-          raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < g.rows) {
+        uint4 raw[8][2];  // all loads before the first conversion: one latency
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (4 * i < per && r < g.rows) {
             const uint4* p = reinterpret_cast<const uint4*>(src + (size_t(r) * a.Hq + hj) * kHeadDim);
-            raw[0] = p[0];
-            raw[1] = p[1];
+            raw[i][0] = p[0];
+            raw[i][1] = p[1];
           }
           hj += 4;
           while (hj >= G) {
             hj -= G;
             ++r;
           }
-        };
-        load();
+        }
+        if (lane < per) {
+          const int row = (gv0 + lane) / G;
+          sm->qlen[v0 + lane] = row < g.rows ? prefix_len(a, g.first + row, g.nblk) : 0;
+        }
 #pragma unroll 1
         for (int b = 0; b < per; b += 4) {
-          const uint4 cur[2] = {raw[0], raw[1]};
-          load();
+          const uint4 cur[2] = {raw[0][0], raw[0][1]};
+#pragma unroll
+          for (int e = 0; e < 7; ++e) {  // rotate: the loop stays short and every index is known
+            raw[e][0] = raw[e + 1][0];
+            raw[e][1] = raw[e + 1][1];
+          }
           const int at = v0 + b + (lane >> 3);
           float qs, sum;
           put_query<ASYM>(a, cur, f, half, at & (kQ - 1), sub, qs, sum);

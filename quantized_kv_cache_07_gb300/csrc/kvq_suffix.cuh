@@ -34,7 +34,7 @@ struct SufFmt {
 
 // Shared-memory map behind the rings (16-byte aligned offsets).
 struct SufSmem {
-  int merge_o, merge_ml, qh, qlo, qs, qraw, fraw, bar, nblk, groups, total;
+  int merge_o, merge_ml, qh, qlo, qs, nblk, lens, groups, total;
 };
 __host__ __device__ inline SufSmem suf_smem(int rings, int B, bool loq) {
   SufSmem m;
@@ -44,22 +44,19 @@ __host__ __device__ inline SufSmem suf_smem(int rings, int B, bool loq) {
   m.qh = o;       o += kMaxGroup * kHeadDim * 2;
   m.qlo = o;      o += loq ? kMaxGroup * kHeadDim * 2 : 0;
   m.qs = o;       o += 4 * kMaxGroup * 4;
-  m.qraw = o;     o += kMaxGroup * kHeadDim * 2;
-  m.fraw = o;     o += kHeadDim * 4;
-  m.bar = o;      o += 16;
   m.nblk = o;     o += ((B + 1) * 4 + 15) / 16 * 16;  // chunks of one head before sequence b
+  m.lens = o;     o += (B * 4 + 15) / 16 * 16;
   m.groups = o;   o += (int(sizeof(GroupGeo)) + 15) / 16 * 16;
   m.total = o;
   return m;
 }
 
-// Sequence b: its prefix's blocks, tokens behind it (stored ones) and ring tokens.
+// Sequence b of length L: its prefix's blocks, tokens behind it (stored ones) and ring tokens.
 struct SufLen {
   int skip, tokens, ring;
 };
-__device__ __forceinline__ SufLen suffix_len(const DecodeArgs& a, const GroupGeo* groups, int b, bool& bad) {
+__device__ __forceinline__ SufLen suffix_len(const DecodeArgs& a, const GroupGeo* groups, int b, int L, bool& bad) {
   const int W = a.c.window, cap = a.mbps * kBlock + W;
-  int L = a.seq_lens[b];
   if (L < 0 || L > cap) {
     bad = true;
     L = min(max(L, 0), cap);
@@ -70,6 +67,100 @@ __device__ __forceinline__ SufLen suffix_len(const DecodeArgs& a, const GroupGeo
   s.tokens = max(stored - s.skip * kBlock, 0);
   s.ring = min(L, W);
   return s;
+}
+
+// The query group's rows as B operands, as write_query_rows lays them out: 8 lanes a
+// row (16 dims each, their bf16 bits in raw), all rows in one step by warps 0 and 1.
+template <bool kBf16, bool ASYM, bool LOQ>
+__device__ __forceinline__ void put_rows(const DecodeArgs& a, const uint4 (&raw)[2], int h, uint16_t* qh, uint32_t* qlo,
+                                         float* qs, int tid) {
+  if (tid >= 8 * kMaxGroup) return;
+  const int q = tid >> 3, sub = tid & 7;
+  float f[16];
+  uint4* row = reinterpret_cast<uint4*>(qh + q * kHeadDim + 16 * sub);
+  if constexpr (kBf16) {
+    row[0] = raw[0];
+    row[1] = raw[1];
+    if (sub == 0) qs[q] = kLog2e * kInvSqrtD;
+    return;
+  }
+  if (a.c.factor) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 4)
+      *reinterpret_cast<float4*>(f + k) = *reinterpret_cast<const float4*>(a.c.factor + h * kHeadDim + 16 * sub + k);
+  }
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 4 ? (&raw[0].x)[i] : (&raw[1].x)[i - 4];
+    x[2 * i] = __uint_as_float(w << 16);
+    x[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+  if (a.c.factor) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= f[k];
+  }
+  float am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) am = fmaxf(am, fabsf(x[k]));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(kFull, am, o));
+  float scale = kLog2e * kInvSqrtD;
+  if (a.c.q_bits == 8) {
+    float s = 1.f;
+#pragma unroll 1
+    for (int k = 0; k < 16; k += 4) {  // a loop: the rounding with its exact ties is long code
+      const float y[4] = {x[0], x[1], x[2], x[3]};
+      float c[4];
+      s = quantize_int8_row(y, am, c);
+#pragma unroll
+      for (int e = 0; e < 12; ++e) x[e] = x[e + 4];  // rotate, so that every index is known
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[12 + e] = c[e];
+    }
+    scale *= s;
+  } else {
+    // exact powers of two: am * 2^(14 - e) in [2^14, 2^15); below 2^-112 the scores are zero to any precision
+    const uint32_t e = max(__float_as_uint(am) >> 23, 15u);
+    const float f2 = __uint_as_float((268u - e) << 23);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= f2;
+    scale *= __uint_as_float((e - 14u) << 23);
+  }
+  float even = 0.f, odd = 0.f, z = 0.f;  // sums of the row as the MMA sees it: by k-slice, with the low parts
+  uint32_t hi[8], lo[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
+    if (i & 2) odd += y.x + y.y;
+    else even += y.x + y.y;
+    if constexpr (LOQ) {
+      lo[i] = pack_half2(x[2 * i] - y.x, x[2 * i + 1] - y.y);
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&lo[i]));
+      z += w.x + w.y;
+    }
+  }
+  row[0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  row[1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+  if constexpr (LOQ) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(qlo + ((2 * (sub & 1) + i) * 32 + 4 * q + (sub >> 1)) * 4) =
+          make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    even += __shfl_xor_sync(kFull, even, o);
+    odd += __shfl_xor_sync(kFull, odd, o);
+    if constexpr (ASYM && LOQ) z += __shfl_xor_sync(kFull, z, o);
+  }
+  if (sub == 0) {
+    qs[q] = scale;
+    if constexpr (ASYM) qs[kMaxGroup + q] = even + odd + z;
+    qs[2 * kMaxGroup + (q >> 1) * 4 + (q & 1)] = -kOffsetF16 * even;
+    qs[2 * kMaxGroup + (q >> 1) * 4 + 2 + (q & 1)] = -kOffsetF16 * odd;
+  }
 }
 
 template <int KB, int VB, bool ASYM, bool LOQ>
@@ -86,9 +177,8 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
   uint16_t* qh = reinterpret_cast<uint16_t*>(smem + mp.qh);
   uint32_t* qlo_s = reinterpret_cast<uint32_t*>(smem + mp.qlo);
   float* qs = reinterpret_cast<float*>(smem + mp.qs);
-  uint16_t* qraw = reinterpret_cast<uint16_t*>(smem + mp.qraw);
-  float* fraw = reinterpret_cast<float*>(smem + mp.fraw);
   int* pre = reinterpret_cast<int*>(smem + mp.nblk);
+  int* lens = reinterpret_cast<int*>(smem + mp.lens);
   GroupGeo* groups = reinterpret_cast<GroupGeo*>(smem + mp.groups);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int B = a.B, H = a.c.H, G = a.G, W = a.c.window;
@@ -102,6 +192,8 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the first lengths beside the groups: every load that waits for another one costs its latency
+  const int len0 = tid < B ? a.seq_lens[tid] : 0;
   const unsigned gbad = load_groups(groups, a.group_start, a.prefix_blocks, a.num_groups, B, a.mbps, tid, kSufThreads);
   if (gbad && blockIdx.x == 0 && tid == 0) flag(a.err, gbad);
 
@@ -109,7 +201,9 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
   bool bad = false;
   int mine = 0;
   for (int b = tid; b < B; b += kSufThreads) {
-    const int n = (suffix_len(a, groups, b, bad).tokens + kBlock - 1) / kBlock;
+    const int L = b == tid ? len0 : a.seq_lens[b];
+    const int n = (suffix_len(a, groups, b, L, bad).tokens + kBlock - 1) / kBlock;
+    lens[b] = L;
     pre[b + 1] = n;
     mine += n;
   }
@@ -121,7 +215,7 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
   const int* part = reinterpret_cast<const int*>(merge_m);
   const long long blocks = (long long)H * (part[0] + part[1] + part[2] + part[3]);
   constexpr int kGroup4 = kConsumerWarps * NB;
-  const long long want = 2ll * sa.sl.suf_ctas;  // chunks to aim for
+  const long long want = sa.sl.suf_ctas;
   const int C = int(max((blocks + want - 1) / want, (long long)kSufMinGroups * kGroup4));
   __syncthreads();  // part has been read
   if (warp == 0) {
@@ -170,8 +264,16 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
       j = i % nc;
     }
     bool ignored = false;
-    const SufLen sl = suffix_len(a, groups, b, ignored);
+    const SufLen sl = suffix_len(a, groups, b, lens[b], ignored);
     const int b0 = j * C, b1 = win ? 0 : min(b0 + C, (sl.tokens + kBlock - 1) / kBlock);
+    // the queries' loads first, with the table's
+    uint4 raw[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+    if (!win && (tid >> 3) < G) {
+      const uint4* p =
+          reinterpret_cast<const uint4*>(a.q + (size_t(b) * a.Hq + h * G + (tid >> 3)) * kHeadDim + 16 * (tid & 7));
+      raw[0] = p[0];
+      raw[1] = p[1];
+    }
     // ---- this warp's block groups: b0 + (warp + 4 i) * NB
     const int* table = a.table + size_t(b) * a.mbps + sl.skip;
     int ids = 0, ids_base = 0;
@@ -227,13 +329,7 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
     if (win) {
       stage_query<true>(a, b, h, qh, qs, warp, lane);
     } else {
-      const uint16_t* q = a.q + (size_t(b) * a.Hq + h * G) * kHeadDim;
-      for (int i = tid; i < G * kHeadDim / 8; i += kSufThreads)
-        reinterpret_cast<uint4*>(qraw)[i] = reinterpret_cast<const uint4*>(q)[i];
-      if (a.c.factor && tid < kHeadDim / 4)
-        reinterpret_cast<float4*>(fraw)[tid] = reinterpret_cast<const float4*>(a.c.factor + h * kHeadDim)[tid];
-      __syncthreads();
-      write_query_rows<F::kBf16, ASYM>(a, 0, qraw, fraw, qh, qlo_s, qs, warp, lane);
+      put_rows<F::kBf16, ASYM, LOQ>(a, raw, h, qh, qlo_s, qs, tid);
     }
     __syncthreads();
     load_query(qh, qs, qf, qs0, qs1, lane);
