@@ -149,10 +149,18 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> int | None:
+    global _raw_stream
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            # the raw handle without a Stream object per call, where this torch has it
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -172,34 +180,43 @@ def kvq_append(desc: CacheDesc, k_new, v_new, seq_idx, pos, mode: int, block_tab
                              _stream(stream) if n else None), "kvq_append")
 
 
-def _tensor(t, dtype, where: str, shape=None, strided: bool = False):
-    """Pointer of a tensor argument of a newer entry point, None or a raw pointer
-    passed through.  The library cannot see a tensor's type, layout or device:
-    they are checked here, and a mismatch is an invalid argument."""
-    if t is None or isinstance(t, int):
-        return t
-    import torch
-    if (t.dtype is not getattr(torch, dtype) or not t.is_cuda or t.device.index != torch.cuda.current_device()
-            or not (strided or t.is_contiguous()) or (shape is not None and tuple(t.shape) != tuple(shape))):
-        raise KvqError(KVQ_ERR_INVALID_ARG, where)
-    return t.data_ptr()
+class _Args:
+    """Pointers of one call's tensor arguments; None and raw pointers pass through.  The library cannot see a
+    tensor's type, layout or device: they are checked here, and a mismatch is an invalid argument."""
 
+    __slots__ = ("where", "device", "bf16", "f32", "i32", "u8")
 
-def _rows(t, heads: int, n: int, where: str):
-    """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous."""
-    if t is None or isinstance(t, int):
-        return t, 0
-    ptr = _tensor(t, "bfloat16", where, strided=True)
-    inner = t.stride()[1:] if n else ()
-    if (tuple(t.shape) not in ((n, heads * 128), (n, heads, 128)) or
-            (n and inner != ((1,) if t.dim() == 2 else (128, 1)))):
-        raise KvqError(KVQ_ERR_INVALID_ARG, where)
-    return ptr, t.stride(0) if n > 1 else 0
+    def __init__(self, where: str):
+        import torch
+        self.where, self.device = where, torch.cuda.current_device()
+        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+    def __call__(self, t, dtype, shape=None):
+        if t is None or isinstance(t, int):
+            return t
+        if (t.dtype is not dtype or t.get_device() != self.device or not t.is_contiguous()
+                or (shape is not None and t.shape != shape)):
+            raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
+        return t.data_ptr()
+
+    def rows(self, t, heads: int, n: int):
+        """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous."""
+        if t is None or isinstance(t, int):
+            return t, 0
+        ok = t.dtype is self.bf16 and t.get_device() == self.device
+        if ok and t.dim() == 2:
+            ok = t.shape == (n, heads * 128) and (n == 0 or t.stride(1) == 1)
+        elif ok:
+            ok = t.shape == (n, heads, 128) and (n == 0 or t.stride()[1:] == (128, 1))
+        if not ok:
+            raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
+        return t.data_ptr(), t.stride(0) if n > 1 else 0
 
 
 def kvq_rope_table(freqs: RopeFreqs, rotary_dim: int, max_pos: int, table, stream=None):
-    _check(load().kvq_rope_table(ctypes.byref(freqs), rotary_dim, max_pos,
-                                 _tensor(table, "float32", "kvq_rope_table"), _stream(stream)), "kvq_rope_table")
+    arg = _Args("kvq_rope_table")
+    _check(load().kvq_rope_table(ctypes.byref(freqs), rotary_dim, max_pos, arg(table, arg.f32), _stream(stream)),
+           "kvq_rope_table")
 
 
 def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_new, v_new, pos, seq_idx, slot,
@@ -207,17 +224,17 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
     """kvq_rope_append: ``pos`` are the rope positions (int32 [n], None to use ``slot``) and ``slot`` the cache
     positions (the C argument pos).  q, k_new and v_new may be slices of one projection [n, heads * 128]: their row
     strides are taken from the tensors.  q and q_out, or k_new and v_new, may be None."""
-    where = "kvq_rope_append"
+    arg = _Args("kvq_rope_append")
     ref = pos if pos is not None else slot
     n = int(ref.shape[0])
-    qp, qs = _rows(q, q_heads, n, where)
-    kp, ks = _rows(k_new, desc.num_kv_heads, n, where)
-    vp, vs = _rows(v_new, desc.num_kv_heads, n, where)
+    qp, qs = arg.rows(q, q_heads, n)
+    kp, ks = arg.rows(k_new, desc.num_kv_heads, n)
+    vp, vs = arg.rows(v_new, desc.num_kv_heads, n)
     _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
-                                  _tensor(q_out, "bfloat16", where), kp, ks, vp, vs, n,
-                                  _tensor(pos, "int32", where), _tensor(seq_idx, "int32", where),
-                                  _tensor(slot, "int32", where), mode, _tensor(block_table, "int32", where), batch,
-                                  max_blocks_per_seq, _ptr(err_word), _stream(stream) if n else None), where)
+                                  arg(q_out, arg.bf16), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
+                                  arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
+                                  arg(block_table, arg.i32), batch, max_blocks_per_seq, _ptr(err_word),
+                                  _stream(stream) if n else None), arg.where)
 
 
 def kvq_decode_shared_workspace_size(desc: CacheDesc, batch: int, q_heads: int, num_groups: int) -> int:
@@ -230,49 +247,46 @@ def kvq_decode_shared_workspace_size(desc: CacheDesc, batch: int, q_heads: int, 
 def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, block_table, max_blocks_per_seq: int,
                       num_groups: int, group_start, prefix_blocks, out, lse=None, workspace=None,
                       workspace_bytes: int = 0, err_word=None, stream=None, out_fp32: bool | None = None):
-    where = "kvq_decode_shared"
+    arg = _Args("kvq_decode_shared")
     if out_fp32 is None:
-        import torch
-        out_fp32 = out.dtype == torch.float32
-    _check(load().kvq_decode_shared(ctypes.byref(desc), _tensor(q, "bfloat16", where), batch, q_heads,
-                                    _tensor(seq_lens, "int32", where), _tensor(block_table, "int32", where),
-                                    max_blocks_per_seq, num_groups,
-                                    _tensor(group_start, "int32", where, (num_groups + 1,)),
-                                    _tensor(prefix_blocks, "int32", where, (num_groups,)),
-                                    _tensor(out, "float32" if out_fp32 else "bfloat16", where), int(bool(out_fp32)),
-                                    _tensor(lse, "float32", where), _tensor(workspace, "uint8", where),
-                                    workspace_bytes, _ptr(err_word), _stream(stream)), where)
+        out_fp32 = out.dtype is arg.f32
+    rows = (batch, q_heads, 128)
+    _check(load().kvq_decode_shared(ctypes.byref(desc), arg(q, arg.bf16, rows), batch, q_heads,
+                                    arg(seq_lens, arg.i32, (batch,)), arg(block_table, arg.i32, (batch, max_blocks_per_seq)),
+                                    max_blocks_per_seq, num_groups, arg(group_start, arg.i32, (num_groups + 1,)),
+                                    arg(prefix_blocks, arg.i32, (num_groups,)),
+                                    arg(out, arg.f32 if out_fp32 else arg.bf16, rows), int(bool(out_fp32)),
+                                    arg(lse, arg.f32, (batch, q_heads)), arg(workspace, arg.u8), workspace_bytes,
+                                    _ptr(err_word), _stream(stream)), arg.where)
 
 
 def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,
                   mass, decay: float = 1.0, err_word=None, stream=None, mass_stride: int | None = None):
     """kvq_attn_mass; ``mass`` is float32 [batch, kv_heads, mass_stride]."""
-    where = "kvq_attn_mass"
+    arg = _Args("kvq_attn_mass")
     if mass_stride is None:
         mass_stride = int(mass.shape[-1])
-    _check(load().kvq_attn_mass(ctypes.byref(desc), _tensor(q, "bfloat16", where), batch, q_heads,
-                                _tensor(lse, "float32", where), _tensor(seq_lens, "int32", where),
-                                _tensor(block_table, "int32", where), max_blocks_per_seq,
-                                _tensor(mass, "float32", where, (batch, desc.num_kv_heads, mass_stride)), mass_stride,
-                                decay, _ptr(err_word), _stream(stream)), where)
+    _check(load().kvq_attn_mass(ctypes.byref(desc), arg(q, arg.bf16, (batch, q_heads, 128)), batch, q_heads,
+                                arg(lse, arg.f32, (batch, q_heads)), arg(seq_lens, arg.i32, (batch,)),
+                                arg(block_table, arg.i32, (batch, max_blocks_per_seq)), max_blocks_per_seq,
+                                arg(mass, arg.f32, (batch, desc.num_kv_heads, mass_stride)), mass_stride, decay,
+                                _ptr(err_word), _stream(stream)), arg.where)
 
 
 def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batch: int, max_blocks_per_seq: int,
               source, new_lens, protect_first: int = 0, protect_recent: int = 0, token_pos=None, token_pos_out=None,
               next_pos=None, err_word=None, stream=None, mass_stride: int | None = None):
     """kvq_evict; mass, mass_out, source, token_pos and token_pos_out are [batch, kv_heads, mass_stride]."""
-    where = "kvq_evict"
+    arg = _Args("kvq_evict")
     if mass_stride is None:
         mass_stride = int(mass.shape[-1])
-    rows = (batch, desc.num_kv_heads, mass_stride)
-    _check(load().kvq_evict(ctypes.byref(desc), _tensor(mass, "float32", where, rows),
-                            _tensor(mass_out, "float32", where, rows), mass_stride,
-                            _tensor(seq_lens, "int32", where, (batch,)), _tensor(keep, "int32", where, (batch,)),
-                            protect_first, protect_recent, _tensor(token_pos, "int32", where, rows),
-                            _tensor(token_pos_out, "int32", where, rows), _tensor(next_pos, "int32", where, (batch,)),
-                            _tensor(block_table, "int32", where), batch, max_blocks_per_seq,
-                            _tensor(new_lens, "int32", where, (batch,)), _tensor(source, "int32", where, rows),
-                            _ptr(err_word), _stream(stream)), where)
+    rows, each = (batch, desc.num_kv_heads, mass_stride), (batch,)
+    _check(load().kvq_evict(ctypes.byref(desc), arg(mass, arg.f32, rows), arg(mass_out, arg.f32, rows), mass_stride,
+                            arg(seq_lens, arg.i32, each), arg(keep, arg.i32, each), protect_first, protect_recent,
+                            arg(token_pos, arg.i32, rows), arg(token_pos_out, arg.i32, rows),
+                            arg(next_pos, arg.i32, each), arg(block_table, arg.i32, (batch, max_blocks_per_seq)), batch,
+                            max_blocks_per_seq, arg(new_lens, arg.i32, each), arg(source, arg.i32, rows),
+                            _ptr(err_word), _stream(stream)), arg.where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,
