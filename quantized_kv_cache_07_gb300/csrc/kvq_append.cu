@@ -80,15 +80,8 @@ __global__ void __launch_bounds__(kGroupWarps * 32) append_group_kernel(AppendAr
       });
 }
 
-__global__ void __launch_bounds__(256) dequant_kernel(DequantArgs a) {
-  const int lane = threadIdx.x & 31;
-  const long long vec = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+__device__ __forceinline__ void dequant_one(const DequantArgs& a, int r, int slot, bool is_key, int h, int lane) {
   const int H = a.c.H;
-  if (vec >= (long long)a.n * 2 * H) return;
-  const int r = int(vec / (2 * H));
-  const bool is_key = ((vec / H) % 2) == 0;
-  const int h = int(vec % H);
-  const int slot = a.slots[r];
   const int phys = slot / kBlock, tok = slot % kBlock;
   float* out = (is_key ? a.k_out : a.v_out) + (size_t(r) * H + h) * kHeadDim + 4 * lane;
   if (slot < 0 || phys >= a.c.num_blocks) {
@@ -128,6 +121,85 @@ __global__ void __launch_bounds__(256) dequant_kernel(DequantArgs a) {
   }
 }
 
+__global__ void __launch_bounds__(256) dequant_kernel(DequantArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long vec = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int H = a.c.H;
+  if (vec >= (long long)a.n * 2 * H) return;
+  const int r = int(vec / (2 * H));
+  dequant_one(a, r, a.slots[r], ((vec / H) % 2) == 0, int(vec % H), lane);
+}
+
+// Many slots: 16 of the call per warp and (head, K or V).  Where they are one block's 16 tokens in
+// order, the block is read as it lies, 16 bytes a lane, into shared memory and taken apart there; a value
+// token on its own is 128 single bytes of its block.  Other slots go one by one.  Same values.
+constexpr int kDqWarps = 8;
+
+template <int BITS, bool KEY>
+__device__ __forceinline__ int code_at(const uint8_t* img, int tok, int lane, int j) {
+  const Loc L = KEY ? key_loc(BITS, tok, 4 * lane + j) : value_loc(BITS, tok, 4 * lane + j);
+  if constexpr (BITS == 16) return *reinterpret_cast<const uint16_t*>(img + L.byte);
+  return BITS == 8 ? img[L.byte] : (img[L.byte] >> L.shift) & 0xF;
+}
+
+template <int BITS, bool KEY>
+__device__ __forceinline__ void dequant_block(const DequantArgs& a, int r0, int phys, int h, uint8_t* img, int lane) {
+  const CacheView& c = a.c;
+  const size_t hb = size_t(h) * c.num_blocks + phys;
+  const uint4* blk = reinterpret_cast<const uint4*>((KEY ? c.k_codes : c.v_codes) + hb * block_bytes(BITS));
+#pragma unroll
+  for (int i = 0; i < BITS / 2; ++i) reinterpret_cast<uint4*>(img)[i * 32 + lane] = blk[i * 32 + lane];
+  float s_of = 1.f, z_of = 0.f;  // lane i: token i's scale and zero point
+  const bool chan = KEY && c.k_chan;
+  if (BITS != 16 && !chan && lane < kBlock) {
+    const float* rec = c.meta + hb * c.meta_floats + (KEY ? 0 : c.meta_floats / 2);
+    s_of = rec[lane];
+    if (c.asym) z_of = rec[kBlock + lane];
+  }
+  float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (chan) f = *reinterpret_cast<const float4*>(c.factor + h * kHeadDim + 4 * lane);
+  __syncwarp();
+  float* out = (KEY ? a.k_out : a.v_out) + (size_t(r0) * c.H + h) * kHeadDim + 4 * lane;
+  const int bias = c.asym ? 0 : (BITS == 8 ? 128 : 8);
+#pragma unroll
+  for (int i = 0; i < kBlock; ++i) {
+    const float s = __shfl_sync(kFull, s_of, i), z = __shfl_sync(kFull, z_of, i);
+    const float ff[4] = {f.x, f.y, f.z, f.w};
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int raw = code_at<BITS, KEY>(img, i, lane, j);
+      if constexpr (BITS == 16) v[j] = bf16_bits_to_f32(uint16_t(raw));
+      else v[j] = c.asym ? __fmaf_rn(float(raw), s, z) : __fmul_rn(float(raw - bias), chan ? ff[j] : s);
+    }
+    *reinterpret_cast<float4*>(out + size_t(i) * c.H * kHeadDim) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  __syncwarp();
+}
+
+template <int KB, int VB>
+__global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(DequantArgs a) {
+  __shared__ __align__(16) uint8_t img[kDqWarps][kBlock * kHeadDim * 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int H = a.c.H;
+  const long long task = (long long)blockIdx.x * kDqWarps + warp;
+  const long long windows = (a.n + kBlock - 1) / kBlock;
+  if (task >= windows * 2 * H) return;
+  const int r0 = int(task / (2 * H)) * kBlock, kv = int(task % (2 * H));
+  const bool is_key = kv < H;
+  const int h = is_key ? kv : kv - H;
+  const int slot = lane < kBlock && r0 + lane < a.n ? a.slots[r0 + lane] : -1;
+  const int first = __shfl_sync(kFull, slot, 0);
+  if (first >= 0 && first % kBlock == 0 && first / kBlock < a.c.num_blocks &&
+      __all_sync(kFull, lane >= kBlock || slot == first + lane)) {
+    if (is_key) dequant_block<KB, true>(a, r0, first / kBlock, h, img[warp], lane);
+    else dequant_block<VB, false>(a, r0, first / kBlock, h, img[warp], lane);
+    return;
+  }
+  for (int i = 0; i < kBlock && r0 + i < a.n; ++i)
+    dequant_one(a, r0 + i, __shfl_sync(kFull, slot, i), is_key, h, lane);
+}
+
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
@@ -156,6 +228,18 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s) {
   const long long vecs = (long long)a.n * 2 * a.c.H;
   if (vecs == 0) return cudaSuccess;
+  // 16 slots a warp from 256 slots on (fewer are one wave of single-vector warps)
+  if (a.n >= 256 && a.c.k_bits != 2) {
+    const long long tasks = (long long)((a.n + kBlock - 1) / kBlock) * 2 * a.c.H;
+    const unsigned grid = unsigned((tasks + kDqWarps - 1) / kDqWarps);
+    const int kb = a.c.k_bits, vb = a.c.v_bits;
+    if (kb == 8 && vb == 8) dequant_rows_kernel<8, 8><<<grid, kDqWarps * 32, 0, s>>>(a);
+    else if (kb == 4 && vb == 4) dequant_rows_kernel<4, 4><<<grid, kDqWarps * 32, 0, s>>>(a);
+    else if (kb == 4) dequant_rows_kernel<4, 8><<<grid, kDqWarps * 32, 0, s>>>(a);
+    else if (kb == 8) dequant_rows_kernel<8, 4><<<grid, kDqWarps * 32, 0, s>>>(a);
+    else dequant_rows_kernel<16, 16><<<grid, kDqWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   const int warps = 8;
   const long long grid = (vecs + warps - 1) / warps;
   dequant_kernel<<<unsigned(grid), warps * 32, 0, s>>>(a);

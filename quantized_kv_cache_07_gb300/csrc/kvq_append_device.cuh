@@ -15,9 +15,9 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) { return __uint_as
 
 // Warp-cooperative per-vector quantization.
 __device__ __forceinline__ void quantize_warp(const float (&x)[4], int bits, int (&code)[4], float& s) {
-  float a = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(kFull, a, o));
+  // non-negative floats order as their bits: one warp reduction
+  const float a = __uint_as_float(__reduce_max_sync(
+      kFull, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
   const int qmax = bits == 8 ? 127 : 7;
   const int lo = bits == 8 ? -127 : -8;
   if (a == 0.0f) {
@@ -27,9 +27,10 @@ __device__ __forceinline__ void quantize_warp(const float (&x)[4], int bits, int
     return;
   }
   s = __fdiv_rn(a, float(qmax));
+  const float r = __frcp_rn(s);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    int c = int(round_quotient(x[j], s));
+    int c = int(round_quotient_by(x[j], s, r));
     code[j] = min(qmax, max(lo, c));
   }
 }

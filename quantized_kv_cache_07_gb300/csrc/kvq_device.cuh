@@ -88,6 +88,15 @@ __device__ __forceinline__ float round_quotient(float x, float s) {
   return rintf(q);
 }
 
+// round_quotient by the reciprocal r = RN(1 / s): x * r is within 2^-22 of the
+// quotient relatively, so for |x / s| < 400 its nearest integer is the quotient's
+// unless it lies within 10^-4 of a half-integer; there the exact rule decides.
+// Same results in a third of the instructions.
+__device__ __forceinline__ float round_quotient_by(float x, float s, float r) {
+  const float t = x * r, c = rintf(t);
+  return fabsf(t - c) < 0.4999f ? c : round_quotient(x, s);
+}
+
 // Symmetric int8 codes of four values of a warp-wide 128-vector whose max|x| is
 // amax: s = RN32(amax / 127) (1 for a zero vector), c = clamp(rint(x / s)).
 __device__ __forceinline__ float quantize_int8_row(const float (&x)[4], float amax, float (&c)[4]) {

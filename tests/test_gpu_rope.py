@@ -130,6 +130,68 @@ def test_rotated_queries_and_stored_keys_bit_for_bit(fmt, interleaved, R):
     assert int(err.item()) == 0
 
 
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("interleaved,R,lens", [
+    (False, 128, (300, 1, 50)),      # runs of whole blocks that are not aligned with the call's rows, and their ends
+    (True, 64, (16, 17, 15, 240)), (False, 96, (512,)),
+])
+def test_prompts_bit_for_bit(fmt, interleaved, R, lens):
+    """Enough rows for the 16-row windows: whole blocks, their ragged ends, chunks that begin inside a block, rows out
+    of order, and rows that are flagged in between."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import RopeTable
+    rng = np.random.default_rng(13)
+    Hq, H, B = 11, 3, len(lens)
+    n = sum(lens)
+    seq = np.repeat(np.arange(B), lens)
+    start = np.array([0, 32, 5, 16][:B]) if FORMATS[fmt]["k_bits"] != 2 else np.zeros(B, int)
+    slot = np.concatenate([s + np.arange(l) for s, l in zip(start, lens)])
+    pos = slot + np.repeat([1000, 7, 4000, 20][:B], lens)
+    order = np.arange(n)
+    if fmt in ("int8", "asym_k4v8"):   # the last rows shuffled: no runs there
+        order[-40:] = rng.permutation(order[-40:])
+    seq, slot, pos = seq[order], slot[order], pos[order]
+    bad = np.zeros(n, bool)
+    if fmt in ("int8", "bf16", "int4_factor"):
+        bad[[20, n - 7]] = True
+        pos[bad] = 9000                # no such row in the table
+    blocks = 34
+    perm = rng.permutation(blocks * B).reshape(B, blocks)
+    table = _i(perm)
+    qkv = f32_to_bf16_bits(rng.standard_normal((n, (Hq + 2 * H) * 128)).astype(np.float32))
+    rope = RopeTable(8192, rotary_dim=R, interleaved=interleaved)
+    x = _t(qkv)
+    q, k, v = x[:, :Hq * 128], x[:, Hq * 128:(Hq + H) * 128], x[:, (Hq + H) * 128:]
+    q_out = torch.full((n, Hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    state = rng.bit_generator.state
+    c = _cache(fmt, H, blocks * B, rng)
+    _lib.kvq_rope_append(c.desc, rope.desc, q, Hq, q_out, k, v, _i(pos), _i(seq), _i(slot), _lib.APPEND_QUANT, table,
+                         B, blocks, err_word=err)
+    assert int(err.item()) == (_lib.KVQ_DEVERR_POSITION if bad.any() else 0)
+    ok = ~bad
+    cs = rope.table.cpu().numpy().astype(np.float64)[np.where(bad, 0, pos)]
+    heads = qkv.reshape(n, -1, 128)
+    got = q_out.view(torch.int16).cpu().numpy().view(np.uint16)
+    np.testing.assert_array_equal(got[ok], rotate(heads[:, :Hq], cs, interleaved)[ok])
+    assert torch.all(q_out[torch.from_numpy(bad)] == 7)
+    rng.bit_generator.state = state
+    ref = _cache(fmt, H, blocks * B, rng)
+    # one row at a time would do as well: kvq_append of the rotated rows that are good
+    _lib.kvq_append(ref.desc, _t(rotate(heads[:, Hq:Hq + H], cs, interleaved)[ok]), _t(heads[:, Hq + H:][ok]),
+                    _i(seq[ok]), _i(slot[ok]), _lib.APPEND_QUANT, table, B, blocks)
+    _same(c, ref)
+    # and read back, many slots and few
+    where = _i(perm[seq, slot // 16] * 16 + slot % 16)
+    many = [torch.empty(n, H, 128, device="cuda") for _ in range(2)]
+    _lib.kvq_dequant(c.desc, where, *many)
+    for a in range(0, n, 100):
+        few = [torch.empty(min(100, n - a), H, 128, device="cuda") for _ in range(2)]
+        _lib.kvq_dequant(c.desc, where[a:a + 100].contiguous(), *few)
+        for m, f in zip(many, few):
+            assert torch.equal(m[a:a + 100], f)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "int4_factor", "asym_k4v8"])
 def test_steps_through_the_window(fmt):
     """Token by token through the bf16 window (KVQ_APPEND_STEP), every step with its own positions."""
