@@ -18,21 +18,15 @@ __device__ __forceinline__ void quantize_warp(const float (&x)[4], int bits, int
   // non-negative floats order as their bits: one warp reduction
   const float a = __uint_as_float(__reduce_max_sync(
       kFull, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
-  const int qmax = bits == 8 ? 127 : 7;
-  const int lo = bits == 8 ? -127 : -8;
   if (a == 0.0f) {
     s = 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) code[j] = 0;
     return;
   }
-  s = __fdiv_rn(a, float(qmax));
-  const float r = __frcp_rn(s);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    int c = int(round_quotient_by(x[j], s, r));
-    code[j] = min(qmax, max(lo, c));
-  }
+  // |x / s| <= qmax (1 + 2^-23): the nearest integer is within +-qmax by itself
+  s = __fdiv_rn(a, bits == 8 ? 127.f : 7.f);
+  round_quotients(x, s, __frcp_rn(s), code);
 }
 
 // Warp-cooperative asymmetric quantization: m = min(x), s = RN32((max - min) /
@@ -56,6 +50,18 @@ __device__ __forceinline__ void quantize_asym_warp(const float (&x)[4], int bits
     const double r = rint(__ddiv_rn(__dsub_rn(double(x[j]), double(lo)), double(s)));
     u[j] = r >= double(qmaxu) ? qmaxu : (r > 0.0 ? int(r) : 0);  // clamp before the conversion
   }
+}
+
+// The asymmetric quantizer out of line (its divisions in double are long code).
+struct AsymCodes {
+  int u[4];
+  float s, m;
+};
+static __device__ __noinline__ AsymCodes quantize_asym_far(float4 v, int bits) {
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  AsymCodes r;
+  quantize_asym_warp(x, bits, r.u, r.s, r.m);
+  return r;
 }
 
 // Store the codes of one quantized vector (token `tok`) into its block.  The

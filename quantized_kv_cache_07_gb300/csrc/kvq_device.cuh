@@ -88,13 +88,28 @@ __device__ __forceinline__ float round_quotient(float x, float s) {
   return rintf(q);
 }
 
-// round_quotient by the reciprocal r = RN(1 / s): x * r is within 2^-22 of the
-// quotient relatively, so for |x / s| < 400 its nearest integer is the quotient's
-// unless it lies within 10^-4 of a half-integer; there the exact rule decides.
-// Same results in a third of the instructions.
-__device__ __forceinline__ float round_quotient_by(float x, float s, float r) {
-  const float t = x * r, c = rintf(t);
-  return fabsf(t - c) < 0.4999f ? c : round_quotient(x, s);
+// Out of line for callers whose common path is short: code that is not in the
+// instruction cache costs more than the call.
+static __device__ __noinline__ float round_quotient_far(float x, float s) { return round_quotient(x, s); }
+
+// round_quotient of four values by the reciprocal r = RN(1 / s): x * r is within
+// 2^-22 of the quotient relatively, so for |x / s| < 400 its nearest integer is the
+// quotient's unless it lies within 10^-4 of a half-integer; there the exact rule
+// decides.  The nearest integer comes from adding and subtracting 1.5 * 2^23.
+// Same results in a quarter of the instructions.
+__device__ __forceinline__ void round_quotients(const float (&x)[4], float s, float r, int (&c)[4]) {
+  constexpr float kRound = 12582912.f;
+  float far = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float t = __fmul_rn(x[j], r), m = __fadd_rn(t, kRound);
+    c[j] = __float_as_int(m) - __float_as_int(kRound);
+    far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(m, kRound))));
+  }
+  if (!(far < 0.4999f && fabsf(r) < 3e38f)) {  // or a reciprocal beyond float32
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = int(round_quotient_far(x[j], s));
+  }
 }
 
 // Symmetric int8 codes of four values of a warp-wide 128-vector whose max|x| is

@@ -8,13 +8,11 @@
 // fills from angles in double: at position 10^5 a float32 angle would already
 // be off by 4e-3.
 //
-// Rounding.  The two products and their sum are carried with their rounding
-// errors, so y is the exact value rounded once to float32 (up to one case in
-// about 2^24) and then to bf16.  That makes the stored codes those of kvq_append on the
-// rotated vectors bit for bit: a plain float32 sum differs from the exact one
-// in its last bit often enough to move a bf16 rounding, with it a vector's
-// largest value, and with that a whole vector's codes.  It costs 14 instead of 3
-// instructions per value, which the loads hide.
+// Rounding.  y is the exact value rounded to float32 (up to one case in about 2^24) and then to bf16.
+// That makes the stored codes those of kvq_append on the rotated vectors bit for bit: a plain
+// float32 sum differs from the exact one in its last bit often enough to move a bf16 rounding, with it
+// a vector's largest value, and with that a whole vector's codes.  The sum with all its rounding errors is 14
+// instructions a value; a float32 sum with a bound on its error is 7 and decides all but one value in 10^4.
 //
 // One warp turns and writes one 128-element vector; lane l owns dims 4l..4l+3,
 // so a pair's other half is in the same lane (interleaved) or R / 8 lanes away.
@@ -23,45 +21,89 @@
 namespace kvq {
 namespace {
 
-// RN32(a c - b s): both products and the difference with their errors.
-__device__ __forceinline__ float turn(float a, float c, float b, float s) {
+// RN32(a c + b s): both products and the sum with their errors.
+static __device__ __noinline__ float turn_exact(float a, float c, float b, float s) {
   const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
   const float w = __fmul_rn(b, s), we = __fmaf_rn(b, s, -w);
-  const float d = __fsub_rn(p, w);
+  const float d = __fadd_rn(p, w);
   const float v = __fsub_rn(d, p);
-  const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, v)), __fadd_rn(w, v));
-  const float rest = __fadd_rn(e, __fsub_rn(pe, we));
+  const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(d, v)), __fsub_rn(w, v));
+  const float rest = __fadd_rn(e, __fadd_rn(pe, we));
   // an infinite product has no error term, and a zero keeps its sign
   return fabsf(d) <= 3.4028234663852886e38f && rest != 0.f ? __fadd_rn(d, rest) : d;
 }
 
-// One lane's four values turned by the table row cs (R / 2 pairs of cos, sin).
-__device__ __forceinline__ void rotate4(float (&x)[4], const float* cs, int R, bool interleaved, int lane) {
+// What turns a lane's four dims: y_j = x_j c_j + m_j s_j with m_j the other half of the pair (its sine's
+// sign in s_j); dims behind R have c = 1, s = 0.
+struct Turn {
+  float c[4], s[4];
+};
+__device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleaved, int lane) {
   const int d = 4 * lane;
+  Turn t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    t.c[j] = 1.f;
+    t.s[j] = 0.f;
+  }
+  if (d >= R) return t;
   if (interleaved) {
-    if (d < R) {
-      const float4 t = *reinterpret_cast<const float4*>(cs + d);
-      const float a0 = x[0], b0 = x[1], a1 = x[2], b1 = x[3];
-      x[0] = turn(a0, t.x, b0, t.y);
-      x[1] = turn(a0, t.y, b0, -t.x);
-      x[2] = turn(a1, t.z, b1, t.w);
-      x[3] = turn(a1, t.w, b1, -t.z);
-    }
-    return;
+    const float4 v = *reinterpret_cast<const float4*>(cs + d);
+    t.c[0] = t.c[1] = v.x;
+    t.c[2] = t.c[3] = v.z;
+    t.s[0] = -v.y;
+    t.s[1] = v.y;
+    t.s[2] = -v.w;
+    t.s[3] = v.w;
+  } else {
+    const bool low = d < (R >> 1);
+    const float4* p = reinterpret_cast<const float4*>(cs + 2 * (low ? d : d - (R >> 1)));
+    const float4 a = p[0], b = p[1];
+    const float f = low ? -1.f : 1.f;
+    t.c[0] = a.x;
+    t.c[1] = a.z;
+    t.c[2] = b.x;
+    t.c[3] = b.z;
+    t.s[0] = f * a.y;
+    t.s[1] = f * a.w;
+    t.s[2] = f * b.y;
+    t.s[3] = f * b.w;
   }
-  const int half = R >> 1;
-  const bool low = d < half;
-  const int mate = d < R ? (low ? lane + (R >> 3) : lane - (R >> 3)) : lane;
-  float y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = __shfl_sync(kFull, x[j], mate);
-  if (d < R) {
-    const float4* t = reinterpret_cast<const float4*>(cs + 2 * (low ? d : d - half));
-    const float4 t0 = t[0], t1 = t[1];
-    const float c[4] = {t0.x, t0.z, t1.x, t1.z}, s[4] = {t0.y, t0.w, t1.y, t1.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = low ? turn(x[j], c[j], y[j], s[j]) : turn(y[j], s[j], x[j], -c[j]);
+  return t;
+}
+
+// One lane's four bf16 values turned and rounded to bf16.  A product, a fused product and sum, and a bound
+// on their error (2^-22 of the terms, twice what it can be): where both ends of it round to the same bf16
+// value that is the exact one's; otherwise (a value in 10^4) the exact sum decides.
+__device__ __forceinline__ uint2 rotate4(uint2 raw, const Turn& t, int R, bool interleaved, int lane) {
+  float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
+                __uint_as_float(raw.y & 0xFFFF0000u)};
+  uint2 other;
+  if (interleaved) {
+    other = make_uint2(__byte_perm(raw.x, 0, 0x1032), __byte_perm(raw.y, 0, 0x1032));
+  } else {
+    const int d = 4 * lane, step = R >> 3;
+    const int mate = d < R ? (d < (R >> 1) ? lane + step : lane - step) : lane;
+    other = make_uint2(__shfl_sync(kFull, raw.x, mate), __shfl_sync(kFull, raw.y, mate));
   }
+  const float m[4] = {__uint_as_float(other.x << 16), __uint_as_float(other.x & 0xFFFF0000u),
+                      __uint_as_float(other.y << 16), __uint_as_float(other.y & 0xFFFF0000u)};
+  float hi[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float w = __fmul_rn(m[j], t.s[j]);
+    const float y = __fmaf_rn(x[j], t.c[j], w);
+    const float e = __fmul_rn(__fadd_rn(fabsf(w), fabsf(y)), 0x1p-22f);
+    hi[j] = __fadd_rn(y, e);
+    lo[j] = __fsub_rn(y, e);
+  }
+  uint2 y = make_uint2(pack_bf162(hi[0], hi[1]), pack_bf162(hi[2], hi[3]));
+  if (y.x != pack_bf162(lo[0], lo[1]) || y.y != pack_bf162(lo[2], lo[3])) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hi[j] = turn_exact(x[j], t.c[j], m[j], t.s[j]);
+    y = make_uint2(pack_bf162(hi[0], hi[1]), pack_bf162(hi[2], hi[3]));
+  }
+  return 4 * lane < R ? y : raw;
 }
 
 __device__ __forceinline__ void unpack4(uint2 v, float (&x)[4]) {
@@ -76,8 +118,6 @@ __device__ __forceinline__ int rope_row(const RopeArgs& a, int r) {
   const int p = a.rope_pos[r];
   return p >= 0 && p < a.max_pos ? p : -1;
 }
-
-__device__ __forceinline__ bool rope_row_ok(const RopeArgs& a, int r) { return rope_row(a, r) >= 0; }
 
 __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -94,11 +134,9 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
   }
   const float* cs = a.table + size_t(rp) * a.R;
   if (i < a.Hq) {
-    float x[4];
-    unpack4(*reinterpret_cast<const uint2*>(a.q + r * a.q_stride + i * kHeadDim + 4 * lane), x);
-    rotate4(x, cs, a.R, a.interleaved, lane);
-    const uint2 y = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
-    *reinterpret_cast<uint2*>(a.q_out + (size_t(r) * a.Hq + i) * kHeadDim + 4 * lane) = y;
+    const uint2 x = *reinterpret_cast<const uint2*>(a.q + r * a.q_stride + i * kHeadDim + 4 * lane);
+    *reinterpret_cast<uint2*>(a.q_out + (size_t(r) * a.Hq + i) * kHeadDim + 4 * lane) =
+        rotate4(x, load_turn(cs, a.R, a.interleaved, lane), a.R, a.interleaved, lane);
     return;
   }
   const bool is_key = i < a.Hq + H;
@@ -111,12 +149,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
     if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
     return;
   }
-  if (is_key) {
-    float x[4];
-    unpack4(v, x);
-    rotate4(x, cs, a.R, a.interleaved, lane);
-    v = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
-  }
+  if (is_key) v = rotate4(v, load_turn(cs, a.R, a.interleaved, lane), a.R, a.interleaved, lane);
   const uint16_t xb[4] = {uint16_t(v.x & 0xFFFF), uint16_t(v.x >> 16), uint16_t(v.y & 0xFFFF), uint16_t(v.y >> 16)};
   append_vector(a.ap, is_key, b, p, h, xb, lane);
 }
@@ -136,13 +169,13 @@ __global__ void __launch_bounds__(kGroupWarps * 32) rope_append_group_kernel(con
   append_group(
       a.ap, r, is_key, h, img[wslot], lane, [&](int row) { return rope_row(a, row) >= 0; },
       [&](int row, float(&x)[4]) {
-        unpack4(*reinterpret_cast<const uint2*>(
-                    (is_key ? a.ap.k_new + row * a.k_stride : a.ap.v_new + row * a.v_stride) + h * kHeadDim + 4 * lane),
-                x);
-        if (!is_key) return;
-        rotate4(x, a.table + size_t(rope_row(a, row)) * a.R, a.R, a.interleaved, lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = __bfloat162float(__float2bfloat16_rn(x[j]));
+        uint2 v = *reinterpret_cast<const uint2*>(
+            (is_key ? a.ap.k_new + row * a.k_stride : a.ap.v_new + row * a.v_stride) + h * kHeadDim + 4 * lane);
+        if (is_key) {
+          const Turn t = load_turn(a.table + size_t(rope_row(a, row)) * a.R, a.R, a.interleaved, lane);
+          v = rotate4(v, t, a.R, a.interleaved, lane);
+        }
+        unpack4(v, x);
       });
 }
 
@@ -160,68 +193,66 @@ constexpr int kRows = 16;
 struct RopeSmem {
   alignas(16) float cs[2 * kRows][kHeadDim];      // table rows of the window and of the run
   alignas(16) uint8_t img[8][kBlock * kHeadDim * 2];  // one block image per warp
-  int rp[2 * kRows];                 // rope positions (-1: none) of rows r0 .. r0 + 15, then of the run's
-  int seq[3 * kRows], pos[3 * kRows];  // rows r0 - 15 .. r0 + 31 (seq -1: no such row)
-  int lead;                          // first row of the run in this window, or -1
+  int rp[2 * kRows];  // rope positions (-1: none) of rows r0 .. r0 + 15, then of the run's
+  int seq[3 * kRows], pos[3 * kRows], rope[3 * kRows];  // rows r0 - 15 .. r0 + 32 (seq, rope -1: no such row)
+  int lead;           // first row of the run in this window, or -1
+  unsigned single;    // rows of the window that are written one by one
 };
 
-// Codes of 16 tokens (lane l: dims 4l..4l+3; u: stored byte, nibble or bf16 bits of token i) into the
-// image of a key or value block.
+// Codes of tokens 2t, 2t + 8, 2t + 1, 2t + 9 (lane l: dims 4l..4l+3; u: stored byte, nibble or bf16 bits)
+// into the image of a key or value block.
 template <int BITS, bool KEY>
-__device__ __forceinline__ void put_block(uint8_t* img, const uint32_t (&u)[kBlock][4], int lane) {
+__device__ __forceinline__ void put_tokens(uint8_t* img, int t, const uint32_t (&u)[4][4], int lane) {
   if constexpr (KEY) {
-    const int t = lane >> 3, e = (4 * lane) & 31;
+    const int q = lane >> 3, e = (4 * lane) & 31;
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i) {
-      const int g = i & 7, hi = i >> 3, at = (4 * g + t) * 16;
+    for (int k = 0; k < 4; ++k) {
+      const int g = 2 * t + (k >> 1), hi = k & 1, at = (4 * g + q) * 16;  // token g + 8 hi
       if constexpr (BITS == 8) {
         *reinterpret_cast<uint32_t*>(img + (2 * hi + (e >> 4)) * 512 + at + (e & 15)) =
-            u[i][0] | u[i][1] << 8 | u[i][2] << 16 | u[i][3] << 24;
+            u[k][0] | u[k][1] << 8 | u[k][2] << 16 | u[k][3] << 24;
       } else if constexpr (BITS == 4) {
-        // dims 4l..4l+3 are nibbles 2q, 2q + 4, 2q + 1, 2q + 5 (q = lane & 1) of a word shared with lane ^ 1
-        const uint32_t part = (u[i][0] | u[i][1] << 16 | u[i][2] << 4 | u[i][3] << 20) << (8 * (lane & 1));
+        // dims 4l..4l+3 are nibbles 2p, 2p + 4, 2p + 1, 2p + 5 (p = lane & 1) of a word shared with lane ^ 1
+        const uint32_t part = (u[k][0] | u[k][1] << 16 | u[k][2] << 4 | u[k][3] << 20) << (8 * (lane & 1));
         const uint32_t word = part | __shfl_xor_sync(kFull, part, 1);
         if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(img + hi * 512 + at + (e >> 3) * 4) = word;
       } else {
         *reinterpret_cast<uint2*>(img + (4 * hi + (e >> 3)) * 512 + at + 2 * (e & 7)) =
-            make_uint2(u[i][0] | u[i][1] << 16, u[i][2] | u[i][3] << 16);
+            make_uint2(u[k][0] | u[k][1] << 16, u[k][2] | u[k][3] << 16);
       }
     }
   } else {
     const int mt = lane >> 2, hi = (lane & 3) >> 1;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {
-      const int g = 4 * (lane & 1) + d;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        // tokens 2t, 2t + 8, 2t + 1, 2t + 9 of this dim
-        const uint32_t a = u[2 * t][d], b = u[2 * t + 8][d], c = u[2 * t + 1][d], e = u[2 * t + 9][d];
-        uint8_t* at = img + (4 * g + t) * 16;
-        if constexpr (BITS == 8) {
-          *reinterpret_cast<uint32_t*>(at + (mt >> 1) * 512 + (2 * (mt & 1) + hi) * 4) = a | b << 8 | c << 16 | e << 24;
-        } else if constexpr (BITS == 4) {
-          // dims d and d + 8 (lane ^ 2) share a word: nibbles 0, 4, 1, 5 and 2, 6, 3, 7
-          const uint32_t part = (a | b << 16 | c << 4 | e << 20) << (8 * hi);
-          const uint32_t word = part | __shfl_xor_sync(kFull, part, 2);
-          if (hi == 0) *reinterpret_cast<uint32_t*>(at + (mt >> 2) * 512 + (mt & 3) * 4) = word;
-        } else {
-          *reinterpret_cast<uint2*>(at + mt * 512 + 8 * hi) = make_uint2(a | b << 16, c | e << 16);
-        }
+      uint8_t* at = img + (4 * (4 * (lane & 1) + d) + t) * 16;
+      if constexpr (BITS == 8) {
+        *reinterpret_cast<uint32_t*>(at + (mt >> 1) * 512 + (2 * (mt & 1) + hi) * 4) =
+            u[0][d] | u[1][d] << 8 | u[2][d] << 16 | u[3][d] << 24;
+      } else if constexpr (BITS == 4) {
+        // dims d and d + 8 (lane ^ 2) share a word: nibbles 0, 4, 1, 5 and 2, 6, 3, 7
+        const uint32_t part = (u[0][d] | u[1][d] << 16 | u[2][d] << 4 | u[3][d] << 20) << (8 * hi);
+        const uint32_t word = part | __shfl_xor_sync(kFull, part, 2);
+        if (hi == 0) *reinterpret_cast<uint32_t*>(at + (mt >> 2) * 512 + (mt & 3) * 4) = word;
+      } else {
+        *reinterpret_cast<uint2*>(at + mt * 512 + 8 * hi) =
+            make_uint2(u[0][d] | u[1][d] << 16, u[2][d] | u[3][d] << 16);
       }
     }
   }
 }
 
-// One full block of head h: tokens r .. r + 15 of the call.
+// One full block of head h: tokens r .. r + 15 of the call, four at a time in a loop: unrolled over the 16
+// tokens the kernel waited on instruction fetches (6.6 of 12 stalled warps; 209 us for 8192 rows).
 template <int BITS, bool KEY>
 __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int r, int h, uint8_t* img, int lane) {
   const CacheView& c = a.ap.c;
-  uint2 raw[kBlock];
-  const uint16_t* src =
-      (KEY ? a.ap.k_new + (long long)r * a.k_stride : a.ap.v_new + (long long)r * a.v_stride) + h * kHeadDim + 4 * lane;
   const long long stride = KEY ? a.k_stride : a.v_stride;
+  const uint16_t* src = (KEY ? a.ap.k_new : a.ap.v_new) + r * stride + h * kHeadDim + 4 * lane;
+  auto token = [](int t, int k) { return 2 * t + (k >> 1) + 8 * (k & 1); };
+  uint2 next[4];
 #pragma unroll
-  for (int i = 0; i < kBlock; ++i) raw[i] = *reinterpret_cast<const uint2*>(src + i * stride);
+  for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint2*>(src + token(0, k) * stride);
   const int b = sm->seq[r - blockIdx.x * kRows + kRows - 1], p = sm->pos[r - blockIdx.x * kRows + kRows - 1];
   if (p + kBlock > a.ap.mbps * kBlock) {
     if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
@@ -234,54 +265,65 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
   }
   float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
   if (KEY && c.factor) f = *reinterpret_cast<const float4*>(c.factor + h * kHeadDim + 4 * lane);
-  const float ff[4] = {f.x, f.y, f.z, f.w};
-  uint32_t u[kBlock][4];
   float s_of = 1.f, z_of = 0.f;  // lane i < 16: token i's scale and zero point
+#pragma unroll 1
+  for (int t = 0; t < 4; ++t) {
+    uint2 raw[4];
 #pragma unroll
-  for (int i = 0; i < kBlock; ++i) {
-    float x[4];
-    unpack4(raw[i], x);
-    uint2 bits = raw[i];
-    if constexpr (KEY) {
-      rotate4(x, sm->cs[kRows + i], a.R, a.interleaved, lane);
-      bits = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
+    for (int k = 0; k < 4; ++k) {
+      raw[k] = next[k];
+      if (t < 3) next[k] = *reinterpret_cast<const uint2*>(src + token(t + 1, k) * stride);
+    }
+    uint32_t u[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int tok = token(t, k);
+      uint2 bits = raw[k];
+      if constexpr (KEY)
+        bits = rotate4(bits, load_turn(sm->cs[kRows + tok], a.R, a.interleaved, lane), a.R, a.interleaved, lane);
+      float x[4];
       unpack4(bits, x);
-    }
-    if constexpr (BITS == 16) {
-      u[i][0] = bits.x & 0xFFFFu;
-      u[i][1] = bits.x >> 16;
-      u[i][2] = bits.y & 0xFFFFu;
-      u[i][3] = bits.y >> 16;
-    } else {
-      int code[4];
-      float s = 1.f, m = 0.f;
-      constexpr int kBias = BITS == 8 ? 128 : 8, kTop = BITS == 8 ? 127 : 7;
-      if (KEY && c.k_chan) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          code[j] = int(fminf(float(kTop), fmaxf(BITS == 8 ? -127.f : -8.f, round_quotient(x[j], ff[j])))) + kBias;
+      if constexpr (BITS == 16) {
+        u[k][0] = bits.x & 0xFFFFu;
+        u[k][1] = bits.x >> 16;
+        u[k][2] = bits.y & 0xFFFFu;
+        u[k][3] = bits.y >> 16;
       } else {
-        if (KEY && c.factor) {
+        float s = 1.f, m = 0.f;
+        constexpr int kBias = BITS == 8 ? 128 : 8, kTop = BITS == 8 ? 127 : 7;
+        if (KEY && c.k_chan) {
+          const float ff[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = __fdiv_rn(x[j], ff[j]);
-        }
-        if (c.asym) {
-          quantize_asym_warp(x, BITS, code, s, m);
+          for (int j = 0; j < 4; ++j)
+            u[k][j] = int(fminf(float(kTop), fmaxf(BITS == 8 ? -127.f : -8.f, round_quotient_far(x[j], ff[j])))) + kBias;
         } else {
-          quantize_warp(x, BITS, code, s);
+          if (KEY && c.factor) {
+            x[0] = __fdiv_rn(x[0], f.x);
+            x[1] = __fdiv_rn(x[1], f.y);
+            x[2] = __fdiv_rn(x[2], f.z);
+            x[3] = __fdiv_rn(x[3], f.w);
+          }
+          if (c.asym) {
+            const AsymCodes ac = quantize_asym_far(make_float4(x[0], x[1], x[2], x[3]), BITS);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) code[j] += kBias;
+            for (int j = 0; j < 4; ++j) u[k][j] = uint32_t(ac.u[j]);
+            s = ac.s;
+            m = ac.m;
+          } else {
+            int code[4];
+            quantize_warp(x, BITS, code, s);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[k][j] = uint32_t(code[j] + kBias);
+          }
         }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) u[i][j] = uint32_t(code[j]);
-      if (lane == i) {
-        s_of = s;
-        z_of = m;
+        if (lane == tok) {
+          s_of = s;
+          z_of = m;
+        }
       }
     }
+    put_tokens<BITS, KEY>(img, t, u, lane);
   }
-  put_block<BITS, KEY>(img, u, lane);
   __syncwarp();
   constexpr int kBytes = block_bytes(BITS);
   uint8_t* blk = (KEY ? c.k_codes : c.v_codes) + (size_t(h) * c.num_blocks + phys) * kBytes;
@@ -296,8 +338,13 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
   __syncwarp();  // the image is free for the warp's next block
 }
 
+static __device__ __noinline__ void append_single(const AppendArgs& a, bool is_key, int b, int p, int h, uint2 v, int lane) {
+  const uint16_t xb[4] = {uint16_t(v.x & 0xFFFF), uint16_t(v.x >> 16), uint16_t(v.y & 0xFFFF), uint16_t(v.y >> 16)};
+  append_vector(a, is_key, b, p, h, xb, lane);
+}
+
 template <int KB, int VB>
-__global__ void __launch_bounds__(256, 2) rope_rows_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
   extern __shared__ __align__(16) uint8_t raw_smem[];
   RopeSmem* sm = reinterpret_cast<RopeSmem*>(raw_smem);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -307,30 +354,40 @@ __global__ void __launch_bounds__(256, 2) rope_rows_kernel(const RopeArgs a) {
   // ---- the rows around the window, and the run in it
   if (tid < 3 * kRows) {
     const int r = r0 - (kRows - 1) + tid;
-    const bool in = a.write && r >= 0 && r < n;
-    sm->seq[tid] = in ? a.ap.seq_idx[r] : -1;
-    sm->pos[tid] = in ? a.ap.pos[r] : -1;
-  } else if (tid >= 64 && tid < 64 + kRows) {
-    const int r = r0 + tid - 64;
-    sm->rp[tid - 64] = r < n ? rope_row(a, r) : -1;
+    const bool in = r >= 0 && r < n;
+    sm->seq[tid] = in && a.write ? a.ap.seq_idx[r] : -1;
+    sm->pos[tid] = in && a.write ? a.ap.pos[r] : -1;
+    sm->rope[tid] = in ? rope_row(a, r) : -1;
   }
-  if (tid == 0) sm->lead = -1;
   __syncthreads();
   if (warp == 0) {
     // row r0 + lane (lane < 16) leads a run if 16 rows from it are one sequence's positions p, p + 1, .. with
     // p a multiple of 16, all of them with a rope position; at most one row of a window does
-    bool lead = lane < kRows && r0 + lane < n;
+    bool lead = lane < kRows;
     const int s = lane < kRows ? lane + kRows - 1 : 0, b = sm->seq[s], p = sm->pos[s];
     lead = lead && b >= 0 && b < a.ap.batch && p >= 0 && p % kBlock == 0;
-    for (int i = 1; i < kBlock && lead; ++i) lead = sm->seq[s + i] == b && sm->pos[s + i] == p + i;
-    if (lead) {
-      for (int i = 0; i < kBlock && lead; ++i) lead = rope_row(a, r0 + lane + i) >= 0;
-      if (lead) sm->lead = r0 + lane;
+    for (int i = 0; i < kBlock && lead; ++i)
+      lead = sm->seq[s + i] == b && sm->pos[s + i] == p + i && sm->rope[s + i] >= 0;
+    const unsigned found = __ballot_sync(kFull, lead);
+    if (lane == 0) sm->lead = found ? r0 + __ffs(found) - 1 : -1;
+    // rows in no run of this window's or the one before: those are written one by one
+    bool single = a.write && lane < kRows && sm->rope[s] >= 0;
+    if (single && b >= 0 && b < a.ap.batch && p >= 0) {
+      const int first = s - p % kBlock;
+      bool run = first >= 0;
+      for (int i = 0; i < kBlock && run; ++i)
+        run = sm->seq[first + i] == b && sm->pos[first + i] == p - p % kBlock + i && sm->rope[first + i] >= 0;
+      single = !run;
     }
+    const unsigned singles = __ballot_sync(kFull, single);
+    if (lane == 0) sm->single = singles;
   }
   __syncthreads();
   const int lead = sm->lead;
-  if (tid < kRows) sm->rp[kRows + tid] = lead >= 0 ? rope_row(a, lead + tid) : -1;
+  if (tid < kRows) {
+    sm->rp[tid] = sm->rope[tid + kRows - 1];
+    sm->rp[kRows + tid] = lead >= 0 ? sm->rope[lead - r0 + kRows - 1 + tid] : -1;
+  }
   __syncthreads();
   for (int i = tid; i < 2 * kRows * R4; i += 256) {
     const int row = i / R4, at = i % R4;
@@ -342,7 +399,7 @@ __global__ void __launch_bounds__(256, 2) rope_rows_kernel(const RopeArgs a) {
   __syncthreads();
 
   // ---- tasks: the run's blocks, the single rows' vectors, the queries 8 at a time
-  const int blocks = lead >= 0 ? 2 * H : 0, singles = a.write ? 2 * H : 0;
+  const int blocks = lead >= 0 ? 2 * H : 0, singles = sm->single ? 2 * H : 0;
   const int q8 = (a.Hq + 7) / 8, queries = kRows * q8;
   const int step = 8 * gridDim.y;
   for (int task = blockIdx.y * 8 + warp; task < blocks + singles + queries; task += step) {
@@ -354,52 +411,39 @@ __global__ void __launch_bounds__(256, 2) rope_rows_kernel(const RopeArgs a) {
     if (task < blocks + singles) {
       const bool is_key = task - blocks < H;
       const int h = is_key ? task - blocks : task - blocks - H;
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i, s = i + kRows - 1;
-        if (r >= n || sm->rp[i] < 0) continue;
+      for (unsigned left = sm->single; left; left &= left - 1) {
+        const int i = __ffs(left) - 1, r = r0 + i, s = i + kRows - 1;
         const int b = sm->seq[s], p = sm->pos[s];
         if (b < 0 || b >= a.ap.batch || p < 0) {
           if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
           continue;
         }
-        // part of a full run, led by row r - p % 16 of this window or the one before?  Its rows are in view.
-        const int j = p % kBlock;
-        bool run = s - j >= 0;
-        if (run) {
-          const int at = min(lane, kBlock - 1), k = s - j + at;
-          run = __all_sync(kFull, sm->seq[k] == b && sm->pos[k] == p - j + at && rope_row_ok(a, r - j + at));
-        }
-        if (run) continue;
         uint2 v = *reinterpret_cast<const uint2*>(
             (is_key ? a.ap.k_new + (long long)r * a.k_stride : a.ap.v_new + (long long)r * a.v_stride) + h * kHeadDim +
             4 * lane);
-        if (is_key) {
-          float x[4];
-          unpack4(v, x);
-          rotate4(x, sm->cs[i], a.R, a.interleaved, lane);
-          v = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
-        }
-        const uint16_t xb[4] = {uint16_t(v.x & 0xFFFF), uint16_t(v.x >> 16), uint16_t(v.y & 0xFFFF),
-                                uint16_t(v.y >> 16)};
-        append_vector(a.ap, is_key, b, p, h, xb, lane);
+        if (is_key) v = rotate4(v, load_turn(sm->cs[i], a.R, a.interleaved, lane), a.R, a.interleaved, lane);
+        append_single(a.ap, is_key, b, p, h, v, lane);
       }
       continue;
     }
-    const int t = task - blocks - singles, i = t / q8, h0 = (t % q8) * 8, r = r0 + i;
+    const int qt = task - blocks - singles, i = qt / q8, h0 = (qt % q8) * 8, r = r0 + i;
     if (r >= n || sm->rp[i] < 0) continue;
     const uint16_t* src = a.q + (long long)r * a.q_stride + h0 * kHeadDim + 4 * lane;
     uint2 raw[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (h0 + k < a.Hq) raw[k] = *reinterpret_cast<const uint2*>(src + k * kHeadDim);
+      raw[k] = h0 + k < a.Hq ? *reinterpret_cast<const uint2*>(src + k * kHeadDim) : make_uint2(0u, 0u);
     uint16_t* dst = a.q_out + ((size_t)r * a.Hq + h0) * kHeadDim + 4 * lane;
+    const Turn t = load_turn(sm->cs[i], a.R, a.interleaved, lane);
+#pragma unroll 1
+    for (int k = 0; k < 8; k += 2) {  // a short loop; the registers rotate, so that every index is known
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (h0 + k >= a.Hq) break;
-      float x[4];
-      unpack4(raw[k], x);
-      rotate4(x, sm->cs[i], a.R, a.interleaved, lane);
-      *reinterpret_cast<uint2*>(dst + k * kHeadDim) = make_uint2(pack_bf162(x[0], x[1]), pack_bf162(x[2], x[3]));
+      for (int e = 0; e < 2; ++e) {
+        const uint2 y = rotate4(raw[e], t, a.R, a.interleaved, lane);
+        if (h0 + k + e < a.Hq) *reinterpret_cast<uint2*>(dst + (k + e) * kHeadDim) = y;
+      }
+#pragma unroll
+      for (int e = 0; e < 6; ++e) raw[e] = raw[e + 2];
     }
   }
 }
