@@ -457,7 +457,7 @@ cudaError_t launch_rows(const RopeArgs& a, int sms, cudaStream_t s) {
   const int windows = (a.ap.n + kRows - 1) / kRows;
   const int tasks = (a.write ? 4 * a.ap.c.H : 0) + kRows * ((a.Hq + 7) / 8);
   // few windows: their tasks over several CTAs, up to two tasks a warp
-  int y = (4 * sms + windows - 1) / windows;
+  int y = (8 * sms + windows - 1) / windows;
   y = y > (tasks + 15) / 16 ? (tasks + 15) / 16 : y;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(windows), unsigned(y < 1 ? 1 : y));

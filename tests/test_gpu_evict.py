@@ -265,6 +265,34 @@ def test_eviction_of_one_row(L, keep):
         np.testing.assert_array_equal(got[K:], ref[K:])
 
 
+@pytest.mark.parametrize("L,keep,order", [(32768, 20000, "spread"), (32769, 20000, "spread"), (60000, 30000, "rising"),
+                                          (60000, 30000, "equal"), (40000, 8000, "steps")])
+def test_sums_and_positions_follow_in_place(L, keep, order):
+    """Rows about and beyond what stays on the chip, more moves than one walk matches, many equal sums."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache
+    rng = np.random.default_rng(L + keep)
+    nb = (L + 15) // 16
+    c = KVCache(nb, 2, 4, 4)
+    x = dict(spread=rng.random((2, L)), rising=np.arange(2 * L).reshape(2, L), equal=np.ones((2, L)),
+             steps=rng.integers(0, 4, (2, L)))[order].astype(np.float32)
+    pos = np.sort(rng.permutation(2 * L)[:L]).astype(np.int32)
+    i = lambda v: torch.as_tensor(v, dtype=torch.int32).cuda()
+    mass = torch.from_numpy(x).cuda()[None].contiguous()
+    tp = i(np.stack([pos, pos]))[None].contiguous()
+    new = torch.zeros(1, dtype=torch.int32, device="cuda")
+    src = torch.zeros(1, 2, L, dtype=torch.int32, device="cuda")
+    _lib.kvq_evict(c.desc, mass, mass, i([L]), i([keep]), torch.arange(nb).int().cuda()[None], 1, nb, src, new,
+                   token_pos=tp, token_pos_out=tp, next_pos=i([2 * L]))
+    for h in range(2):
+        s, _ = choose(x[h], L, keep, 0, 0, 0, pos, 2 * L)
+        assert int(new) == len(s)
+        np.testing.assert_array_equal(src[0, h, :len(s)].cpu().numpy(), s)
+        np.testing.assert_array_equal(mass[0, h, :len(s)].cpu().numpy(), x[h][s])
+        np.testing.assert_array_equal(tp[0, h, :len(s)].cpu().numpy(), pos[s])
+        np.testing.assert_array_equal(mass[0, h, len(s):].cpu().numpy(), x[h][len(s):])
+
+
 def test_eviction_flags_bad_lengths_and_blocks():
     inp = make_inputs(small_workload("evict_bad", batch=3, len_range=(100, 200)))
     w = inp.workload
