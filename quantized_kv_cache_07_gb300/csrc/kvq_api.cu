@@ -13,7 +13,6 @@ namespace {
 
 using kvq::kHeadDim;
 
-constexpr int kMaxBatch = 4096;  // sequence geometry is staged in shared memory
 constexpr int kMaxWindow = 128;  // window ring: at most 8 bf16 blocks per (sequence, kv head)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -105,7 +104,7 @@ int auto_stream_ctas(const kvq_cache_desc* c, int batch, bool rows = false) {
 
 kvq_status check_decode_shape(const kvq_cache_desc* c, int batch, int q_heads) {
   if (batch < 0 || q_heads < 1) return KVQ_ERR_INVALID_ARG;
-  if (batch > kMaxBatch) return KVQ_ERR_UNSUPPORTED;
+  if (batch > kvq::kMaxBatch) return KVQ_ERR_UNSUPPORTED;
   if (q_heads % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
   if (q_heads / c->num_kv_heads > kvq::kMaxGroup) return KVQ_ERR_UNSUPPORTED;
   if (c->window > 0 && c->window_batch < batch) return KVQ_ERR_INVALID_ARG;

@@ -73,6 +73,8 @@ struct MassArgs {
   uint32_t* err;
 };
 
+constexpr int kMaxBatch = 4096;  // sequence geometry is staged in shared memory
+
 struct EvictArgs {
   CacheView c;
   const float* mass;  // [B][H][stride], as all per-token rows

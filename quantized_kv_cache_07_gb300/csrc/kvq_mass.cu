@@ -29,11 +29,15 @@ constexpr int kMassThreads = kMassWarps * 32;
 template <int KB>
 struct MassFmt {
   static constexpr bool kBf16 = KB == 16, kGroup = KB == 2;
+  // Blocks of a step, copied and worked on together: the two blocks' chains of loads, products, exponentials
+  // and shuffles overlap, and the sums of 32 tokens end up one in each lane.
+  static constexpr int kNB = kBf16 ? 1 : 2;
   static constexpr int kRaw = block_bytes(KB);  // key codes of one block
   static constexpr int kChunks = kRaw / 512;
-  static constexpr int kOffKs = kRaw, kOffKo = kRaw + 64, kOffMass = kRaw + 128;
-  static constexpr int kStageBytes = kRaw + 192;  // scales, zero points, mass: 16 floats each
-  static constexpr int kStages = KB == 16 ? 2 : (KB == 8 ? 4 : 6);
+  static constexpr int kSide = 192;             // scales, zero points, mass: 16 floats each
+  static constexpr int kOffSide = kNB * kRaw, kOffKo = 64, kOffMass = 128;
+  static constexpr int kStageBytes = kOffSide + kNB * kSide;
+  static constexpr int kStages = KB == 16 ? 2 : (KB == 8 ? 3 : 4);
   static constexpr int kRingBytes = kStages * kStageBytes * kMassWarps;
 };
 
@@ -208,12 +212,32 @@ __device__ __forceinline__ int mass_len(const MassArgs& a, int b, bool& bad) {
   return L;
 }
 
+// Where a warp's copying or computing side is: step j of n, of unit (b, h).
+struct MassPlace {
+  int b, h, j, n;
+  // to the next step of a range that ends after `left` more; whether the unit changed
+  __device__ __forceinline__ bool advance(const int* pre, int H, bool more) {
+    if (++j < n) return false;
+    j = 0;
+    if (++h == H) {
+      h = 0;
+      if (more) {
+        do { ++b; } while (pre[b + 1] == pre[b]);
+        n = pre[b + 1] - pre[b];
+      }
+    }
+    return true;
+  }
+};
+
 // RING: the blocks are those of the bf16 window (KB = 16).
 template <int KB, bool ASYM, bool LOQ, bool RING>
 __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
   using F = MassFmt<KB>;
+  constexpr int NB = F::kNB;
   extern __shared__ __align__(128) uint8_t smem[];
-  int* pre = reinterpret_cast<int*>(smem + F::kRingBytes);  // [B + 1] blocks of one head before sequence b
+  int* pre = reinterpret_cast<int*>(smem + F::kRingBytes);  // [B + 1] steps of one head before sequence b
+  int* lens = pre + a.B + 1;                                // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int B = a.B, H = a.c.H, W = a.c.window;
@@ -223,7 +247,8 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
   for (int b = tid; b < B; b += kMassThreads) {
     const int L = mass_len(a, b, bad);
     const int n = RING ? min(L, W) : max(L - W, 0);
-    pre[b + 1] = (n + kBlock - 1) / kBlock;
+    lens[b] = L;
+    pre[b + 1] = (n + kBlock * NB - 1) / (kBlock * NB);
   }
   if (bad && blockIdx.x == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
   if (tid == 0) pre[0] = 0;
@@ -245,10 +270,11 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
   __syncthreads();
   const long long T = (long long)H * pre[B];
   const long long NW = (long long)gridDim.x * kMassWarps, w = (long long)blockIdx.x * kMassWarps + warp;
-  const long long x0 = w * T / NW, x1 = (w + 1) * T / NW;
-  if (x0 >= x1) return;
+  const long long x0 = w * T / NW;
+  const int steps = int((w + 1) * T / NW - x0);
+  if (steps <= 0) return;
 
-  // unit of block x0: the largest b with H * pre[b] <= x0 that has blocks
+  // unit of step x0: the largest b with H * pre[b] <= x0 that has blocks
   int lo = 0, hi = B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -256,146 +282,156 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
     else hi = mid - 1;
   }
   while (pre[lo + 1] == pre[lo]) ++lo;
+  const int first_n = pre[lo + 1] - pre[lo];
+  const int first_x = int(x0 - (long long)H * pre[lo]);
+  MassPlace in{lo, first_x / first_n, first_x % first_n, first_n}, at = in;
 
-  // ---- the copying side: block x_in of unit (b_in, h_in), its table entries 32 at a time
-  int b_in = lo, nb_in = pre[lo + 1] - pre[lo];
-  int h_in = int((x0 - (long long)H * pre[lo]) / nb_in), j_in = int((x0 - (long long)H * pre[lo]) % nb_in);
-  long long x_in = x0;
-  int ids = 0, ids_b = -1, ids_base = 0;
-  int s_in = 0;
+  // ---- the copying side
   uint8_t* const ring = smem + warp * (F::kStages * F::kStageBytes);
-  int state[F::kStages];  // physical block of each stage (-1: skipped), kept by every lane
-  auto fetch = [&](int& phys) {
-    if (x_in < x1) {
-      if constexpr (RING) {
-        phys = j_in;
-      } else {
-        if (ids_b != b_in || j_in < ids_base || j_in >= ids_base + 32) {
-          ids_b = b_in;
-          ids_base = j_in;
-          ids = 0;
-          if (j_in + lane < nb_in) {
-            ids = a.table[size_t(b_in) * a.mbps + j_in + lane];
-            if (ids < 0 || ids >= a.c.num_blocks) {
-              flag(a.err, KVQ_DEVERR_BLOCK_ID);
-              ids = -1;
-            }
-          }
+  const uint8_t* codes = nullptr;  // this lane's first piece of block 0 of the head, of its window
+  const float* side = nullptr;     // this lane's piece of the head's block 0 record, or of the unit's mass
+  const int* table = nullptr;
+  int blocks = 0;
+  // lanes 12 i + r: pieces of block i's scales and zero points (r < 8) and mass
+  const int side_i = lane >= 12, side_r = lane - 12 * side_i;
+  const bool side_mass = side_r >= 8;
+  const bool side_on = !RING && lane < 12 * NB &&
+                       (side_mass || (!F::kBf16 && !a.c.k_chan && side_r < (F::kGroup ? 1 : (ASYM ? 8 : 4))));
+  const int side_step = side_mass ? kBlock : a.c.meta_floats;
+  int ids = -1, ids_next = -1, ids_base = 0;  // 32 table entries, and the 32 behind them on their way
+  auto entry = [&](int i) { return i + lane < blocks ? table[i + lane] : -1; };
+  auto check = [&](int i) {
+    if (i + lane < blocks && (ids < 0 || ids >= a.c.num_blocks)) {
+      flag(a.err, KVQ_DEVERR_BLOCK_ID);
+      ids = -1;
+    }
+  };
+  auto enter = [&]() {
+    const size_t unit = size_t(in.b) * H + in.h;
+    if constexpr (RING) {
+      codes = a.c.k_win + unit * (W / kBlock) * F::kRaw + lane * 16;
+    } else {
+      const size_t hb = size_t(in.h) * a.c.num_blocks;
+      codes = a.c.k_codes + hb * F::kRaw + lane * 16;
+      side = side_mass ? a.mass + unit * a.stride + (side_r - 8) * 4 : a.c.meta + hb * a.c.meta_floats + side_r * 4;
+      table = a.table + size_t(in.b) * a.mbps;
+      blocks = (lens[in.b] - W + kBlock - 1) / kBlock;
+      ids_base = in.j * NB;
+      ids = entry(ids_base);
+      ids_next = entry(ids_base + 32);
+      check(ids_base);
+    }
+  };
+  enter();
+  uint32_t valid = 0u;  // blocks of the ring's stages that are to be read (a bad table entry is not)
+  int s_in = 0, left = steps;
+  auto fetch = [&]() {
+    if (left > 0) {
+      uint8_t* st = ring + s_in * F::kStageBytes;
+      const int j = in.j * NB;
+      if constexpr (!RING) {
+        if (j - ids_base == 32) {
+          ids_base = j;
+          ids = ids_next;
+          ids_next = entry(j + 32);
+          check(j);
         }
-        phys = __shfl_sync(kFull, ids, j_in - ids_base);
       }
-      if (phys >= 0) {
-        uint8_t* st = ring + s_in * F::kStageBytes;
-        const size_t hb = RING ? (size_t(b_in) * H + h_in) * (W / kBlock) + j_in : size_t(h_in) * a.c.num_blocks + phys;
-        const uint8_t* src = (RING ? a.c.k_win : a.c.k_codes) + hb * F::kRaw + lane * 16;
+      uint32_t ok = 0u;
 #pragma unroll
-        for (int i = 0; i < F::kChunks; ++i) cp_async16(st + lane * 16 + i * 512, src + i * 512);
-        if (!F::kBf16) {
-          const float* rec = a.c.meta + hb * a.c.meta_floats;
-          if (F::kGroup) {
-            if (lane == 0) cp_async16(st + F::kOffKs, rec);
-          } else if (!a.c.k_chan) {
-            if (lane < (ASYM ? 8 : 4)) cp_async16(st + F::kOffKs + lane * 16, rec + lane * 4);
-          }
-        }
-        // ring tokens' slots are not in order of their positions; a row may end inside its last block
-        if (!RING && lane >= 8 && lane < 12 && j_in * kBlock + (lane - 8) * 4 < a.stride)
-          cp_async16(st + F::kOffMass + (lane - 8) * 16,
-                     a.mass + (size_t(b_in) * H + h_in) * a.stride + size_t(j_in) * kBlock + (lane - 8) * 4);
-      }
-      ++x_in;
-      if (++j_in == nb_in) {
-        j_in = 0;
-        if (++h_in == H) {
-          h_in = 0;
-          if (x_in < x1) {
-            do { ++b_in; } while (pre[b_in + 1] == pre[b_in]);
-            nb_in = pre[b_in + 1] - pre[b_in];
-          }
+      for (int i = 0; i < NB; ++i) {
+        const int phys = RING ? j : __shfl_sync(kFull, ids, j - ids_base + i);
+        if (phys >= 0) {
+          ok |= 1u << i;
+          const uint8_t* src = codes + size_t(phys) * F::kRaw;
+#pragma unroll
+          for (int c = 0; c < F::kChunks; ++c) cp_async16(st + i * F::kRaw + lane * 16 + c * 512, src + c * 512);
         }
       }
+      valid = (valid & ~(((1u << NB) - 1u) << (s_in * NB))) | (ok << (s_in * NB));
+      if constexpr (!RING) {
+        const int phys = __shfl_sync(kFull, ids, j - ids_base + (NB > 1 ? side_i : 0));
+        const int blk = side_mass ? j + side_i : phys;
+        // the row may end inside its last block
+        if (side_on && phys >= 0 && (!side_mass || blk * kBlock + (side_r - 8) * 4 < a.stride))
+          cp_async16(st + F::kOffSide + side_i * F::kSide + side_r * 16, side + (long long)blk * side_step);
+      }
+      --left;
+      if (in.advance(pre, H, left > 0) && left > 0) enter();
       if (++s_in == F::kStages) s_in = 0;
     }
     cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < F::kStages; ++i) state[i] = -1;
-#pragma unroll
-  for (int i = 0; i < F::kStages - 1; ++i) fetch(state[i]);
+#pragma unroll 1
+  for (int i = 0; i < F::kStages - 1; ++i) fetch();
 
   // ---- the computing side
   const uint32_t km = magic_f16x2(B);
-  int b = lo, nb = pre[lo + 1] - pre[lo];
-  int h = int((x0 - (long long)H * pre[lo]) / nb), j = int((x0 - (long long)H * pre[lo]) % nb);
-  bool ignored = false;
-  int L = mass_len(a, b, ignored);
   MassQuery<KB, ASYM, LOQ> mq;
-  mq.load(a, b, h, lane);
-  long long x = x0;
-  while (x < x1) {
+  mq.load(a, at.b, at.h, lane);
+  float* row = a.mass + (size_t(at.b) * H + at.h) * a.stride;
+  int L = lens[at.b], s = 0;
+  // not unrolled over the stages: the code of one step has to stay in the instruction cache
+#pragma unroll 1
+  for (int x = steps; x > 0; --x) {
+    fetch();  // the step after the ring's others goes into the stage freed last
+    cp_async_wait<F::kStages - 1>();
+    __syncwarp();
+    const uint8_t* st = ring + s * F::kStageBytes;
+    float wt[NB][2];
 #pragma unroll
-    for (int s = 0; s < F::kStages; ++s) {
-      if (x >= x1) break;
-      // the block after the ring's others goes into the stage freed last
-      fetch(state[(s + F::kStages - 1) % F::kStages]);
-      cp_async_wait<F::kStages - 1>();
-      __syncwarp();
-      if (state[s] >= 0) {
-        const uint8_t* st = ring + s * F::kStageBytes;
-        float acc[4];
-        mass_scores<KB, LOQ>(st, mq.qf, mq.ql, acc, lane, km);
-        const float* ks = reinterpret_cast<const float*>(st + F::kOffKs);
-        float sk[2] = {1.f, 1.f}, mk[2] = {0.f, 0.f};
-        if (!F::kBf16 && !a.c.k_chan) {
-          sk[0] = ks[F::kGroup ? 0 : g];
-          sk[1] = ks[F::kGroup ? 0 : g + 8];
-          if (ASYM) {
-            constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f);
-            const float* ko = F::kGroup ? ks + 1 : reinterpret_cast<const float*>(st + F::kOffKo);
-            mk[0] = fmaf(kKC, sk[0], ko[F::kGroup ? 0 : g]);
-            mk[1] = fmaf(kKC, sk[1], ko[F::kGroup ? 0 : g + 8]);
-          }
-        }
-        float wt[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // token g, g + 8
-          wt[i] = 0.f;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {  // query 2t, 2t + 1
-            const float v = ASYM ? fmaf(acc[2 * i + c], sk[i], mk[i] * mq.qz[c]) : acc[2 * i + c] * sk[i];
-            wt[i] += ex2(fmaf(v, mq.qs[c], -mq.ls[c]));
-          }
-          wt[i] += __shfl_xor_sync(kFull, wt[i], 1);
-          wt[i] += __shfl_xor_sync(kFull, wt[i], 2);
-        }
-        if (t < 2) {  // lane t writes token g + 8t
-          const int tok = g + 8 * t;
-          const float add = t ? wt[1] : wt[0];
-          const size_t row = (size_t(b) * H + h) * a.stride;
-          if constexpr (RING) {
-            const int first = L - min(L, W), slot = j * kBlock + tok;
-            const int p = first + ((slot - first) % W + W) % W;
-            if (p < L) a.mass[row + p] = fmaf(a.decay, a.mass[row + p], add);
-          } else {
-            const int p = j * kBlock + tok;
-            if (p < L - W) a.mass[row + p] = fmaf(a.decay, reinterpret_cast<const float*>(st + F::kOffMass)[tok], add);
-          }
+    for (int n = 0; n < NB; ++n) {
+      float acc[4];
+      mass_scores<KB, LOQ>(st + n * F::kRaw, mq.qf, mq.ql, acc, lane, km);
+      const float* ks = reinterpret_cast<const float*>(st + F::kOffSide + n * F::kSide);
+      float sk[2] = {1.f, 1.f}, mk[2] = {0.f, 0.f};
+      if (!F::kBf16 && !a.c.k_chan) {
+        sk[0] = ks[F::kGroup ? 0 : g];
+        sk[1] = ks[F::kGroup ? 0 : g + 8];
+        if (ASYM) {
+          constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f);
+          const float* ko = F::kGroup ? ks + 1 : ks + F::kOffKo / 4;
+          mk[0] = fmaf(kKC, sk[0], ko[F::kGroup ? 0 : g]);
+          mk[1] = fmaf(kKC, sk[1], ko[F::kGroup ? 0 : g + 8]);
         }
       }
-      __syncwarp();  // every lane has read the stage before it is filled again
-      ++x;
-      if (++j == nb) {
-        j = 0;
-        if (++h == H) {
-          h = 0;
-          if (x < x1) {
-            do { ++b; } while (pre[b + 1] == pre[b]);
-            nb = pre[b + 1] - pre[b];
-            L = mass_len(a, b, ignored);
-          }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // token g, g + 8
+        wt[n][i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // query 2t, 2t + 1
+          const float v = ASYM ? fmaf(acc[2 * i + c], sk[i], mk[i] * mq.qz[c]) : acc[2 * i + c] * sk[i];
+          wt[n][i] += ex2(fmaf(v, mq.qs[c], -mq.ls[c]));
         }
-        if (x < x1) mq.load(a, b, h, lane);
       }
+    }
+    // sums over the four lanes of a token: lane t ends with token g + 8 (t & 1) of block t >> 1
+    float add[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+      add[n] = ((t & 1) ? wt[n][1] : wt[n][0]) + __shfl_xor_sync(kFull, (t & 1) ? wt[n][0] : wt[n][1], 1);
+    float sum;
+    if constexpr (NB == 2) {
+      sum = ((t & 2) ? add[1] : add[0]) + __shfl_xor_sync(kFull, (t & 2) ? add[0] : add[1], 2);
+    } else {
+      sum = add[0] + __shfl_xor_sync(kFull, add[0], 2);
+    }
+    const int n = NB == 2 ? t >> 1 : 0, tok = g + 8 * (t & 1), slot = (at.j * NB + n) * kBlock + tok;
+    if ((valid >> (s * NB + n) & 1u) && (NB == 2 || t < 2)) {
+      if constexpr (RING) {  // ring tokens' slots are not in order of their positions
+        const int first = L - min(L, W), p = first + ((slot - first) % W + W) % W;
+        if (p < L) row[p] = fmaf(a.decay, row[p], sum);
+      } else {
+        const float old = reinterpret_cast<const float*>(st + F::kOffSide + n * F::kSide + F::kOffMass)[tok];
+        if (slot < L - W) row[slot] = fmaf(a.decay, old, sum);
+      }
+    }
+    __syncwarp();  // every lane has read the stage before it is filled again
+    if (++s == F::kStages) s = 0;
+    if (at.advance(pre, H, x > 1) && x > 1) {
+      L = lens[at.b];
+      row = a.mass + (size_t(at.b) * H + at.h) * a.stride;
+      mq.load(a, at.b, at.h, lane);
     }
   }
 }
@@ -403,7 +439,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
 template <int KB, bool ASYM, bool LOQ, bool RING>
 cudaError_t launch_one(const MassArgs& a, cudaStream_t s) {
   using F = MassFmt<KB>;
-  const int smem = F::kRingBytes + ((a.B + 1) * 4 + 15) / 16 * 16;
+  const int smem = F::kRingBytes + (2 * a.B + 1) * 4;
   static std::mutex mu;
   static std::map<std::pair<int, int>, int> grids;  // CTAs of one wave, by device and shared memory
   int dev = 0;
@@ -417,7 +453,7 @@ cudaError_t launch_one(const MassArgs& a, cudaStream_t s) {
       int sms = 0, per = 0;
       if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
       e = cudaFuncSetAttribute(mass_kernel<KB, ASYM, LOQ, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               F::kRingBytes + 16400);
+                               F::kRingBytes + (2 * kMaxBatch + 1) * 4);
       if (e != cudaSuccess) return e;
       e = cudaFuncSetAttribute(mass_kernel<KB, ASYM, LOQ, RING>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                cudaSharedmemCarveoutMaxShared);
