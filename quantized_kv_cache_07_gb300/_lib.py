@@ -149,18 +149,27 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_raw_stream = None
+_torch = _current_device = _raw_stream = None
 
 
-def _stream(stream) -> int | None:
-    global _raw_stream
-    if stream is None:
+def _need_torch():
+    """torch, imported by the first call that needs it."""
+    global _torch, _current_device, _raw_stream
+    if _torch is None:
         import torch
-        if _raw_stream is None:
-            # the raw handle without a Stream object per call, where this torch has it
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-                lambda device: torch.cuda.current_stream(device).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        _current_device = torch.cuda.current_device
+        # the raw handle without a Stream object per call, where this torch has it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _torch = torch
+    return _torch
+
+
+def _stream(stream, device: int | None = None) -> int | None:
+    if stream is None:
+        if _torch is None:
+            _need_torch()
+        return _raw_stream(_current_device() if device is None else device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -187,9 +196,12 @@ class _Args:
     __slots__ = ("where", "device", "bf16", "f32", "i32", "u8")
 
     def __init__(self, where: str):
-        import torch
-        self.where, self.device = where, torch.cuda.current_device()
+        torch = _torch or _need_torch()
+        self.where, self.device = where, _current_device()
         self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+    def stream(self, stream):
+        return _stream(stream, self.device)
 
     def __call__(self, t, dtype, shape=None):
         if t is None or isinstance(t, int):
@@ -234,7 +246,7 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
                                   arg(q_out, arg.bf16), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
                                   arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
                                   arg(block_table, arg.i32), batch, max_blocks_per_seq, _ptr(err_word),
-                                  _stream(stream) if n else None), arg.where)
+                                  arg.stream(stream) if n else None), arg.where)
 
 
 def kvq_decode_shared_workspace_size(desc: CacheDesc, batch: int, q_heads: int, num_groups: int) -> int:
@@ -257,7 +269,7 @@ def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, bl
                                     arg(prefix_blocks, arg.i32, (num_groups,)),
                                     arg(out, arg.f32 if out_fp32 else arg.bf16, rows), int(bool(out_fp32)),
                                     arg(lse, arg.f32, (batch, q_heads)), arg(workspace, arg.u8), workspace_bytes,
-                                    _ptr(err_word), _stream(stream)), arg.where)
+                                    _ptr(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,
@@ -270,7 +282,7 @@ def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, b
                                 arg(lse, arg.f32, (batch, q_heads)), arg(seq_lens, arg.i32, (batch,)),
                                 arg(block_table, arg.i32, (batch, max_blocks_per_seq)), max_blocks_per_seq,
                                 arg(mass, arg.f32, (batch, desc.num_kv_heads, mass_stride)), mass_stride, decay,
-                                _ptr(err_word), _stream(stream)), arg.where)
+                                _ptr(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batch: int, max_blocks_per_seq: int,
@@ -286,7 +298,7 @@ def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batc
                             arg(token_pos, arg.i32, rows), arg(token_pos_out, arg.i32, rows),
                             arg(next_pos, arg.i32, each), arg(block_table, arg.i32, (batch, max_blocks_per_seq)), batch,
                             max_blocks_per_seq, arg(new_lens, arg.i32, each), arg(source, arg.i32, rows),
-                            _ptr(err_word), _stream(stream)), arg.where)
+                            _ptr(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,
