@@ -461,6 +461,7 @@ kvq_status kvq_dequant(const kvq_cache_desc* cache, const int32_t* slots, int32_
   a.n = n;
   a.k_out = k_out;
   a.v_out = v_out;
+  a.wide = aligned16(k_out) && aligned16(v_out);
   if (kvq::launch_dequant(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
   return KVQ_OK;
 }

@@ -80,15 +80,11 @@ __global__ void __launch_bounds__(kGroupWarps * 32) append_group_kernel(AppendAr
       });
 }
 
-__device__ __forceinline__ void dequant_one(const DequantArgs& a, int r, int slot, bool is_key, int h, int lane) {
-  const int H = a.c.H;
+// Dims 4 lane..4 lane + 3 of one slot's key or value; zeros where there is no such slot.
+__device__ __forceinline__ float4 dequant_load(const DequantArgs& a, int slot, bool is_key, int h, int lane) {
   const int phys = slot / kBlock, tok = slot % kBlock;
-  float* out = (is_key ? a.k_out : a.v_out) + (size_t(r) * H + h) * kHeadDim + 4 * lane;
-  if (slot < 0 || phys >= a.c.num_blocks) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = 0.0f;
-    return;
-  }
+  if (slot < 0 || phys >= a.c.num_blocks) return make_float4(0.f, 0.f, 0.f, 0.f);
+  float o[4];
   const int bits = is_key ? a.c.k_bits : a.c.v_bits;
   const uint8_t* blk = (is_key ? a.c.k_codes : a.c.v_codes) + (size_t(h) * a.c.num_blocks + phys) * block_bytes(bits);
   float s = 1.0f, m = 0.0f;
@@ -117,22 +113,40 @@ __device__ __forceinline__ void dequant_one(const DequantArgs& a, int r, int slo
       const float sd = chan ? a.c.factor[h * kHeadDim + d] : s;
       v = asym ? __fmaf_rn(float(raw), s, m) : __fmul_rn(float(raw - bias), sd);
     }
-    out[j] = v;
+    o[j] = v;
+  }
+  return make_float4(o[0], o[1], o[2], o[3]);
+}
+
+__device__ __forceinline__ void dequant_store(const DequantArgs& a, int r, bool is_key, int h, int lane, float4 v) {
+  float* out = (is_key ? a.k_out : a.v_out) + (size_t(r) * a.c.H + h) * kHeadDim + 4 * lane;
+  if (a.wide) {
+    *reinterpret_cast<float4*>(out) = v;
+  } else {
+    out[0] = v.x;
+    out[1] = v.y;
+    out[2] = v.z;
+    out[3] = v.w;
   }
 }
 
-__global__ void __launch_bounds__(256) dequant_kernel(DequantArgs a) {
+__global__ void __launch_bounds__(256) dequant_kernel(const DequantArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const long long vec = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int H = a.c.H;
   if (vec >= (long long)a.n * 2 * H) return;
   const int r = int(vec / (2 * H));
-  dequant_one(a, r, a.slots[r], ((vec / H) % 2) == 0, int(vec % H), lane);
+  const bool is_key = ((vec / H) % 2) == 0;
+  const int h = int(vec % H);
+  dequant_store(a, r, is_key, h, lane, dequant_load(a, a.slots[r], is_key, h, lane));
 }
 
-// Many slots: 16 of the call per warp and (head, K or V).  Where they are one block's 16 tokens in
-// order, the block is read as it lies, 16 bytes a lane, into shared memory and taken apart there; a value
-// token on its own is 128 single bytes of its block.  Other slots go one by one.  Same values.
+// Many slots: 16 of the call per warp and (head, K or V).  A run of 16 slots that are one block's 16
+// tokens in order is taken by the warp of the 16 that it starts in: the block is read as it lies, 16 bytes a
+// lane, into shared memory and taken apart there; a value token on its own is 128 single bytes of
+// its block.  Other slots go one by one, four in flight (one after another, 1337 slots of 8 sequences, int4,
+// took 17 us, now 12).  Same values.
 constexpr int kDqWarps = 8;
 
 template <int BITS, bool KEY>
@@ -159,7 +173,6 @@ __device__ __forceinline__ void dequant_block(const DequantArgs& a, int r0, int 
   float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
   if (chan) f = *reinterpret_cast<const float4*>(c.factor + h * kHeadDim + 4 * lane);
   __syncwarp();
-  float* out = (KEY ? a.k_out : a.v_out) + (size_t(r0) * c.H + h) * kHeadDim + 4 * lane;
   const int bias = c.asym ? 0 : (BITS == 8 ? 128 : 8);
 #pragma unroll
   for (int i = 0; i < kBlock; ++i) {
@@ -172,14 +185,15 @@ __device__ __forceinline__ void dequant_block(const DequantArgs& a, int r0, int 
       if constexpr (BITS == 16) v[j] = bf16_bits_to_f32(uint16_t(raw));
       else v[j] = c.asym ? __fmaf_rn(float(raw), s, z) : __fmul_rn(float(raw - bias), chan ? ff[j] : s);
     }
-    *reinterpret_cast<float4*>(out + size_t(i) * c.H * kHeadDim) = make_float4(v[0], v[1], v[2], v[3]);
+    dequant_store(a, r0 + i, KEY, h, lane, make_float4(v[0], v[1], v[2], v[3]));
   }
   __syncwarp();
 }
 
 template <int KB, int VB>
-__global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(DequantArgs a) {
+__global__ void __launch_bounds__(kDqWarps * 32, 4) dequant_rows_kernel(const DequantArgs a) {
   __shared__ __align__(16) uint8_t img[kDqWarps][kBlock * kHeadDim * 2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int H = a.c.H;
   const long long task = (long long)blockIdx.x * kDqWarps + warp;
@@ -188,31 +202,57 @@ __global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(DequantArgs
   const int r0 = int(task / (2 * H)) * kBlock, kv = int(task % (2 * H));
   const bool is_key = kv < H;
   const int h = is_key ? kv : kv - H;
-  const int slot = lane < kBlock && r0 + lane < a.n ? a.slots[r0 + lane] : -1;
-  const int first = __shfl_sync(kFull, slot, 0);
-  if (first >= 0 && first % kBlock == 0 && first / kBlock < a.c.num_blocks &&
-      __all_sync(kFull, lane >= kBlock || slot == first + lane)) {
-    if (is_key) dequant_block<KB, true>(a, r0, first / kBlock, h, img[warp], lane);
-    else dequant_block<VB, false>(a, r0, first / kBlock, h, img[warp], lane);
-    return;
+  // rows r0 - 16 .. r0 + 15 and r0 + 16 .. r0 + 31, one a lane; bit i: row r0 - 16 + i
+  auto slot_at = [&](long long r) { return r >= 0 && r < a.n ? a.slots[r] : -1; };
+  const int lo = slot_at((long long)r0 - kBlock + lane), hi = lane < kBlock ? slot_at((long long)r0 + kBlock + lane) : -1;
+  const int after_lo = __shfl_down_sync(kFull, lo, 1), first_hi = __shfl_sync(kFull, hi, 0);
+  const int after_hi = __shfl_down_sync(kFull, hi, 1);
+  auto mask64 = [](bool l, bool h) {
+    const unsigned long long low = __ballot_sync(kFull, l);
+    return low | (unsigned long long)(__ballot_sync(kFull, h)) << 32;
+  };
+  const unsigned long long starts =
+      mask64(lo >= 0 && lo % kBlock == 0 && lo / kBlock < a.c.num_blocks, false);
+  unsigned long long next = mask64(lo >= 0 && (lane < 31 ? after_lo : first_hi) == lo + 1,
+                                   hi >= 0 && lane < kBlock - 1 && after_hi == hi + 1);  // the row behind is the next slot
+  next &= next >> 1;
+  next &= next >> 2;
+  next &= next >> 4;
+  const unsigned runs = unsigned(starts & next & next >> 7);  // 15 such rows in a row
+  const unsigned before = runs & 0xFFFFu, lead = runs >> kBlock;  // at most one of each
+  unsigned rest = a.n - r0 >= kBlock ? 0xFFFFu : (1u << (a.n - r0)) - 1u;  // rows of the 16 that no run covers
+  if (before) rest &= ~0u << (__ffs(before) - 1);
+  if (lead) {
+    const int l = __ffs(lead) - 1, first = __shfl_sync(kFull, lo, kBlock + l);
+    rest &= (1u << l) - 1u;
+    if (is_key) dequant_block<KB, true>(a, r0 + l, first / kBlock, h, img[warp], lane);
+    else dequant_block<VB, false>(a, r0 + l, first / kBlock, h, img[warp], lane);
   }
-  for (int i = 0; i < kBlock && r0 + i < a.n; ++i)
-    dequant_one(a, r0 + i, __shfl_sync(kFull, slot, i), is_key, h, lane);
+#pragma unroll 1
+  while (rest) {
+    int row[4];
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      row[i] = rest ? __ffs(rest) - 1 : -1;
+      rest &= rest - 1;
+      if (row[i] >= 0) v[i] = dequant_load(a, __shfl_sync(kFull, lo, kBlock + row[i]), is_key, h, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (row[i] >= 0) dequant_store(a, r0 + row[i], is_key, h, lane, v[i]);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
-  const long long vecs = (long long)a.n * 2 * a.c.H;
-  if (vecs == 0) return cudaSuccess;
-  const bool group = a.c.k_bits == 2 && a.mode == KVQ_APPEND_QUANT;
-  const int warps = group ? kGroupWarps : 8;
-  const long long grid = (vecs + warps - 1) / warps;
-  // launched with programmatic stream serialisation, so the launch overlaps the
-  // tail of the previous kernel (the kernel waits for it before reading memory)
+// Launched with programmatic stream serialisation, so the launch overlaps the tail of the
+// previous kernel (the kernels wait for it before reading memory).
+template <class Kernel, class Args>
+static cudaError_t launch_pdl(Kernel kernel, const Args& a, long long grid, int threads, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(warps * 32);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -220,9 +260,18 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = group ? cudaLaunchKernelEx(&cfg, append_group_kernel, a) : cudaLaunchKernelEx(&cfg, append_kernel, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+  const long long vecs = (long long)a.n * 2 * a.c.H;
+  if (vecs == 0) return cudaSuccess;
+  const bool group = a.c.k_bits == 2 && a.mode == KVQ_APPEND_QUANT;
+  const int warps = group ? kGroupWarps : 8;
+  const long long grid = (vecs + warps - 1) / warps;
+  return group ? launch_pdl(append_group_kernel, a, grid, warps * 32, s) : launch_pdl(append_kernel, a, grid, warps * 32, s);
 }
 
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s) {
@@ -231,19 +280,15 @@ cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s) {
   // 16 slots a warp from 256 slots on (fewer are one wave of single-vector warps)
   if (a.n >= 256 && a.c.k_bits != 2) {
     const long long tasks = (long long)((a.n + kBlock - 1) / kBlock) * 2 * a.c.H;
-    const unsigned grid = unsigned((tasks + kDqWarps - 1) / kDqWarps);
-    const int kb = a.c.k_bits, vb = a.c.v_bits;
-    if (kb == 8 && vb == 8) dequant_rows_kernel<8, 8><<<grid, kDqWarps * 32, 0, s>>>(a);
-    else if (kb == 4 && vb == 4) dequant_rows_kernel<4, 4><<<grid, kDqWarps * 32, 0, s>>>(a);
-    else if (kb == 4) dequant_rows_kernel<4, 8><<<grid, kDqWarps * 32, 0, s>>>(a);
-    else if (kb == 8) dequant_rows_kernel<8, 4><<<grid, kDqWarps * 32, 0, s>>>(a);
-    else dequant_rows_kernel<16, 16><<<grid, kDqWarps * 32, 0, s>>>(a);
-    return cudaGetLastError();
+    const long long grid = (tasks + kDqWarps - 1) / kDqWarps;
+    const int kb = a.c.k_bits, vb = a.c.v_bits, threads = kDqWarps * 32;
+    if (kb == 8 && vb == 8) return launch_pdl(dequant_rows_kernel<8, 8>, a, grid, threads, s);
+    if (kb == 4 && vb == 4) return launch_pdl(dequant_rows_kernel<4, 4>, a, grid, threads, s);
+    if (kb == 4) return launch_pdl(dequant_rows_kernel<4, 8>, a, grid, threads, s);
+    if (kb == 8) return launch_pdl(dequant_rows_kernel<8, 4>, a, grid, threads, s);
+    return launch_pdl(dequant_rows_kernel<16, 16>, a, grid, threads, s);
   }
-  const int warps = 8;
-  const long long grid = (vecs + warps - 1) / warps;
-  dequant_kernel<<<unsigned(grid), warps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(dequant_kernel, a, (vecs + 7) / 8, 256, s);
 }
 
 }  // namespace kvq

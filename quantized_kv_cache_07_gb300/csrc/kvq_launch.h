@@ -98,6 +98,7 @@ struct DequantArgs {
   int n;
   float* k_out;
   float* v_out;
+  bool wide;  // outputs aligned to 16 bytes
 };
 
 // Workspace layout of a decode call (byte offsets from the workspace base).

@@ -307,3 +307,40 @@ def test_captured_and_replayed_on_a_side_stream():
         torch.cuda.synchronize()
         want = rotate(bits, rope.table.cpu().numpy().astype(np.float64)[p], False)
         np.testing.assert_array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), want)
+
+
+@pytest.mark.parametrize("k_bits,v_bits,asym,kchan", [(8, 8, False, False), (4, 4, True, False), (4, 8, False, False),
+                                                      (8, 4, False, True), (16, 16, False, False)])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_read_back_of_many_slots(k_bits, v_bits, asym, kchan, shift):
+    """Whole blocks at any row of the call, parts of blocks, repeated, missing and foreign slots, in one call and a few
+    at a time; outputs that are not aligned to 16 bytes."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache
+    rng = np.random.default_rng(k_bits + v_bits)
+    H, nb = 2, 40
+    factor = rng.random((H, 128)) + 0.5 if kchan else None
+    c = KVCache(nb, H, k_bits, v_bits, asym=asym, channel_factor=factor, k_per_channel=kchan)
+    for pool in (c.k_codes, c.v_codes):
+        raw = rng.standard_normal(pool.numel() // 2).astype(np.float32) if k_bits == 16 else None
+        if raw is None:
+            pool.copy_(torch.from_numpy(rng.integers(1, 256, pool.numel()).astype(np.uint8)))
+        else:
+            pool.copy_(torch.from_numpy(raw).bfloat16().view(torch.uint8))
+    if c.meta is not None:
+        c.meta.copy_(torch.from_numpy(rng.random(c.meta.numel()).astype(np.float32)))
+    block = lambda b: np.arange(16 * b, 16 * b + 16)
+    parts = [block(3), block(5)[2:], block(7), [-1, 16 * nb, 16 * nb + 16], block(7), block(8), block(9)[:15], block(11),
+             [3], block(12), block(13)[::-1], block(39), block(2)[1:], block(2)[:1], block(20), [-5], block(21)]
+    slots = np.concatenate([np.asarray(p, np.int32) for p in parts] + [np.asarray(p, np.int32) for p in parts[::-1]])
+    assert slots.size >= 256 and slots.size % 16 != 0
+    n = slots.size
+    s = torch.from_numpy(slots).cuda()
+    whole = [torch.full((n * H * 128 + shift,), 7.0, device="cuda")[shift:] for _ in range(2)]
+    _lib.kvq_dequant(c.desc, s, *whole)
+    few = [torch.zeros(n, H, 128, device="cuda") for _ in range(2)]
+    for r in range(0, n, 100):
+        _lib.kvq_dequant(c.desc, s[r:r + 100], few[0][r:], few[1][r:])
+    for x, y in zip(whole, few):
+        assert torch.equal(x.view(n, H, 128), y)
+        assert not x.view(n, H, 128)[s < 0].any() and x.view(n, H, 128)[s == 48].any()
