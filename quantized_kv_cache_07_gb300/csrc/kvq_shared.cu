@@ -14,6 +14,8 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   __shared__ SharedGeo geo;
   const DecodeArgs& a = sa.d;
   const int tid = threadIdx.x, lane = tid & 31;
+  // the groups are as old as what the prefix kernel reads before its wait
+  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long q = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
@@ -22,7 +24,6 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   // ---- where the records are: prefix ones (np), the suffix's chunks (ns), the window's
   const int2 ch = reinterpret_cast<const int2*>(a.ws + sa.sl.off_chunks)[b];
   const int2 last = reinterpret_cast<const int2*>(a.ws + sa.sl.off_chunks)[a.B - 1];
-  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
   if (!any) return;
   const int H = a.c.H, ns = ch.y;
   const size_t first_s = size_t(ch.x) + size_t(h) * ns;  // suffix record of chunk 0 of this unit

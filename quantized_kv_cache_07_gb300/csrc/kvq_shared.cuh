@@ -5,6 +5,11 @@
 // the group) and one KV head; it has blocks[g] 16-token blocks.  Units are
 // ordered by (group, tile, head); their blocks form one range of T blocks that
 // the CTAs cut evenly, in steps of `step` blocks.
+//
+// Launches: suffix, prefix, merge, each with programmatic serialisation.  The suffix waits for the
+// kernels before it and then lets the prefix kernel start, which runs beside it: their records lie apart,
+// and what it reads was complete when the suffix's wait ended (its own reads of it bypass L1).  It
+// waits for the suffix only before it ends, so that the merge, which waits for it, follows both.
 #pragma once
 
 #include "kvq_decode_impl.cuh"
@@ -26,7 +31,7 @@ __device__ __forceinline__ unsigned load_groups(GroupGeo* geo, const int* start,
                                                 int mbps, int tid, int threads) {
   unsigned bad = 0u;
   for (int i = tid; i < n; i += threads) {
-    const int p = blocks[i];
+    const int p = __ldcg(blocks + i);
     if (p < 0 || p > mbps) bad |= KVQ_DEVERR_SEQ_LEN;
     geo->blocks[i] = min(max(p, 0), mbps);
   }
@@ -34,7 +39,7 @@ __device__ __forceinline__ unsigned load_groups(GroupGeo* geo, const int* start,
     int top = 0;
     for (int base = 0; base <= n; base += 32) {
       const int i = base + tid;
-      const int raw = i <= n ? start[i] : 0;
+      const int raw = i <= n ? __ldcg(start + i) : 0;
       int v = max(i <= n ? min(raw, B) : 0, 0);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -149,10 +154,12 @@ __device__ __forceinline__ SharedUnit unit_at(const SharedGeo* s, int n, int H, 
   return r;
 }
 
+__device__ __forceinline__ void wait_for_suffix() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Tokens of the prefix that sequence b attends to.
 __device__ __forceinline__ int prefix_len(const DecodeArgs& a, int b, int blocks) {
   const int cap = a.mbps * kBlock + a.c.window;
-  const int L = min(max(a.seq_lens[b], 0), cap);
+  const int L = min(max(__ldcg(a.seq_lens + b), 0), cap);
   return min(max(L - a.c.window, 0), blocks * kBlock);
 }
 

@@ -325,14 +325,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
       }
     fence_mbar_init();
   }
+  // Beside the suffix kernel, see kvq_shared.cuh: the wait for it comes last.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   shared_geometry(&sm->geo, a, 2 * kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix kernel
   const SharedGeo* geo = &sm->geo;
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
-  if (ci >= Pe) return;
+  if (ci >= Pe) return wait_for_suffix();
   const long long x0 = (long long)ci * geo->T / Pe, x1 = (long long)(ci + 1) * geo->T / Pe;
-  if (x0 >= x1) return;
+  if (x0 >= x1) return wait_for_suffix();
   if (warp == 12) tmem_alloc(&sm->tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
         const int blk = (g.t0 + i + lane) * kStep + w;
         int id = -1;
         if (i + lane < g.nt && blk < g.nblk) {
-          id = table[blk];
+          id = __ldcg(table + blk);
           if (id < 0 || id >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
             id = 0;
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
 #pragma unroll
           for (int k = 0; k < 16; k += 4)
             *reinterpret_cast<float4*>(f + k) =
-                *reinterpret_cast<const float4*>(a.c.factor + g.un.h * kHeadDim + 16 * sub + k);
+                __ldcg(reinterpret_cast<const float4*>(a.c.factor + g.un.h * kHeadDim + 16 * sub + k));
         }
         uint8_t* half = sm->q[g.both ? j : 0][sub & 1];
         int r = (gv0 + (lane >> 3)) / G, hj = (gv0 + (lane >> 3)) % G;
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
           raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
           if (4 * i < per && r < g.rows) {
             const uint4* p = reinterpret_cast<const uint4*>(src + (size_t(r) * a.Hq + hj) * kHeadDim);
-            raw[i][0] = p[0];
-            raw[i][1] = p[1];
+            raw[i][0] = __ldcg(p);
+            raw[i][1] = __ldcg(p + 1);
           }
           hj += 4;
           while (hj >= G) {
@@ -723,6 +723,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
     }
   }
   if (!ok) flag(a.err, KVQ_DEVERR_TIMEOUT);
+  wait_for_suffix();
   __syncwarp();
   tc_fence_before();
   __syncthreads();

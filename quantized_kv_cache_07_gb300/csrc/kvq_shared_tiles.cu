@@ -56,13 +56,13 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
     }
   };
   if (!F::kBf16 && a.c.k_chan) unit_key_scales(tid, kThreads);
+  // Beside the suffix kernel, see kvq_shared.cuh: the producer waits for it last.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   shared_geometry(geo, a, kTileQ, kStep, tid, kThreads, false);  // errors are reported by the suffix kernel
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
-  if (ci >= Pe) return;
+  if (ci >= Pe) return wait_for_suffix();
   const long long x0 = (long long)ci * geo->T / Pe, x1 = (long long)(ci + 1) * geo->T / Pe;
-  if (x0 >= x1) return;
+  if (x0 >= x1) return wait_for_suffix();
 
   if (warp == kConsumerWarps) {
     // ---------------------------------------------------------------- producer
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
         }
         int phys = 0;
         if (lane < nb) {
-          phys = table[b0 + lane];
+          phys = __ldcg(table + b0 + lane);
           if (phys < 0 || phys >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
             phys = 0;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
     if (lane == 0)
       for (int k = max(0, it - S); k < it; ++k)
         if (!mbar_wait(&full[k % S], (k / S) & 1)) flag(a.err, KVQ_DEVERR_TIMEOUT);
-    return;
+    return wait_for_suffix();
   }
 
   // ------------------------------------------------------------------ consumers

@@ -190,8 +190,9 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
         reinterpret_cast<float*>(ring + (i / (NB * kBlock)) * T::kStage + T::kOffMeta)[(i / kBlock % NB) * F::kMF + F::kKS +
                                                                                       i % kBlock] = 1.f;
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the prefix kernel may start: it reads nothing that is not complete by now
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the first lengths beside the groups: every load that waits for another one costs its latency
   const int len0 = tid < B ? a.seq_lens[tid] : 0;
   const unsigned gbad = load_groups(groups, a.group_start, a.prefix_blocks, a.num_groups, B, a.mbps, tid, kSufThreads);

@@ -438,13 +438,13 @@ __device__ __forceinline__ float stage_tile_vector(const DecodeArgs& a, const ui
                                                    uint32_t* qlo, float* qz_s, float* zo_s, int lane) {
   float x[4] = {0.f, 0.f, 0.f, 0.f};
   if (src) {
-    const uint2 raw = *reinterpret_cast<const uint2*>(src + 4 * lane);
+    const uint2 raw = __ldcg(reinterpret_cast<const uint2*>(src + 4 * lane));
     x[0] = __uint_as_float(raw.x << 16);
     x[1] = __uint_as_float(raw.x & 0xFFFF0000u);
     x[2] = __uint_as_float(raw.y << 16);
     x[3] = __uint_as_float(raw.y & 0xFFFF0000u);
     if (a.c.factor) {
-      const float4 c = *reinterpret_cast<const float4*>(a.c.factor + h * kHeadDim + 4 * lane);
+      const float4 c = __ldcg(reinterpret_cast<const float4*>(a.c.factor + h * kHeadDim + 4 * lane));
       x[0] *= c.x;
       x[1] *= c.y;
       x[2] *= c.z;

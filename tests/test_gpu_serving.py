@@ -33,7 +33,7 @@ def test_serving_steps_with_eviction(k_bits, v_bits, asym):
     rng = np.random.default_rng(k_bits + 10 * v_bits)
     mbps, own = 9, [40, 1, 17, 33]
     stream = torch.cuda.Stream()
-    i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
     with torch.cuda.stream(stream):
         cache = KVCache(PREFIX + B * mbps, H, k_bits, v_bits, asym=asym)
         rope = RopeTable(4096, rotary_dim=64)
