@@ -4,7 +4,14 @@
  * Two operations make up the decode hot path:
  *   kvq_append  quantize-on-write of new key/value vectors into a paged cache
  *   kvq_decode  fused dequantize-on-load split attention for one decode step
- * plus kvq_dequant (reads the stored cache back for tests) and a few helpers.
+ * Beside them:
+ *   kvq_rope_append    kvq_append of keys turned by their rotary positions, and the
+ *                      turned queries, in one call (kvq_rope_table: its cosines and sines)
+ *   kvq_decode_shared  kvq_decode for sequences that share a prefix, read once for all
+ *   kvq_attn_mass      the attention weight each cached token received, summed up
+ *   kvq_evict          keep each sequence's heaviest tokens, in place
+ *   kvq_prefill        causal attention of a chunk of new tokens
+ * plus kvq_dequant (reads the stored cache back) and a few helpers.
  *
  * Sources (page title, section):
  *   [P1] "KV Cache Quantization Perturbs Attention Through Stored Keys and Values"
@@ -545,10 +552,11 @@ kvq_status kvq_attn_mass(const kvq_cache_desc* cache, const void* q, int32_t bat
  *   token_pos_out : positions by new slots; may be token_pos itself, or NULL
  *   next_pos      : device int32 [batch], the position of each sequence's next token; NULL
  *                   (without token_pos only): seq_lens.  token_pos needs token_pos_out too.
- *   new_lens      : device int32 [batch], not seq_lens itself (KVQ_ERR_INVALID_ARG)
+ *   new_lens      : device int32 [batch], not seq_lens, keep or next_pos itself
+ *                   (KVQ_ERR_INVALID_ARG)
  *   source        : device int32 [batch][num_kv_heads][mass_stride]: the slot that each new
- *                   slot's token came from
- *   mass_stride   : entries of a row of mass, token_pos and source
+ *                   slot's token came from; not token_pos or token_pos_out itself
+ *   mass_stride   : entries of a row of mass, token_pos and source, at most 2^30
  * Entries at and behind new_lens[b] are left as they are, in every output and in the cache.
  * Caches with a bf16 window: ring tokens are kept, and the number evicted is rounded down to a
  * multiple of window, so that ring tokens keep their slots.  Their rows' entries move down with

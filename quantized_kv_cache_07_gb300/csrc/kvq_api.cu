@@ -667,7 +667,8 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
   if (protect_first < 0 || protect_recent < 0) return KVQ_ERR_INVALID_ARG;
   if (batch == 0) return KVQ_OK;
   if (!mass || !seq_lens || !keep || !block_table || !new_lens || !source || max_blocks_per_seq < 1 ||
-      mass_stride < 1 || mass_stride > (1 << 30) || new_lens == seq_lens || new_lens == keep)
+      mass_stride < 1 || mass_stride > (1 << 30) || new_lens == seq_lens || new_lens == keep ||
+      new_lens == next_pos || source == token_pos || source == token_pos_out)
     return KVQ_ERR_INVALID_ARG;
   if (token_pos && (!token_pos_out || !next_pos)) return KVQ_ERR_INVALID_ARG;  // positions would be lost, or misread
   kvq::EvictArgs a;

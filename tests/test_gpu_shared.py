@@ -288,3 +288,49 @@ def test_captured_and_replayed_with_other_groups():
         torch.cuda.synchronize()
         ref, _ = run.decode()
         np.testing.assert_allclose(out.cpu().numpy(), ref, rtol=0, atol=2e-3)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(k_bits=4, v_bits=4, channel_factor=True), dict(q_bits=32)])
+def test_groups_without_a_prefix(kw):
+    """Nothing is shared: the prefix kernel has no work, the result is kvq_decode's."""
+    run = DeviceRun(make_inputs(small_workload("shared_none", **dict(dict(batch=16, len_range=(1, 300)), **kw))))
+    out, lse = decode_shared(run, [(0, 16, 0)])
+    ref, ref_lse = run.decode()
+    np.testing.assert_allclose(out, ref, rtol=0, atol=2e-3)
+    np.testing.assert_allclose(lse, ref_lse, rtol=0, atol=2e-3)
+    assert run.err_bits() == 0
+
+
+@pytest.mark.parametrize("batch,kw", [(16, dict()), (16, dict(k_bits=4, v_bits=4, channel_factor=True)), (3, dict())])
+def test_inputs_written_by_the_kernels_just_before(batch, kw):
+    """Queries, lengths, groups and the table change between calls that are queued without a wait."""
+    from quantized_kv_cache_07_gb300.cache import SharedWorkspace
+    w = small_workload("shared_queued", **dict(dict(batch=batch, len_range=(400, 420), paged=True), **kw))
+    inp = shared_inputs(w, [(0, batch, 20)])
+    run = DeviceRun(inp)
+    ws = SharedWorkspace(run.cache, batch, w.q_heads, 2)
+    i = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    g = torch.Generator(device="cuda").manual_seed(5)
+    sets = []
+    for k in range(12):
+        P = (20, 13, 1, 17)[k % 4]
+        # other blocks for the sequences' own tokens: two swapped rows behind the prefix
+        table = run.table.clone()
+        table[:, 20:] = table[:, 20:].roll(k % 3, 0)
+        sets.append((torch.randn(run.q.shape, generator=g, device="cuda").bfloat16(),
+                     torch.randint(330, 400, (batch,), generator=g, device="cuda").int(), table,
+                     i([0, (k * 5) % (batch + 1), batch]), i([P, (P + k) % 21])))
+    q, lens, table, start, blocks = (t.clone() for t in sets[0])
+    outs = [torch.empty(batch, w.q_heads, 128, device="cuda") for _ in sets]
+    torch.cuda.synchronize()
+    for s, out in zip(sets, outs):
+        for dst, src in zip((q, lens, table, start, blocks), s):
+            dst.copy_(src)
+        run.lib.kvq_decode_shared(run.cache.desc, q, batch, w.q_heads, lens, table, inp.max_blocks, 2, start, blocks, out,
+                                  workspace=ws.buf, workspace_bytes=ws.nbytes, err_word=run.err)
+    for s, out in zip(sets, outs):
+        run.q.copy_(s[0])
+        run.table.copy_(s[2])
+        ref, _ = run.decode(lens=s[1])
+        np.testing.assert_allclose(out.cpu().numpy(), ref, rtol=0, atol=2e-3)
+    assert run.err_bits() == 0

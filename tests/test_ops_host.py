@@ -109,6 +109,8 @@ def test_attn_mass_refusals(lib, cache, kw, status):
     # the lengths are read by both launches
     ({}, dict(new_lens=0x6000), 1), ({}, dict(new_lens=0x7000), 1),
     # positions in need positions out and the next position
+    ({}, dict(new_lens=0xB000, next=0xB000), 1), ({}, dict(source=0xA000, pos=0xA000, pos_out=0xB000, next=0xE000), 1),
+    ({}, dict(source=0xB000, pos=0xA000, pos_out=0xB000, next=0xE000), 1), ({}, dict(stride=(1 << 30) + 1), 1),
     ({}, dict(pos=0xA000), 1), ({}, dict(pos=0xA000, pos_out=0xA000), 1), ({}, dict(pos=0xA000, next=0xB000), 1),
     ({}, dict(batch=0, mass=None), 0),
 ])
