@@ -120,18 +120,28 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
 }
 
 // Workspace of kvq_decode_shared: the records of the prefix and of the suffixes.
+// The cache as the kernels of kvq_decode_shared see it: under a key factor the query times the factor
+// needs more than fp16's 11 bits (one part: the log-sum-exp is off by 1.3e-5 of it on 33 sequences of 8k
+// tokens, two: 1e-7), so it goes in two parts.
+kvq::CacheView shared_view(const kvq_cache_desc* c) {
+  kvq::CacheView v = view(c);
+  if (c->k_bits != 16 && c->k_channel_factor && v.q_bits == 16) v.q_bits = 32;
+  return v;
+}
+
 kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::SharedLayout* sl) {
-  const kvq::CacheView v = view(c);
+  const kvq::CacheView v = shared_view(c);
   const int H = c->num_kv_heads, G = q_heads / H;
   // 256-vector units on tcgen05 where the groups fill them, 16-vector tiles
   // otherwise, for bf16 blocks and for the two-part mode.
-  sl->tc = c->k_bits != 16 && v.q_bits != 32 && batch * G >= 32 * num_groups;
+  sl->tc = c->k_bits != 16 && c->q_bits != 32 && batch * G >= 32 * num_groups;
   sl->tile = sl->tc ? 256 : 16;
+  sl->unit = sl->tc && v.q_bits == 32 ? 128 : sl->tile;
   sl->ctas = sl->tc ? kvq::shared_tc_ctas(v) : kvq::shared_tiles_ctas(v);
   sl->suf_ctas = kvq::suffix_ctas(v, batch);
   if (sl->ctas <= 0 || sl->suf_ctas <= 0) return KVQ_ERR_CUDA;
   // every group adds at most one tile that is not full; every unit at most one chunk that is not
-  const long long units = ((long long)batch * G / sl->tile + num_groups) * H;
+  const long long units = ((long long)batch * G / sl->unit + num_groups) * H;
   sl->slots = sl->ctas + int(units);
   sl->suf_slots = 2 * sl->suf_ctas + (c->window > 0 ? 2 : 1) * batch * H;
   size_t o = 0;
@@ -598,7 +608,7 @@ kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t
   if ((st = shared_layout(cache, batch, q_heads, num_groups, &s.sl)) != KVQ_OK) return st;
   if (workspace_bytes < s.sl.total) return KVQ_ERR_WORKSPACE;
   kvq::DecodeArgs& a = s.d;
-  a.c = view(cache);
+  a.c = shared_view(cache);
   a.q = static_cast<const uint16_t*>(q);
   a.B = batch;
   a.Hq = q_heads;

@@ -143,7 +143,7 @@ constexpr int kMaxGroups = 256;
 // The suffixes are split into chunks over `suf_ctas` CTAs, one record each, and one per unit for a
 // bf16 window behind them.
 struct SharedLayout {
-  int ctas, tile, slots;
+  int ctas, tile, unit, slots;  // tile: vectors of a record, unit: of a unit
   bool tc;  // tcgen05 path (tile 256), else mma.sync (tile 16)
   int suf_ctas, suf_slots;
   size_t off_m, off_l, off_rec;     // prefix records: float [slots][tile], twice, and [slots][tile][128]

@@ -15,7 +15,7 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   const DecodeArgs& a = sa.d;
   const int tid = threadIdx.x, lane = tid & 31;
   // the groups are as old as what the prefix kernel reads before its wait
-  shared_geometry(&geo, a, sa.sl.tile, step, tid, kMergeThreads, false);
+  shared_geometry(&geo, a, sa.sl.unit, step, tid, kMergeThreads, false);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long q = (long long)blockIdx.x * (kMergeThreads / 32) + (tid >> 5);
@@ -33,16 +33,16 @@ __global__ void __launch_bounds__(kMergeThreads) shared_merge_kernel(const Share
   const int g = group_of(&geo.g, a.num_groups, b);
   if (g >= 0 && geo.g.blocks[g] > 0) {
     v = (b - geo.g.start[g]) * a.G + hj;
-    const int tile = v / sa.sl.tile, steps = steps_of(geo.g.blocks[g], step);
+    const int tile = v / sa.sl.unit, steps = steps_of(geo.g.blocks[g], step);
     const int i = tile * H + h, u = geo.unit0[g] + i;
     const long long x = geo.x0[g] + (long long)i * steps;
     const int Pe = shared_ctas(&geo, sa.sl.ctas);
     const long long c0 = cta_of(x, geo.T, Pe), c1 = cta_of(x + steps - 1, geo.T, Pe);
     // On tcgen05 a unit of at most 128 vectors has two records per CTA, the second one's rows behind the first's.
-    const int nv = min((geo.g.start[g + 1] - geo.g.start[g]) * a.G - tile * sa.sl.tile, sa.sl.tile);
+    const int nv = min((geo.g.start[g + 1] - geo.g.start[g]) * a.G - tile * sa.sl.unit, sa.sl.unit);
     two = sa.sl.tc && nv <= sa.sl.tile / 2 ? 1 : 0;
     np = int(c1 - c0 + 1) << two;
-    first_p = size_t(c0 + u) * sa.sl.tile + v % sa.sl.tile;
+    first_p = size_t(c0 + u) * sa.sl.tile + v % sa.sl.unit;
   }
   const float* pm = reinterpret_cast<const float*>(a.ws + sa.sl.off_m);
   const float* pl = reinterpret_cast<const float*>(a.ws + sa.sl.off_l);

@@ -207,9 +207,10 @@ __device__ __forceinline__ void put_values(const Raw<VB>& raw, uint8_t* const ti
 // f: their key factors, if the cache has them).  The vector's score scale and sum (as the product sees it) come back.
 // Four vectors a step in a loop, not unrolled: code that runs once is fetched at memory speed (unrolled over the
 // 32 vectors of a warp the staging took 13 us).
-template <bool ASYM>
+// TWO: what the fp16 rounding leaves goes to a second tile `lo` bytes behind.
+template <bool ASYM, bool TWO>
 __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw)[2], const float (&f)[16], uint8_t* half,
-                                          int row, int sub, float& scale, float& sum) {
+                                          int lo, int row, int sub, float& scale, float& sum) {
   float x[16];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -256,16 +257,24 @@ __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw
   const int t = sub >> 1;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {  // dims 32 t + 8 (2 (sub & 1) + i) ..: chunk i of this half
-    uint32_t y[4];
+    uint32_t y[4], z[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      y[k] = pack_half2(x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
-      if constexpr (ASYM) {
+      const float x0 = x[8 * i + 2 * k], x1 = x[8 * i + 2 * k + 1];
+      y[k] = pack_half2(x0, x1);
+      if constexpr (ASYM || TWO) {
         const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&y[k]));
         sum += h.x + h.y;
+        if constexpr (TWO) {
+          z[k] = pack_half2(x0 - h.x, x1 - h.y);
+          const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&z[k]));
+          sum += r.x + r.y;
+        }
       }
     }
-    *reinterpret_cast<uint4*>(half + row * 128 + ((dim_chunk(t, i) ^ (row & 7)) * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
+    uint4* const at = reinterpret_cast<uint4*>(half + row * 128 + ((dim_chunk(t, i) ^ (row & 7)) * 16));
+    *at = make_uint4(y[0], y[1], y[2], y[3]);
+    if constexpr (TWO) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + lo) = make_uint4(z[0], z[1], z[2], z[3]);
   }
   if constexpr (ASYM) {
 #pragma unroll
@@ -286,7 +295,7 @@ struct Segment {
   int nv;     // query vectors of the unit's tile
   bool both;  // more than 128: both warpgroups meet every tile
 };
-__device__ __forceinline__ Segment segment_at(const SharedGeo* geo, const DecodeArgs& a, long long x, long long x1) {
+__device__ __forceinline__ Segment segment_at(const SharedGeo* geo, const DecodeArgs& a, int unit, long long x, long long x1) {
   Segment g;
   g.un = unit_at(geo, a.num_groups, a.c.H, kTok / kBlock, x);
   g.nt = int(min(x1, g.un.start + g.un.steps) - x);
@@ -294,16 +303,18 @@ __device__ __forceinline__ Segment segment_at(const SharedGeo* geo, const Decode
   g.nblk = geo->g.blocks[g.un.group];
   g.first = geo->g.start[g.un.group];
   g.rows = geo->g.start[g.un.group + 1] - g.first;
-  g.nv = min(g.rows * a.G - g.un.tile * 2 * kQ, 2 * kQ);
+  g.nv = min(g.rows * a.G - g.un.tile * unit, unit);
   g.both = g.nv > kQ;
   return g;
 }
 // Tiles of a segment that warpgroup j takes.
 __device__ __forceinline__ int jobs_of(const Segment& g, int j) { return g.both ? g.nt : (g.nt + 1 - j) / 2; }
 
-template <int KB, int VB, bool ASYM>
+// TWO: queries as an fp16 high and low part, the low ones in the second query tile; units of 128 vectors.
+template <int KB, int VB, bool ASYM, bool TWO>
 __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedArgs sa) {
   using F = Fmt<KB, VB, ASYM>;
+  constexpr int kUnit = TWO ? kQ : 2 * kQ;
   constexpr int kStep = kTok / kBlock;
   constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f), kVC = VB == 8 ? 128.f : (VB == 4 ? 8.f : 2.f);
   const DecodeArgs& a = sa.d;
@@ -327,7 +338,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
   }
   // Beside the suffix kernel, see kvq_shared.cuh: the wait for it comes last.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  shared_geometry(&sm->geo, a, 2 * kQ, kStep, tid, kTcThreads, false);  // errors are reported by the suffix kernel
+  shared_geometry(&sm->geo, a, kUnit, kStep, tid, kTcThreads, false);  // errors are reported by the suffix kernel
   const SharedGeo* geo = &sm->geo;
   const int Pe = shared_ctas(geo, sa.sl.ctas), ci = blockIdx.x;
   if (ci >= Pe) return wait_for_suffix();
@@ -351,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
       const uint32_t q_addr = smem_u32(sm->q), st_addr = smem_u32(sm->st);
       int n0 = 0, c0 = 0, c1 = 0, seg = 0;  // tiles and jobs before this segment
       for (long long x = x0; x < x1 && ok; ++seg) {
-        const Segment g = segment_at(geo, a, x, x1);
+        const Segment g = segment_at(geo, a, kUnit, x, x1);
         x += g.nt;
         ok = mbar_wait(&sm->q_full, uint32_t(seg) & 1u);
         // P . V runs one tile behind the scores, two where the warpgroups take turns
@@ -376,6 +387,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
                 for (int k = 0; k < kHeadDim / 16; ++k)
                   tc_mma_ss(d, qd + (k >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (k & 3),
                             kd + (k >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (k & 3), f16_idesc(kQ, kTok), k > 0);
+                if constexpr (TWO) {
+#pragma unroll
+                  for (int k = 0; k < kHeadDim / 16; ++k)
+                    tc_mma_ss(d, qd + (sizeof(sm->q[0]) >> 4) + (k >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (k & 3),
+                              kd + (k >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (k & 3), f16_idesc(kQ, kTok), true);
+                }
                 tc_commit(&sm->s_full[j][c & 1]);
               }
               __syncwarp();
@@ -417,7 +434,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
     const uint32_t c64 = 0x64646464u | (uint32_t(a.B) >> 16);  // a.B <= 4096: the constant itself
     int n = 0;
     for (long long x = x0; x < x1 && ok;) {
-      const Segment g = segment_at(geo, a, x, x1);
+      const Segment g = segment_at(geo, a, kUnit, x, x1);
       x += g.nt;
       const int* table = a.table + size_t(g.first) * a.mbps;
       int ids = -1, ids_next = -1;  // this warp's table entries of 32 tiles, and of the next 32
@@ -435,7 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
       };
       ids_next = load_ids(0);
       int maxlen = 0;  // of the unit's rows: scales of slots behind it are not data
-      for (int r = g.un.tile * 2 * kQ / a.G + lane; r <= (g.un.tile * 2 * kQ + g.nv - 1) / a.G; r += 32)
+      for (int r = g.un.tile * kUnit / a.G + lane; r <= (g.un.tile * kUnit + g.nv - 1) / a.G; r += 32)
         maxlen = max(maxlen, prefix_len(a, g.first + r, g.nblk));
       maxlen = __reduce_max_sync(kFull, maxlen);
       // this warp's block of the tile: codes, and the record entries of token `lane` (lanes 0..15)
@@ -506,9 +523,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
     const int j = warp >> 2, v = tid & (kQ - 1);  // warpgroup, its vector
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t o_cols = lanes + 128 * j, s_cols = lanes + 256 + 128 * j;
-    int n0 = 0, c = 0, seg = 0;  // tiles before this segment; this warpgroup's jobs so far
+    int n0 = 0, c = 0, c_other = 0, seg = 0;  // tiles before this segment; this warpgroup's and the other's jobs so far
     for (long long x = x0; x < x1 && ok; ++seg) {
-      const Segment g = segment_at(geo, a, x, x1);
+      const Segment g = segment_at(geo, a, kUnit, x, x1);
       x += g.nt;
       if (seg > 0) {  // both warpgroups are done with the previous segment's queries
         mbar_arrive(&sm->seg_done);
@@ -518,7 +535,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
       {
         // this warp's 32 vectors (16 of the shared 128), 4 a step
         const int per = g.both ? 32 : 16, v0 = (g.both ? warp : 2 * (warp & 3) + j) * per, sub = lane & 7;
-        const int G = a.G, gv0 = g.un.tile * 2 * kQ + v0;
+        const int G = a.G, gv0 = g.un.tile * kUnit + v0;
         const uint16_t* src = a.q + (size_t(g.first) * a.Hq + g.un.h * G) * kHeadDim + 16 * sub;
         float f[16];
         if (a.c.factor) {
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
           }
           const int at = v0 + b + (lane >> 3);
           float qs, sum;
-          put_query<ASYM>(a, cur, f, half, at & (kQ - 1), sub, qs, sum);
+          put_query<ASYM, TWO>(a, cur, f, half, int(sizeof(sm->q[0])), at & (kQ - 1), sub, qs, sum);
           if (sub == 0) {
             sm->qs[at] = qs;
             sm->qz[at] = sum;
@@ -687,6 +704,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
         if (!ok) break;
         tc_fence_after();
       }
+      if constexpr (TWO) {  // the other warpgroup's scores have read the low query parts, whose place the records pass by
+        const int others = jobs_of(g, 1 - j);
+        c_other += others;
+        if (others > 0) ok = __all_sync(kFull, pair_wait(sm->s_full[1 - j], c_other - 1));
+        if (!ok) break;
+      }
       if (g.both ? tid < g.nv : v < g.nv) {
         const size_t slot = size_t(ci + g.un.u) * 2 * kQ + tid;
         reinterpret_cast<float*>(a.ws + sa.sl.off_m)[slot] = m == kNegInf ? kNegInf : m - sg;
@@ -731,7 +754,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) shared_tc_kernel(const SharedAr
   if (warp == 12) tmem_free(tmem, kTmemCols);
 }
 
-template <int KB, int VB, bool ASYM>
+template <int KB, int VB, bool ASYM, bool TWO>
 struct SharedTcKernel {
   static int smem_bytes() { return int(sizeof(TcSmem)) + 1024; }
   // CTAs of one wave on the current device.
@@ -744,7 +767,7 @@ struct SharedTcKernel {
     auto it = done.find(dev);
     if (it != done.end()) return it->second;
     int sms = 0;
-    const auto k = shared_tc_kernel<KB, VB, ASYM>;
+    const auto k = shared_tc_kernel<KB, VB, ASYM, TWO>;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes()) != cudaSuccess ||
         cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
@@ -763,21 +786,26 @@ struct SharedTcKernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_tc_kernel<KB, VB, ASYM>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_tc_kernel<KB, VB, ASYM, TWO>, a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
   }
 };
 
-template <class F>
-auto by_format(const CacheView& c, F f) {
+template <bool TWO, class F>
+auto by_format_two(const CacheView& c, F f) {
   const int kb = c.k_bits, vb = c.v_bits;
   const bool as = c.asym != 0;
-  if (kb == 8 && vb == 8) return as ? f(SharedTcKernel<8, 8, true>{}) : f(SharedTcKernel<8, 8, false>{});
-  if (kb == 4 && vb == 4) return as ? f(SharedTcKernel<4, 4, true>{}) : f(SharedTcKernel<4, 4, false>{});
-  if (kb == 4 && vb == 8) return as ? f(SharedTcKernel<4, 8, true>{}) : f(SharedTcKernel<4, 8, false>{});
-  if (kb == 8 && vb == 4) return as ? f(SharedTcKernel<8, 4, true>{}) : f(SharedTcKernel<8, 4, false>{});
-  return as ? f(SharedTcKernel<2, 2, true>{}) : f(SharedTcKernel<2, 2, false>{});
+  if (kb == 8 && vb == 8) return as ? f(SharedTcKernel<8, 8, true, TWO>{}) : f(SharedTcKernel<8, 8, false, TWO>{});
+  if (kb == 4 && vb == 4) return as ? f(SharedTcKernel<4, 4, true, TWO>{}) : f(SharedTcKernel<4, 4, false, TWO>{});
+  if (kb == 4 && vb == 8) return as ? f(SharedTcKernel<4, 8, true, TWO>{}) : f(SharedTcKernel<4, 8, false, TWO>{});
+  if (kb == 8 && vb == 4) return as ? f(SharedTcKernel<8, 4, true, TWO>{}) : f(SharedTcKernel<8, 4, false, TWO>{});
+  return as ? f(SharedTcKernel<2, 2, true, TWO>{}) : f(SharedTcKernel<2, 2, false, TWO>{});
+}
+
+template <class F>
+auto by_format(const CacheView& c, F f) {
+  return c.q_bits == 32 ? by_format_two<true>(c, f) : by_format_two<false>(c, f);
 }
 
 }  // namespace

@@ -334,3 +334,37 @@ def test_inputs_written_by_the_kernels_just_before(batch, kw):
         ref, _ = run.decode(lens=s[1])
         np.testing.assert_allclose(out.cpu().numpy(), ref, rtol=0, atol=2e-3)
     assert run.err_bits() == 0
+
+
+@pytest.mark.parametrize("batch", [40, 3])
+@pytest.mark.parametrize("kw", [dict(), dict(k_bits=4, v_bits=4), dict(k_bits=4, asym=True), dict(k_per_channel=True),
+                                dict(window=32)])
+def test_log_sum_exp_under_a_key_factor(batch, kw):
+    """The query times the factor does not fit in fp16's 11 bits: its log-sum-exp holds float32's precision all the same."""
+    from harness import oracle_state
+    from oracle import kvq_oracle as O
+    w = small_workload("shared_lse", **dict(dict(batch=batch, len_range=(300, 420), channel_factor=True,
+                                                 outlier_channels=4), **kw))
+    inp = shared_inputs(w, [(0, batch, 15)])
+    run = DeviceRun(inp)
+    _, lse = decode_shared(run, [(0, batch, 15)])
+    for b in range(batch):
+        st = oracle_state(inp, b)
+        q = O.bf16_to_f64(inp.q[b])
+        for h in range(w.kv_heads):
+            k_hat, _ = O.reconstruct_sequence(st, h)
+            qh = q[h * w.group:(h + 1) * w.group]
+            s = qh @ k_hat.T / np.sqrt(128.0)
+            top = s.max(1, keepdims=True)
+            ref = top[:, 0] + np.log(np.exp(s - top).sum(1))
+            # float32 half-steps (2^-24) of the score's absolute sum: 8 products of 16 terms each added one after
+            # another, the low query parts and the factor, three scale factors: below 32 of them, and as many again
+            # where the tensor cores cut instead of rounding; of the exponents and of lse one each; 2^-22 of ex2,
+            # log2 and the sums' merges each
+            size = np.abs(qh) @ np.abs(k_hat).T / np.sqrt(128.0)
+            if w.asym:  # the code dot and the zero-point term are each larger than their sum
+                size = 4 * size + 4 * np.abs(qh).sum(1, keepdims=True) * np.abs(k_hat).max(1) / np.sqrt(128.0)
+            p = np.exp(s - ref[:, None])
+            tol = (p * (64 * size + np.abs(s) + np.abs(ref[:, None]))).sum(1) * 2.0 ** -24 + 3 * 2.0 ** -22
+            assert np.all(np.abs(lse[b, h * w.group:(h + 1) * w.group] - ref) <= tol), (b, h)
+    assert run.err_bits() == 0
