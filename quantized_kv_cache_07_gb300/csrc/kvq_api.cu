@@ -132,9 +132,10 @@ kvq::CacheView shared_view(const kvq_cache_desc* c) {
 kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::SharedLayout* sl) {
   const kvq::CacheView v = shared_view(c);
   const int H = c->num_kv_heads, G = q_heads / H;
-  // 256-vector units on tcgen05 where the groups fill them, 16-vector tiles
-  // otherwise, for bf16 blocks and for the two-part mode.
-  sl->tc = c->k_bits != 16 && c->q_bits != 32 && batch * G >= 32 * num_groups;
+  // Units of 256 vectors on tcgen05 where groups have 64 on average, 16-vector tiles otherwise, for bf16
+  // blocks and for the two-part mode (prefixes of 8192 tokens, int8, 32 / 48 / 64 vectors: 46 / 48 / 46 us on
+  // tcgen05, 46 / 41 / 46 on tiles; of 16384 tokens 64 / 96: 55 / 54 and 56 / 64; of 2048 64 / 96: 35 / 35 and 28 / 35).
+  sl->tc = c->k_bits != 16 && c->q_bits != 32 && batch * G >= 64 * num_groups;
   sl->tile = sl->tc ? 256 : 16;
   sl->unit = sl->tc && v.q_bits == 32 ? 128 : sl->tile;
   sl->ctas = sl->tc ? kvq::shared_tc_ctas(v) : kvq::shared_tiles_ctas(v);

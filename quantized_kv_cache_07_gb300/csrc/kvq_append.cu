@@ -142,11 +142,10 @@ __global__ void __launch_bounds__(256) dequant_kernel(const DequantArgs a) {
   dequant_store(a, r, is_key, h, lane, dequant_load(a, a.slots[r], is_key, h, lane));
 }
 
-// Many slots: 16 of the call per warp and (head, K or V).  A run of 16 slots that are one block's 16
-// tokens in order is taken by the warp of the 16 that it starts in: the block is read as it lies, 16 bytes a
-// lane, into shared memory and taken apart there; a value token on its own is 128 single bytes of
-// its block.  Other slots go one by one, four in flight (one after another, 1337 slots of 8 sequences, int4,
-// took 17 us, now 12).  Same values.
+// Many slots: 16 rows of the call per warp and (head, K or V).  Rows whose slots follow each other in a block are
+// taken together, by the warp of the 16 that the first of them lies in: the block is read as it lies, 16
+// bytes a lane, into shared memory and taken apart there; a value token on its own is 128 single bytes of its
+// block.  (One row after another for what is not a whole block: 17 us for 1337 slots of 8 sequences.)
 constexpr int kDqWarps = 8;
 
 template <int BITS, bool KEY>
@@ -156,10 +155,13 @@ __device__ __forceinline__ int code_at(const uint8_t* img, int tok, int lane, in
   return BITS == 8 ? img[L.byte] : (img[L.byte] >> L.shift) & 0xF;
 }
 
+// Rows r .. r + count - 1 of the call: tokens tok0 .. of one block.
 template <int BITS, bool KEY>
-__device__ __forceinline__ void dequant_block(const DequantArgs& a, int r0, int phys, int h, uint8_t* img, int lane) {
+__device__ __forceinline__ void dequant_block(const DequantArgs& a, int r, int slot, int count, int h, uint8_t* img,
+                                              int lane) {
   const CacheView& c = a.c;
-  const size_t hb = size_t(h) * c.num_blocks + phys;
+  const size_t hb = size_t(h) * c.num_blocks + slot / kBlock;
+  const int tok0 = slot % kBlock;
   const uint4* blk = reinterpret_cast<const uint4*>((KEY ? c.k_codes : c.v_codes) + hb * block_bytes(BITS));
 #pragma unroll
   for (int i = 0; i < BITS / 2; ++i) reinterpret_cast<uint4*>(img)[i * 32 + lane] = blk[i * 32 + lane];
@@ -174,24 +176,24 @@ __device__ __forceinline__ void dequant_block(const DequantArgs& a, int r0, int 
   if (chan) f = *reinterpret_cast<const float4*>(c.factor + h * kHeadDim + 4 * lane);
   __syncwarp();
   const int bias = c.asym ? 0 : (BITS == 8 ? 128 : 8);
-#pragma unroll
-  for (int i = 0; i < kBlock; ++i) {
-    const float s = __shfl_sync(kFull, s_of, i), z = __shfl_sync(kFull, z_of, i);
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const float s = __shfl_sync(kFull, s_of, tok0 + i), z = __shfl_sync(kFull, z_of, tok0 + i);
     const float ff[4] = {f.x, f.y, f.z, f.w};
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int raw = code_at<BITS, KEY>(img, i, lane, j);
+      const int raw = code_at<BITS, KEY>(img, tok0 + i, lane, j);
       if constexpr (BITS == 16) v[j] = bf16_bits_to_f32(uint16_t(raw));
       else v[j] = c.asym ? __fmaf_rn(float(raw), s, z) : __fmul_rn(float(raw - bias), chan ? ff[j] : s);
     }
-    dequant_store(a, r0 + i, KEY, h, lane, make_float4(v[0], v[1], v[2], v[3]));
+    dequant_store(a, r + i, KEY, h, lane, make_float4(v[0], v[1], v[2], v[3]));
   }
   __syncwarp();
 }
 
 template <int KB, int VB>
-__global__ void __launch_bounds__(kDqWarps * 32, 4) dequant_rows_kernel(const DequantArgs a) {
+__global__ void __launch_bounds__(kDqWarps * 32) dequant_rows_kernel(const DequantArgs a) {
   __shared__ __align__(16) uint8_t img[kDqWarps][kBlock * kHeadDim * 2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -202,45 +204,29 @@ __global__ void __launch_bounds__(kDqWarps * 32, 4) dequant_rows_kernel(const De
   const int r0 = int(task / (2 * H)) * kBlock, kv = int(task % (2 * H));
   const bool is_key = kv < H;
   const int h = is_key ? kv : kv - H;
-  // rows r0 - 16 .. r0 + 15 and r0 + 16 .. r0 + 31, one a lane; bit i: row r0 - 16 + i
-  auto slot_at = [&](long long r) { return r >= 0 && r < a.n ? a.slots[r] : -1; };
-  const int lo = slot_at((long long)r0 - kBlock + lane), hi = lane < kBlock ? slot_at((long long)r0 + kBlock + lane) : -1;
-  const int after_lo = __shfl_down_sync(kFull, lo, 1), first_hi = __shfl_sync(kFull, hi, 0);
-  const int after_hi = __shfl_down_sync(kFull, hi, 1);
-  auto mask64 = [](bool l, bool h) {
-    const unsigned long long low = __ballot_sync(kFull, l);
-    return low | (unsigned long long)(__ballot_sync(kFull, h)) << 32;
-  };
-  const unsigned long long starts =
-      mask64(lo >= 0 && lo % kBlock == 0 && lo / kBlock < a.c.num_blocks, false);
-  unsigned long long next = mask64(lo >= 0 && (lane < 31 ? after_lo : first_hi) == lo + 1,
-                                   hi >= 0 && lane < kBlock - 1 && after_hi == hi + 1);  // the row behind is the next slot
-  next &= next >> 1;
-  next &= next >> 2;
-  next &= next >> 4;
-  const unsigned runs = unsigned(starts & next & next >> 7);  // 15 such rows in a row
-  const unsigned before = runs & 0xFFFFu, lead = runs >> kBlock;  // at most one of each
-  unsigned rest = a.n - r0 >= kBlock ? 0xFFFFu : (1u << (a.n - r0)) - 1u;  // rows of the 16 that no run covers
-  if (before) rest &= ~0u << (__ffs(before) - 1);
-  if (lead) {
-    const int l = __ffs(lead) - 1, first = __shfl_sync(kFull, lo, kBlock + l);
-    rest &= (1u << l) - 1u;
-    if (is_key) dequant_block<KB, true>(a, r0 + l, first / kBlock, h, img[warp], lane);
-    else dequant_block<VB, false>(a, r0 + l, first / kBlock, h, img[warp], lane);
-  }
+  // rows r0 - 1 .. r0 + 30, one a lane, -1 for a row or slot that is not there
+  const long long row = (long long)r0 - 1 + lane;
+  int slot = row >= 0 && row < a.n ? a.slots[row] : -1;
+  if (slot < 0 || slot / kBlock >= a.c.num_blocks) slot = -1;
+  const int before = __shfl_up_sync(kFull, slot, 1);
+  const bool follows = lane > 0 && slot >= 0 && before >= 0 && slot == before + 1 && slot % kBlock != 0;
+  // bit i: row r0 + i
+  const uint32_t goes_on = __ballot_sync(kFull, follows) >> 1;
+  const uint32_t none = __ballot_sync(kFull, slot < 0 && row < a.n) >> 1;
+  uint32_t starts = ~goes_on & ~none & 0xFFFFu;
+  if (a.n - r0 < kBlock) starts &= (1u << (a.n - r0)) - 1u;
 #pragma unroll 1
-  while (rest) {
-    int row[4];
-    float4 v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      row[i] = rest ? __ffs(rest) - 1 : -1;
-      rest &= rest - 1;
-      if (row[i] >= 0) v[i] = dequant_load(a, __shfl_sync(kFull, lo, kBlock + row[i]), is_key, h, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (row[i] >= 0) dequant_store(a, r0 + row[i], is_key, h, lane, v[i]);
+  while (starts) {
+    const int l = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const int first = __shfl_sync(kFull, slot, l + 1);
+    const int count = __ffs(~(goes_on >> l >> 1));  // the rows behind it that go on, and itself
+    if (is_key) dequant_block<KB, true>(a, r0 + l, first, count, h, img[warp], lane);
+    else dequant_block<VB, false>(a, r0 + l, first, count, h, img[warp], lane);
+  }
+  for (uint32_t z = none & 0xFFFFu; z; z &= z - 1) {
+    const int r = r0 + __ffs(z) - 1;
+    if (r < a.n) dequant_store(a, r, is_key, h, lane, make_float4(0.f, 0.f, 0.f, 0.f));
   }
 }
 
@@ -277,8 +263,9 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s) {
   const long long vecs = (long long)a.n * 2 * a.c.H;
   if (vecs == 0) return cudaSuccess;
-  // 16 slots a warp from 256 slots on (fewer are one wave of single-vector warps)
-  if (a.n >= 256 && a.c.k_bits != 2) {
+  // 16 slots a warp from a wave of one-vector warps on (152 SMs x 64 warps; behind the rotary write, 16
+  // vectors a slot: 384 slots take 30 us one by one and 33 so, 640 33 and 31, 2048 48 and 46)
+  if (vecs >= 152 * 64 && a.c.k_bits != 2) {
     const long long tasks = (long long)((a.n + kBlock - 1) / kBlock) * 2 * a.c.H;
     const long long grid = (tasks + kDqWarps - 1) / kDqWarps;
     const int kb = a.c.k_bits, vb = a.c.v_bits, threads = kDqWarps * 32;

@@ -501,9 +501,12 @@ cudaError_t launch_pdl(void (*kernel)(const RopeArgs), const RopeArgs& a, long l
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s) {
   const int kb = a.ap.c.k_bits, vb = a.ap.c.v_bits;
   const bool group = a.write && kb == 2 && a.ap.mode == KVQ_APPEND_QUANT;
-  // Windows of 16 rows from kRowsMin rows on; fewer rows are one wave of single-vector warps and sooner done.
-  constexpr int kRowsMin = 256;
-  if (a.ap.n >= kRowsMin && (!a.write || (a.ap.mode == KVQ_APPEND_QUANT && !group))) {
+  // Windows of 16 rows from three waves of one-vector warps on (152 SMs x 64 warps; with the read-back, 48
+  // vectors a row: 256 rows take 21 us one by one and 31 in windows, 640 33 and 31, 1024 39 and 35, 2048
+  // 58 and 46; 12 vectors a row: 1024 rows 23 and 34, 2048 31 and 33): a window has more to do before its first store.
+  constexpr long long kRowsVectors = 3ll * 152 * 64;
+  const long long vectors = (long long)a.ap.n * (a.Hq + (a.write ? 2 * a.ap.c.H : 0));
+  if (vectors >= kRowsVectors && (!a.write || (a.ap.mode == KVQ_APPEND_QUANT && !group))) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -515,8 +518,7 @@ cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s) {
     return launch_rows<16, 16>(a, sms, s);
   }
   if (!group) {
-    const long long per_row = a.Hq + (a.write ? 2 * a.ap.c.H : 0);
-    return launch_pdl(rope_append_kernel, a, a.ap.n * per_row, s);
+    return launch_pdl(rope_append_kernel, a, vectors, s);
   }
   if (a.Hq > 0) {
     RopeArgs q = a;

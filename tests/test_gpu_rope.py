@@ -332,8 +332,8 @@ def test_read_back_of_many_slots(k_bits, v_bits, asym, kchan, shift):
     block = lambda b: np.arange(16 * b, 16 * b + 16)
     parts = [block(3), block(5)[2:], block(7), [-1, 16 * nb, 16 * nb + 16], block(7), block(8), block(9)[:15], block(11),
              [3], block(12), block(13)[::-1], block(39), block(2)[1:], block(2)[:1], block(20), [-5], block(21)]
-    slots = np.concatenate([np.asarray(p, np.int32) for p in parts] + [np.asarray(p, np.int32) for p in parts[::-1]])
-    assert slots.size >= 256 and slots.size % 16 != 0
+    slots = np.concatenate([np.asarray(p, np.int32) for p in (parts + parts[::-1]) * 8 + [[7]]])
+    assert slots.size * 2 * H >= 152 * 64 and slots.size % 16 != 0
     n = slots.size
     s = torch.from_numpy(slots).cuda()
     whole = [torch.full((n * H * 128 + shift,), 7.0, device="cuda")[shift:] for _ in range(2)]
@@ -344,3 +344,40 @@ def test_read_back_of_many_slots(k_bits, v_bits, asym, kchan, shift):
     for x, y in zip(whole, few):
         assert torch.equal(x.view(n, H, 128), y)
         assert not x.view(n, H, 128)[s < 0].any() and x.view(n, H, 128)[s == 48].any()
+
+
+@pytest.mark.parametrize("k_bits,v_bits,asym,factor,interleaved,R", [
+    (8, 8, False, False, False, 128), (4, 4, True, True, True, 64), (4, 8, False, True, False, 96),
+    (8, 4, True, False, True, 128), (16, 16, False, False, False, 64)])
+def test_many_rows_as_in_small_calls(k_bits, v_bits, asym, factor, interleaved, R):
+    """Enough rows for windows of 16, runs of whole blocks at any row, parts of blocks, bad positions: the same bits as
+    calls of a few rows (which are compared with the oracle above)."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(R + k_bits)
+    H, Hq, lens = 3, 6, [1000, 1, 37, 16, 15, 1531, 17]
+    n, mbps, B = sum(lens), 96, len(lens)
+    assert n * (Hq + 2 * H) >= 3 * 152 * 64
+    rope = RopeTable(2000, rotary_dim=R, interleaved=interleaved)
+    i = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    x = torch.from_numpy(rng.standard_normal((n, (Hq + 2 * H) * 128)).astype(np.float32)).bfloat16().cuda()
+    q, k, v = x[:, :Hq * 128], x[:, Hq * 128:(Hq + H) * 128], x[:, (Hq + H) * 128:]
+    seq = np.repeat(np.arange(B), lens)
+    first = rng.integers(0, 3, B) * 8          # some sequences start inside a block
+    slot = np.concatenate([np.arange(m) + f for m, f in zip(lens, first)])
+    pos = rng.integers(0, 2000, n)
+    pos[[5, 1010, 2000]] = [-1, 2000, -7]      # flagged, their rows left alone
+    table = i(rng.permutation(B * mbps).reshape(B, mbps))
+    c_f = rng.random((H, 128)) + 0.5 if factor else None
+    got = []
+    for step in (n, 100):
+        c = KVCache(B * mbps, H, k_bits, v_bits, asym=asym, channel_factor=c_f)
+        out, err = torch.zeros(n, Hq, 128, dtype=torch.bfloat16, device="cuda"), i([0])
+        for r in range(0, n, step):
+            e = min(n, r + step)
+            _lib.kvq_rope_append(c.desc, rope.desc, q[r:e], Hq, out[r:e], k[r:e], v[r:e], i(pos[r:e]), i(seq[r:e]),
+                                 i(slot[r:e]), _lib.APPEND_QUANT, table, B, mbps, err_word=err)
+        assert int(err) == _lib.KVQ_DEVERR_POSITION
+        got.append([out.view(torch.int16), c.k_codes, c.v_codes] + ([] if c.meta is None else [c.meta.view(torch.int32)]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

@@ -166,7 +166,9 @@ def test_many_vectors_and_long_prefixes(kw, groups):
     assert run.err_bits() == 0
 
 
-@pytest.mark.parametrize("kw", [dict(k_bits=4, v_bits=4, asym=True), dict(k_bits=2, v_bits=2), dict()])
+@pytest.mark.parametrize("kw", [dict(k_bits=4, v_bits=4, asym=True), dict(k_bits=2, v_bits=2), dict(),
+                                dict(k_bits=4, v_bits=4, asym=True, q_heads=16), dict(k_bits=2, v_bits=2, q_heads=16),
+                                dict(q_heads=16), dict(q_heads=16, channel_factor=True)])
 @pytest.mark.parametrize("P", [1, 4, 7, 12, 23])
 def test_short_prefixes_again_and_again(kw, P):
     """A few tiles per CTA, where the conversion runs furthest ahead of the softmax: the same bits every time."""
@@ -301,7 +303,8 @@ def test_groups_without_a_prefix(kw):
     assert run.err_bits() == 0
 
 
-@pytest.mark.parametrize("batch,kw", [(16, dict()), (16, dict(k_bits=4, v_bits=4, channel_factor=True)), (3, dict())])
+@pytest.mark.parametrize("batch,kw", [(16, dict()), (16, dict(q_heads=16)), (3, dict()),
+                                      (16, dict(k_bits=4, v_bits=4, channel_factor=True, q_heads=16))])
 def test_inputs_written_by_the_kernels_just_before(batch, kw):
     """Queries, lengths, groups and the table change between calls that are queued without a wait."""
     from quantized_kv_cache_07_gb300.cache import SharedWorkspace
