@@ -215,14 +215,15 @@ class _Args:
         """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous."""
         if t is None or isinstance(t, int):
             return t, 0
+        shape, stride = t.shape, t.stride()
         ok = t.dtype is self.bf16 and t.get_device() == self.device
-        if ok and t.dim() == 2:
-            ok = t.shape == (n, heads * 128) and (n == 0 or t.stride(1) == 1)
+        if ok and len(shape) == 2:
+            ok = shape[0] == n and shape[1] == heads * 128 and (n == 0 or stride[1] == 1)
         elif ok:
-            ok = t.shape == (n, heads, 128) and (n == 0 or t.stride()[1:] == (128, 1))
+            ok = shape == (n, heads, 128) and (n == 0 or stride[1:] == (128, 1))
         if not ok:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
-        return t.data_ptr(), t.stride(0) if n > 1 else 0
+        return t.data_ptr(), stride[0] if n > 1 else 0
 
 
 def kvq_rope_table(freqs: RopeFreqs, rotary_dim: int, max_pos: int, table, stream=None):

@@ -9,12 +9,18 @@
 // is staged, and only about keep * (1 - keep / len) of the kept tokens move.
 //
 // Two launches.
-//   select: one CTA per unit finds the K-th largest sum by radix selection on the
-//     sums' order-preserving bits (8 bits a pass), then walks the slots in order with
-//     block scans for the ranks of holes and kept tail tokens and writes the source
-//     of every slot.  Ties go to the lowest slot: the result is one and the same
-//     whatever the scheduling.
-//   move: one warp per 16-token block with holes copies codes and scales.  A key
+//   select: a cluster of 1 to 8 CTAs per unit, each with a run of its slots, finds the K-th largest sum by radix
+//     selection on the sums' order-preserving bits (11 bits a pass, up to three; the sums are
+//     read once, their keys stay in shared memory), then ranks holes and kept tail
+//     tokens by warp runs and ballots and matches them through lists in the cluster's shared
+//     memory.  Ties go to the lowest slot: the result is one and the same whatever the
+//     scheduling.  Bound by latency: three rounds through the cluster (30 us for 32 units of 32768
+//     tokens on 4 CTAs each; on one CTA, the sums read in every pass, 96).
+//   move: one warp per 16-token block with holes copies codes and scales, the sources of a block fetched two blocks
+//     ahead and their places one: 43 us for 32 x 8192 slots, 230 MB at 5.3 TB/s.  The
+//     layout costs that: a value token is one byte of every word of its block, so each source
+//     block is read whole for a quarter of its tokens (the moved bytes alone are 16 us).
+//     A key
 //     token is 16-byte pieces of the fragment-native block; a value token is one
 //     field (byte, nibbles or half) of every word of four lanes' pieces, merged
 //     into the destination's words, which only this warp writes.
@@ -29,8 +35,9 @@ constexpr int kWin = 8192;       // holes matched per walk; more take another wa
 constexpr int kKeyCap = 32768;   // tokens whose keys stay in shared memory; longer rows read their sums again
 constexpr int kBins = 2048, kReplicas = 4;
 constexpr int kLoads = 8;
-constexpr int kMinSpan = 2048;   // stored tokens that make another CTA of the cluster worth it
-constexpr long long kMoveCtas = 4;
+constexpr int kMinSpan = 2048;   // stored tokens that make another CTA of the cluster worth it (64 units of 4096: 39 us
+                                 // with one CTA a unit, 37 with two)
+constexpr long long kMoveCtas = 4;  // of the move an SM, two of which are resident (4 / 8 / 16: 74 / 76 / 81 us)
 static_assert(kBins == 2 * kSelThreads && kReplicas * kBins <= 2 * kWin && kSelWarps == 32, "");
 
 // What one sequence keeps: of Lq stored tokens (and the ring's), n go.

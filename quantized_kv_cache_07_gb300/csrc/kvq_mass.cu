@@ -8,12 +8,17 @@
 // no maximum, no merge, no atomics, one pass over the keys (the values are
 // not read).  Bound: HBM, the key codes and scales plus 8 bytes of mass a token.
 //
-// Work: the 16-token blocks of all (sequence, KV head) units form one range cut
+// Measured: 4 sequences of 131072 tokens, int4 keys, 64 query heads: 66 us, 319 MB at 4.8 TB/s (the copy rate
+// would take 47); 32 of 1k-8k, int4: 25 us (13.6).  Issue slots are 63 % busy at 180 instructions a block, about
+// 80 of them the exact conversion of 4-bit codes, with 16 warps an SM (the query group and two blocks in flight
+// are 128 registers; at 85 they spill and it takes 136 us).
+//
+// Work: the 16-token blocks of all (sequence, KV head) units, two a step, form one range cut
 // evenly over all warps of one wave.  A warp keeps its unit's query
 // group in registers as the B operand of m16n8k16 (tokens on M, queries on N) and streams blocks
 // through its own ring of shared-memory stages with 16-byte asynchronous
 // copies; the fragment-native block order gives each lane the bytes it copied
-// itself.  Scores as in the decode kernel: exact codes in fp16, the key
+// itself.  (One block a step, the stages unrolled: 268 instructions a block, 99 us.)  Scores as in the decode kernel: exact codes in fp16, the key
 // scale after the dot product.  The query is exact in fp16 (bf16 has 8
 // significant bits) unless a per-channel key factor is folded in: then it is
 // carried as an fp16 high and low part, because a weight's relative error is

@@ -15,7 +15,10 @@
 // instructions a value; a float32 sum with a bound on its error is 7 and decides all but one value in 10^4.
 //
 // One warp turns and writes one 128-element vector; lane l owns dims 4l..4l+3,
-// so a pair's other half is in the same lane (interleaved) or R / 8 lanes away.
+// so a pair's other half is in the same lane (interleaved) or R / 8 lanes away.  Many rows go 16 at a time
+// (rope_rows_kernel), which is what 8192 rows of 48 heads spend 78 us in: 200 MB moved at 2.6 TB/s, bound by the
+// instructions (about 130 a vector, issue slots 57 % busy; the copy rate would allow 30 us).  64 rows are one
+// launch's latency: 4 us.
 #include "kvq_append_device.cuh"
 
 namespace kvq {
@@ -183,7 +186,7 @@ __global__ void __launch_bounds__(kGroupWarps * 32) rope_append_group_kernel(con
 //
 // A row at a time, a value vector's codes are 128 single bytes (or nibbles) spread over its whole
 // block, and every warp waits for its own loads: 185 us for 8192 rows that take 27 us to move.
-// Here a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
+// Here (78 us) a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
 // from a multiple of 16: prompts), a warp turns and quantizes the 16 vectors of a head, puts the block
 // together in shared memory and writes it as it lies, 16 bytes a lane; rows outside such runs are
 // written one by one.  The window's rows of the table are staged once for all heads; queries go 8
@@ -193,8 +196,7 @@ constexpr int kRows = 16;
 struct RopeSmem {
   alignas(16) float cs[2 * kRows][kHeadDim];      // table rows of the window and of the run
   alignas(16) uint8_t img[8][kBlock * kHeadDim * 2];  // one block image per warp
-  int rp[2 * kRows];  // rope positions (-1: none) of rows r0 .. r0 + 15, then of the run's
-  int seq[3 * kRows], pos[3 * kRows], rope[3 * kRows];  // rows r0 - 15 .. r0 + 32 (seq, rope -1: no such row)
+  int seq[3 * kRows], pos[3 * kRows], rope[3 * kRows];  // rows r0 - 15 .. r0 + 32 (-1: no such row)
   int lead;           // first row of the run in this window, or -1
   unsigned single;    // rows of the window that are written one by one
 };
@@ -361,41 +363,47 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
   }
   __syncthreads();
   if (warp == 0) {
-    // row r0 + lane (lane < 16) leads a run if 16 rows from it are one sequence's positions p, p + 1, .. with
-    // p a multiple of 16, all of them with a rope position; at most one row of a window does
-    bool lead = lane < kRows;
-    const int s = lane < kRows ? lane + kRows - 1 : 0, b = sm->seq[s], p = sm->pos[s];
-    lead = lead && b >= 0 && b < a.ap.batch && p >= 0 && p % kBlock == 0;
-    for (int i = 0; i < kBlock && lead; ++i)
-      lead = sm->seq[s + i] == b && sm->pos[s + i] == p + i && sm->rope[s + i] >= 0;
-    const unsigned found = __ballot_sync(kFull, lead);
-    if (lane == 0) sm->lead = found ? r0 + __ffs(found) - 1 : -1;
-    // rows in no run of this window's or the one before: those are written one by one
-    bool single = a.write && lane < kRows && sm->rope[s] >= 0;
-    if (single && b >= 0 && b < a.ap.batch && p >= 0) {
-      const int first = s - p % kBlock;
-      bool run = first >= 0;
-      for (int i = 0; i < kBlock && run; ++i)
-        run = sm->seq[first + i] == b && sm->pos[first + i] == p - p % kBlock + i && sm->rope[first + i] >= 0;
-      single = !run;
+    // bit i: row r0 - 15 + i.  A row leads a run if 16 rows from it are one sequence's positions p, p + 1, .. with p a
+    // multiple of 16, all of them with a rope position; at most one row of a window does
+    auto bits = [&](int i, unsigned& first, unsigned& next, unsigned& there) {
+      const bool in = i < 3 * kRows, on = in && sm->rope[i] >= 0;
+      const int b = in ? sm->seq[i] : -1, p = in ? sm->pos[i] : -1;
+      first = __ballot_sync(kFull, on && b >= 0 && b < a.ap.batch && p >= 0 && p % kBlock == 0);
+      next = __ballot_sync(kFull, on && i + 1 < 3 * kRows && sm->rope[i + 1] >= 0 && sm->seq[i + 1] == b &&
+                                      p >= 0 && sm->pos[i + 1] == p + 1);
+      there = __ballot_sync(kFull, on);
+    };
+    unsigned first, next_lo, next_hi, there, unused[2];
+    bits(lane, first, next_lo, there);
+    bits(32 + lane, unused[0], next_hi, unused[1]);
+    unsigned long long next = next_lo | (unsigned long long)next_hi << 32;
+    next &= next >> 1;
+    next &= next >> 2;
+    next &= next >> 4;
+    const unsigned runs = first & unsigned(next & next >> 7);  // 15 rows that the next one follows
+    unsigned covered = runs | runs << 1;
+    covered |= covered << 2;
+    covered |= covered << 4;
+    covered |= covered << 8;
+    const unsigned leads = runs >> (kRows - 1) & 0xFFFFu;
+    if (lane == 0) {
+      sm->lead = leads ? r0 + __ffs(leads) - 1 : -1;
+      // rows in no run of this window's or the one before: those are written one by one
+      sm->single = a.write ? (there & ~covered) >> (kRows - 1) & 0xFFFFu : 0u;
     }
-    const unsigned singles = __ballot_sync(kFull, single);
-    if (lane == 0) sm->single = singles;
   }
   __syncthreads();
   const int lead = sm->lead;
-  if (tid < kRows) {
-    sm->rp[tid] = sm->rope[tid + kRows - 1];
-    sm->rp[kRows + tid] = lead >= 0 ? sm->rope[lead - r0 + kRows - 1 + tid] : -1;
-  }
-  __syncthreads();
+  auto rope_of = [&](int row) {  // row 0..15 of the window, 16..31 of the run
+    const int at = row < kRows ? row : (lead >= 0 ? lead - r0 + row - kRows : -1);
+    return at >= 0 ? sm->rope[at + kRows - 1] : -1;
+  };
   for (int i = tid; i < 2 * kRows * R4; i += 256) {
-    const int row = i / R4, at = i % R4;
-    if (sm->rp[row] >= 0)
-      reinterpret_cast<float4*>(sm->cs[row])[at] =
-          reinterpret_cast<const float4*>(a.table + size_t(sm->rp[row]) * a.R)[at];
+    const int row = i / R4, at = i % R4, rp = rope_of(row);
+    if (rp >= 0)
+      reinterpret_cast<float4*>(sm->cs[row])[at] = reinterpret_cast<const float4*>(a.table + size_t(rp) * a.R)[at];
   }
-  if (tid < kRows && r0 + tid < n && sm->rp[tid] < 0 && blockIdx.y == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
+  if (tid < kRows && r0 + tid < n && rope_of(tid) < 0 && blockIdx.y == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
   __syncthreads();
 
   // ---- tasks: the run's blocks, the single rows' vectors, the queries 8 at a time
@@ -427,7 +435,7 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
       continue;
     }
     const int qt = task - blocks - singles, i = qt / q8, h0 = (qt % q8) * 8, r = r0 + i;
-    if (r >= n || sm->rp[i] < 0) continue;
+    if (r >= n || sm->rope[i + kRows - 1] < 0) continue;
     const uint16_t* src = a.q + (long long)r * a.q_stride + h0 * kHeadDim + 4 * lane;
     uint2 raw[8];
 #pragma unroll

@@ -1,7 +1,7 @@
 // The shared prefix of kvq_decode_shared on tcgen05, for groups of many query vectors.
 //
-// A CTA takes 128 query vectors of one group and KV head and streams its share
-// of the prefix 64 tokens (4 blocks) at a time:
+// A CTA takes up to 256 query vectors of one group and KV head, 128 a softmax warpgroup, and streams its share
+// of the prefix 64 tokens (4 blocks) at a time; of 128 vectors:
 //   S (128 x 64, tensor memory) = Q (fp16, shared memory) . K^T (codes converted to fp16, shared memory)
 //   P = exp2(S * s_k * scale - m), one thread per query vector, fp16 weights P * s_v back to tensor memory
 //   O (128 x 128, tensor memory) += P . V (codes converted to fp16, shared memory)
@@ -21,6 +21,17 @@
 // (Measured before: the same products issued by softmax threads between their steps, two CTAs of
 // 256 threads per SM: 75 us for 64 sequences on 32768 tokens, each issue holding its warp for 1000 cycles.)
 //
+// Measured: 64 sequences x 32 heads on 32768 shared tokens, int8: 84 us a call, about 55 of them here (the
+// products alone would take 18, 2 x 128 vectors of a tile 1024 cycles).  A tile of 256 vectors takes
+// 3000 to 3600 cycles; its shared-memory traffic takes 2340 of them: the operands of the products
+// 1024, the scales that every softmax thread reads, 16 bytes at 4 wavefronts, 1024, the converted
+// codes 293.  Before the first tile a CTA spends 8 us on geometry, tensor memory and
+// queries, behind the last one 2 us on its record.
+//
+// Under a key factor (TWO) the query times the factor does not fit in 11 bits: an fp16 high and low part, both
+// multiplied with the same K tile.  The low part takes the second query tile, so a unit is 128
+// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 59 us a call, 50 with one part.
+//
 // Orders inside a tile.  The tokens and dims of a block are permuted so that a lane's codes
 // (fragment-native order, include/kvq.h) go to shared memory as 16-byte (K) and
 // 8-byte (V) stores without bank conflicts:
@@ -28,8 +39,8 @@
 //   dim 32 t + 8 i + e:  half i >> 1, 16-byte chunk (t & 1) + 4 (t >> 1) + 2 (i & 1), element e
 // (the same dim order for Q and K; the same token order for the columns of S and the k-index of P . V).
 //
-// Precision as in the decode kernel: exact codes, the query exact in fp16 (or
-// int8 codes), scales in fp32, fp16 weights kept in range by the sigma offset
+// Precision as in the decode kernel: exact codes, the query exact in fp16 (bf16 has 8 bits; or
+// int8 codes, or two parts), scales in fp32, fp16 weights kept in range by the sigma offset
 // (kvq_decode_impl.cuh), fp32 sums of the unrounded weights.
 #include "kvq_shared.cuh"
 #include "kvq_tcgen05.cuh"

@@ -5,7 +5,10 @@
 // CTA streams its share of the prefix once for the tile, as the chunked prefill
 // does (kvq_tiles.cuh).  The prefix of a unit is cut over several CTAs; each
 // writes one record (m, l, o) per vector, and kvq_shared.cu merges the records
-// with those of the suffixes.  Every cache format and query mode.
+// with those of the suffixes.  Every cache format and query mode.  Every CTA converts each block for its 16
+// vectors, so the time grows with the vectors: prefixes of 8192 tokens, int8, take 37 us a call with 16
+// vectors and 46 with 64, where tcgen05 units take over (kvq_shared_tc.cu); 4 sequences on 2048 tokens: 22 us,
+// latency of three launches.
 #include "kvq_shared.cuh"
 #include "kvq_tiles.cuh"
 

@@ -7,7 +7,9 @@
 // each), so that one long suffix among short ones is shared out too.  There are no
 // tickets and no waiting: chunk k writes record k.  (The Stream-K decode
 // kernel over the same tokens spends about 8 us per unit start on its flush, ticket and
-// merge: 34 us for 64 x 8 suffixes of 500 tokens that take 10 us to read.)
+// merge: 34 us for 64 x 8 suffixes of 500 tokens that take 10 us to read.)  Here they take 20 (27 from a cold L2,
+// 72 MB), bound by latency: a chunk is three steps a warp, behind the lengths, the groups, the table and the queries, each a
+// load that waits for the one before.
 //
 // A warp streams its blocks through its own shared-memory stages with 16-byte
 // asynchronous copies (each lane copies the pieces it will read) and runs the decode
