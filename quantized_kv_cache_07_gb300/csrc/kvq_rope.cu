@@ -16,7 +16,7 @@
 //
 // One warp turns and writes one 128-element vector; lane l owns dims 4l..4l+3,
 // so a pair's other half is in the same lane (interleaved) or R / 8 lanes away.  Many rows go 16 at a time
-// (rope_rows_kernel), which is what 8192 rows of 48 heads spend 78 us in: 200 MB moved at 2.6 TB/s, bound by the
+// (rope_rows_kernel), which is what 8192 rows of 48 heads spend 70 us in: 200 MB moved at 2.9 TB/s, bound by the
 // instructions (about 130 a vector, issue slots 57 % busy; the copy rate would allow 30 us).  64 rows are one
 // launch's latency: 4 us.
 #include "kvq_append_device.cuh"
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kGroupWarps * 32) rope_append_group_kernel(con
 //
 // A row at a time, a value vector's codes are 128 single bytes (or nibbles) spread over its whole
 // block, and every warp waits for its own loads: 185 us for 8192 rows that take 27 us to move.
-// Here (78 us) a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
+// Here (70 us) a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
 // from a multiple of 16: prompts), a warp turns and quantizes the 16 vectors of a head, puts the block
 // together in shared memory and writes it as it lies, 16 bytes a lane; rows outside such runs are
 // written one by one.  The window's rows of the table are staged once for all heads; queries go 8

@@ -21,7 +21,7 @@
 // (Measured before: the same products issued by softmax threads between their steps, two CTAs of
 // 256 threads per SM: 75 us for 64 sequences on 32768 tokens, each issue holding its warp for 1000 cycles.)
 //
-// Measured: 64 sequences x 32 heads on 32768 shared tokens, int8: 84 us a call, about 55 of them here (the
+// Measured: 64 sequences x 32 heads on 32768 shared tokens, int8: 80 us a call, about 55 of them here (the
 // products alone would take 18, 2 x 128 vectors of a tile 1024 cycles).  A tile of 256 vectors takes
 // 3000 to 3600 cycles; its shared-memory traffic takes 2340 of them: the operands of the products
 // 1024, the scales that every softmax thread reads, 16 bytes at 4 wavefronts, 1024, the converted
@@ -30,7 +30,7 @@
 //
 // Under a key factor (TWO) the query times the factor does not fit in 11 bits: an fp16 high and low part, both
 // multiplied with the same K tile.  The low part takes the second query tile, so a unit is 128
-// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 59 us a call, 50 with one part.
+// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 57 us a call, 50 with one part.
 //
 // Orders inside a tile.  The tokens and dims of a block are permuted so that a lane's codes
 // (fragment-native order, include/kvq.h) go to shared memory as 16-byte (K) and

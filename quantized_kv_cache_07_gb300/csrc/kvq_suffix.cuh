@@ -3,8 +3,8 @@
 //
 // The suffixes are short and many, and a merge follows in any case, so the work
 // is cut into chunks of whole (sequence, KV head) units or parts of them: a chunk
-// has C blocks, C from the total number of blocks and the CTAs (about two chunks
-// each), so that one long suffix among short ones is shared out too.  There are no
+// has C blocks, C from the total number of blocks and the CTAs (about one chunk for
+// two of them), so that one long suffix among short ones is shared out too.  There are no
 // tickets and no waiting: chunk k writes record k.  (The Stream-K decode
 // kernel over the same tokens spends about 8 us per unit start on its flush, ticket and
 // merge: 34 us for 64 x 8 suffixes of 500 tokens that take 10 us to read.)  Here they take 20 (27 from a cold L2,
@@ -29,7 +29,7 @@ struct SufFmt {
   using F = Fmt<KB, VB, ASYM>;
   static constexpr int kNB = F::kBPW;  // blocks a warp takes together
   static constexpr int kStage = kNB * F::kPerBlock;
-  static constexpr int kStages = KB == 16 ? 2 : (KB == 8 && VB == 8 ? 3 : 4);
+  static constexpr int kStages = KB == 16 ? 2 : (KB == 8 && VB == 8 ? 2 : 3);
   static constexpr int kRing = kStages * kStage;  // of one warp
   static constexpr int kOffV = kNB * F::kKBB, kOffMeta = kOffV + kNB * F::kVBB;
 };
@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(kSufThreads, 4) suffix_kernel(const SharedArgs
   const int* part = reinterpret_cast<const int*>(merge_m);
   const long long blocks = (long long)H * (part[0] + part[1] + part[2] + part[3]);
   constexpr int kGroup4 = kConsumerWarps * NB;
-  const long long want = sa.sl.suf_ctas;
+  // half a wave of chunks: fewer starts and records, and SMs that the prefix kernel can have (64 sequences of 1..1000
+  // own tokens on 32768 shared ones: 80 us a call, 84 with a whole wave and 80 with a quarter)
+  const long long want = (sa.sl.suf_ctas + 1) / 2;
   const int C = int(max((blocks + want - 1) / want, (long long)kSufMinGroups * kGroup4));
   __syncthreads();  // part has been read
   if (warp == 0) {
