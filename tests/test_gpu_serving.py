@@ -135,3 +135,57 @@ def test_serving_steps_with_eviction(k_bits, v_bits, asym):
                 np.testing.assert_array_equal(kr.double().cpu().numpy(), k2)
                 np.testing.assert_array_equal(vr.double().cpu().numpy(), v2)
         assert evicted and int(err) == 0
+
+
+def test_two_streams_at_once():
+    """Calls of two loops on two streams, with workspaces and caches of their own: the bits of the calls one by one."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable, SharedWorkspace
+    batch, heads, group, mbps, prefix = 20, 2, 4, 24, 16
+    rope = RopeTable(4096)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+    def loop(seed, bits):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        cache = KVCache(batch * mbps, heads, bits, bits)
+        ws = SharedWorkspace(cache, batch, heads * group, 1)
+        table = torch.arange(batch * mbps, device="cuda").int().view(batch, mbps)
+        table[:, :prefix] = table[0, :prefix]
+        n = prefix * T + batch * 100
+        seq = i32([0] * (prefix * T) + sum([[b] * 100 for b in range(batch)], []))
+        slot = i32(list(range(prefix * T)) + list(range(prefix * T, prefix * T + 100)) * batch)
+        k, v = (torch.randn(n, heads, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn(batch, heads * group, D, generator=g, device="cuda").bfloat16()
+        lens = torch.randint(prefix * T + 20, prefix * T + 101, (batch,), generator=g, device="cuda").int()
+        start, blocks, keep = i32([0, batch]), i32([prefix]), i32([prefix * T + 15] * batch)
+        out = torch.zeros(batch, heads * group, D, device="cuda")
+        lse = torch.zeros(batch, heads * group, device="cuda")
+        mass = torch.zeros(batch, heads, mbps * T, device="cuda")
+        source, new = torch.zeros(batch, heads, mbps * T, dtype=torch.int32, device="cuda"), torch.zeros_like(lens)
+
+        def run():
+            mass.zero_()
+            _lib.kvq_rope_append(cache.desc, rope.desc, None, 0, None, k, v, None, seq, slot, _lib.APPEND_QUANT, table,
+                                 batch, mbps)
+            _lib.kvq_decode_shared(cache.desc, q, batch, heads * group, lens, table, mbps, 1, start, blocks, out, lse=lse,
+                                   workspace=ws.buf, workspace_bytes=ws.nbytes)
+            _lib.kvq_attn_mass(cache.desc, q, batch, heads * group, lse, lens, table, mbps, mass)
+            _lib.kvq_evict(cache.desc, mass, mass, lens, keep, table, batch, mbps, source, new, protect_first=prefix * T)
+        return run, lambda: [t.clone() for t in (out, lse, mass, source, new, cache.k_codes, cache.v_codes)]
+
+    loops = [loop(1, 8), loop(2, 4)]
+    want = []
+    for run, read in loops:
+        run()
+        torch.cuda.synchronize()
+        want.append(read())
+    streams = [torch.cuda.Stream() for _ in loops]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (run, _) in zip(streams, loops):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for (_, read), w in zip(loops, want):
+        for a, b in zip(read(), w):
+            assert torch.equal(a, b)
