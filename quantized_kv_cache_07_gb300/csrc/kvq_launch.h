@@ -139,11 +139,12 @@ struct DecodeArgs {
 constexpr int kMaxGroups = 256;
 
 // Workspace of kvq_decode_shared (byte offsets).  The prefix is split over `ctas` CTAs; a unit is
-// a tile of `tile` query vectors of one group and KV head; CTA c's share of unit u is record c + u.
+// a tile of `unit` query vectors of one group and KV head; CTA c's share of unit u is record c + u, with room for
+// `tile` vectors (twice the unit where two warpgroups leave a record each).
 // The suffixes are split into chunks over `suf_ctas` CTAs, one record each, and one per unit for a
 // bf16 window behind them.
 struct SharedLayout {
-  int ctas, tile, unit, slots;  // tile: vectors of a record, unit: of a unit
+  int ctas, tile, unit, slots;
   bool tc;  // tcgen05 path (tile 256), else mma.sync (tile 16)
   int suf_ctas, suf_slots;
   size_t off_m, off_l, off_rec;     // prefix records: float [slots][tile], twice, and [slots][tile][128]
