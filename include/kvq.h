@@ -404,7 +404,9 @@ kvq_status kvq_decode_ex(const kvq_cache_desc* cache, const void* q, int32_t bat
  *   workspace    : >= kvq_decode_shared_workspace_size bytes, zeroed once by kvq_workspace_init;
  *                  one per concurrently running call
  * Everything else as kvq_decode, every cache format and query mode, the bf16
- * window (which holds each sequence's own last tokens) included.
+ * window (which holds each sequence's own last tokens) included.  Under a key factor
+ * the query times the factor is carried in two fp16 parts (as with q_bits 32), so that
+ * lse holds float32's precision.
  */
 kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
                              const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,

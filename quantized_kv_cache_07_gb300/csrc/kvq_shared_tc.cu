@@ -30,7 +30,7 @@
 //
 // Under a key factor (TWO) the query times the factor does not fit in 11 bits: an fp16 high and low part, both
 // multiplied with the same K tile.  The low part takes the second query tile, so a unit is 128
-// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 57 us a call, 50 with one part.
+// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 55 us a call, 50 with one part.
 //
 // Orders inside a tile.  The tokens and dims of a block are permuted so that a lane's codes
 // (fragment-native order, include/kvq.h) go to shared memory as 16-byte (K) and
