@@ -15,18 +15,17 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint16_t b) { return __uint_as
 
 // Warp-cooperative per-vector quantization.
 __device__ __forceinline__ void quantize_warp(const float (&x)[4], int bits, int (&code)[4], float& s) {
-  // non-negative floats order as their bits: one warp reduction
-  const float a = __uint_as_float(__reduce_max_sync(
-      kFull, __float_as_uint(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))))));
+  // non-negative floats order as their bits: one warp reduction; NaN counts as the least
+  const float own = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+  const float a = __int_as_float(__reduce_max_sync(kFull, own != own ? -1 : __float_as_int(own)));
   if (a == 0.0f) {
     s = 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) code[j] = 0;
     return;
   }
-  // |x / s| <= qmax (1 + 2^-23): the nearest integer is within +-qmax by itself
   s = __fdiv_rn(a, bits == 8 ? 127.f : 7.f);
-  round_quotients(x, s, __frcp_rn(s), code);
+  round_quotients(x, s, __frcp_rn(s), bits == 8 ? -127 : -8, bits == 8 ? 127 : 7, code);
 }
 
 // Warp-cooperative asymmetric quantization: m = min(x), s = RN32((max - min) /

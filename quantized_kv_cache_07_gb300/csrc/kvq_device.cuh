@@ -92,23 +92,32 @@ __device__ __forceinline__ float round_quotient(float x, float s) {
 // instruction cache costs more than the call.
 static __device__ __noinline__ float round_quotient_far(float x, float s) { return round_quotient(x, s); }
 
-// round_quotient of four values by the reciprocal r = RN(1 / s): x * r is within
+// The larger value, NaN if either is (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// round_quotient of four values by the reciprocal r = RN(1 / s), within [lo, hi]: x * r is within
 // 2^-22 of the quotient relatively, so for |x / s| < 400 its nearest integer is the
 // quotient's unless it lies within 10^-4 of a half-integer; there the exact rule
-// decides.  The nearest integer comes from adding and subtracting 1.5 * 2^23.
-// Same results in a quarter of the instructions.
-__device__ __forceinline__ void round_quotients(const float (&x)[4], float s, float r, int (&c)[4]) {
+// decides, and with it the bounds.  The nearest integer comes from adding and subtracting 1.5 * 2^23.
+// The exact rule also takes what is not a number (code 0, also an infinity over an infinite scale) and
+// scales whose reciprocal is beyond float32: such a scale is a subnormal of few bits, or 0, and
+// its quotients may pass the bounds.  Same results as round_quotient in a quarter of the instructions.
+__device__ __forceinline__ void round_quotients(const float (&x)[4], float s, float r, int lo, int hi, int (&c)[4]) {
   constexpr float kRound = 12582912.f;
   float far = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float t = __fmul_rn(x[j], r), m = __fadd_rn(t, kRound);
     c[j] = __float_as_int(m) - __float_as_int(kRound);
-    far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(m, kRound))));
+    far = max_nan(far, fabsf(__fsub_rn(t, __fsub_rn(m, kRound))));
   }
-  if (!(far < 0.4999f && fabsf(r) < 3e38f)) {  // or a reciprocal beyond float32
+  if (!(far < 0.4999f && fabsf(r) < 3e38f)) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = int(round_quotient_far(x[j], s));
+    for (int j = 0; j < 4; ++j) c[j] = min(hi, max(lo, int(round_quotient_far(x[j], s))));
   }
 }
 

@@ -1,0 +1,146 @@
+"""Keys and values that are not finite, and scales below float32's normal range: what one token's vector stores is its
+own alone.  The rule: NaN counts as nothing in the largest value and stores code 0; under an infinite scale every code is
+0; codes stay within their bounds whatever the quotient."""
+import numpy as np
+import pytest
+
+from layout_ref import meta_by_block, unpack_blocks
+from oracle import kvq_oracle as O
+from synth import f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+TOP = {8: 127, 4: 7}
+LOW = {8: -127, 4: -8}
+FORMATS = {"int8": dict(k_bits=8, v_bits=8), "int4": dict(k_bits=4, v_bits=4), "k4v8": dict(k_bits=4, v_bits=8),
+           "k8v4": dict(k_bits=8, v_bits=4), "asym_int8": dict(k_bits=8, v_bits=8, asym=True),
+           "asym_int4": dict(k_bits=4, v_bits=4, asym=True)}
+
+
+def _t(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def _i(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
+
+
+def _pools(c):
+    return [t.view(torch.uint8).cpu().numpy() for t in (c.k_codes, c.v_codes, c.meta)]
+
+
+def symmetric(x, bits):
+    """Codes and float32 scales of float32 vectors along the last axis, by the rule above."""
+    x = x.astype(np.float64)
+    a = np.nanmax(np.abs(x), -1, keepdims=True)
+    with np.errstate(all="ignore"):
+        s = np.where(a == 0, 1.0, (a / TOP[bits])).astype(np.float32)
+        q = np.rint(x / s.astype(np.float64))
+    return np.where(np.isnan(q), 0, np.clip(q, LOW[bits], TOP[bits])).astype(np.int32), s[..., 0]
+
+
+def bad_rows(rng, n, H):
+    """Vectors [n, H, 128] of bf16 bits with NaN and infinities in some rows (their numbers come back), each kind alone."""
+    x = rng.standard_normal((n, H, 128)).astype(np.float32)
+    rows = np.array([3, 7, 8, 12, 17, n - 2])
+    x[3, :, 5] = np.nan
+    x[7, 0, 100] = np.inf
+    x[8, H - 1, 0:4] = np.nan          # one lane's four
+    x[12, :, [0, 64, 127]] = -np.inf
+    x[17, 0, ::2] = np.nan
+    x[n - 2, :, 31], x[n - 2, :, 32] = np.inf, np.nan
+    return f32_to_bf16_bits(x), rows
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+def test_append_stores_bad_values_in_their_own_place(fmt):
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache
+    rng = np.random.default_rng(1)
+    n, H = 40, 2
+    k, rows = bad_rows(rng, n, H)
+    v, _ = bad_rows(rng, n, H)
+    got = []
+    for zero in (False, True):
+        kk, vv = k.copy(), v.copy()
+        if zero:
+            kk[rows], vv[rows] = 0, 0
+        c = KVCache(3, H, **FORMATS[fmt])
+        _lib.kvq_append(c.desc, _t(kk), _t(vv), _i(np.zeros(n)), _i(np.arange(n)), _lib.APPEND_QUANT,
+                        _i([[2, 0, 1]]), 1, 3)
+        got.append(_pools(c))
+    blocks = np.array([2, 0, 1])
+    at = (blocks[np.arange(n) // 16], np.arange(n) % 16)
+    others = np.setdiff1d(np.arange(n), rows)
+    for i, (name, x) in enumerate((("k_bits", k), ("v_bits", v))):
+        bits, asym = FORMATS[fmt][name], FORMATS[fmt].get("asym", False)
+        codes = [unpack_blocks(g[i], bits, i == 0, H, asym).transpose(0, 2, 1, 3)[at] for g in got]
+        np.testing.assert_array_equal(codes[0][others], codes[1][others])
+        if not asym:
+            want, s = symmetric(O.bf16_to_f64(x), bits)
+            np.testing.assert_array_equal(codes[0], want)
+            scale = meta_by_block(got[0][2].view(np.float32), H)["v_scale" if i else "k_scale"]
+            np.testing.assert_array_equal(scale.transpose(0, 2, 1)[at], s)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("n", [40, 1000])     # a warp a vector; windows of 16 rows
+def test_rotary_write_as_the_append_of_the_rotated_rows(fmt, n):
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(2)
+    H, Hq, blocks = 3, 26, 64
+    assert n < 1000 or n * (Hq + 2 * H) >= 3 * 152 * 64
+    k, _ = bad_rows(rng, n, H)
+    v, _ = bad_rows(rng, n, H)
+    q = f32_to_bf16_bits(rng.standard_normal((n, Hq, 128)).astype(np.float32))
+    rope = RopeTable(2000)
+    pos = 1 + rng.integers(0, 1999, n)
+    cs = rope.table.cpu().numpy().astype(np.float64)[pos][:, None]
+    x = O.bf16_to_f64(k)
+    with np.errstate(all="ignore"):
+        y = np.concatenate([x[..., :64] * cs[..., 0] - x[..., 64:] * cs[..., 1],
+                            x[..., :64] * cs[..., 1] + x[..., 64:] * cs[..., 0]], -1).astype(np.float32)
+    y[np.isnan(y)] = np.nan
+    table = _i(rng.permutation(blocks)[None])
+    a, b = (KVCache(blocks, H, **FORMATS[fmt]) for _ in range(2))
+    out = torch.empty(n, Hq, 128, dtype=torch.bfloat16, device="cuda")
+    zero, slot = _i(np.zeros(n)), _i(np.arange(n))
+    _lib.kvq_rope_append(a.desc, rope.desc, _t(q), Hq, out, _t(k), _t(v), _i(pos), zero, slot, _lib.APPEND_QUANT, table, 1,
+                         blocks)
+    _lib.kvq_append(b.desc, _t(f32_to_bf16_bits(y)), _t(v), zero, slot, _lib.APPEND_QUANT, table, 1, blocks)
+    for p, r in zip(_pools(a), _pools(b)):
+        np.testing.assert_array_equal(p, r)
+    assert bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("rope", [False, True])
+def test_codes_stay_within_their_bounds_under_subnormal_scales(bits, rope):
+    """Keys over a large key factor: largest values of a few steps of 2^-149, whose scale is one step or 0."""
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache, RopeTable
+    rng = np.random.default_rng(3)
+    n, top = 32, TOP[bits]
+    steps = np.concatenate([[1, 2, 3, 10, 50, 63, 64, 90, 127, 128, 188, 190, 191, 200, 255], 1 + np.arange(17) * 14])[:n]
+    x = (rng.integers(-8, 9, (n, 1, 128)) * (steps[:, None, None] // 8)).astype(np.float64)
+    x[:, 0, 1], x[:, 0, 2], x[:, 0, 3] = steps, -steps, 0
+    k = f32_to_bf16_bits((x * 2.0 ** -49).astype(np.float32))
+    kq = O.bf16_to_f64(k) * 2.0 ** -100       # exact: multiples of 2^-149
+    np.testing.assert_array_equal(kq, x * 2.0 ** -149)
+    c = KVCache(2, 1, k_bits=bits, v_bits=bits, channel_factor=np.full((1, 128), 2.0 ** 100, np.float32))
+    table, seq, pos = _i([[0, 1]]), _i(np.zeros(n)), _i(np.arange(n))
+    if rope:      # position 0: cosine 1, sine 0
+        turns = RopeTable(1)
+        _lib.kvq_rope_append(c.desc, turns.desc, None, 0, None, _t(k), _t(k), seq, seq, pos, _lib.APPEND_QUANT,
+                             table, 1, 2)
+    else:
+        _lib.kvq_append(c.desc, _t(k), _t(k), seq, pos, _lib.APPEND_QUANT, table, 1, 2)
+    want, s = symmetric(kq.astype(np.float32), bits)
+    assert (s == 0).any() and (s == 2.0 ** -149).any() and (np.abs(kq) > top * s[..., None].astype(np.float64)).any()
+    codes = unpack_blocks(_pools(c)[0], bits, True, 1).transpose(0, 2, 1, 3).reshape(n, 1, 128)
+    np.testing.assert_array_equal(codes, want)
