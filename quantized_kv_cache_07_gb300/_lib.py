@@ -212,7 +212,8 @@ class _Args:
         return t.data_ptr()
 
     def rows(self, t, heads: int, n: int):
-        """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous."""
+        """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous and whose
+        rows do not overlap (an expanded row has stride 0, which the library takes for heads * 128)."""
         if t is None or isinstance(t, int):
             return t, 0
         shape, stride = t.shape, t.stride()
@@ -221,7 +222,7 @@ class _Args:
             ok = shape[0] == n and shape[1] == heads * 128 and (n == 0 or stride[1] == 1)
         elif ok:
             ok = shape == (n, heads, 128) and (n == 0 or stride[1:] == (128, 1))
-        if not ok:
+        if not ok or (n > 1 and stride[0] < heads * 128):
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
         return t.data_ptr(), stride[0] if n > 1 else 0
 

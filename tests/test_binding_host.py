@@ -1,0 +1,72 @@
+"""The binding's own checks, without a GPU: tensors on the CPU stand for the current device's, and a recorder for the
+library, so that what would be read or written out of range is seen to be refused before any call."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+class Recorder:
+    """Takes the library's place: every entry point notes its arguments and succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def entry(*args):
+            self.calls.append((name, args))
+            return 0
+        return entry
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    from quantized_kv_cache_07_gb300 import _lib
+    _lib._need_torch()
+    so = Recorder()
+    monkeypatch.setattr(_lib, "_current_device", lambda: -1)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(_lib, "load", lambda: so)
+    monkeypatch.setattr(_lib, "status_string", str)
+    monkeypatch.setattr(_lib, "recorder", so, raising=False)
+    return _lib
+
+
+def refused(lib, call, **kw):
+    """The call with these arguments is an invalid argument, and nothing reaches the library."""
+    before = len(lib.recorder.calls)
+    with pytest.raises(lib.KvqError) as e:
+        call(**kw)
+    assert e.value.status == lib.KVQ_ERR_INVALID_ARG
+    assert len(lib.recorder.calls) == before
+
+
+def _i(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def rope_call(lib, n=3, heads=2, **kw):
+    """kvq_rope_append of n rows into a cache of `heads` KV heads, with these arguments replaced."""
+    x = torch.zeros(n, heads, 128, dtype=torch.bfloat16)
+    i = torch.arange(n, dtype=torch.int32)
+    a = dict(q=x, q_heads=heads, q_out=torch.empty_like(x), k_new=x, v_new=x, pos=i, seq_idx=i * 0, slot=i,
+             mode=lib.APPEND_QUANT, block_table=_i(0, 1).view(1, 2), batch=1, max_blocks_per_seq=2)
+    a.update(kw)
+    lib.kvq_rope_append(lib.CacheDesc(num_kv_heads=heads), lib.RopeDesc(), **a)
+    return lib.recorder.calls[-1]
+
+
+def test_expanded_rows_are_refused(lib):
+    """A row stride of 0 stands for contiguous rows in the library: rows behind the one that exists would be read."""
+    name, args = rope_call(lib)
+    assert name == "kvq_rope_append"
+    one = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    flat = torch.zeros(1, 256, dtype=torch.bfloat16)
+    for arg in ("q", "k_new", "v_new"):
+        refused(lib, lambda **kw: rope_call(lib, **kw), **{arg: one.expand(3, 2, 128)})
+        refused(lib, lambda **kw: rope_call(lib, **kw), **{arg: flat.expand(3, 256)})
+    # rows that overlap in part
+    refused(lib, lambda **kw: rope_call(lib, **kw), k_new=torch.zeros(600, dtype=torch.bfloat16).as_strided((3, 256), (128, 1)))
+    # one row has no stride that matters; slices of a wider projection keep theirs
+    rope_call(lib, n=1, k_new=one.expand(1, 2, 128))
+    wide = torch.zeros(3, 700, dtype=torch.bfloat16)
+    assert rope_call(lib, k_new=wide[:, 256:512])[1][7] == 700
