@@ -211,6 +211,13 @@ class _Args:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
         return t.data_ptr()
 
+    def holds(self, t, dtype, count: int):
+        """The pointer of a contiguous tensor of `count` elements in any shape."""
+        at = self(t, dtype)
+        if t is not None and not isinstance(t, int) and t.numel() != count:
+            raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
+        return at
+
     def rows(self, t, heads: int, n: int):
         """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous and whose
         rows do not overlap (an expanded row has stride 0, which the library takes for heads * 128)."""
@@ -245,7 +252,7 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
     kp, ks = arg.rows(k_new, desc.num_kv_heads, n)
     vp, vs = arg.rows(v_new, desc.num_kv_heads, n)
     _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
-                                  arg(q_out, arg.bf16), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
+                                  arg.holds(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
                                   arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
                                   arg(block_table, arg.i32), batch, max_blocks_per_seq, _ptr(err_word),
                                   arg.stream(stream) if n else None), arg.where)

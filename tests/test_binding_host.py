@@ -70,3 +70,12 @@ def test_expanded_rows_are_refused(lib):
     rope_call(lib, n=1, k_new=one.expand(1, 2, 128))
     wide = torch.zeros(3, 700, dtype=torch.bfloat16)
     assert rope_call(lib, k_new=wide[:, 256:512])[1][7] == 700
+
+
+def test_the_rotated_queries_fill_their_output(lib):
+    """q_out is written whole: a tensor of other sizes is refused, one of the same elements in another shape is not."""
+    new = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16)
+    for out in (new(1, 2, 128), new(3, 1, 128), new(2, 2, 128), new(0), new(4, 2, 128)):
+        refused(lib, lambda **kw: rope_call(lib, **kw), q_out=out)
+    rope_call(lib, q_out=new(3, 256))
+    rope_call(lib, q=None, q_heads=0, q_out=None)
