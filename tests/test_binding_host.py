@@ -79,3 +79,15 @@ def test_the_rotated_queries_fill_their_output(lib):
         refused(lib, lambda **kw: rope_call(lib, **kw), q_out=out)
     rope_call(lib, q_out=new(3, 256))
     rope_call(lib, q=None, q_heads=0, q_out=None)
+
+
+def test_the_block_table_of_the_rotary_write_has_its_shape(lib):
+    """Rows and entries behind the table would be read by batch and max_blocks_per_seq."""
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    for kw in (dict(batch=3, max_blocks_per_seq=4), dict(batch=2, max_blocks_per_seq=5), dict(batch=4, max_blocks_per_seq=2)):
+        refused(lib, lambda **k: rope_call(lib, **k), block_table=table, **kw)
+    rope_call(lib, block_table=table, batch=2, max_blocks_per_seq=4)
+    # not read by the ring, nor for queries alone
+    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=1, mode=lib.APPEND_RING)
+    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=1, k_new=None, v_new=None, seq_idx=None)
+    rope_call(lib, block_table=None, batch=0, max_blocks_per_seq=0, k_new=None, v_new=None, seq_idx=None, slot=None)
