@@ -211,10 +211,10 @@ class _Args:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
         return t.data_ptr()
 
-    def holds(self, t, dtype, count: int):
-        """The pointer of a contiguous tensor of `count` elements in any shape."""
+    def room(self, t, dtype, count: int):
+        """The pointer of a contiguous tensor of any shape that holds `count` elements, or more."""
         at = self(t, dtype)
-        if t is not None and not isinstance(t, int) and t.numel() != count:
+        if t is not None and not isinstance(t, int) and t.numel() < count:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
         return at
 
@@ -251,11 +251,11 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
     qp, qs = arg.rows(q, q_heads, n)
     kp, ks = arg.rows(k_new, desc.num_kv_heads, n)
     vp, vs = arg.rows(v_new, desc.num_kv_heads, n)
-    places = (batch, max_blocks_per_seq) if k_new is not None and mode != APPEND_RING else None  # read by the write alone
+    places = batch * max_blocks_per_seq if k_new is not None and mode != APPEND_RING else 0  # read by the write alone
     _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
-                                  arg.holds(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
+                                  arg.room(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
                                   arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
-                                  arg(block_table, arg.i32, places), batch, max_blocks_per_seq, _ptr(err_word),
+                                  arg.room(block_table, arg.i32, places), batch, max_blocks_per_seq, _ptr(err_word),
                                   arg.stream(stream) if n else None), arg.where)
 
 

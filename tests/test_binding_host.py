@@ -72,22 +72,24 @@ def test_expanded_rows_are_refused(lib):
     assert rope_call(lib, k_new=wide[:, 256:512])[1][7] == 700
 
 
-def test_the_rotated_queries_fill_their_output(lib):
-    """q_out is written whole: a tensor of other sizes is refused, one of the same elements in another shape is not."""
+def test_the_rotated_queries_fit_their_output(lib):
+    """n rows of q_out are written: a smaller tensor is refused; more rows, or another shape, are not."""
     new = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16)
-    for out in (new(1, 2, 128), new(3, 1, 128), new(2, 2, 128), new(0), new(4, 2, 128)):
+    for out in (new(1, 2, 128), new(3, 1, 128), new(2, 2, 128), new(0)):
         refused(lib, lambda **kw: rope_call(lib, **kw), q_out=out)
-    rope_call(lib, q_out=new(3, 256))
+    for out in (new(3, 256), new(64, 2, 128)):
+        rope_call(lib, q_out=out)
     rope_call(lib, q=None, q_heads=0, q_out=None)
 
 
-def test_the_block_table_of_the_rotary_write_has_its_shape(lib):
-    """Rows and entries behind the table would be read by batch and max_blocks_per_seq."""
+def test_the_block_table_of_the_rotary_write_is_not_too_small(lib):
+    """Entries behind the table would be read by a larger batch or max_blocks_per_seq."""
     table = torch.zeros(2, 4, dtype=torch.int32)
-    for kw in (dict(batch=3, max_blocks_per_seq=4), dict(batch=2, max_blocks_per_seq=5), dict(batch=4, max_blocks_per_seq=2)):
+    for kw in (dict(batch=3, max_blocks_per_seq=4), dict(batch=2, max_blocks_per_seq=5), dict(batch=9, max_blocks_per_seq=1)):
         refused(lib, lambda **k: rope_call(lib, **k), block_table=table, **kw)
-    rope_call(lib, block_table=table, batch=2, max_blocks_per_seq=4)
+    for t in (table, table.flatten(), torch.zeros(50, 4, dtype=torch.int32)):
+        rope_call(lib, block_table=t, batch=2, max_blocks_per_seq=4)
     # not read by the ring, nor for queries alone
-    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=1, mode=lib.APPEND_RING)
-    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=1, k_new=None, v_new=None, seq_idx=None)
+    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=4, mode=lib.APPEND_RING)
+    rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=4, k_new=None, v_new=None, seq_idx=None)
     rope_call(lib, block_table=None, batch=0, max_blocks_per_seq=0, k_new=None, v_new=None, seq_idx=None, slot=None)
