@@ -278,7 +278,8 @@ def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, bl
                                     max_blocks_per_seq, num_groups, arg(group_start, arg.i32, (num_groups + 1,)),
                                     arg(prefix_blocks, arg.i32, (num_groups,)),
                                     arg(out, arg.f32 if out_fp32 else arg.bf16, rows), int(bool(out_fp32)),
-                                    arg(lse, arg.f32, (batch, q_heads)), arg(workspace, arg.u8), workspace_bytes,
+                                    arg(lse, arg.f32, (batch, q_heads)),
+                                    arg.room(workspace, arg.u8, workspace_bytes), workspace_bytes,
                                     _ptr(err_word), arg.stream(stream)), arg.where)
 
 

@@ -93,3 +93,22 @@ def test_the_block_table_of_the_rotary_write_is_not_too_small(lib):
     rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=4, mode=lib.APPEND_RING)
     rope_call(lib, block_table=table, batch=3, max_blocks_per_seq=4, k_new=None, v_new=None, seq_idx=None)
     rope_call(lib, block_table=None, batch=0, max_blocks_per_seq=0, k_new=None, v_new=None, seq_idx=None, slot=None)
+
+
+def shared_call(lib, batch=2, **kw):
+    """kvq_decode_shared of a batch with 4 query heads, with these arguments replaced."""
+    a = dict(q=torch.zeros(batch, 4, 128, dtype=torch.bfloat16), batch=batch, q_heads=4,
+             seq_lens=torch.zeros(batch, dtype=torch.int32), block_table=torch.zeros(batch, 3, dtype=torch.int32),
+             max_blocks_per_seq=3, num_groups=1, group_start=_i(0, batch), prefix_blocks=_i(1),
+             out=torch.empty(batch, 4, 128, dtype=torch.bfloat16), workspace=torch.empty(512, dtype=torch.uint8),
+             workspace_bytes=512)
+    a.update(kw)
+    lib.kvq_decode_shared(lib.CacheDesc(), **a)
+    return lib.recorder.calls[-1]
+
+
+def test_a_workspace_holds_the_bytes_that_are_named(lib):
+    """The library goes by workspace_bytes: a smaller tensor would be written behind its end."""
+    refused(lib, lambda **kw: shared_call(lib, **kw), workspace_bytes=513)
+    refused(lib, lambda **kw: shared_call(lib, **kw), workspace=torch.empty(100, dtype=torch.uint8))
+    assert shared_call(lib, workspace_bytes=500)[1][14] == 500
