@@ -236,8 +236,8 @@ class _Args:
 
 def kvq_rope_table(freqs: RopeFreqs, rotary_dim: int, max_pos: int, table, stream=None):
     arg = _Args("kvq_rope_table")
-    _check(load().kvq_rope_table(ctypes.byref(freqs), rotary_dim, max_pos, arg(table, arg.f32), _stream(stream)),
-           "kvq_rope_table")
+    _check(load().kvq_rope_table(ctypes.byref(freqs), rotary_dim, max_pos,
+                                 arg.room(table, arg.f32, max_pos * rotary_dim), arg.stream(stream)), arg.where)
 
 
 def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_new, v_new, pos, seq_idx, slot,

@@ -112,3 +112,12 @@ def test_a_workspace_holds_the_bytes_that_are_named(lib):
     refused(lib, lambda **kw: shared_call(lib, **kw), workspace_bytes=513)
     refused(lib, lambda **kw: shared_call(lib, **kw), workspace=torch.empty(100, dtype=torch.uint8))
     assert shared_call(lib, workspace_bytes=500)[1][14] == 500
+
+
+def test_a_rotary_table_holds_its_positions(lib):
+    """max_pos rows of rotary_dim / 2 pairs are written."""
+    call = lambda **kw: lib.kvq_rope_table(lib.RopeFreqs(), **kw)
+    for shape in ((7, 64, 2), (8, 63, 2), (8, 64)):
+        refused(lib, call, rotary_dim=128, max_pos=8, table=torch.empty(shape))
+    call(rotary_dim=128, max_pos=8, table=torch.empty(8, 64, 2))
+    call(rotary_dim=64, max_pos=8, table=torch.empty(600))
