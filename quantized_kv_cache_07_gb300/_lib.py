@@ -218,6 +218,12 @@ class _Args:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
         return at
 
+    def word(self, t):
+        """The pointer of an error word: 4 bytes or more of the device."""
+        if t is not None and not isinstance(t, int) and (t.get_device() != self.device or t.nbytes < 4):
+            raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
+        return _ptr(t)
+
     def rows(self, t, heads: int, n: int):
         """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous and whose
         rows do not overlap (an expanded row has stride 0, which the library takes for heads * 128)."""
@@ -255,7 +261,7 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
     _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
                                   arg.room(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
                                   arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
-                                  arg.room(block_table, arg.i32, places), batch, max_blocks_per_seq, _ptr(err_word),
+                                  arg.room(block_table, arg.i32, places), batch, max_blocks_per_seq, arg.word(err_word),
                                   arg.stream(stream) if n else None), arg.where)
 
 
@@ -280,7 +286,7 @@ def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, bl
                                     arg(out, arg.f32 if out_fp32 else arg.bf16, rows), int(bool(out_fp32)),
                                     arg(lse, arg.f32, (batch, q_heads)),
                                     arg.room(workspace, arg.u8, workspace_bytes), workspace_bytes,
-                                    _ptr(err_word), arg.stream(stream)), arg.where)
+                                    arg.word(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,
@@ -293,7 +299,7 @@ def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, b
                                 arg(lse, arg.f32, (batch, q_heads)), arg(seq_lens, arg.i32, (batch,)),
                                 arg(block_table, arg.i32, (batch, max_blocks_per_seq)), max_blocks_per_seq,
                                 arg(mass, arg.f32, (batch, desc.num_kv_heads, mass_stride)), mass_stride, decay,
-                                _ptr(err_word), arg.stream(stream)), arg.where)
+                                arg.word(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batch: int, max_blocks_per_seq: int,
@@ -309,7 +315,7 @@ def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batc
                             arg(token_pos, arg.i32, rows), arg(token_pos_out, arg.i32, rows),
                             arg(next_pos, arg.i32, each), arg(block_table, arg.i32, (batch, max_blocks_per_seq)), batch,
                             max_blocks_per_seq, arg(new_lens, arg.i32, each), arg(source, arg.i32, rows),
-                            _ptr(err_word), arg.stream(stream)), arg.where)
+                            arg.word(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,

@@ -121,3 +121,35 @@ def test_a_rotary_table_holds_its_positions(lib):
         refused(lib, call, rotary_dim=128, max_pos=8, table=torch.empty(shape))
     call(rotary_dim=128, max_pos=8, table=torch.empty(8, 64, 2))
     call(rotary_dim=64, max_pos=8, table=torch.empty(600))
+
+
+def mass_call(lib, **kw):
+    """kvq_attn_mass of two sequences, with these arguments replaced."""
+    i = torch.zeros(2, dtype=torch.int32)
+    a = dict(q=torch.zeros(2, 4, 128, dtype=torch.bfloat16), batch=2, q_heads=4, lse=torch.zeros(2, 4), seq_lens=i,
+             block_table=torch.zeros(2, 3, dtype=torch.int32), max_blocks_per_seq=3, mass=torch.zeros(2, 1, 48))
+    a.update(kw)
+    lib.kvq_attn_mass(lib.CacheDesc(num_kv_heads=1), **a)
+
+
+def evict_call(lib, **kw):
+    """kvq_evict of two sequences, with these arguments replaced."""
+    i, rows = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 1, 48, dtype=torch.int32)
+    a = dict(mass=torch.zeros(2, 1, 48), mass_out=None, seq_lens=i, keep=i, block_table=torch.zeros(2, 3, dtype=torch.int32),
+             batch=2, max_blocks_per_seq=3, source=rows, new_lens=i.clone())
+    a.update(kw)
+    lib.kvq_evict(lib.CacheDesc(num_kv_heads=1), **a)
+
+
+@pytest.mark.parametrize("call", [rope_call, shared_call, mass_call, evict_call])
+def test_the_error_word_is_on_the_device(lib, call):
+    """Kernels write it: a word of another device, or a tensor without one, is refused."""
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    word = torch.zeros(1, dtype=torch.int32)
+    refused(lib, lambda **kw: call(lib, **kw), err_word=word.as_subclass(Elsewhere))
+    refused(lib, lambda **kw: call(lib, **kw), err_word=word[:0])
+    for w in (None, word, 0x1000, torch.zeros(4, dtype=torch.uint8), torch.zeros((), dtype=torch.int64)):
+        call(lib, err_word=w)
