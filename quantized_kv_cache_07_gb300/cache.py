@@ -107,6 +107,7 @@ class RopeTable:
         _lib.kvq_rope_table(freqs, rotary_dim, max_pos, self.table)
         self.desc = _lib.RopeDesc(rotary_dim=rotary_dim, interleaved=int(interleaved), max_pos=max_pos,
                                   table=self.table.data_ptr())
+        self.desc.held = self.table  # a descriptor kept without its RopeTable still points at live memory
 
 
 class DecodeWorkspace:

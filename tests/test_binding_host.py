@@ -153,3 +153,17 @@ def test_the_error_word_is_on_the_device(lib, call):
     refused(lib, lambda **kw: call(lib, **kw), err_word=word[:0])
     for w in (None, word, 0x1000, torch.zeros(4, dtype=torch.uint8), torch.zeros((), dtype=torch.int64)):
         call(lib, err_word=w)
+
+
+def test_a_rotary_descriptor_keeps_its_table(lib, monkeypatch):
+    """The descriptor holds a raw pointer: taken from a RopeTable that nothing else refers to, it must not dangle."""
+    import gc
+    import weakref
+
+    from quantized_kv_cache_07_gb300 import cache
+    monkeypatch.setattr(cache, "_require_cuda", lambda: None)
+    turns = cache.RopeTable(16, device="cpu")
+    desc, table = turns.desc, weakref.ref(turns.table)
+    del turns
+    gc.collect()
+    assert table() is not None and table().data_ptr() == desc.table
