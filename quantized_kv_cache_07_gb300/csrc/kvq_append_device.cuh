@@ -119,7 +119,7 @@ __device__ void store_bf16(bool is_key, uint8_t* blk, int tok, const uint16_t (&
 __device__ void write_block_store(const AppendArgs& a, bool is_key, int b, int p, int h, const uint16_t (&xb)[4],
                                   int lane) {
   const CacheView& c = a.c;
-  if (p >= a.mbps * kBlock) {
+  if (p / kBlock >= a.mbps) {  // (in blocks: neither side passes 32 bits)
     if (lane == 0) flag(a.err, KVQ_DEVERR_POSITION);
     return;
   }
@@ -237,7 +237,7 @@ __device__ __forceinline__ void append_group(const AppendArgs& a, int r, bool is
   }
   int m = 1;
   while (m < kBlock && r + m < a.n && a.seq_idx[r + m] == b && a.pos[r + m] == p + m && ok(r + m)) ++m;
-  if (p + m > a.mbps * kBlock) {
+  if (p / kBlock >= a.mbps) {  // p is a block's first position
     if (lane == 0) flag(a.err, KVQ_DEVERR_POSITION);
     return;
   }

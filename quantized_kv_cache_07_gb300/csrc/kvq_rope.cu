@@ -256,7 +256,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
 #pragma unroll
   for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint2*>(src + token(0, k) * stride);
   const int b = sm->seq[r - blockIdx.x * kRows + kRows - 1], p = sm->pos[r - blockIdx.x * kRows + kRows - 1];
-  if (p + kBlock > a.ap.mbps * kBlock) {
+  if (p / kBlock >= a.ap.mbps) {
     if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
     return;
   }
