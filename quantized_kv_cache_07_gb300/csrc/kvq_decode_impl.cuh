@@ -1053,7 +1053,7 @@ __device__ __forceinline__ bool finish_segment(const DecodeArgs& a, WarpState& s
 template <typename LoadLen>
 __device__ __forceinline__ bool scan_geometry(const DecodeArgs& a, int B, int W, int X, int* len_s, int* pre_s,
                                               int* vpre_s, LoadLen load, int tid, int warp, int lane) {
-  const int cap = a.mbps * kBlock;
+  const int cap = table_tokens(a.mbps, 0);
   int bad = 0;
   for (int b = tid; b < B; b += kThreads) {
     int L = load(b);

@@ -21,6 +21,13 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;
 
 __host__ __device__ constexpr int block_bytes(int bits) { return kBlock * kHeadDim * bits / 8; }
 
+// Tokens that a row of a block table (and a bf16 window behind it) can hold: 16 an entry, as far as a
+// position, a window more and the rounding up to whole blocks stay within 32 bits.
+__host__ __device__ __forceinline__ int table_tokens(int entries, int window) {
+  const long long most = (1ll << 31) - 256, n = (long long)entries * kBlock + window;
+  return int(n < most ? n : most);
+}
+
 // ------------------------------------------------------------------ layout
 // Byte offset (and nibble shift for 4-bit codes) of key element (token i, dim d)
 // inside one 16-token block of one head.

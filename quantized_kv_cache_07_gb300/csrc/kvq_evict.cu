@@ -48,12 +48,12 @@ struct EvictLen {
 __device__ __forceinline__ EvictLen evict_len(const EvictArgs& a, int b, bool& bad) {
   EvictLen e;
   const int W = a.c.window;
-  const long long room = min((long long)a.mbps * kBlock + W, (long long)a.stride);
+  const int room = min(table_tokens(a.mbps, W), a.stride);
   e.L = a.seq_lens[b];
   int keep = a.keep[b];
   if (e.L < 0 || e.L > room || keep < 0) {
     bad = true;
-    e.L = e.L < 0 ? 0 : int(min((long long)e.L, room));
+    e.L = e.L < 0 ? 0 : min(e.L, room);
     keep = max(keep, 0);
   }
   e.Lq = max(e.L - W, 0);

@@ -209,10 +209,10 @@ struct MassQuery {
 __device__ __forceinline__ int mass_len(const MassArgs& a, int b, bool& bad) {
   int L = a.seq_lens[b];
   const int W = a.c.window;
-  const long long room = min((long long)a.mbps * kBlock + W, (long long)a.stride);
+  const int room = min(table_tokens(a.mbps, W), a.stride);
   if (L < 0 || L > room) {
     bad = true;
-    L = L < 0 ? 0 : int(room);
+    L = L < 0 ? 0 : room;
   }
   return L;
 }

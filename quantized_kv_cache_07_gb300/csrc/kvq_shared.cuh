@@ -33,7 +33,7 @@ __device__ __forceinline__ unsigned load_groups(GroupGeo* geo, const int* start,
   for (int i = tid; i < n; i += threads) {
     const int p = __ldcg(blocks + i);
     if (p < 0 || p > mbps) bad |= KVQ_DEVERR_SEQ_LEN;
-    geo->blocks[i] = min(max(p, 0), mbps);
+    geo->blocks[i] = min(max(p, 0), table_tokens(mbps, 0) / kBlock);  // behind it lies no token
   }
   if (tid < 32) {
     int top = 0;
@@ -158,8 +158,7 @@ __device__ __forceinline__ void wait_for_suffix() { asm volatile("griddepcontrol
 
 // Tokens of the prefix that sequence b attends to.
 __device__ __forceinline__ int prefix_len(const DecodeArgs& a, int b, int blocks) {
-  const int cap = a.mbps * kBlock + a.c.window;
-  const int L = min(max(__ldcg(a.seq_lens + b), 0), cap);
+  const int L = min(max(__ldcg(a.seq_lens + b), 0), table_tokens(a.mbps, a.c.window));
   return min(max(L - a.c.window, 0), blocks * kBlock);
 }
 

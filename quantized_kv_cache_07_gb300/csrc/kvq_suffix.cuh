@@ -58,7 +58,7 @@ struct SufLen {
   int skip, tokens, ring;
 };
 __device__ __forceinline__ SufLen suffix_len(const DecodeArgs& a, const GroupGeo* groups, int b, int L, bool& bad) {
-  const int W = a.c.window, cap = a.mbps * kBlock + W;
+  const int W = a.c.window, cap = table_tokens(a.mbps, W);
   if (L < 0 || L > cap) {
     bad = true;
     L = min(max(L, 0), cap);

@@ -82,3 +82,53 @@ def test_rows_of_a_table_that_covers_every_position(fmt, how, n):
         got.append(_pools(c))
     for a, b in zip(*got):
         assert torch.equal(a, b) and a.any()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(window=32), dict(k_bits=16, v_bits=16, q_heads=14)])
+@pytest.mark.parametrize("batch", [2, 9])     # shared prefixes on 16-vector tiles; on tcgen05 (not bf16)
+def test_attention_over_a_table_that_covers_every_position(kw, batch):
+    """The same results from tables of 2^27 + 1 entries a row as from short ones, in every call that reads a table."""
+    from harness import DeviceRun, small_workload
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import DecodeWorkspace, SharedWorkspace
+    from synth import make_inputs
+    w = small_workload("wide_table", **dict(dict(batch=batch, q_heads=16, kv_heads=2, len_range=(100, 160)), **kw))
+    inp = make_inputs(w)
+    inp.block_table[:, :4] = inp.block_table[0, :4]
+    run = DeviceRun(inp)
+    Hq, H, W = w.q_heads, w.kv_heads, w.window
+    wide = torch.full((batch, 2 ** 27 + 1), -1, dtype=torch.int32, device="cuda")
+    wide[:, :inp.max_blocks] = run.table
+    got = []
+    for table in (run.table, wide):
+        mbps, err = table.shape[1], _i([0])
+        new = lambda *shape, t=torch.float32: torch.zeros(*shape, dtype=t, device="cuda")
+        res = [new(batch, Hq, 128), new(batch, Hq), new(batch, Hq, 128), new(batch, Hq), new(batch, H, 160)]
+        ws, sw = DecodeWorkspace(run.cache, batch, Hq), SharedWorkspace(run.cache, batch, Hq, 1)
+        _lib.kvq_decode(run.cache.desc, run.q, batch, Hq, run.lens, table, mbps, res[0], lse=res[1], workspace=ws.buf,
+                        workspace_bytes=ws.nbytes, err_word=err)
+        _lib.kvq_decode_shared(run.cache.desc, run.q, batch, Hq, run.lens, table, mbps, 1, _i([0, batch]), _i([4]), res[2],
+                               lse=res[3], workspace=sw.buf, workspace_bytes=sw.nbytes, err_word=err)
+        _lib.kvq_attn_mass(run.cache.desc, run.q, batch, Hq, res[1], run.lens, table, mbps, res[4], err_word=err)
+        source, lens = new(batch, H, 160, t=torch.int32), new(batch, t=torch.int32)
+        if not W:
+            seq, pos = torch.arange(batch, device="cuda").int(), run.lens - 1
+            for ctas in (5, -1) if w.k_bits != 16 else (5,):
+                out = new(batch, Hq, 128)
+                nb = _lib.kvq_prefill_workspace_size(run.cache.desc, batch, Hq, ctas)
+                pw = new(max(nb, 16), t=torch.uint8)
+                _lib.kvq_prefill(run.cache.desc, run.q, Hq, seq, pos, table, batch, mbps, out, workspace=pw,
+                                 workspace_bytes=nb, stream_ctas=ctas, err_word=err)
+                res.append(out)
+        pools = [t for t in (run.cache.k_codes, run.cache.v_codes, run.cache.meta) if t is not None]
+        before = [t.clone() for t in pools]
+        _lib.kvq_evict(run.cache.desc, res[4], None, run.lens, run.lens - 64, table, batch, mbps, source, lens,
+                       protect_first=64, err_word=err)
+        res += [source] + [t.clone() for t in pools] + [lens]
+        for t, old in zip(pools, before):      # the eviction's moves back
+            t.copy_(old)
+        assert int(err) == 0
+        got.append(res)
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool((got[0][-1] < run.lens).all())
