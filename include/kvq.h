@@ -406,7 +406,9 @@ kvq_status kvq_decode_ex(const kvq_cache_desc* cache, const void* q, int32_t bat
  * Everything else as kvq_decode, every cache format and query mode, the bf16
  * window (which holds each sequence's own last tokens) included.  Under a key factor
  * the query times the factor is carried in two fp16 parts (as with q_bits 32), so that
- * lse holds float32's precision.
+ * lse holds float32's precision.  A prefix token with values that are not finite, or far out
+ * of the others' range, changes the outputs of the sequences that attend to it and of no
+ * others; in a bf16 cache one that is not finite may reach every sequence of its group.
  */
 kvq_status kvq_decode_shared(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
                              const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
       if (blk < nblk) {
         const uint8_t* stg = smem + s * T::kStageBytes;
         const float* meta = reinterpret_cast<const float*>(stg + T::kOffMeta + warp * F::kMB);
-        tile_block<KB, VB, ASYM, LOQ>(stg + T::kOffK + warp * F::kKBB, stg + T::kOffV + warp * F::kVBB,
+        tile_block<KB, VB, ASYM, LOQ, true>(stg + T::kOffK + warp * F::kKBB, stg + T::kOffV + warp * F::kVBB,
                                       meta + F::kKS, meta + F::kVS, ASYM ? meta + F::kKO : nullptr,
                                       ASYM ? meta + F::kVO : nullptr, blk * kBlock, maxlen, len0, len1, qs0, qs1, qz0,
                                       qz1, reinterpret_cast<const uint4*>(qf), reinterpret_cast<const uint4*>(qlo),
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kThreads, 3) shared_tile_kernel(const SharedAr
     }
     if (!sync()) return;  // every warp has read its last block
     if (t == 0) {
-      cm[warp * kTileQ + g] = st.m0 == kNegInf ? kNegInf : st.m0 - st.sg;
-      cm[warp * kTileQ + g + 8] = st.m1 == kNegInf ? kNegInf : st.m1 - st.sg;
+      cm[warp * kTileQ + g] = st.m0 == kNegInf ? kNegInf : st.m0 - st.sg0;
+      cm[warp * kTileQ + g + 8] = st.m1 == kNegInf ? kNegInf : st.m1 - st.sg1;
       cl[warp * kTileQ + g] = st.l0;
       cl[warp * kTileQ + g + 8] = st.l1;
     }

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kTileQ = 16;       // query vectors per tile: one m16 row tile
 constexpr int kOStride = 132;    // float row stride of the combine buffer (bank spread)
+constexpr float kFloatMax = 3.4028234663852886e38f;
 constexpr int kCombineBytes = kConsumerWarps * kTileQ * kOStride * 4;
 
 template <int KB, int VB, bool ASYM>
@@ -100,12 +101,13 @@ struct TileState {
   float O[16][4];
   float m0, m1, l0, l1;
   float z0, z1;     // asymmetric values: sum of p * m'_v of this thread's tokens per row
-  float sg, svlim;  // sigma and the largest value scale it allows (as in decode)
+  float sg0, sg1;   // sigma of each row (as in decode), by the value scales that the row sees (one chunk: sg0 for both),
+  float svlim;      // and the largest value scale that both allow
   __device__ __forceinline__ void reset() {
     m0 = m1 = kNegInf;
     l0 = l1 = 0.f;
     z0 = z1 = 0.f;
-    sg = float(kSigma0);
+    sg0 = sg1 = float(kSigma0);
     svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
 #pragma unroll
     for (int i = 0; i < 16; ++i) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
@@ -288,7 +290,11 @@ __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&
 
 // One block of one consumer warp: scores, causal mask, online softmax with the
 // lazy maximum and the sigma offset of the decode kernel, value product.
-template <int KB, int VB, bool ASYM, bool LOQ>
+// APART: the rows are those of different sequences, and a value scale that is out of the others' range, or not
+// finite, counts in the rows that see its token alone; otherwise (rows of one chunk) one sigma serves both
+// rows (separate ones cost the chunked prefill 1.7 %: 201.0 us for 197.6; the shared prefix of 4 sequences of 2048
+// tokens 1 %).
+template <int KB, int VB, bool ASYM, bool LOQ, bool APART>
 __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb, const float* ks, const float* vs,
                                            const float* ko, const float* vo, int tok0, int maxlen, int len0,
                                            int len1, float qs0, float qs1, float qz0, float qz1, const uint4* qf,
@@ -342,7 +348,7 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
       }
       // scales of slots past the sub-pass's longest row are not data
       vsc[n][j] = pos < maxlen ? vsc[n][j] : 0.f;
-      svm = fmaxf(svm, vsc[n][j]);
+      svm = APART ? max_nan(svm, vsc[n][j]) : fmaxf(svm, vsc[n][j]);
     }
   float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
   float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
@@ -369,29 +375,66 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
     st.m0 = mn0;
     st.m1 = mn1;
   }
-  if (__any_sync(kFull, svm > st.svlim)) {
+  if (__any_sync(kFull, APART ? !(svm <= st.svlim) : svm > st.svlim)) {
+    int sn0, sn1;
+    float q0 = 1.f, q1 = 1.f;  // not a number for a row whose outputs are none
+    if constexpr (APART) {
+      // Each row by the scales that it sees: a token of one sequence leaves the others alone.  One whose scale is not
+      // finite makes the outputs of the rows that see it no number, and then counts as 0 (a hidden one would be 0 x inf).
+      float s0 = 0.f, s1 = 0.f;
+      bool bad0 = false, bad1 = false;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) svm = fmaxf(svm, __shfl_xor_sync(kFull, svm, o));
-    int ex;
-    frexpf(svm, &ex);  // svm < 2^ex
-    const int sg_new = min(int(st.sg), kWeightExp - int(kMaxSlack) - ex);
-    const float f = ldexpf(1.f, sg_new - int(st.sg));  // exact power of two
-    st.l0 *= f;
-    st.l1 *= f;
-    st.z0 *= f;
-    st.z1 *= f;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int pos = tok0 + 8 * n + 2 * t + j;
+          const bool in0 = pos < len0, in1 = pos < len1;
+          if (!(vsc[n][j] <= kFloatMax)) {
+            bad0 |= in0;
+            bad1 |= in1;
+            vsc[n][j] = mv[n][j] = 0.f;
+          }
+          s0 = in0 ? fmaxf(s0, vsc[n][j]) : s0;
+          s1 = in1 ? fmaxf(s1, vsc[n][j]) : s1;
+        }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        s0 = fmaxf(s0, __shfl_xor_sync(kFull, s0, o));
+        s1 = fmaxf(s1, __shfl_xor_sync(kFull, s1, o));
+      }
+      const unsigned row = 0xFu << (lane & ~3);  // the four lanes of the rows
+      q0 = __ballot_sync(kFull, bad0) & row ? __int_as_float(0x7fffffff) : 1.f;
+      q1 = __ballot_sync(kFull, bad1) & row ? __int_as_float(0x7fffffff) : 1.f;
+      int e0, e1;
+      frexpf(s0, &e0);  // s0 < 2^e0
+      frexpf(s1, &e1);
+      sn0 = s0 > 0.f ? min(int(st.sg0), kWeightExp - int(kMaxSlack) - e0) : int(st.sg0);
+      sn1 = s1 > 0.f ? min(int(st.sg1), kWeightExp - int(kMaxSlack) - e1) : int(st.sg1);
+    } else {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) svm = fmaxf(svm, __shfl_xor_sync(kFull, svm, o));
+      int ex;
+      frexpf(svm, &ex);  // svm < 2^ex
+      sn0 = sn1 = min(int(st.sg0), kWeightExp - int(kMaxSlack) - ex);
+    }
+    const float f0 = ldexpf(1.f, sn0 - int(st.sg0)), f1 = APART ? ldexpf(1.f, sn1 - int(st.sg1)) : f0;  // exact powers of two
+    st.l0 *= f0;
+    st.l1 *= f1;
+    st.z0 *= f0;
+    st.z1 *= f1;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      st.O[i][0] *= f;
-      st.O[i][1] *= f;
-      st.O[i][2] *= f;
-      st.O[i][3] *= f;
+      st.O[i][0] *= APART ? f0 * q0 : f0;
+      st.O[i][1] *= APART ? f0 * q0 : f0;
+      st.O[i][2] *= APART ? f1 * q1 : f1;
+      st.O[i][3] *= APART ? f1 * q1 : f1;
     }
-    st.sg = float(sg_new);
-    st.svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - sg_new);
+    st.sg0 = float(sn0);
+    st.sg1 = float(sn1);
+    st.svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - max(sn0, sn1));
   }
-  const float base0 = (st.m0 == kNegInf) ? 0.f : st.m0 - st.sg;
-  const float base1 = (st.m1 == kNegInf) ? 0.f : st.m1 - st.sg;
+  const float base0 = (st.m0 == kNegInf) ? 0.f : st.m0 - st.sg0;
+  const float base1 = (st.m1 == kNegInf) ? 0.f : st.m1 - (APART ? st.sg1 : st.sg0);
   float w[2][4];
 #pragma unroll
   for (int n = 0; n < 2; ++n)

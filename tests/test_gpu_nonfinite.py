@@ -144,3 +144,59 @@ def test_codes_stay_within_their_bounds_under_subnormal_scales(bits, rope):
     assert (s == 0).any() and (s == 2.0 ** -149).any() and (np.abs(kq) > top * s[..., None].astype(np.float64)).any()
     codes = unpack_blocks(_pools(c)[0], bits, True, 1).transpose(0, 2, 1, 3).reshape(n, 1, 128)
     np.testing.assert_array_equal(codes, want)
+
+
+SHARED = {
+    # query vectors of a group: few (16-vector tiles), many (tcgen05, one and two warpgroups' worth)
+    "tiles_int8": dict(batch=6), "tiles_asym_int4_factor": dict(batch=6, k_bits=4, v_bits=4, asym=True, channel_factor=True),
+    "tiles_int2": dict(batch=6, k_bits=2, v_bits=2), "tiles_q32_int8": dict(batch=20, q_bits=32, q_heads=16),
+    "int8": dict(batch=20), "k8v4": dict(batch=40, v_bits=4, q_heads=16), "asym_k4v8": dict(batch=20, k_bits=4, asym=True),
+    "asym_int8": dict(batch=40, q_heads=16, asym=True), "int4_factor": dict(batch=20, k_bits=4, v_bits=4, channel_factor=True),
+    "asym_int4_factor": dict(batch=20, k_bits=4, v_bits=4, asym=True, channel_factor=True),
+    "asym_int2": dict(batch=20, k_bits=2, v_bits=2, asym=True),
+}
+
+
+@pytest.mark.parametrize("fmt", list(SHARED))
+@pytest.mark.parametrize("bad", ["inf", "-inf", "nan", "1e36"])
+def test_a_prefix_token_reaches_only_the_sequences_that_hold_it(fmt, bad):
+    """Token 150 of a shared prefix of 208 has a value that is not finite, or far out of the others' range: sequences that
+    end before it are as kvq_decode has them; for those that hold it the log-sum-exp and what is not finite are."""
+    from harness import DeviceRun, small_workload
+    from test_gpu_shared import decode_shared, shared_inputs
+    w = small_workload("shared_masked", **dict(dict(len_range=(300, 420), paged=True), **SHARED[fmt]))
+    groups = [(0, w.batch, 13)]
+    inp = shared_inputs(w, groups)
+    lead = int(np.argmax(inp.lengths))
+    value = np.array([float(bad)], np.float32)
+    for b in range(w.batch):
+        at = inp.seq_offsets[b] + 150
+        if bad == "nan":       # every dim: no number is left to give a scale
+            inp.v[at] = f32_to_bf16_bits(value)[0]
+        else:
+            inp.v[at, :, 77] = f32_to_bf16_bits(value)[0]
+    assert inp.lengths[lead] > 208
+    run = DeviceRun(inp)
+    lens = np.array(inp.lengths)
+    before = np.arange(w.batch) % 3 != 1
+    lens[before] = np.resize([149, 150, 37, 1, 144, 100, 64, 129], int(before.sum()))
+    if w.k_bits == 2:          # the token's block has one scale: only what lies before the block is apart from it
+        lens[before] = np.minimum(lens[before], 144)
+    lens_t = torch.from_numpy(lens.astype(np.int32)).cuda()
+    ref, ref_lse = run.decode(lens=lens_t)
+    out, lse = decode_shared(run, groups, lens=lens_t)
+    assert np.isfinite(ref[before]).all() and run.err_bits() == 0
+    np.testing.assert_allclose(out[before], ref[before], rtol=0, atol=2e-3)
+    np.testing.assert_allclose(lse, ref_lse, rtol=0, atol=2e-3)
+    out, ref = out[~before], ref[~before]
+    np.testing.assert_array_equal(np.isfinite(out), np.isfinite(ref))
+    if bad == "1e36":
+        # the token's weight times its value scale decides: one fp16 rounding (2^-11) in each call; under a key factor
+        # kvq_decode's query is one fp16 part, and its score off by 2^-11 of the products' sum, below 12 here
+        tol = 2.0 ** -10 + (12 * 2.0 ** -11 if w.channel_factor else 0.0)
+        # an asymmetric 2-bit group's 16 tokens all have the scale s = 10^36 / 3, and code 0 as 2 s from the middle code's
+        # value: 2^-11 of each weight times 2 s, the weights' sum below 1, in each call
+        atol = 2.0 ** -10 * 2 / 3 * 1e36 if w.k_bits == 2 and w.asym else 0.0
+        assert np.all(np.abs(out - ref) <= tol * np.abs(ref).max(-1, keepdims=True) + atol)
+    elif not (w.k_bits == 2 and bad == "nan"):      # a 2-bit group's scale comes from its numbers
+        assert not np.isfinite(ref).any()
