@@ -314,6 +314,24 @@ __device__ __forceinline__ void value_block(const uint8_t* vb, uint32_t b0, uint
   }
 }
 
+// A bf16 block whose first `valid` tokens are data: what the other slots hold (0 times it may be no number) is
+// not read as values.  Lane t's words are tokens (2t, 2t + 8) and (2t + 1, 2t + 9).
+__device__ __forceinline__ uint32_t bf16_data(int lane, int odd, int valid) {
+  const int i = 2 * (lane & 3) + odd;
+  return (i < valid ? 0xFFFFu : 0u) | (i + 8 < valid ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ void value_block_part(const uint8_t* vb, int valid, uint32_t b0, uint32_t b1, uint32_t b0lo,
+                                                 uint32_t b1lo, float (&O)[8][4], int lane) {
+  const uint4* p = reinterpret_cast<const uint4*>(vb) + lane;
+  const uint32_t even = bf16_data(lane, 0, valid), odd = bf16_data(lane, 1, valid);
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    const uint4 r = p[mt * 32], c = make_uint4(r.x & even, r.y & odd, r.z & even, r.w & odd);
+    mma_bf16(O[mt], c.x, c.z, c.y, c.w, b0, b1);
+    mma_bf16(O[mt], c.x, c.z, c.y, c.w, b0lo, b1lo);
+  }
+}
+
 struct Params {
   DecodeArgs a;
   int P;   // stream CTAs launched (after the window CTAs)
@@ -636,7 +654,8 @@ __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], c
       b0lo = (g & 1) ? q01 : q00;
       b1lo = (g & 1) ? q11 : q10;
     }
-    value_block<VB, kBf16 || LOQ>(vb[j], b0, b1, b0lo, b1lo, st.O, lane, km);
+    if (kBf16 && valid[j] < kBlock) value_block_part(vb[j], valid[j], b0, b1, b0lo, b1lo, st.O, lane);
+    else value_block<VB, kBf16 || LOQ>(vb[j], b0, b1, b0lo, b1lo, st.O, lane, km);
   }
 }
 

@@ -227,7 +227,7 @@ __device__ __forceinline__ void tile_scores(const uint8_t* kb, const uint4* qf, 
 // of dims 16 mt + g (O[2 mt]) and 16 mt + 8 + g (O[2 mt + 1]).
 template <int VB, bool LOW>
 __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&ph)[4], const uint32_t (&pl)[4],
-                                            float (&O)[16][4], int lane, uint32_t km, uint32_t c64) {
+                                            float (&O)[16][4], int lane, uint32_t km, uint32_t c64, int valid) {
   const uint4* p = reinterpret_cast<const uint4*>(vb) + lane;
   // the high weights, then (two-part mode) the low weights into the same accumulator
   auto mma2 = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
@@ -268,7 +268,11 @@ __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&
   } else if constexpr (VB == 16) {
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
-      const uint4 c = p[mt * 32];  // dims lo (x, y), dims hi (z, w): token pairs of the two slot halves
+      uint4 c = p[mt * 32];  // dims lo (x, y), dims hi (z, w): token pairs of the two slot halves
+      if (valid < kBlock) {  // slots behind the longest row are not data
+        const uint32_t even = bf16_data(lane, 0, valid), odd = bf16_data(lane, 1, valid);
+        c = make_uint4(c.x & even, c.y & odd, c.z & even, c.w & odd);
+      }
       mma2(O[2 * mt], c.x, c.y);
       mma2(O[2 * mt + 1], c.z, c.w);
     }
@@ -468,7 +472,7 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
       pl[i] = pack_half2(wr[i][0] - hf.x, wr[i][1] - hf.y);
     }
   }
-  tile_values<VB, LOQ>(vb, ph, pl, st.O, lane, km, c64);
+  tile_values<VB, LOQ>(vb, ph, pl, st.O, lane, km, c64, maxlen - tok0);
 }
 
 // Query vector v of a tile (src: its 128 bf16 values, or null for an unused

@@ -200,3 +200,49 @@ def test_a_prefix_token_reaches_only_the_sequences_that_hold_it(fmt, bad):
         assert np.all(np.abs(out - ref) <= tol * np.abs(ref).max(-1, keepdims=True) + atol)
     elif not (w.k_bits == 2 and bad == "nan"):      # a 2-bit group's scale comes from its numbers
         assert not np.isfinite(ref).any()
+
+
+@pytest.mark.parametrize("kw", [dict(k_bits=16, v_bits=16, q_heads=14), dict(k_bits=16, v_bits=16, q_heads=14, paged=True),
+                                dict(window=32), dict(window=32, k_bits=4, asym=True)])
+@pytest.mark.parametrize("batch", [5, 20])
+def test_slots_without_a_token_hold_anything(kw, batch):
+    """Block stores and rings full of NaN before the tokens are written: lengths of 1, inside and at the end of a block, in
+    kvq_decode, kvq_decode_shared and kvq_attn_mass as from zeroed memory."""
+    from harness import DeviceRun, small_workload
+    from quantized_kv_cache_07_gb300 import _lib
+    from synth import make_inputs
+    from test_gpu_shared import decode_shared
+    w = small_workload("stale", **dict(dict(batch=batch, len_range=(33, 120)), **kw))
+    window = w.window
+    inp = make_inputs(w)
+    run = DeviceRun(inp)
+    if window:       # rings that are not full: 1 to 31 tokens each
+        short = torch.from_numpy(np.resize([1, 5, 16, 17, 31], batch).astype(np.int32)).cuda()
+    else:            # prefixes of 2 blocks of which less is held
+        short = torch.from_numpy(np.resize([1, 19, 16, 17, 8], batch).astype(np.int32)).cuda()
+    got = []
+    for stale in (0, 0x7FC1):
+        for t in (run.cache.k_codes, run.cache.v_codes, run.cache.meta, run.cache.k_window, run.cache.v_window):
+            if t is not None:
+                t.view(torch.int16).fill_(stale)
+        n = int(short.sum())
+        seq = torch.repeat_interleave(torch.arange(batch, device="cuda").int(), short.long())
+        pos = (torch.arange(n, device="cuda") - torch.repeat_interleave(short.cumsum(0) - short, short.long())).int()
+        g = torch.Generator(device="cuda").manual_seed(1)
+        rows = torch.randn(2, 40, w.kv_heads, 128, generator=g, device="cuda").bfloat16()
+        k, v = rows[0][pos.long()], rows[1][pos.long()]      # the same tokens in every sequence: a shared prefix
+        table = run.table.clone()
+        table[:, :2] = table[0, :2]
+        one = torch.ones_like(seq, dtype=torch.bool) if window else seq == 1        # the longest, for all
+        _lib.kvq_append(run.cache.desc, k[one].contiguous(), v[one].contiguous(), seq[one].contiguous(),
+                        pos[one].contiguous(), _lib.APPEND_RING if window else _lib.APPEND_QUANT, table, batch, inp.max_blocks)
+        run.table = table
+        o, l = run.decode(lens=short)
+        groups = [(0, batch, 0 if window else 2)]
+        so, sl = decode_shared(run, groups, lens=short)
+        mass = torch.zeros(batch, w.kv_heads, 64, device="cuda")
+        _lib.kvq_attn_mass(run.cache.desc, run.q, batch, w.q_heads, torch.from_numpy(l).cuda(), short, table, inp.max_blocks, mass)
+        got.append((o, l, so, sl, mass.cpu().numpy()))
+    for a, b in zip(*got):
+        assert np.isfinite(b).all()
+        np.testing.assert_array_equal(a, b)
