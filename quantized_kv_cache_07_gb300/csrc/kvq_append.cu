@@ -246,9 +246,7 @@ static cudaError_t launch_pdl(Kernel kernel, const Args& a, long long grid, int 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {

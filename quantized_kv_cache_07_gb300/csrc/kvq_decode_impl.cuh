@@ -1547,9 +1547,7 @@ struct Kernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ>, p);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ>, p);
   }
 };
 

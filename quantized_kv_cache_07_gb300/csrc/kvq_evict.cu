@@ -523,9 +523,7 @@ cudaError_t launch_move(const EvictArgs& a, int sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_move_kernel<KB, VB>, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel<KB, VB>, a);
 }
 
 }  // namespace

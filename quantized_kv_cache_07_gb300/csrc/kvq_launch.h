@@ -167,6 +167,8 @@ int switch_blocks_for(int k_bits);
 // switch_cost: the unit-start charge when the split is not unit-aligned.
 DecodeLayout decode_layout(int B, int Hq, int H, int window, int stream_ctas, int switch_cost);
 
+// Every launch gives its own status (cudaLaunchKernelEx returns it): the runtime's last error is not read, since it
+// may be that of an earlier call that the caller has dealt with.
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float* table, cudaStream_t s);

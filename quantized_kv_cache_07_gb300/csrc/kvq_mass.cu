@@ -479,9 +479,7 @@ cudaError_t launch_one(const MassArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, mass_kernel<KB, ASYM, LOQ, RING>, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, mass_kernel<KB, ASYM, LOQ, RING>, a);
 }
 
 template <int KB>

@@ -393,9 +393,7 @@ struct TileKernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tile_kernel<KB, VB, ASYM, LOQ>, a, n_tiles, TR);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, prefill_tile_kernel<KB, VB, ASYM, LOQ>, a, n_tiles, TR);
   }
 };
 

@@ -477,8 +477,7 @@ cudaError_t launch_rows(const RopeArgs& a, int sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&cfg, k, a)) != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const RopeFreqs f, int pairs, long long n, float* table) {
@@ -499,9 +498,7 @@ cudaError_t launch_pdl(void (*kernel)(const RopeArgs), const RopeArgs& a, long l
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
@@ -539,8 +536,11 @@ cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s) {
 
 cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float* table, cudaStream_t s) {
   const long long n = (long long)max_pos * pairs;
-  rope_table_kernel<<<unsigned((n + 255) / 256), 256, 0, s>>>(f, pairs, n, table);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((n + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, rope_table_kernel, f, pairs, n, table);
 }
 
 }  // namespace kvq

@@ -120,9 +120,7 @@ cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_merge_kernel, a, kConsumerWarps);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel, a, kConsumerWarps);
 }
 
 }  // namespace kvq

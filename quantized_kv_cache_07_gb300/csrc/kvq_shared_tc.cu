@@ -826,9 +826,7 @@ struct SharedTcKernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_tc_kernel<KB, VB, ASYM, TWO>, a);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, shared_tc_kernel<KB, VB, ASYM, TWO>, a);
   }
 };
 

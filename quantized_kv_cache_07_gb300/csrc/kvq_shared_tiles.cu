@@ -305,9 +305,7 @@ struct SharedTileKernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_tile_kernel<KB, VB, ASYM, LOQ>, a);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, shared_tile_kernel<KB, VB, ASYM, LOQ>, a);
   }
 };
 

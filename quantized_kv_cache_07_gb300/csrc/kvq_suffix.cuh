@@ -490,9 +490,7 @@ struct SuffixKernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, suffix_kernel<KB, VB, ASYM, LOQ>, a);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, suffix_kernel<KB, VB, ASYM, LOQ>, a);
   }
 };
 
