@@ -204,17 +204,12 @@ struct MassQuery {
   }
 };
 
-// Stored tokens and ring tokens of sequence b, clamped; `bad` reports a length
-// beyond the table or the mass rows.
+// The length of sequence b, clamped to the table's (its last tokens are in the ring, whatever a row of sums holds);
+// `bad` reports one beyond the table or the row.
 __device__ __forceinline__ int mass_len(const MassArgs& a, int b, bool& bad) {
-  int L = a.seq_lens[b];
-  const int W = a.c.window;
-  const int room = min(table_tokens(a.mbps, W), a.stride);
-  if (L < 0 || L > room) {
-    bad = true;
-    L = L < 0 ? 0 : room;
-  }
-  return L;
+  const int L = a.seq_lens[b], room = table_tokens(a.mbps, a.c.window);
+  bad = bad || L < 0 || L > min(room, a.stride);
+  return min(max(L, 0), room);
 }
 
 // Where a warp's copying or computing side is: step j of n, of unit (b, h).
@@ -251,7 +246,7 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
   bool bad = false;
   for (int b = tid; b < B; b += kMassThreads) {
     const int L = mass_len(a, b, bad);
-    const int n = RING ? min(L, W) : max(L - W, 0);
+    const int n = RING ? min(L, W) : min(max(L - W, 0), a.stride);
     lens[b] = L;
     pre[b + 1] = (n + kBlock * NB - 1) / (kBlock * NB);
   }
@@ -375,7 +370,8 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
   MassQuery<KB, ASYM, LOQ> mq;
   mq.load(a, at.b, at.h, lane);
   float* row = a.mass + (size_t(at.b) * H + at.h) * a.stride;
-  int L = lens[at.b], s = 0;
+  auto length = [&](int b) { return RING ? lens[b] : min(lens[b] - W, a.stride); };  // of the unit; its stored tokens in the row
+  int L = length(at.b), s = 0;
   // not unrolled over the stages: the code of one step has to stay in the instruction cache
 #pragma unroll 1
   for (int x = steps; x > 0; --x) {
@@ -425,16 +421,16 @@ __global__ void __launch_bounds__(kMassThreads) mass_kernel(const MassArgs a) {
     if ((valid >> (s * NB + n) & 1u) && (NB == 2 || t < 2)) {
       if constexpr (RING) {  // ring tokens' slots are not in order of their positions
         const int first = L - min(L, W), p = first + ((slot - first) % W + W) % W;
-        if (p < L) row[p] = fmaf(a.decay, row[p], sum);
+        if (p < min(L, a.stride)) row[p] = fmaf(a.decay, row[p], sum);
       } else {
         const float old = reinterpret_cast<const float*>(st + F::kOffSide + n * F::kSide + F::kOffMass)[tok];
-        if (slot < L - W) row[slot] = fmaf(a.decay, old, sum);
+        if (slot < L) row[slot] = fmaf(a.decay, old, sum);
       }
     }
     __syncwarp();  // every lane has read the stage before it is filled again
     if (++s == F::kStages) s = 0;
     if (at.advance(pre, H, x > 1) && x > 1) {
-      L = lens[at.b];
+      L = length(at.b);
       row = a.mass + (size_t(at.b) * H + at.h) * a.stride;
       mq.load(a, at.b, at.h, lane);
     }

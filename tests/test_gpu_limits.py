@@ -132,3 +132,26 @@ def test_attention_over_a_table_that_covers_every_position(kw, batch):
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert bool((got[0][-1] < run.lens).all())
+
+
+@pytest.mark.parametrize("kw", [dict(window=32), dict(window=32, k_bits=4, asym=True, q_heads=16), dict(), dict(k_bits=4)])
+@pytest.mark.parametrize("stride", [20, 64, 100])
+def test_attention_mass_of_sequences_longer_than_their_row(kw, stride):
+    """Flagged, and what the row holds is the sums of its tokens: the window's last tokens are those of the whole sequence."""
+    from harness import DeviceRun, small_workload
+    from quantized_kv_cache_07_gb300 import _lib
+    from synth import make_inputs
+    w = small_workload("short_rows", **dict(dict(batch=6, len_range=(40, 130)), **kw))
+    run = DeviceRun(make_inputs(w))
+    assert (run.lens > stride).any()
+    _, lse = run.decode()
+    lse = torch.from_numpy(lse).cuda()
+    got = []
+    for width in (160, stride):
+        # a guard row behind the last: nothing may be written there
+        mass, err = torch.ones(w.batch + 1, w.kv_heads, width, device="cuda"), _i([0])
+        _lib.kvq_attn_mass(run.cache.desc, run.q, w.batch, w.q_heads, lse, run.lens, run.table, run.inp.max_blocks,
+                           mass[:w.batch], decay=0.5, err_word=err)
+        assert int(err) == (0 if width == 160 else _lib.KVQ_DEVERR_SEQ_LEN) and bool((mass[w.batch] == 1).all())
+        got.append(mass[:w.batch])
+    assert torch.equal(got[0][..., :stride], got[1])
