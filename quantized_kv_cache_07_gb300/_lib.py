@@ -213,16 +213,19 @@ class _Args:
 
     def room(self, t, dtype, count: int):
         """The pointer of a contiguous tensor of any shape that holds `count` elements, or more."""
-        at = self(t, dtype)
-        if t is not None and not isinstance(t, int) and t.numel() < count:
+        if t is None or isinstance(t, int):
+            return t
+        if t.dtype is not dtype or t.get_device() != self.device or not t.is_contiguous() or t.numel() < count:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
-        return at
+        return t.data_ptr()
 
     def word(self, t):
         """The pointer of an error word: 4 bytes or more of the device."""
-        if t is not None and not isinstance(t, int) and (t.get_device() != self.device or t.nbytes < 4):
+        if t is None or isinstance(t, int):
+            return t
+        if t.get_device() != self.device or t.nbytes < 4:
             raise KvqError(KVQ_ERR_INVALID_ARG, self.where)
-        return _ptr(t)
+        return t.data_ptr()
 
     def rows(self, t, heads: int, n: int):
         """(pointer, row stride) of bf16 rows [n, heads * 128] or [n, heads, 128] whose heads are contiguous and whose
