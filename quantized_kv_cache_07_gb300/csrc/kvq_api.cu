@@ -119,7 +119,6 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
   return (long long)((n + TR - 1) / TR) * kv_heads;
 }
 
-// Workspace of kvq_decode_shared: the records of the prefix and of the suffixes.
 // The cache as the kernels of kvq_decode_shared see it: under a key factor the query times the factor
 // needs more than fp16's 11 bits (one part: the log-sum-exp is off by 1.3e-5 of it on 33 sequences of 8k
 // tokens, two: 1e-7), so it goes in two parts.
@@ -129,12 +128,15 @@ kvq::CacheView shared_view(const kvq_cache_desc* c) {
   return v;
 }
 
+// Workspace of kvq_decode_shared: the records of the prefix and of the suffixes.
 kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::SharedLayout* sl) {
   const kvq::CacheView v = shared_view(c);
   const int H = c->num_kv_heads, G = q_heads / H;
   // Units of 256 vectors on tcgen05 where groups have 64 on average, 16-vector tiles otherwise, for bf16
   // blocks and for the two-part mode (prefixes of 8192 tokens, int8, 32 / 48 / 64 vectors: 46 / 48 / 46 us on
   // tcgen05, 46 / 41 / 46 on tiles; of 16384 tokens 64 / 96: 55 / 54 and 56 / 64; of 2048 64 / 96: 35 / 35 and 28 / 35).
+  // The groups and their prefixes are on the device, so the rule has only their number: 64 vectors on a short prefix
+  // lose 7 us by it, and a large group among many small ones goes by their average.
   sl->tc = c->k_bits != 16 && c->q_bits != 32 && batch * G >= 64 * num_groups;
   sl->tile = sl->tc ? 256 : 16;
   sl->unit = sl->tc && v.q_bits == 32 ? 128 : sl->tile;

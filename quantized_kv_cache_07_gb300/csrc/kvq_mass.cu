@@ -9,9 +9,10 @@
 // not read).  Bound: HBM, the key codes and scales plus 8 bytes of mass a token.
 //
 // Measured: 4 sequences of 131072 tokens, int4 keys, 64 query heads: 66 us, 319 MB at 4.8 TB/s (the copy rate
-// would take 47); 32 of 1k-8k, int4: 25 us (13.6).  Issue slots are 63 % busy at 180 instructions a block, about
-// 80 of them the exact conversion of 4-bit codes, with 16 warps an SM (the query group and two blocks in flight
-// are 128 registers; at 85 they spill and it takes 136 us).
+// would take 47); 32 of 1k-8k, int4: 26 us (13.6).  180 instructions a block, about 80 of them the exact conversion
+// of 4-bit codes, keep the issue slots 58 % and the ALU 49 % busy: neither is full, but with 16 warps an SM the waits of
+// one instruction on another are not covered (the query group and two blocks in flight are 128 registers; at 85 they
+// spill and it takes 136 us).
 //
 // Work: the 16-token blocks of all (sequence, KV head) units, two a step, form one range cut
 // evenly over all warps of one wave.  A warp keeps its unit's query

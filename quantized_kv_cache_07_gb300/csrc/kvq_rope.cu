@@ -11,14 +11,16 @@
 // Rounding.  y is the exact value rounded to float32 (up to one case in about 2^24) and then to bf16.
 // That makes the stored codes those of kvq_append on the rotated vectors bit for bit: a plain
 // float32 sum differs from the exact one in its last bit often enough to move a bf16 rounding, with it
-// a vector's largest value, and with that a whole vector's codes.  The sum with all its rounding errors is 14
+// a vector's largest value, and with that a whole vector's codes.  The sum with all its rounding errors (the
+// products' by fused multiply-adds, the sum's by Knuth's two-sum) is 14
 // instructions a value; a float32 sum with a bound on its error is 7 and decides all but one value in 10^4.
 //
 // One warp turns and writes one 128-element vector; lane l owns dims 4l..4l+3,
 // so a pair's other half is in the same lane (interleaved) or R / 8 lanes away.  Many rows go 16 at a time
-// (rope_rows_kernel), which is what 8192 rows of 48 heads spend 70 us in: 200 MB moved at 2.9 TB/s, bound by the
-// instructions (about 130 a vector, issue slots 57 % busy; the copy rate would allow 30 us).  64 rows are one
-// launch's latency: 4 us.
+// (rope_rows_kernel), which is what 8192 rows of 48 heads spend 72 us in: 200 MB moved at 2.8 TB/s (the copy rate
+// would allow 30 us).  No unit is saturated: 130 instructions a vector keep the issue slots 57 % busy with the 24 warps
+// an SM that 80 registers leave, and what fills the rest is latency (of each instruction's result 1.7 warps, loads 1.2,
+// instruction fetches 1.0, shared memory 0.8, barriers 0.5).  64 rows are one launch's latency: 4 us.
 #include "kvq_append_device.cuh"
 
 namespace kvq {
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kGroupWarps * 32) rope_append_group_kernel(con
 //
 // A row at a time, a value vector's codes are 128 single bytes (or nibbles) spread over its whole
 // block, and every warp waits for its own loads: 185 us for 8192 rows that take 27 us to move.
-// Here (70 us) a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
+// Here (72 us) a CTA takes a window of 16 rows.  Where 16 rows of the call fill one block (a run of 16 positions
 // from a multiple of 16: prompts), a warp turns and quantizes the 16 vectors of a head, puts the block
 // together in shared memory and writes it as it lies, 16 bytes a lane; rows outside such runs are
 // written one by one.  The window's rows of the table are staged once for all heads; queries go 8

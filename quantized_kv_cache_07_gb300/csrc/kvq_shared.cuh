@@ -10,6 +10,11 @@
 // kernels before it and then lets the prefix kernel start, which runs beside it: their records lie apart,
 // and what it reads was complete when the suffix's wait ended (its own reads of it bypass L1).  It
 // waits for the suffix only before it ends, so that the merge, which waits for it, follows both.
+// The wait instruction promises the writes of the grid that it waits for to the threads that have executed it.  The
+// prefix kernel (and the merge, for the groups) reads what kernels before the suffix wrote without having executed it,
+// and relies on two things beyond that promise: that a grid whose end another grid has waited for has its writes in L2,
+// and that a CTA which starts after every suffix CTA has let it start reads L2 after that.  So every such read goes to
+// L2: ld.global.cg, or a bulk copy.
 #pragma once
 
 #include "kvq_decode_impl.cuh"

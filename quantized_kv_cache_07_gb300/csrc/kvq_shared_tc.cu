@@ -21,7 +21,7 @@
 // (Measured before: the same products issued by softmax threads between their steps, two CTAs of
 // 256 threads per SM: 75 us for 64 sequences on 32768 tokens, each issue holding its warp for 1000 cycles.)
 //
-// Measured: 64 sequences x 32 heads on 32768 shared tokens, int8: 80 us a call, about 55 of them here (the
+// Measured: 64 sequences x 32 heads on 32768 shared tokens, int8: 79 us a call, about 50 of them here (the
 // products alone would take 18, 2 x 128 vectors of a tile 1024 cycles).  A tile of 256 vectors takes
 // 3000 to 3600 cycles; its shared-memory traffic takes 2340 of them: the operands of the products
 // 1024, the scales that every softmax thread reads, 16 bytes at 4 wavefronts, 1024, the converted
@@ -30,7 +30,9 @@
 //
 // Under a key factor (TWO) the query times the factor does not fit in 11 bits: an fp16 high and low part, both
 // multiplied with the same K tile.  The low part takes the second query tile, so a unit is 128
-// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 55 us a call, 50 with one part.
+// vectors whose two warpgroups take turns: 33 sequences of 8176 tokens, int4: 55 us a call, 50 with one part.  A group's
+// last unit costs a whole pass over the prefix however few its vectors: those 33 sequences are 128 + 4 vectors a KV head,
+// 2048 tile steps where 128 vectors would take 1024.
 //
 // Orders inside a tile.  The tokens and dims of a block are permuted so that a lane's codes
 // (fragment-native order, include/kvq.h) go to shared memory as 16-byte (K) and
@@ -45,7 +47,9 @@
 //
 // Precision as in the decode kernel: exact codes, the query exact in fp16 (bf16 has 8 bits; or
 // int8 codes, or two parts), scales in fp32, fp16 weights kept in range by the sigma offset
-// (kvq_decode_impl.cuh), fp32 sums of the unrounded weights.
+// (kvq_decode_impl.cuh), fp32 sums of the unrounded weights.  The weight's one rounding to fp16 (2^-11 of it at most) is
+// what the outputs differ by from the formula in float32: 2.0e-4 of their norm (4 of 2048 to 64 of 32768 tokens, int8
+// and int4), an eighth of what rounding the outputs to bf16 takes (1.6e-3); q_bits 32 carries the weights in two parts.
 #include "kvq_shared.cuh"
 #include "kvq_tcgen05.cuh"
 #include "kvq_tiles.cuh"
