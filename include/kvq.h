@@ -402,7 +402,8 @@ kvq_status kvq_decode_ex(const kvq_cache_desc* cache, const void* q, int32_t bat
  *                  otherwise KVQ_DEVERR_SEQ_LEN (and the nearest is used)
  *   num_groups   : 1..256 (more: KVQ_ERR_UNSUPPORTED)
  *   workspace    : >= kvq_decode_shared_workspace_size bytes, zeroed once by kvq_workspace_init;
- *                  one per concurrently running call
+ *                  one per concurrently running call, and not one that kvq_decode or kvq_prefill
+ *                  also uses (their counters would not be zero afterwards)
  * Everything else as kvq_decode, every cache format and query mode, the bf16
  * window (which holds each sequence's own last tokens) included.  Under a key factor
  * the query times the factor is carried in two fp16 parts (as with q_bits 32), so that
