@@ -524,8 +524,8 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, in
  *   lse         : device float [batch][q_heads]
  *   mass        : device float [batch][num_kv_heads][mass_stride], 16-byte aligned;
  *                 entries at and behind seq_lens[b] are left as they are
- *   mass_stride : a multiple of 4; a sequence longer than it sets KVQ_DEVERR_SEQ_LEN
- *                 and is cut
+ *   mass_stride : a multiple of 4; a sequence longer than it sets KVQ_DEVERR_SEQ_LEN,
+ *                 and the sums of the tokens behind the row are dropped
  *   decay       : finite; 1 keeps the whole history, less forgets it
  * A block whose table entry is out of range sets KVQ_DEVERR_BLOCK_ID and its
  * tokens' sums stay as they are.
