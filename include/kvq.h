@@ -8,6 +8,7 @@
  *   kvq_rope_append    kvq_append of keys turned by their rotary positions, and the
  *                      turned queries, in one call (kvq_rope_table: its cosines and sines)
  *   kvq_decode_shared  kvq_decode for sequences that share a prefix, read once for all
+ *   kvq_decode_sinks, kvq_prefill_sinks   a sliding window and first tokens that stay visible
  *   kvq_attn_mass      the attention weight each cached token received, summed up
  *   kvq_evict          keep each sequence's heaviest tokens, in place
  *   kvq_prefill        causal attention of a chunk of new tokens
@@ -509,6 +510,38 @@ kvq_status kvq_prefill(const kvq_cache_desc* cache, const void* q, int32_t n, in
  * the automatic choice may take that path). */
 kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, int32_t q_heads, int32_t stream_ctas,
                                       size_t* bytes);
+
+/*
+ * kvq_decode_sinks -- kvq_decode with a sliding window and first tokens that stay visible.
+ * The pages name eviction beside quantization ([P3] "Precision floors and mixed cache formats") and keep
+ * recent tokens apart ([P1] "Cache growth changes the serving trade") without a rule for whole layers; here
+ * token i of a sequence of L = seq_lens[b] tokens is attended to if
+ *   i < sinks  or  i >= L - span.
+ *   sinks : >= 0 (0: the window alone)
+ *   span  : >= 1, the query's own token among them; at least the cache's bf16 window
+ *           (KVQ_ERR_UNSUPPORTED otherwise)
+ * Only blocks that hold such a token are read; the other entries of the block table may be anything
+ * (kvq_pages_update frees their blocks and sets them to -1).  Hidden tokens that share a block with
+ * seen ones have no effect, whatever they hold.  Everything else as kvq_decode, with
+ * kvq_decode_workspace_size and the same workspace; under a key factor the query times the factor
+ * is carried in two fp16 parts (as with q_bits 32), so that lse holds float32's precision.
+ */
+kvq_status kvq_decode_sinks(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t sinks, int32_t span, void* out, int32_t out_fp32, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t stream_ctas, uint32_t* err_word, void* stream);
+
+/*
+ * kvq_prefill_sinks -- kvq_prefill with a sliding window and sinks: the row at position p attends to
+ * tokens i <= p with i < sinks or i > p - span (a chunk of single rows is kvq_decode_sinks).  Every
+ * row sees its own tokens alone, whatever the others hold.  Everything else as kvq_prefill (both attention
+ * paths, kvq_prefill_workspace_size, the chunk's own write), block table and key factor as kvq_decode_sinks.
+ */
+kvq_status kvq_prefill_sinks(const kvq_cache_desc* cache, const void* q, int32_t n, int32_t q_heads,
+                             const int32_t* seq_idx, const int32_t* pos, const void* k_new, const void* v_new,
+                             const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, int32_t sinks,
+                             int32_t span, void* out, int32_t out_fp32, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t stream_ctas, uint32_t* err_word, void* stream);
 
 /*
  * kvq_attn_mass -- add the attention weight that every cached token received in

@@ -90,6 +90,12 @@ SIGNATURES = {
                                     c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p,
                                     c_void_p]),
     "kvq_decode_shared_workspace_size": (c_int32, [POINTER(CacheDesc), c_int32, c_int32, c_int32, POINTER(c_size_t)]),
+    "kvq_decode_sinks": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                                   c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_int32, c_void_p,
+                                   c_void_p]),
+    "kvq_prefill_sinks": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int32, c_void_p,
+                                    c_void_p, c_size_t, c_int32, c_void_p, c_void_p]),
     "kvq_attn_mass": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int32,
                                 c_void_p, c_int32, c_float, c_void_p, c_void_p]),
     "kvq_evict": (c_int32, [POINTER(CacheDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
@@ -290,6 +296,38 @@ def kvq_decode_shared(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, bl
                                     arg(lse, arg.f32, (batch, q_heads)),
                                     arg.room(workspace, arg.u8, workspace_bytes), workspace_bytes,
                                     arg.word(err_word), arg.stream(stream)), arg.where)
+
+
+def kvq_decode_sinks(desc: CacheDesc, q, batch: int, q_heads: int, seq_lens, block_table, max_blocks_per_seq: int,
+                     sinks: int, span: int, out, lse=None, workspace=None, workspace_bytes: int = 0,
+                     stream_ctas: int = 0, err_word=None, stream=None, out_fp32: bool | None = None):
+    arg = _Args("kvq_decode_sinks")
+    if out_fp32 is None:
+        out_fp32 = out.dtype is arg.f32
+    rows = (batch, q_heads, 128)
+    _check(load().kvq_decode_sinks(ctypes.byref(desc), arg(q, arg.bf16, rows), batch, q_heads,
+                                   arg(seq_lens, arg.i32, (batch,)), arg(block_table, arg.i32, (batch, max_blocks_per_seq)),
+                                   max_blocks_per_seq, sinks, span, arg(out, arg.f32 if out_fp32 else arg.bf16, rows),
+                                   int(bool(out_fp32)), arg(lse, arg.f32, (batch, q_heads)),
+                                   arg.room(workspace, arg.u8, workspace_bytes), workspace_bytes, stream_ctas,
+                                   arg.word(err_word), arg.stream(stream)), arg.where)
+
+
+def kvq_prefill_sinks(desc: CacheDesc, q, q_heads: int, seq_idx, pos, block_table, batch: int, max_blocks_per_seq: int,
+                      sinks: int, span: int, out, k_new=None, v_new=None, lse=None, workspace=None,
+                      workspace_bytes: int = 0, stream_ctas: int = 0, err_word=None, stream=None,
+                      out_fp32: bool | None = None):
+    arg = _Args("kvq_prefill_sinks")
+    n = int(pos.shape[0])
+    if out_fp32 is None:
+        out_fp32 = out.dtype is arg.f32
+    rows, new = (n, q_heads, 128), (n, desc.num_kv_heads, 128)
+    _check(load().kvq_prefill_sinks(ctypes.byref(desc), arg(q, arg.bf16, rows), n, q_heads, arg(seq_idx, arg.i32, (n,)),
+                                    arg(pos, arg.i32, (n,)), arg(k_new, arg.bf16, new), arg(v_new, arg.bf16, new),
+                                    arg(block_table, arg.i32, (batch, max_blocks_per_seq)), batch, max_blocks_per_seq,
+                                    sinks, span, arg(out, arg.f32 if out_fp32 else arg.bf16, rows), int(bool(out_fp32)),
+                                    arg(lse, arg.f32, (n, q_heads)), arg.room(workspace, arg.u8, workspace_bytes),
+                                    workspace_bytes, stream_ctas, arg.word(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_attn_mass(desc: CacheDesc, q, batch: int, q_heads: int, lse, seq_lens, block_table, max_blocks_per_seq: int,

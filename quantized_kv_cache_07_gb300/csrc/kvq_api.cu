@@ -128,6 +128,23 @@ kvq::CacheView shared_view(const kvq_cache_desc* c) {
   return v;
 }
 
+// Stream CTAs of attention with sinks: the wave of its own kernel, and no more than the workspace size counts with
+// (0 on failure).
+int sinks_stream_ctas(const kvq_cache_desc* c, const kvq::CacheView& v, int batch, bool rows) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  const int units = batch * c->num_kv_heads, room = auto_stream_ctas(c, batch, rows);
+  const int own = stream_ctas_for(sms * kvq::sinks_ctas_per_sm(v, batch, rows), c->window > 0 ? units : 0, units);
+  return own < room ? own : room;
+}
+
+// What attention with sinks takes: a query that sees itself, and the whole bf16 window.
+kvq_status check_span(const kvq_cache_desc* c, int sinks, int span) {
+  if (sinks < 0 || span < 1) return KVQ_ERR_INVALID_ARG;
+  return span < c->window ? KVQ_ERR_UNSUPPORTED : KVQ_OK;
+}
+
 // Workspace of kvq_decode_shared: the records of the prefix and of the suffixes.
 kvq_status shared_layout(const kvq_cache_desc* c, int batch, int q_heads, int num_groups, kvq::SharedLayout* sl) {
   const kvq::CacheView v = shared_view(c);
@@ -208,6 +225,146 @@ DecodeLayout decode_layout(int B, int Hq, int H, int window, int stream_ctas, in
 }
 
 }  // namespace kvq
+
+namespace {
+
+// Attention with sinks and a sliding window.
+struct Sinks {
+  int sinks, span;
+};
+
+// kvq_decode_ex (sinks null) and kvq_decode_sinks.
+kvq_status decode_call(const kvq_cache_desc* cache, const void* q, int batch, int q_heads, const int32_t* seq_lens,
+                       const int32_t* block_table, int max_blocks_per_seq, const Sinks* sinks, void* out, int out_fp32,
+                       float* lse, void* workspace, size_t workspace_bytes, int stream_ctas, uint32_t flags,
+                       uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_decode_shape(cache, batch, q_heads);
+  if (st != KVQ_OK) return st;
+  if (sinks && (st = check_span(cache, sinks->sinks, sinks->span)) != KVQ_OK) return st;
+  if (batch == 0) return KVQ_OK;
+  if (!q || !seq_lens || !block_table || !out || max_blocks_per_seq < 1) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
+  if (stream_ctas < 0) return KVQ_ERR_INVALID_ARG;
+  const kvq::CacheView v = sinks ? shared_view(cache) : view(cache);
+  const int P = stream_ctas > 0 ? stream_ctas
+                : sinks         ? sinks_stream_ctas(cache, v, batch, false)
+                                : auto_stream_ctas(cache, batch);
+  if (P <= 0) return KVQ_ERR_CUDA;
+  const kvq::DecodeLayout L = kvq::decode_layout(batch, q_heads, cache->num_kv_heads, cache->window, P,
+                                                 kvq::switch_blocks_for(cache->k_bits));
+  if (!workspace || workspace_bytes < L.total) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  kvq::DecodeArgs a;
+  a.c = v;
+  a.q = static_cast<const uint16_t*>(q);
+  a.B = batch;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->num_kv_heads;
+  a.seq_lens = seq_lens;
+  a.pos = nullptr;
+  a.seq_of = nullptr;
+  a.nseq = batch;
+  a.table = block_table;
+  a.mbps = max_blocks_per_seq;
+  a.out = out;
+  a.out_fp32 = out_fp32 ? 1 : 0;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.lay = L;
+  a.err = err_word;
+  a.ahead = (flags & KVQ_DECODE_GEOMETRY_READY) ? 1 : 0;
+  if (sinks) {
+    a.sinks = sinks->sinks;
+    a.span = sinks->span;
+  }
+  const cudaError_t e = sinks ? kvq::launch_sinks(a, static_cast<cudaStream_t>(stream))
+                              : kvq::launch_decode(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+// kvq_prefill (sinks null) and kvq_prefill_sinks.
+kvq_status prefill_call(const kvq_cache_desc* cache, const void* q, int n, int q_heads, const int32_t* seq_idx,
+                        const int32_t* pos, const void* k_new, const void* v_new, const int32_t* block_table, int batch,
+                        int max_blocks_per_seq, const Sinks* sinks, void* out, int out_fp32, float* lse, void* workspace,
+                        size_t workspace_bytes, int stream_ctas, uint32_t* err_word, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (cache->window != 0) return KVQ_ERR_UNSUPPORTED;  // positions live in the block store only
+  st = check_decode_shape(cache, n, q_heads);
+  if (st != KVQ_OK) return st;
+  if (sinks && (st = check_span(cache, sinks->sinks, sinks->span)) != KVQ_OK) return st;
+  if (n == 0) return KVQ_OK;
+  if (!q || !seq_idx || !pos || !block_table || !out || max_blocks_per_seq < 1 || batch < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if ((k_new == nullptr) != (v_new == nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
+  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES) return KVQ_ERR_INVALID_ARG;
+  const kvq::CacheView v = sinks ? shared_view(cache) : view(cache);
+  const bool tiles_ok = kvq::prefill_tiles_supported(v);
+  if (stream_ctas == KVQ_PREFILL_TILES && !tiles_ok) return KVQ_ERR_UNSUPPORTED;
+  bool tiles = stream_ctas == KVQ_PREFILL_TILES;
+  if (stream_ctas == 0 && tiles_ok) {
+    // Tiles once their CTAs fill at least 9/16 of the SMs; fewer tiles leave
+    // the long prefixes to too few CTAs and split rows (every row one query
+    // group of the decode split over all SMs) are faster.  Measured crossover
+    // (8k-32k prefixes, int8, 32/8 heads): split rows ahead at 48 and 64 tile
+    // CTAs (1.2-1.6x), tiles ahead at 96 (1.04-1.1x) and 128 (1.3x).
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
+                                                  cudaSuccess)
+      return KVQ_ERR_CUDA;
+    tiles = prefill_tiles(n, q_heads, cache->num_kv_heads) * 16 >= 9ll * sms;
+  }
+  kvq::DecodeLayout L{};
+  if (!tiles) {
+    const int P = stream_ctas > 0 ? stream_ctas
+                  : sinks         ? sinks_stream_ctas(cache, v, n, true)
+                                  : auto_stream_ctas(cache, n, true);
+    if (P <= 0) return KVQ_ERR_CUDA;
+    L = kvq::decode_layout(n, q_heads, cache->num_kv_heads, 0, P, kvq::switch_blocks_for(cache->k_bits));
+    if (!workspace || workspace_bytes < L.total) return KVQ_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  }
+  if (k_new) {  // the chunk's own keys and values first: quantize-on-write
+    st = kvq_append(cache, k_new, v_new, n, seq_idx, pos, KVQ_APPEND_QUANT, block_table, batch, max_blocks_per_seq,
+                    err_word, stream);
+    if (st != KVQ_OK) return st;
+  }
+  kvq::DecodeArgs a;
+  a.c = v;
+  a.q = static_cast<const uint16_t*>(q);
+  a.B = n;
+  a.Hq = q_heads;
+  a.G = q_heads / cache->num_kv_heads;
+  a.seq_lens = nullptr;
+  a.pos = pos;
+  a.seq_of = seq_idx;
+  a.nseq = batch;
+  a.table = block_table;
+  a.mbps = max_blocks_per_seq;
+  a.out = out;
+  a.out_fp32 = out_fp32 ? 1 : 0;
+  a.lse = lse;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.lay = L;
+  a.err = err_word;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (sinks) {
+    a.sinks = sinks->sinks;
+    a.span = sinks->span;
+    e = tiles ? kvq::launch_sinks_tiles(a, cs) : kvq::launch_sinks(a, cs);
+  } else {
+    e = tiles ? kvq::launch_prefill_tiles(a, cs) : kvq::launch_decode(a, cs);
+  }
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -336,41 +493,17 @@ kvq_status kvq_decode_ex(const kvq_cache_desc* cache, const void* q, int32_t bat
                          int32_t out_fp32, float* lse, void* workspace, size_t workspace_bytes, int32_t stream_ctas,
                          uint32_t flags, uint32_t* err_word, void* stream) {
   if (flags & ~uint32_t(KVQ_DECODE_GEOMETRY_READY)) return KVQ_ERR_INVALID_ARG;
-  kvq_status st = check_cache(cache);
-  if (st != KVQ_OK) return st;
-  st = check_decode_shape(cache, batch, q_heads);
-  if (st != KVQ_OK) return st;
-  if (batch == 0) return KVQ_OK;
-  if (!q || !seq_lens || !block_table || !out || max_blocks_per_seq < 1) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
-  if (stream_ctas < 0) return KVQ_ERR_INVALID_ARG;
-  const int P = stream_ctas > 0 ? stream_ctas : auto_stream_ctas(cache, batch);
-  if (P <= 0) return KVQ_ERR_CUDA;
-  const kvq::DecodeLayout L = kvq::decode_layout(batch, q_heads, cache->num_kv_heads, cache->window, P,
-                                                 kvq::switch_blocks_for(cache->k_bits));
-  if (!workspace || workspace_bytes < L.total) return KVQ_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  kvq::DecodeArgs a;
-  a.c = view(cache);
-  a.q = static_cast<const uint16_t*>(q);
-  a.B = batch;
-  a.Hq = q_heads;
-  a.G = q_heads / cache->num_kv_heads;
-  a.seq_lens = seq_lens;
-  a.pos = nullptr;
-  a.seq_of = nullptr;
-  a.nseq = batch;
-  a.table = block_table;
-  a.mbps = max_blocks_per_seq;
-  a.out = out;
-  a.out_fp32 = out_fp32 ? 1 : 0;
-  a.lse = lse;
-  a.ws = static_cast<uint8_t*>(workspace);
-  a.lay = L;
-  a.err = err_word;
-  a.ahead = (flags & KVQ_DECODE_GEOMETRY_READY) ? 1 : 0;
-  if (kvq::launch_decode(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
-  return KVQ_OK;
+  return decode_call(cache, q, batch, q_heads, seq_lens, block_table, max_blocks_per_seq, nullptr, out, out_fp32, lse,
+                     workspace, workspace_bytes, stream_ctas, flags, err_word, stream);
+}
+
+kvq_status kvq_decode_sinks(const kvq_cache_desc* cache, const void* q, int32_t batch, int32_t q_heads,
+                            const int32_t* seq_lens, const int32_t* block_table, int32_t max_blocks_per_seq,
+                            int32_t sinks, int32_t span, void* out, int32_t out_fp32, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t stream_ctas, uint32_t* err_word, void* stream) {
+  const Sinks sk{sinks, span};
+  return decode_call(cache, q, batch, q_heads, seq_lens, block_table, max_blocks_per_seq, &sk, out, out_fp32, lse,
+                     workspace, workspace_bytes, stream_ctas, 0u, err_word, stream);
 }
 
 kvq_status kvq_prefill(const kvq_cache_desc* cache, const void* q, int32_t n, int32_t q_heads,
@@ -378,67 +511,18 @@ kvq_status kvq_prefill(const kvq_cache_desc* cache, const void* q, int32_t n, in
                        const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, void* out,
                        int32_t out_fp32, float* lse, void* workspace, size_t workspace_bytes, int32_t stream_ctas,
                        uint32_t* err_word, void* stream) {
-  kvq_status st = check_cache(cache);
-  if (st != KVQ_OK) return st;
-  if (cache->window != 0) return KVQ_ERR_UNSUPPORTED;  // positions live in the block store only
-  st = check_decode_shape(cache, n, q_heads);
-  if (st != KVQ_OK) return st;
-  if (n == 0) return KVQ_OK;
-  if (!q || !seq_idx || !pos || !block_table || !out || max_blocks_per_seq < 1 || batch < 1)
-    return KVQ_ERR_INVALID_ARG;
-  if ((k_new == nullptr) != (v_new == nullptr)) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
-  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES) return KVQ_ERR_INVALID_ARG;
-  const bool tiles_ok = kvq::prefill_tiles_supported(view(cache));
-  if (stream_ctas == KVQ_PREFILL_TILES && !tiles_ok) return KVQ_ERR_UNSUPPORTED;
-  bool tiles = stream_ctas == KVQ_PREFILL_TILES;
-  if (stream_ctas == 0 && tiles_ok) {
-    // Tiles once their CTAs fill at least 9/16 of the SMs; fewer tiles leave
-    // the long prefixes to too few CTAs and split rows (every row one query
-    // group of the decode split over all SMs) are faster.  Measured crossover
-    // (8k-32k prefixes, int8, 32/8 heads): split rows ahead at 48 and 64 tile
-    // CTAs (1.2-1.6x), tiles ahead at 96 (1.04-1.1x) and 128 (1.3x).
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
-                                                  cudaSuccess)
-      return KVQ_ERR_CUDA;
-    tiles = prefill_tiles(n, q_heads, cache->num_kv_heads) * 16 >= 9ll * sms;
-  }
-  kvq::DecodeLayout L{};
-  if (!tiles) {
-    const int P = stream_ctas > 0 ? stream_ctas : auto_stream_ctas(cache, n, true);
-    if (P <= 0) return KVQ_ERR_CUDA;
-    L = kvq::decode_layout(n, q_heads, cache->num_kv_heads, 0, P, kvq::switch_blocks_for(cache->k_bits));
-    if (!workspace || workspace_bytes < L.total) return KVQ_ERR_WORKSPACE;
-    if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
-  }
-  if (k_new) {  // the chunk's own keys and values first: quantize-on-write
-    st = kvq_append(cache, k_new, v_new, n, seq_idx, pos, KVQ_APPEND_QUANT, block_table, batch, max_blocks_per_seq,
-                    err_word, stream);
-    if (st != KVQ_OK) return st;
-  }
-  kvq::DecodeArgs a;
-  a.c = view(cache);
-  a.q = static_cast<const uint16_t*>(q);
-  a.B = n;
-  a.Hq = q_heads;
-  a.G = q_heads / cache->num_kv_heads;
-  a.seq_lens = nullptr;
-  a.pos = pos;
-  a.seq_of = seq_idx;
-  a.nseq = batch;
-  a.table = block_table;
-  a.mbps = max_blocks_per_seq;
-  a.out = out;
-  a.out_fp32 = out_fp32 ? 1 : 0;
-  a.lse = lse;
-  a.ws = static_cast<uint8_t*>(workspace);
-  a.lay = L;
-  a.err = err_word;
-  const cudaError_t e = tiles ? kvq::launch_prefill_tiles(a, static_cast<cudaStream_t>(stream))
-                              : kvq::launch_decode(a, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return KVQ_ERR_CUDA;
-  return KVQ_OK;
+  return prefill_call(cache, q, n, q_heads, seq_idx, pos, k_new, v_new, block_table, batch, max_blocks_per_seq, nullptr,
+                      out, out_fp32, lse, workspace, workspace_bytes, stream_ctas, err_word, stream);
+}
+
+kvq_status kvq_prefill_sinks(const kvq_cache_desc* cache, const void* q, int32_t n, int32_t q_heads,
+                             const int32_t* seq_idx, const int32_t* pos, const void* k_new, const void* v_new,
+                             const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, int32_t sinks,
+                             int32_t span, void* out, int32_t out_fp32, float* lse, void* workspace,
+                             size_t workspace_bytes, int32_t stream_ctas, uint32_t* err_word, void* stream) {
+  const Sinks sk{sinks, span};
+  return prefill_call(cache, q, n, q_heads, seq_idx, pos, k_new, v_new, block_table, batch, max_blocks_per_seq, &sk, out,
+                      out_fp32, lse, workspace, workspace_bytes, stream_ctas, err_word, stream);
 }
 
 kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, int32_t q_heads, int32_t stream_ctas,

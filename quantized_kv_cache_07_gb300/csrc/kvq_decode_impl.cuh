@@ -315,15 +315,16 @@ __device__ __forceinline__ void value_block(const uint8_t* vb, uint32_t b0, uint
 }
 
 // A bf16 block whose first `valid` tokens are data: what the other slots hold (0 times it may be no number) is
-// not read as values.  Lane t's words are tokens (2t, 2t + 8) and (2t + 1, 2t + 9).
-__device__ __forceinline__ uint32_t bf16_data(int lane, int odd, int valid) {
+// not read as values, nor are tokens head .. from - 1.  Lane t's words are tokens (2t, 2t + 8) and (2t + 1, 2t + 9).
+__device__ __forceinline__ uint32_t bf16_data(int lane, int odd, int valid, int head = kBlock, int from = 0) {
   const int i = 2 * (lane & 3) + odd;
-  return (i < valid ? 0xFFFFu : 0u) | (i + 8 < valid ? 0xFFFF0000u : 0u);
+  return (i < valid && (i < head || i >= from) ? 0xFFFFu : 0u) |
+         (i + 8 < valid && (i + 8 < head || i + 8 >= from) ? 0xFFFF0000u : 0u);
 }
-__device__ __forceinline__ void value_block_part(const uint8_t* vb, int valid, uint32_t b0, uint32_t b1, uint32_t b0lo,
-                                                 uint32_t b1lo, float (&O)[8][4], int lane) {
+__device__ __forceinline__ void value_block_part(const uint8_t* vb, int valid, int head, int from, uint32_t b0,
+                                                 uint32_t b1, uint32_t b0lo, uint32_t b1lo, float (&O)[8][4], int lane) {
   const uint4* p = reinterpret_cast<const uint4*>(vb) + lane;
-  const uint32_t even = bf16_data(lane, 0, valid), odd = bf16_data(lane, 1, valid);
+  const uint32_t even = bf16_data(lane, 0, valid, head, from), odd = bf16_data(lane, 1, valid, head, from);
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) {
     const uint4 r = p[mt * 32], c = make_uint4(r.x & even, r.y & odd, r.z & even, r.w & odd);
@@ -368,6 +369,29 @@ __device__ __forceinline__ void locate_unit(const Geo& g, long long x, int& b, i
   while (geo_vlen(g, b) == 0) ++b;
   h = int((x - (long long)g.H * g.vpre[b]) / geo_vlen(g, b));
 }
+
+// Attention with sinks and a sliding window: of a sequence of L tokens, Lq of them in blocks, a query
+// behind the last one sees tokens below `sinks` and from L - span on.  Its blocks are those of the
+// sinks (`front`) and then all from the window's first on: block i of them is logical
+// block i, or i + skip from `front` on.  Every one of them holds a token that is seen.
+struct SpanBlocks {
+  int front, skip, count;
+  __device__ __forceinline__ int logical(int i) const { return i < front ? i : i + skip; }
+};
+__device__ __forceinline__ SpanBlocks span_blocks(int L, int Lq, int sinks, int span) {
+  SpanBlocks s;
+  const int all = (Lq + kBlock - 1) / kBlock, lo = max(L - span, 0);
+  s.front = min((min(sinks, Lq) + kBlock - 1) / kBlock, all);
+  s.skip = max((lo >= Lq ? all : lo / kBlock) - s.front, 0);
+  s.count = all - s.skip;
+  return s;
+}
+
+// Which tokens of NB blocks a query sees (SPAN): the first `head` and those from `from` on.
+template <int NB>
+struct Seen {
+  int head[NB], from[NB];
+};
 
 // Base-2 exponential: the PTX ex2.approx.ftz.f32 instruction (max relative
 // error about 2^-22 per the PTX ISA; ex2(-inf) = +0).  Results below 2^-126
@@ -479,14 +503,21 @@ struct OffsetKeys {
 //
 // Asymmetric blocks (ASYM) add the key zero-point term m'_k * sum(q) to each
 // score and accumulate the value zero-point term p * m'_v per query.
-template <int KB, int VB, int NB, bool ASYM, bool LOQ>
+//
+// SPAN: tokens between a block's head and its window (`seen`) are hidden, as those behind `valid` are: neither
+// their scores nor their scales, zero points or bf16 values are read as data.
+template <int KB, int VB, int NB, bool ASYM, bool LOQ, bool SPAN = false>
 __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], const uint8_t* const (&vb)[NB],
                                                const float* const (&ks)[NB], const float* const (&vs)[NB],
                                                const float* const (&ko)[NB], const float* const (&vo)[NB],
                                                const int (&valid)[NB], const uint32_t (&qf)[16],
                                                const uint4* qlo, const float4* qzo, float qs0, float qs1, float qz0,
-                                               float qz1, WarpState& st, int lane, uint32_t km) {
+                                               float qz1, WarpState& st, int lane, uint32_t km,
+                                               const Seen<NB>& seen = Seen<NB>{}) {
   constexpr bool kBf16 = (KB == 16);
+  // does block j hide slots, and does it show token i
+  auto part = [&](int j) { return valid[j] < kBlock || (SPAN && seen.from[j] > 0 && seen.head[j] < kBlock); };
+  auto shows = [&](int j, int i) { return i < valid[j] && (!SPAN || i < seen.head[j] || i >= seen.from[j]); };
   constexpr bool kOffK = OffsetKeys<KB, LOQ>::kOn;
   // offset-binary centre of the code conversion: c' = u - kKC
   constexpr float kKC = (KB == 8) ? 128.f : (KB == 4 ? 8.f : 2.f), kVC = (VB == 8) ? 128.f : (VB == 4 ? 8.f : 2.f);
@@ -524,8 +555,8 @@ __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], c
       x[j][2] = acc[2] * (sk1 * qs0);  // token g+8, query 2t
       x[j][3] = acc[3] * (sk1 * qs1);  // token g+8, query 2t+1
     }
-    if (valid[j] < kBlock) {  // the last block of a unit may be partial
-      const bool v0 = g < valid[j], v1 = g + 8 < valid[j];
+    if (part(j)) {  // the last block of a unit may be partial
+      const bool v0 = shows(j, g), v1 = shows(j, g + 8);
       x[j][0] = v0 ? x[j][0] : kNegInf;
       x[j][1] = v0 ? x[j][1] : kNegInf;
       x[j][2] = v1 ? x[j][2] : kNegInf;
@@ -572,7 +603,7 @@ __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], c
     float svm = 0.f;
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-      const bool v0 = valid[j] >= kBlock || g < valid[j], v1 = valid[j] >= kBlock || g + 8 < valid[j];
+      const bool v0 = !part(j) || shows(j, g), v1 = !part(j) || shows(j, g + 8);
       svm = fmaxf(svm, fmaxf(v0 ? sv[j][0] : 0.f, v1 ? sv[j][1] : 0.f));
     }
     if (__any_sync(kFull, svm > st.svlim)) {
@@ -618,8 +649,8 @@ __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], c
     } else {
       // weights are at most 2^(kMaxSlack + sigma) and s_v <= svlim: p * s_v <= 2^kWeightExp
       float w00 = p00 * sv[j][0], w10 = p10 * sv[j][1], w01 = p01 * sv[j][0], w11 = p11 * sv[j][1];
-      if (valid[j] < kBlock) {  // scales of empty slots of a partial block are not data
-        const bool v0 = g < valid[j], v1 = g + 8 < valid[j];
+      if (part(j)) {  // scales of empty slots of a partial block are not data
+        const bool v0 = shows(j, g), v1 = shows(j, g + 8);
         w00 = v0 ? w00 : 0.f;
         w01 = v0 ? w01 : 0.f;
         w10 = v1 ? w10 : 0.f;
@@ -654,7 +685,9 @@ __device__ __forceinline__ void process_blocks(const uint8_t* const (&kb)[NB], c
       b0lo = (g & 1) ? q01 : q00;
       b1lo = (g & 1) ? q11 : q10;
     }
-    if (kBf16 && valid[j] < kBlock) value_block_part(vb[j], valid[j], b0, b1, b0lo, b1lo, st.O, lane);
+    if (kBf16 && part(j))
+      value_block_part(vb[j], valid[j], SPAN ? seen.head[j] : kBlock, SPAN ? seen.from[j] : 0, b0, b1, b0lo, b1lo, st.O,
+                       lane);
     else value_block<VB, kBf16 || LOQ>(vb[j], b0, b1, b0lo, b1lo, st.O, lane, km);
   }
 }
@@ -1069,7 +1102,7 @@ __device__ __forceinline__ bool finish_segment(const DecodeArgs& a, WarpState& s
 // memory (all threads; ends with a block barrier).  `load` reads a length.
 // Returns (in every thread) whether a length was negative or beyond the
 // table's capacity; the caller reports it.
-template <typename LoadLen>
+template <bool SPAN = false, typename LoadLen>
 __device__ __forceinline__ bool scan_geometry(const DecodeArgs& a, int B, int W, int X, int* len_s, int* pre_s,
                                               int* vpre_s, LoadLen load, int tid, int warp, int lane) {
   const int cap = table_tokens(a.mbps, 0);
@@ -1087,7 +1120,7 @@ __device__ __forceinline__ bool scan_geometry(const DecodeArgs& a, int B, int W,
       L = W > 0 ? cap + W : cap;
     }
     len_s[b] = L;
-    const int nb = (Lq + kBlock - 1) / kBlock;
+    const int nb = SPAN ? span_blocks(L, Lq, a.sinks, a.span).count : (Lq + kBlock - 1) / kBlock;
     pre_s[b + 1] = nb;                    // block count, scanned below
     vpre_s[b + 1] = nb > 0 ? nb + X : 0;  // virtual blocks: start cost + data
   }
@@ -1116,7 +1149,8 @@ __device__ __forceinline__ bool scan_geometry(const DecodeArgs& a, int B, int W,
 
 // LOQ: the two-part mode (q_bits 32) of code blocks: the query and the value
 // weights p * s_v each carried as fp16 high + low parts.
-template <int KB, int VB, bool ASYM, bool LOQ>
+// SPAN: attention with sinks and a sliding window (a.sinks, a.span): the units hold the blocks that are seen alone.
+template <int KB, int VB, bool ASYM, bool LOQ, bool SPAN>
 __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   using F = Fmt<KB, VB, ASYM>;
   constexpr int S = F::kStages;
@@ -1190,11 +1224,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   // first block-table entries ahead as well measured slower (register
   // pressure in the block loop), so the table is read after the wait.
   bool len_bad = false;
-  if (a.ahead) len_bad = scan_geometry(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
+  if (a.ahead) len_bad = scan_geometry<SPAN>(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- sequence geometry: clamped lengths and block prefix sums
-  if (!a.ahead) len_bad = scan_geometry(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
+  if (!a.ahead) len_bad = scan_geometry<SPAN>(a, B, W, X, len_s, pre_s, vpre_s, load_len, tid, warp, lane);
   if (len_bad && blockIdx.x == 0 && tid == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
   const long long T = (long long)H * vpre_s[B];  // virtual blocks in total
   const int U = B * H;
@@ -1292,7 +1326,8 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
         const int idx = local + lane;
         int v = 0;
         if (idx < nblk) {
-          v = a.table[size_t(a.pos ? rows_s[b] : b) * a.mbps + idx];
+          const int at = SPAN ? span_blocks(len_s[b], max(len_s[b] - W, 0), a.sinks, a.span).logical(idx) : idx;
+          v = a.table[size_t(a.pos ? rows_s[b] : b) * a.mbps + at];
           if (v < 0 || v >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
             v = 0;
@@ -1388,12 +1423,21 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   uint32_t qf[16];
   float qs0 = 0.f, qs1 = 0.f, qz0 = 0.f, qz1 = 0.f;
   int cur, cur_lq, qbuf = 0, nxt;
+  SpanBlocks cur_span{};
+  int cur_lo = 0;  // SPAN: the window's first token
+  auto span_of = [&](int b) {
+    if constexpr (SPAN) {
+      cur_span = span_blocks(len_s[b], cur_lq, a.sinks, a.span);
+      cur_lo = max(len_s[b] - a.span, 0);
+    }
+  };
   {
     // the first unit is known from x0: fetch its query group (and the next
     // unit's) while the first stage is still in flight
     const int b0 = b_first, h0 = h_first;
     cur = b0 * H + h0;
     cur_lq = W > 0 ? max(len_s[b0] - W, 0) : len_s[b0];
+    span_of(b0);
     prefetch_query(a, cur, 0, qraw, fraw, warp, lane);
     nxt = next_unit_in_range(geo, cur, x1);
     if (nxt >= 0) {
@@ -1434,6 +1478,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
       qbuf ^= 1;
       const int cb = cur / H;
       cur_lq = W > 0 ? max(len_s[cb] - W, 0) : len_s[cb];
+      span_of(cb);
       cp_async_wait<0>();
       if (!convert_query<F::kBf16, ASYM>(a, qbuf, qraw, fraw, qh, qlo_s, qs, sc, cphase, warp, lane, qf, qs0, qs1, qz0,
                                       qz1)) {
@@ -1455,7 +1500,8 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
       };
       auto kop = [&](int j) { return ASYM ? meta(j) + F::kKO : nullptr; };
       auto vop = [&](int j) { return ASYM ? meta(j) + F::kVO : nullptr; };
-      auto val = [&](int j) { return min(kBlock, cur_lq - (hd.y + j) * kBlock); };
+      auto tok = [&](int j) { return (SPAN ? cur_span.logical(hd.y + j) : hd.y + j) * kBlock; };  // first token
+      auto val = [&](int j) { return min(kBlock, cur_lq - tok(j)); };
       const int j0 = warp, j1 = warp + kConsumerWarps;
       if (F::kBPW == 2 && j1 < hd.z) {
         const uint8_t* const kbs[2] = {kp(j0), kp(j1)};
@@ -1465,8 +1511,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
         const float* const kos[2] = {kop(j0), kop(j1)};
         const float* const vos[2] = {vop(j0), vop(j1)};
         const int vals[2] = {val(j0), val(j1)};
-        process_blocks<KB, VB, 2, ASYM, LOQ>(kbs, vbs, kss, vss, kos, vos, vals, qf, qlo, qzo, qs0, qs1, qz0, qz1, st, lane,
-                                        km);
+        Seen<2> seen{};
+        if constexpr (SPAN)
+          seen = Seen<2>{{a.sinks - tok(j0), a.sinks - tok(j1)}, {cur_lo - tok(j0), cur_lo - tok(j1)}};
+        process_blocks<KB, VB, 2, ASYM, LOQ, SPAN>(kbs, vbs, kss, vss, kos, vos, vals, qf, qlo, qzo, qs0, qs1, qz0, qz1, st,
+                                              lane, km, seen);
       } else {
         const uint8_t* const kbs[1] = {kp(j0)};
         const uint8_t* const vbs[1] = {vp(j0)};
@@ -1475,8 +1524,10 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
         const float* const kos[1] = {kop(j0)};
         const float* const vos[1] = {vop(j0)};
         const int vals[1] = {val(j0)};
-        process_blocks<KB, VB, 1, ASYM, LOQ>(kbs, vbs, kss, vss, kos, vos, vals, qf, qlo, qzo, qs0, qs1, qz0, qz1, st, lane,
-                                        km);
+        Seen<1> seen{};
+        if constexpr (SPAN) seen = Seen<1>{{a.sinks - tok(j0)}, {cur_lo - tok(j0)}};
+        process_blocks<KB, VB, 1, ASYM, LOQ, SPAN>(kbs, vbs, kss, vss, kos, vos, vals, qf, qlo, qzo, qs0, qs1, qz0, qz1, st,
+                                              lane, km, seen);
       }
     }
     __syncwarp();
@@ -1489,7 +1540,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
 }
 
 // ------------------------------------------------------------------ host side
-template <int KB, int VB, bool ASYM, bool LOQ>
+template <int KB, int VB, bool ASYM, bool LOQ, bool SPAN = false>
 struct Kernel {
   using F = Fmt<KB, VB, ASYM>;
   static int smem_bytes(int B, bool rows) {
@@ -1504,11 +1555,11 @@ struct Kernel {
     if (done.count(dev)) return;
     int optin = 0;
     cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
+    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ, SPAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
     // Ask for the largest shared-memory carveout: the occupancy used to size
     // the single wave assumes it, and a smaller split (chosen by default)
     // would fit one CTA fewer per SM and turn the wave into 1.5 waves.
-    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    cudaFuncSetAttribute(decode_kernel<KB, VB, ASYM, LOQ, SPAN>, cudaFuncAttributePreferredSharedMemoryCarveout,
                          cudaSharedmemCarveoutMaxShared);
     done[dev] = true;
   }
@@ -1524,7 +1575,7 @@ struct Kernel {
     auto itc = cache.find(key);
     if (itc != cache.end()) return itc->second;
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<KB, VB, ASYM, LOQ>, kThreads, smem) != cudaSuccess)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_kernel<KB, VB, ASYM, LOQ, SPAN>, kThreads, smem) != cudaSuccess)
       n = 1;
     n = n < 1 ? 1 : n;
     cache[key] = n;
@@ -1547,7 +1598,7 @@ struct Kernel {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ>, p);
+    return cudaLaunchKernelEx(&cfg, decode_kernel<KB, VB, ASYM, LOQ, SPAN>, p);
   }
 };
 

@@ -134,6 +134,8 @@ struct DecodeArgs {
   const int* group_start = nullptr;    // [num_groups + 1]
   const int* prefix_blocks = nullptr;  // [num_groups]
   int num_groups = 0;
+  // attention with sinks: a query at position p sees tokens below `sinks` and behind p - span (0: all)
+  int sinks = 0, span = 0;
 };
 
 constexpr int kMaxGroups = 256;
@@ -185,6 +187,13 @@ cudaError_t launch_decode_asym(const DecodeArgs& a, cudaStream_t s);
 // The two-part fp16 query instantiations (kvq_decode_q32.cu).
 int decode_ctas_per_sm_q32(int k_bits, int v_bits, bool asym, int batch, bool rows);
 cudaError_t launch_decode_q32(const DecodeArgs& a, cudaStream_t s);
+// Attention with sinks and a sliding window: the same kernel over the blocks that are seen (kvq_sinks*.cu).
+int sinks_ctas_per_sm(const CacheView& c, int batch, bool rows);
+cudaError_t launch_sinks(const DecodeArgs& a, cudaStream_t s);
+int sinks_ctas_per_sm_asym(const CacheView& c, int batch, bool rows);
+cudaError_t launch_sinks_asym(const DecodeArgs& a, cudaStream_t s);
+int sinks_ctas_per_sm_q32(const CacheView& c, int batch, bool rows);
+cudaError_t launch_sinks_q32(const DecodeArgs& a, cudaStream_t s);
 // kvq_decode_shared: the suffixes (kvq_suffix*.cu), the prefix on query tiles
 // (kvq_shared_tiles.cu: mma.sync, kvq_shared_tc.cu: tcgen05) and the merge (kvq_shared.cu).
 // The *_ctas functions give one wave on the current device, 0 on failure.
@@ -202,5 +211,6 @@ cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s);
 // Needs no workspace.
 bool prefill_tiles_supported(const CacheView& c);
 cudaError_t launch_prefill_tiles(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_sinks_tiles(const DecodeArgs& a, cudaStream_t s);
 
 }  // namespace kvq

@@ -227,7 +227,8 @@ __device__ __forceinline__ void tile_scores(const uint8_t* kb, const uint4* qf, 
 // of dims 16 mt + g (O[2 mt]) and 16 mt + 8 + g (O[2 mt + 1]).
 template <int VB, bool LOW>
 __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&ph)[4], const uint32_t (&pl)[4],
-                                            float (&O)[16][4], int lane, uint32_t km, uint32_t c64, int valid) {
+                                            float (&O)[16][4], int lane, uint32_t km, uint32_t c64, int valid,
+                                            int head, int from) {
   const uint4* p = reinterpret_cast<const uint4*>(vb) + lane;
   // the high weights, then (two-part mode) the low weights into the same accumulator
   auto mma2 = [&](float (&d)[4], uint32_t b0, uint32_t b1) {
@@ -269,8 +270,8 @@ __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
       uint4 c = p[mt * 32];  // dims lo (x, y), dims hi (z, w): token pairs of the two slot halves
-      if (valid < kBlock) {  // slots behind the longest row are not data
-        const uint32_t even = bf16_data(lane, 0, valid), odd = bf16_data(lane, 1, valid);
+      if (valid < kBlock || (from > 0 && head < kBlock)) {  // slots that no row sees are not data
+        const uint32_t even = bf16_data(lane, 0, valid, head, from), odd = bf16_data(lane, 1, valid, head, from);
         c = make_uint4(c.x & even, c.y & odd, c.z & even, c.w & odd);
       }
       mma2(O[2 * mt], c.x, c.y);
@@ -298,12 +299,20 @@ __device__ __forceinline__ void tile_values(const uint8_t* vb, const uint32_t (&
 // finite, counts in the rows that see its token alone; otherwise (rows of one chunk) one sigma serves both
 // rows (separate ones cost the chunked prefill 1.7 %: 201.0 us for 197.6; the shared prefix of 4 sequences of 2048
 // tokens 2 %, 21.8 us and 22.3).
-template <int KB, int VB, bool ASYM, bool LOQ, bool APART>
+// SPAN: row r sees tokens below ts.sinks and from its length - ts.span on; none of the rows sees those between
+// ts.sinks and ts.from.
+struct TileSpan {
+  int sinks, span, from;
+};
+template <int KB, int VB, bool ASYM, bool LOQ, bool APART, bool SPAN = false>
 __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb, const float* ks, const float* vs,
                                            const float* ko, const float* vo, int tok0, int maxlen, int len0,
                                            int len1, float qs0, float qs1, float qz0, float qz1, const uint4* qf,
                                            const uint4* qlo, const float4* zo, TileState& st, int lane, uint32_t km,
-                                           uint32_t c64) {
+                                           uint32_t c64, const TileSpan& ts = TileSpan{}) {
+  // does a row of this length, and does any row, see the token at pos
+  auto sees = [&](int pos, int len) { return pos < len && (!SPAN || pos < ts.sinks || pos >= len - ts.span); };
+  auto seen = [&](int pos) { return pos < maxlen && (!SPAN || pos < ts.sinks || pos >= ts.from); };
   // offset-binary centre of the code conversion: c' = u - kKC (zero points: m' = m + kKC * s)
   constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f), kVC = VB == 8 ? 128.f : (VB == 4 ? 8.f : 2.f);
   // 2-bit blocks: one scale (and zero point) for the whole block
@@ -343,15 +352,15 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
     for (int j = 0; j < 2; ++j) {
       const int pos = tok0 + 8 * n + 2 * t + j;
       if constexpr (ASYM) {
-        x[n][j] = pos < len0 ? fmaf(x[n][j], ksc[n][j], mk[n][j] * qz0) * qs0 : kNegInf;
-        x[n][2 + j] = pos < len1 ? fmaf(x[n][2 + j], ksc[n][j], mk[n][j] * qz1) * qs1 : kNegInf;
-        mv[n][j] = pos < maxlen ? mv[n][j] : 0.f;
+        x[n][j] = sees(pos, len0) ? fmaf(x[n][j], ksc[n][j], mk[n][j] * qz0) * qs0 : kNegInf;
+        x[n][2 + j] = sees(pos, len1) ? fmaf(x[n][2 + j], ksc[n][j], mk[n][j] * qz1) * qs1 : kNegInf;
+        mv[n][j] = seen(pos) ? mv[n][j] : 0.f;
       } else {
-        x[n][j] = pos < len0 ? x[n][j] * (ksc[n][j] * qs0) : kNegInf;
-        x[n][2 + j] = pos < len1 ? x[n][2 + j] * (ksc[n][j] * qs1) : kNegInf;
+        x[n][j] = sees(pos, len0) ? x[n][j] * (ksc[n][j] * qs0) : kNegInf;
+        x[n][2 + j] = sees(pos, len1) ? x[n][2 + j] * (ksc[n][j] * qs1) : kNegInf;
       }
       // scales of slots past the sub-pass's longest row are not data
-      vsc[n][j] = pos < maxlen ? vsc[n][j] : 0.f;
+      vsc[n][j] = seen(pos) ? vsc[n][j] : 0.f;
       svm = APART ? max_nan(svm, vsc[n][j]) : fmaxf(svm, vsc[n][j]);
     }
   float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
@@ -392,7 +401,7 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int pos = tok0 + 8 * n + 2 * t + j;
-          const bool in0 = pos < len0, in1 = pos < len1;
+          const bool in0 = sees(pos, len0), in1 = sees(pos, len1);
           if (!(vsc[n][j] <= kFloatMax)) {
             bad0 |= in0;
             bad1 |= in1;
@@ -474,7 +483,8 @@ __device__ __forceinline__ void tile_block(const uint8_t* kb, const uint8_t* vb,
       pl[i] = pack_half2(wr[i][0] - hf.x, wr[i][1] - hf.y);
     }
   }
-  tile_values<VB, LOQ>(vb, ph, pl, st.O, lane, km, c64, maxlen - tok0);
+  tile_values<VB, LOQ>(vb, ph, pl, st.O, lane, km, c64, maxlen - tok0, SPAN ? ts.sinks - tok0 : kBlock,
+                       SPAN ? ts.from - tok0 : 0);
 }
 
 // Query vector v of a tile (src: its 128 bf16 values, or null for an unused
