@@ -11,6 +11,8 @@
  *   kvq_decode_sinks, kvq_prefill_sinks   a sliding window and first tokens that stay visible
  *   kvq_attn_mass      the attention weight each cached token received, summed up
  *   kvq_evict          keep each sequence's heaviest tokens, in place
+ *   kvq_pages_update   blocks shared, forked, freed and handed out on the device; kvq_pages_compact,
+ *                      kvq_copy_blocks, kvq_fork_windows
  *   kvq_prefill        causal attention of a chunk of new tokens
  * plus kvq_dequant (reads the stored cache back) and a few helpers.
  *
@@ -109,6 +111,7 @@ typedef enum {
 #define KVQ_DEVERR_RANGE 8u     /* reserved: no longer raised (any value scale is   */
                                 /* decoded; the weights are kept in fp16 range)     */
 #define KVQ_DEVERR_POSITION 16u /* append: sequence index or position out of range  */
+#define KVQ_DEVERR_NO_BLOCKS 32u /* kvq_pages_update: too few free blocks            */
 
 /* kvq_append modes */
 #define KVQ_APPEND_QUANT 0 /* quantize the new vectors into the block store at pos      */
@@ -608,6 +611,85 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
                      const int32_t* token_pos, int32_t* token_pos_out, const int32_t* next_pos,
                      const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq, int32_t* new_lens,
                      int32_t* source, uint32_t* err_word, void* stream);
+
+/*
+ * kvq_pages_update -- the blocks of a batch between two steps: rows fork, end, lose what a sliding window
+ * has passed, and get room for coming tokens.  The pages take the block table as given; this keeps one on the
+ * device.  One block number stands for that block of every layer's pools.
+ *   refs : device int32 [num_blocks], how many table entries hold each block, and the caller's own
+ *          claims on it (a prefix kept for later requests); 0 is free
+ * Row r of the batch becomes sequence parent[r] (its own if parent is NULL; -1: the row ends):
+ *   lens_out[r]  = seq_lens[parent[r]], 0 for a row that has ended
+ *   table_out[r] = the parent's blocks that hold tokens (of length - window, where the last `window`
+ *                  tokens are in a bf16 ring), but those that no coming query of kvq_decode_sinks sees (span > 0:
+ *                  blocks behind the sinks whose last token is below length - span): -1;
+ *                  a row that is its own parent keeps the blocks handed out to it that are still empty
+ * and then, for every row that goes on,
+ *   - its last block, if there is room left in it, is its own: of the rows that share it the lowest keeps it
+ *     unless other entries or claims hold it too, the others get a new block and a pair (source,
+ *     destination) in `copies`, in the order of rows
+ *   - it has a block of its own for each of the next `room` tokens
+ * New blocks are the free ones from the lowest number on, in the order of rows and their entries.
+ * Blocks that no entry holds any more are free at once, for this call's rows as well.
+ *   block_table  : device int32 [batch][max_blocks_per_seq], -1 where there is no block
+ *   window       : the caches' bf16 window, or 0; span 0: no sliding window, else at least `window`
+ *                  (KVQ_ERR_UNSUPPORTED)
+ *   refs_out     : may be refs itself; table_out and lens_out are not block_table and seq_lens
+ *                  (KVQ_ERR_INVALID_ARG): a program keeps two of each and uses them in turn
+ *   copies       : device int32 [batch][2], 8-byte aligned; num_copies: device int32.  kvq_copy_blocks next on
+ *                  the stream, in every layer; kvq_fork_windows too, where there is a bf16 window
+ *   workspace    : >= kvq_pages_workspace_size bytes; what it holds does not matter, one per
+ *                  concurrently running call
+ * Errors: NO_BLOCKS: the free blocks do not suffice, and nothing changes (the outputs are the inputs, no copies);
+ * POSITION: a parent outside [-1, batch), the row stays itself; SEQ_LEN: a length (or length and room) < 0
+ * or beyond the table's capacity: cut; BLOCK_ID: an entry outside [-1, num_blocks), or a last block that is missing: -1.
+ * refs that are less than the entries in the table are the caller's mistake: blocks in use may be handed out.
+ * Requirements: batch in 1..4096.
+ */
+kvq_status kvq_pages_update(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* parent, int32_t batch, int32_t max_blocks_per_seq, int32_t window,
+                            int32_t room, int32_t sinks, int32_t span, int32_t* refs_out, int32_t* table_out,
+                            int32_t* lens_out, int32_t* copies, int32_t* num_copies, void* workspace,
+                            size_t workspace_bytes, uint32_t* err_word, void* stream);
+
+/*
+ * kvq_pages_compact -- the blocks in use (refs > 0) to the front of their pools, so that the pools can be cut to
+ * counts[1] blocks, or grown ones copied cheaply.  Blocks that are there already stay; the i-th free block of
+ * the front takes the i-th block in use from behind it.
+ *   refs_out, table_out : may be refs and block_table themselves; batch 0: no table
+ *   moves  : device int32 [num_blocks / 2][2] (at least one pair), 8-byte aligned: (source, destination),
+ *            for kvq_copy_blocks in every layer
+ *   counts : device int32 [2]: moves, blocks in use
+ * A table entry outside [-1, num_blocks), or one that holds a free block behind the front, is left as it is
+ * (BLOCK_ID).  Workspace as kvq_pages_update.
+ */
+kvq_status kvq_pages_compact(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, int32_t batch,
+                             int32_t max_blocks_per_seq, int32_t* refs_out, int32_t* table_out, int32_t* moves,
+                             int32_t* counts, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                             void* stream);
+
+kvq_status kvq_pages_workspace_size(int32_t num_blocks, size_t* bytes);
+
+/*
+ * kvq_copy_blocks -- copy whole blocks (codes, scales, zero points as they are stored) within the pools of every cache.
+ *   caches   : host, [num_caches]: the layers
+ *   copies   : device int32 [max_copies][2]: source and destination; the first *num_copies (device) of them are
+ *              done.  No destination is a source or another's destination (kvq_pages_update and
+ *              kvq_pages_compact give such pairs).
+ * A pair out of range sets KVQ_DEVERR_BLOCK_ID and is skipped.
+ */
+kvq_status kvq_copy_blocks(const kvq_cache_desc* caches, int32_t num_caches, const int32_t* copies,
+                           const int32_t* num_copies, int32_t max_copies, uint32_t* err_word, void* stream);
+
+/*
+ * kvq_fork_windows -- the bf16 rings of a batch whose rows become other rows' sequences, in every cache and in
+ * place: row r's ring is what row parent[r]'s was (parent[r] = -1: left as it is).  Every parent may have any
+ * number of children.
+ *   parent : device int32 [batch]; one outside [-1, batch) sets KVQ_DEVERR_POSITION and the row is left as it is
+ * Requirements: every cache has a window of `batch` rows at least, batch <= 4096.
+ */
+kvq_status kvq_fork_windows(const kvq_cache_desc* caches, int32_t num_caches, const int32_t* parent, int32_t batch,
+                            uint32_t* err_word, void* stream);
 
 /*
  * kvq_dequant -- read the block store back: x_hat = RN32(code * s)

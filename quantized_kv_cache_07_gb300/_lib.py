@@ -26,6 +26,7 @@ KVQ_DEVERR_SEQ_LEN = 2
 KVQ_DEVERR_TIMEOUT = 4
 KVQ_DEVERR_RANGE = 8
 KVQ_DEVERR_POSITION = 16
+KVQ_DEVERR_NO_BLOCKS = 32
 
 APPEND_QUANT = 0
 APPEND_RING = 1
@@ -74,6 +75,14 @@ class DecodePlan(ctypes.Structure):
                 ("partial_slots", c_int32), ("workspace_bytes", c_size_t)]
 
 
+class CacheList:
+    """The caches of a model's layers as one argument (kvq_copy_blocks, kvq_fork_windows); made once."""
+
+    def __init__(self, descs):
+        self.held = list(descs)  # with the tensors that they keep
+        self.array = (CacheDesc * len(self.held))(*self.held)
+
+
 _lib = None
 
 # Exported symbol -> (restype, argtypes)
@@ -101,6 +110,14 @@ SIGNATURES = {
     "kvq_evict": (c_int32, [POINTER(CacheDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
                             c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
                             c_void_p]),
+    "kvq_pages_update": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                   c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_size_t, c_void_p, c_void_p]),
+    "kvq_pages_compact": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "kvq_pages_workspace_size": (c_int32, [c_int32, POINTER(c_size_t)]),
+    "kvq_copy_blocks": (c_int32, [POINTER(CacheDesc), c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
+    "kvq_fork_windows": (c_int32, [POINTER(CacheDesc), c_int32, c_void_p, c_int32, c_void_p, c_void_p]),
     "kvq_make_decode_plan": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
                                        POINTER(DecodePlan)]),
     "kvq_decode_device_plan": (c_int32, [POINTER(CacheDesc), c_int32, c_int32, c_int32, POINTER(DecodePlan)]),
@@ -357,6 +374,55 @@ def kvq_evict(desc: CacheDesc, mass, mass_out, seq_lens, keep, block_table, batc
                             arg(next_pos, arg.i32, each), arg(block_table, arg.i32, (batch, max_blocks_per_seq)), batch,
                             max_blocks_per_seq, arg(new_lens, arg.i32, each), arg(source, arg.i32, rows),
                             arg.word(err_word), arg.stream(stream)), arg.where)
+
+
+def kvq_pages_workspace_size(num_blocks: int) -> int:
+    out = c_size_t(0)
+    _check(load().kvq_pages_workspace_size(num_blocks, ctypes.byref(out)), "kvq_pages_workspace_size")
+    return out.value
+
+
+def kvq_pages_update(refs, block_table, seq_lens, refs_out, table_out, lens_out, copies, num_copies, parent=None,
+                     room: int = 0, window: int = 0, sinks: int = 0, span: int = 0, workspace=None, err_word=None,
+                     stream=None):
+    """kvq_pages_update; refs are int32 [num_blocks], tables [batch, max_blocks_per_seq], copies [batch, 2]."""
+    arg = _Args("kvq_pages_update")
+    n, (batch, width) = int(refs.shape[0]), block_table.shape
+    _check(load().kvq_pages_update(arg(refs, arg.i32, (n,)), n, arg(block_table, arg.i32, (batch, width)),
+                                   arg(seq_lens, arg.i32, (batch,)), arg(parent, arg.i32, (batch,)), batch, width, window,
+                                   room, sinks, span, arg(refs_out, arg.i32, (n,)), arg(table_out, arg.i32, (batch, width)),
+                                   arg(lens_out, arg.i32, (batch,)), arg.room(copies, arg.i32, 2 * batch),
+                                   arg.room(num_copies, arg.i32, 1), arg.room(workspace, arg.u8, 0),
+                                   0 if workspace is None else workspace.numel(), arg.word(err_word),
+                                   arg.stream(stream)), arg.where)
+
+
+def kvq_pages_compact(refs, block_table, refs_out, table_out, moves, counts, workspace=None, err_word=None, stream=None):
+    """kvq_pages_compact; moves are int32 [num_blocks / 2, 2] (one pair at least), counts [2]; without a table, None
+    twice."""
+    arg = _Args("kvq_pages_compact")
+    n = int(refs.shape[0])
+    batch, width = (0, 0) if block_table is None else block_table.shape
+    _check(load().kvq_pages_compact(arg(refs, arg.i32, (n,)), n, arg(block_table, arg.i32, (batch, width)), batch, width,
+                                    arg(refs_out, arg.i32, (n,)), arg(table_out, arg.i32, (batch, width)),
+                                    arg.room(moves, arg.i32, 2 * max(n // 2, 1)), arg.room(counts, arg.i32, 2),
+                                    arg.room(workspace, arg.u8, 0), 0 if workspace is None else workspace.numel(),
+                                    arg.word(err_word), arg.stream(stream)), arg.where)
+
+
+def kvq_copy_blocks(caches: CacheList, copies, num_copies, err_word=None, stream=None):
+    """kvq_copy_blocks of the first num_copies[0] pairs of copies (int32 [.., 2])."""
+    arg = _Args("kvq_copy_blocks")
+    pairs = copies.numel() // 2
+    _check(load().kvq_copy_blocks(caches.array, len(caches.held), arg.room(copies, arg.i32, 2 * pairs),
+                                  arg.room(num_copies, arg.i32, 1), pairs, arg.word(err_word), arg.stream(stream)),
+           arg.where)
+
+
+def kvq_fork_windows(caches: CacheList, parent, batch: int, err_word=None, stream=None):
+    arg = _Args("kvq_fork_windows")
+    _check(load().kvq_fork_windows(caches.array, len(caches.held), arg(parent, arg.i32, (batch,)), batch,
+                                   arg.word(err_word), arg.stream(stream)), arg.where)
 
 
 def kvq_make_decode_plan(batch: int, q_heads: int, kv_heads: int, window: int, num_sms: int, ctas_per_sm: int,

@@ -790,4 +790,135 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
   return KVQ_OK;
 }
 
+kvq_status kvq_pages_workspace_size(int32_t num_blocks, size_t* bytes) {
+  if (!bytes || num_blocks < 1) return KVQ_ERR_INVALID_ARG;
+  *bytes = kvq::pages_workspace_bytes(num_blocks);
+  return KVQ_OK;
+}
+
+kvq_status kvq_pages_update(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* parent, int32_t batch, int32_t max_blocks_per_seq, int32_t window,
+                            int32_t room, int32_t sinks, int32_t span, int32_t* refs_out, int32_t* table_out,
+                            int32_t* lens_out, int32_t* copies, int32_t* num_copies, void* workspace,
+                            size_t workspace_bytes, uint32_t* err_word, void* stream) {
+  if (num_blocks < 1 || batch < 1 || max_blocks_per_seq < 1 || window < 0 || room < 0 || sinks < 0 || span < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (batch > kvq::kMaxBatch || window > kMaxWindow || window % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (span > 0 && span < window) return KVQ_ERR_UNSUPPORTED;
+  if ((long long)batch * max_blocks_per_seq > 0x7fffffffll) return KVQ_ERR_UNSUPPORTED;  // entries are counted in 32 bits
+  if (!refs || !block_table || !seq_lens || !refs_out || !table_out || !lens_out || !copies || !num_copies)
+    return KVQ_ERR_INVALID_ARG;
+  // rows read one another's entries
+  if (table_out == block_table || lens_out == seq_lens) return KVQ_ERR_INVALID_ARG;
+  if (!aligned8(copies)) return KVQ_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kvq::pages_workspace_bytes(num_blocks)) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  kvq::PagesArgs a{};
+  a.refs = refs;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.parent = parent;
+  a.num_blocks = num_blocks;
+  a.B = batch;
+  a.width = max_blocks_per_seq;
+  a.window = window;
+  a.room = room;
+  a.sinks = sinks;
+  a.span = span;
+  a.refs_out = refs_out;
+  a.table_out = table_out;
+  a.lens_out = lens_out;
+  a.copies = copies;
+  a.num_copies = num_copies;
+  a.ws = static_cast<int*>(workspace);
+  a.err = err_word;
+  return kvq::launch_pages_update(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_pages_compact(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, int32_t batch,
+                             int32_t max_blocks_per_seq, int32_t* refs_out, int32_t* table_out, int32_t* moves,
+                             int32_t* counts, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                             void* stream) {
+  if (num_blocks < 1 || batch < 0 || (batch > 0 && max_blocks_per_seq < 1)) return KVQ_ERR_INVALID_ARG;
+  if (!refs || !refs_out || !moves || !counts || (batch > 0 && (!block_table || !table_out))) return KVQ_ERR_INVALID_ARG;
+  if (!aligned8(moves)) return KVQ_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < kvq::pages_workspace_bytes(num_blocks)) return KVQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
+  kvq::PagesArgs a{};
+  a.refs = refs;
+  a.table = block_table;
+  a.num_blocks = num_blocks;
+  a.B = batch;
+  a.width = max_blocks_per_seq;
+  a.refs_out = refs_out;
+  a.table_out = table_out;
+  a.copies = moves;
+  a.num_copies = counts;
+  a.ws = static_cast<int*>(workspace);
+  a.err = err_word;
+  return kvq::launch_pages_compact(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_copy_blocks(const kvq_cache_desc* caches, int32_t num_caches, const int32_t* copies,
+                           const int32_t* num_copies, int32_t max_copies, uint32_t* err_word, void* stream) {
+  if (num_caches < 0 || max_copies < 0 || (num_caches > 0 && !caches)) return KVQ_ERR_INVALID_ARG;
+  for (int i = 0; i < num_caches; ++i) {
+    const kvq_status st = check_cache(&caches[i]);
+    if (st != KVQ_OK) return st;
+  }
+  if (num_caches == 0 || max_copies == 0) return KVQ_OK;
+  if (!copies || !num_copies) return KVQ_ERR_INVALID_ARG;
+  if (!aligned8(copies)) return KVQ_ERR_ALIGNMENT;
+  for (int first = 0, last = 0; first < num_caches; first = last) {
+    // a run of layers of one shape
+    const kvq::CacheView c = view(&caches[first]);
+    kvq::CopyArgs a{};
+    a.H = c.H;
+    a.num_blocks = c.num_blocks;
+    a.k_bytes = kvq::block_bytes(c.k_bits);
+    a.v_bytes = kvq::block_bytes(c.v_bits);
+    a.meta_bytes = c.k_bits == 16 ? 0 : c.meta_floats * 4;
+    a.copies = copies;
+    a.num_copies = num_copies;
+    a.max_copies = max_copies;
+    a.err = err_word;
+    for (last = first; last < num_caches && a.layers < kvq::kCopyLayers; ++last) {
+      const kvq::CacheView l = view(&caches[last]);
+      if (l.H != c.H || l.num_blocks != c.num_blocks || l.k_bits != c.k_bits || l.v_bits != c.v_bits ||
+          l.meta_floats != c.meta_floats)
+        break;
+      a.pools[a.layers++] = {l.k_codes, l.v_codes, reinterpret_cast<uint8_t*>(l.meta)};
+    }
+    if (kvq::launch_copy_blocks(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  }
+  return KVQ_OK;
+}
+
+kvq_status kvq_fork_windows(const kvq_cache_desc* caches, int32_t num_caches, const int32_t* parent, int32_t batch,
+                            uint32_t* err_word, void* stream) {
+  if (num_caches < 0 || batch < 0 || (num_caches > 0 && !caches)) return KVQ_ERR_INVALID_ARG;
+  if (batch > kvq::kMaxBatch) return KVQ_ERR_UNSUPPORTED;
+  for (int i = 0; i < num_caches; ++i) {
+    const kvq_status st = check_cache(&caches[i]);
+    if (st != KVQ_OK) return st;
+    if (caches[i].window == 0 || caches[i].window_batch < batch) return KVQ_ERR_INVALID_ARG;
+  }
+  if (num_caches == 0 || batch == 0) return KVQ_OK;
+  if (!parent) return KVQ_ERR_INVALID_ARG;
+  for (int first = 0, last = 0; first < num_caches; first = last) {
+    const int row = caches[first].num_kv_heads * caches[first].window * kHeadDim * 2;
+    kvq::RingArgs a{};
+    a.B = batch;
+    a.row_bytes = row;
+    a.parent = parent;
+    a.err = err_word;
+    for (last = first; last < num_caches && a.layers < kvq::kCopyLayers; ++last) {
+      if (caches[last].num_kv_heads * caches[last].window * kHeadDim * 2 != row) break;
+      a.rings[a.layers++] = {static_cast<uint8_t*>(caches[last].k_window), static_cast<uint8_t*>(caches[last].v_window)};
+    }
+    if (kvq::launch_fork_windows(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
+  }
+  return KVQ_OK;
+}
+
 }  // extern "C"

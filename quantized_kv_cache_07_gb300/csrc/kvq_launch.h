@@ -92,6 +92,54 @@ struct EvictArgs {
   uint32_t* err;
 };
 
+// kvq_pages_update and kvq_pages_compact (which has no parents, lengths or windows; copies: its moves,
+// num_copies: moves and live pages).
+struct PagesArgs {
+  const int* refs;
+  const int* table;   // [B][width]
+  const int* lens;    // [B]
+  const int* parent;  // [B] or null: every row its own
+  int num_blocks, B, width;
+  int window, room, sinks, span;
+  int* refs_out;
+  int* table_out;
+  int* lens_out;
+  int* copies;  // [..][2]
+  int* num_copies;
+  int* ws;
+  uint32_t* err;
+};
+
+constexpr int kCopyLayers = 64;  // of one launch
+
+struct CopyPools {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* meta;
+};
+
+struct CopyArgs {
+  CopyPools pools[kCopyLayers];
+  int layers, H, num_blocks;
+  int k_bytes, v_bytes, meta_bytes;  // of a block of one head
+  const int* copies;
+  const int* num_copies;
+  int max_copies;
+  uint32_t* err;
+};
+
+struct RingPools {
+  uint8_t* k;
+  uint8_t* v;
+};
+
+struct RingArgs {
+  RingPools rings[kCopyLayers];
+  int layers, B, row_bytes, slice_bytes;
+  const int* parent;
+  uint32_t* err;
+};
+
 struct DequantArgs {
   CacheView c;
   const int* slots;
@@ -177,6 +225,12 @@ cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float*
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t s);
+// Pages (kvq_pages.cu).
+size_t pages_workspace_bytes(int num_blocks);
+cudaError_t launch_pages_update(PagesArgs a, cudaStream_t s);
+cudaError_t launch_pages_compact(PagesArgs a, cudaStream_t s);
+cudaError_t launch_copy_blocks(CopyArgs a, cudaStream_t s);
+cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s);
 // Resident decode CTAs per SM for this cache format and batch (occupancy
 // query on the current device, cached); 0 for an unsupported format.
 int decode_ctas_per_sm_for(int k_bits, int v_bits, bool asym, int q_bits, int batch, bool rows = false);
