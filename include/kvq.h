@@ -6,7 +6,8 @@
  *   kvq_decode  fused dequantize-on-load split attention for one decode step
  * Beside them:
  *   kvq_rope_append    kvq_append of keys turned by their rotary positions, and the
- *                      turned queries, in one call (kvq_rope_table: its cosines and sines)
+ *                      turned queries, in one call (kvq_rope_table: its cosines and sines);
+ *                      kvq_norm_rope_append: with norms of the heads before
  *   kvq_decode_shared  kvq_decode for sequences that share a prefix, read once for all
  *   kvq_decode_sinks, kvq_prefill_sinks   a sliding window and first tokens that stay visible
  *   kvq_attn_mass      the attention weight each cached token received, summed up
@@ -297,6 +298,28 @@ kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rop
                            int64_t v_stride, int32_t n, const int32_t* rope_pos, const int32_t* seq_idx,
                            const int32_t* pos, int32_t mode, const int32_t* block_table, int32_t batch,
                            int32_t max_blocks_per_seq, uint32_t* err_word, void* stream);
+
+/* Norms of each head of queries and keys. */
+typedef struct {
+  float eps;                /* 1e-12 .. 1                                                    */
+  int32_t per_head;         /* 0: one weight vector [128] for all heads; 1: [heads][128]     */
+  const float* q_weight;    /* device float32, 16-byte aligned, or NULL: ones                */
+  const float* k_weight;
+} kvq_norm_desc;
+
+/*
+ * kvq_norm_rope_append -- kvq_rope_append of queries and keys whose heads are normed first:
+ *   z_j = x_j / sqrt(mean(x^2) + eps) * weight_j over the head's 128 dimensions,
+ * then turned (dimensions behind rotary_dim are normed too).  Computed as the exact value rounded to float32 and
+ * then to bf16, once, up to one case in about 2^30 (weights that differ from one are float32: 1 + w of a
+ * model that stores w is added by the caller).  Values are stored as they come.  Everything else as kvq_rope_append.
+ */
+kvq_status kvq_norm_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const kvq_norm_desc* norm,
+                                const void* q, int32_t q_heads, int64_t q_stride, void* q_out, const void* k_new,
+                                int64_t k_stride, const void* v_new, int64_t v_stride, int32_t n,
+                                const int32_t* rope_pos, const int32_t* seq_idx, const int32_t* pos, int32_t mode,
+                                const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq,
+                                uint32_t* err_word, void* stream);
 
 /* Work decomposition of kvq_decode (host-only arithmetic, no CUDA calls). */
 typedef struct {

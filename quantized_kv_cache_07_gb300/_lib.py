@@ -69,6 +69,11 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("rotary_dim", c_int32), ("interleaved", c_int32), ("max_pos", c_int32), ("table", c_void_p)]
 
 
+class NormDesc(ctypes.Structure):
+    """Mirror of kvq_norm_desc."""
+    _fields_ = [("eps", c_float), ("per_head", c_int32), ("q_weight", c_void_p), ("k_weight", c_void_p)]
+
+
 class DecodePlan(ctypes.Structure):
     """Mirror of kvq_decode_plan."""
     _fields_ = [("stream_ctas", c_int32), ("window_ctas", c_int32), ("units", c_int32),
@@ -95,6 +100,9 @@ SIGNATURES = {
     "kvq_rope_append": (c_int32, [POINTER(CacheDesc), POINTER(RopeDesc), c_void_p, c_int32, c_int64, c_void_p,
                                   c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p, c_void_p,
                                   c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "kvq_norm_rope_append": (c_int32, [POINTER(CacheDesc), POINTER(RopeDesc), POINTER(NormDesc), c_void_p, c_int32, c_int64,
+                                       c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_void_p, c_void_p,
+                                       c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
     "kvq_decode_shared": (c_int32, [POINTER(CacheDesc), c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int32, c_int32,
                                     c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_size_t, c_void_p,
                                     c_void_p]),
@@ -277,18 +285,35 @@ def kvq_rope_append(desc: CacheDesc, rope: RopeDesc, q, q_heads: int, q_out, k_n
     """kvq_rope_append: ``pos`` are the rope positions (int32 [n], None to use ``slot``) and ``slot`` the cache
     positions (the C argument pos).  q, k_new and v_new may be slices of one projection [n, heads * 128]: their row
     strides are taken from the tensors.  q and q_out, or k_new and v_new, may be None."""
-    arg = _Args("kvq_rope_append")
+    _rope_append(_Args("kvq_rope_append"), desc, rope, (), q, q_heads, q_out, k_new, v_new, pos, seq_idx, slot, mode,
+                 block_table, batch, max_blocks_per_seq, err_word, stream)
+
+
+def kvq_norm_rope_append(desc: CacheDesc, rope: RopeDesc, norm: NormDesc, q, q_heads: int, q_out, k_new, v_new, pos,
+                         seq_idx, slot, mode: int, block_table, batch: int, max_blocks_per_seq: int, err_word=None,
+                         stream=None):
+    """kvq_norm_rope_append; ``norm`` as cache.HeadNorm makes it, the other arguments as kvq_rope_append's."""
+    arg = _Args("kvq_norm_rope_append")
+    for held, heads in zip(getattr(norm, "heads", ()), (q_heads, desc.num_kv_heads)):
+        if held is not None and held < heads:  # weights of fewer heads than there are
+            raise KvqError(KVQ_ERR_INVALID_ARG, arg.where)
+    _rope_append(arg, desc, rope, (ctypes.byref(norm),), q, q_heads, q_out, k_new, v_new, pos,
+                 seq_idx, slot, mode, block_table, batch, max_blocks_per_seq, err_word, stream)
+
+
+def _rope_append(arg, desc, rope, norm, q, q_heads, q_out, k_new, v_new, pos, seq_idx, slot, mode, block_table, batch,
+                 max_blocks_per_seq, err_word, stream):
     ref = pos if pos is not None else slot
     n = int(ref.shape[0])
     qp, qs = arg.rows(q, q_heads, n)
     kp, ks = arg.rows(k_new, desc.num_kv_heads, n)
     vp, vs = arg.rows(v_new, desc.num_kv_heads, n)
     places = batch * max_blocks_per_seq if k_new is not None and mode != APPEND_RING else 0  # read by the write alone
-    _check(load().kvq_rope_append(ctypes.byref(desc), ctypes.byref(rope), qp, q_heads, qs,
-                                  arg.room(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
-                                  arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode,
-                                  arg.room(block_table, arg.i32, places), batch, max_blocks_per_seq, arg.word(err_word),
-                                  arg.stream(stream) if n else None), arg.where)
+    entry = getattr(load(), arg.where)
+    _check(entry(ctypes.byref(desc), ctypes.byref(rope), *norm, qp, q_heads, qs,
+                 arg.room(q_out, arg.bf16, n * q_heads * 128), kp, ks, vp, vs, n, arg(pos, arg.i32, (n,)),
+                 arg(seq_idx, arg.i32, (n,)), arg(slot, arg.i32, (n,)), mode, arg.room(block_table, arg.i32, places), batch,
+                 max_blocks_per_seq, arg.word(err_word), arg.stream(stream) if n else None), arg.where)
 
 
 def kvq_decode_shared_workspace_size(desc: CacheDesc, batch: int, q_heads: int, num_groups: int) -> int:

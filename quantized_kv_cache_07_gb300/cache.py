@@ -110,6 +110,66 @@ class RopeTable:
         self.desc.held = self.table  # a descriptor kept without its RopeTable still points at live memory
 
 
+class HeadNorm:
+    """Weights and eps of one layer's norms of query and key heads; ``desc`` goes to _lib.kvq_norm_rope_append.
+
+    A weight is [128] for all heads, [heads, 128] for one each (both then), or None for ones; kept as float32.
+    """
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, device="cuda"):
+        def held(w):
+            return None if w is None else torch.as_tensor(w).to(device=device, dtype=torch.float32).contiguous()
+        self.q_weight, self.k_weight = held(q_weight), held(k_weight)
+        given = [w for w in (self.q_weight, self.k_weight) if w is not None]
+        if any(w.dim() not in (1, 2) or w.shape[-1] != HEAD_DIM for w in given) or len({w.dim() for w in given}) > 1:
+            raise ValueError("weights are [128] or [heads, 128], both alike")
+        self.heads = tuple(w.shape[0] if w is not None and w.dim() == 2 else None for w in (self.q_weight, self.k_weight))
+        self.desc = _lib.NormDesc(eps=eps, per_head=int(bool(given) and given[0].dim() == 2),
+                                  q_weight=None if self.q_weight is None else self.q_weight.data_ptr(),
+                                  k_weight=None if self.k_weight is None else self.k_weight.data_ptr())
+        self.desc.held = given  # as RopeTable's descriptor
+        self.desc.heads = self.heads
+
+
+class Pages:
+    """Block tables, lengths and reference counts of a batch that shares one block number space over all layers' caches.
+
+    ``table``, ``lens`` and ``refs`` are what the other calls read; update() and compact() change them (tables and
+    lengths swap with a second pair, so a captured update is captured with the next one).  A call of either goes to every cache
+    of ``caches``: pages that have to be copied or moved are, and so are the rings of a bf16 window.
+    """
+
+    def __init__(self, caches, batch: int, max_blocks: int, sinks: int = 0, span: int = 0):
+        first = caches[0]
+        if any((c.num_blocks, c.window) != (first.num_blocks, first.window) for c in caches):
+            raise ValueError("the caches of one model hold the same blocks and the same window")
+        self.window, self.sinks, self.span = first.window, sinks, span
+        self.caches = _lib.CacheList([c.desc for c in caches])
+        self.held = list(caches)
+        zeros = lambda *shape: torch.zeros(*shape, dtype=torch.int32, device=first.device)
+        self.refs = zeros(first.num_blocks)
+        self.table, self._table = zeros(batch, max_blocks) - 1, zeros(batch, max_blocks)
+        self.lens, self._lens = zeros(batch), zeros(batch)
+        self.copies, self.counts = zeros(max(batch, first.num_blocks // 2, 1), 2), zeros(2)
+        self.workspace = torch.empty(_lib.kvq_pages_workspace_size(first.num_blocks), dtype=torch.uint8, device=first.device)
+
+    def update(self, parent=None, room: int = 1, err_word=None, stream=None):
+        """kvq_pages_update: rows become their parents' sequences (-1 ends one), with room for the next ``room`` tokens."""
+        _lib.kvq_pages_update(self.refs, self.table, self.lens, self.refs, self._table, self._lens, self.copies, self.counts,
+                              parent=parent, room=room, window=self.window, sinks=self.sinks, span=self.span,
+                              workspace=self.workspace, err_word=err_word, stream=stream)
+        self.table, self._table, self.lens, self._lens = self._table, self.table, self._lens, self.lens
+        _lib.kvq_copy_blocks(self.caches, self.copies[: len(self.lens)], self.counts, err_word=err_word, stream=stream)
+        if self.window and parent is not None:
+            _lib.kvq_fork_windows(self.caches, parent, len(self.lens), err_word=err_word, stream=stream)
+
+    def compact(self, err_word=None, stream=None):
+        """kvq_pages_compact; ``counts[1]`` is then the number of blocks in use, all of them in front."""
+        _lib.kvq_pages_compact(self.refs, self.table, self.refs, self.table, self.copies, self.counts,
+                               workspace=self.workspace, err_word=err_word, stream=stream)
+        _lib.kvq_copy_blocks(self.caches, self.copies, self.counts, err_word=err_word, stream=stream)
+
+
 class DecodeWorkspace:
     """Scratch for the split-attention partials and merge counters of kvq_decode."""
 

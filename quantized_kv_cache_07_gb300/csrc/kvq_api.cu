@@ -364,6 +364,85 @@ kvq_status prefill_call(const kvq_cache_desc* cache, const void* q, int n, int q
   return KVQ_OK;
 }
 
+// kvq_rope_append (norm null) and kvq_norm_rope_append.
+kvq_status rope_call(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const kvq_norm_desc* norm, const void* q,
+                     int q_heads, int64_t q_stride, void* q_out, const void* k_new, int64_t k_stride, const void* v_new,
+                     int64_t v_stride, int n, const int32_t* rope_pos, const int32_t* seq_idx, const int32_t* pos,
+                     int mode, const int32_t* block_table, int batch, int max_blocks_per_seq, uint32_t* err_word,
+                     void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (norm) {
+    if (!(norm->eps >= 1e-12f && norm->eps <= 1.f)) return KVQ_ERR_INVALID_ARG;
+    if (norm->per_head != 0 && norm->per_head != 1) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(norm->q_weight) || !aligned16(norm->k_weight)) return KVQ_ERR_ALIGNMENT;
+  }
+  if (!rope || n < 0 || q_heads < 0 || rope->max_pos < 1) return KVQ_ERR_INVALID_ARG;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return KVQ_ERR_INVALID_ARG;
+  if (!rotary_dim_ok(rope->rotary_dim)) return KVQ_ERR_UNSUPPORTED;
+  if (mode != KVQ_APPEND_QUANT && mode != KVQ_APPEND_RING && mode != KVQ_APPEND_STEP) return KVQ_ERR_INVALID_ARG;
+  const int64_t q_row = int64_t(q_heads) * kHeadDim, kv_row = int64_t(cache->num_kv_heads) * kHeadDim;
+  if (q_stride == 0) q_stride = q_row;
+  if (k_stride == 0) k_stride = kv_row;
+  if (v_stride == 0) v_stride = kv_row;
+  if (n == 0) return KVQ_OK;
+  if (!rope->table) return KVQ_ERR_INVALID_ARG;
+  if (!aligned16(rope->table)) return KVQ_ERR_ALIGNMENT;
+  const bool write = k_new != nullptr;
+  if (write != (v_new != nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (!write && q_heads == 0) return KVQ_ERR_INVALID_ARG;
+  if ((q != nullptr) != (q_heads > 0) || (q_out != nullptr) != (q_heads > 0)) return KVQ_ERR_INVALID_ARG;
+  if (q_heads > 0) {
+    if (q_stride < q_row) return KVQ_ERR_INVALID_ARG;
+    if (q == q_out && q_stride != q_row) return KVQ_ERR_INVALID_ARG;
+    if (!aligned8(q) || !aligned8(q_out) || q_stride % 4) return KVQ_ERR_ALIGNMENT;
+  }
+  if (write) {
+    if (!seq_idx || !pos || batch < 1) return KVQ_ERR_INVALID_ARG;
+    if (k_stride < kv_row || v_stride < kv_row) return KVQ_ERR_INVALID_ARG;
+    if (!aligned8(k_new) || !aligned8(v_new) || k_stride % 4 || v_stride % 4) return KVQ_ERR_ALIGNMENT;
+    if (mode != KVQ_APPEND_QUANT && cache->window == 0) return KVQ_ERR_INVALID_ARG;
+    if (mode == KVQ_APPEND_STEP && cache->k_bits == 2) return KVQ_ERR_UNSUPPORTED;
+    if (mode != KVQ_APPEND_RING && (!block_table || max_blocks_per_seq < 1)) return KVQ_ERR_INVALID_ARG;
+  }
+  if (!rope_pos && !pos) return KVQ_ERR_INVALID_ARG;
+  if (n * (int64_t(q_heads) + 2ll * cache->num_kv_heads) > (1ll << 33)) return KVQ_ERR_UNSUPPORTED;  // grid limit
+  kvq::RopeArgs a;
+  a.ap.c = view(cache);
+  a.ap.k_new = static_cast<const uint16_t*>(k_new);
+  a.ap.v_new = static_cast<const uint16_t*>(v_new);
+  a.ap.n = n;
+  a.ap.seq_idx = seq_idx;
+  a.ap.pos = pos;
+  a.ap.mode = mode;
+  a.ap.table = block_table;
+  a.ap.batch = batch;
+  a.ap.mbps = max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
+  a.ap.err = err_word;
+  a.write = write;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.Hq = q_heads;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.table = rope->table;
+  a.R = rope->rotary_dim;
+  a.max_pos = rope->max_pos;
+  a.interleaved = rope->interleaved != 0;
+  a.rope_pos = rope_pos ? rope_pos : pos;
+  if (norm) {
+    a.q_weight = norm->q_weight;
+    a.k_weight = norm->k_weight;
+    a.per_head = norm->per_head != 0;
+    a.eps = norm->eps;
+  }
+  const cudaError_t e = norm ? kvq::launch_norm_rope_append(a, static_cast<cudaStream_t>(stream))
+                             : kvq::launch_rope_append(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return KVQ_ERR_CUDA;
+  return KVQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -603,64 +682,19 @@ kvq_status kvq_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rop
                            int64_t v_stride, int32_t n, const int32_t* rope_pos, const int32_t* seq_idx,
                            const int32_t* pos, int32_t mode, const int32_t* block_table, int32_t batch,
                            int32_t max_blocks_per_seq, uint32_t* err_word, void* stream) {
-  kvq_status st = check_cache(cache);
-  if (st != KVQ_OK) return st;
-  if (!rope || n < 0 || q_heads < 0 || rope->max_pos < 1) return KVQ_ERR_INVALID_ARG;
-  if (rope->interleaved != 0 && rope->interleaved != 1) return KVQ_ERR_INVALID_ARG;
-  if (!rotary_dim_ok(rope->rotary_dim)) return KVQ_ERR_UNSUPPORTED;
-  if (mode != KVQ_APPEND_QUANT && mode != KVQ_APPEND_RING && mode != KVQ_APPEND_STEP) return KVQ_ERR_INVALID_ARG;
-  const int64_t q_row = int64_t(q_heads) * kHeadDim, kv_row = int64_t(cache->num_kv_heads) * kHeadDim;
-  if (q_stride == 0) q_stride = q_row;
-  if (k_stride == 0) k_stride = kv_row;
-  if (v_stride == 0) v_stride = kv_row;
-  if (n == 0) return KVQ_OK;
-  if (!rope->table) return KVQ_ERR_INVALID_ARG;
-  if (!aligned16(rope->table)) return KVQ_ERR_ALIGNMENT;
-  const bool write = k_new != nullptr;
-  if (write != (v_new != nullptr)) return KVQ_ERR_INVALID_ARG;
-  if (!write && q_heads == 0) return KVQ_ERR_INVALID_ARG;
-  if ((q != nullptr) != (q_heads > 0) || (q_out != nullptr) != (q_heads > 0)) return KVQ_ERR_INVALID_ARG;
-  if (q_heads > 0) {
-    if (q_stride < q_row) return KVQ_ERR_INVALID_ARG;
-    if (q == q_out && q_stride != q_row) return KVQ_ERR_INVALID_ARG;
-    if (!aligned8(q) || !aligned8(q_out) || q_stride % 4) return KVQ_ERR_ALIGNMENT;
-  }
-  if (write) {
-    if (!seq_idx || !pos || batch < 1) return KVQ_ERR_INVALID_ARG;
-    if (k_stride < kv_row || v_stride < kv_row) return KVQ_ERR_INVALID_ARG;
-    if (!aligned8(k_new) || !aligned8(v_new) || k_stride % 4 || v_stride % 4) return KVQ_ERR_ALIGNMENT;
-    if (mode != KVQ_APPEND_QUANT && cache->window == 0) return KVQ_ERR_INVALID_ARG;
-    if (mode == KVQ_APPEND_STEP && cache->k_bits == 2) return KVQ_ERR_UNSUPPORTED;
-    if (mode != KVQ_APPEND_RING && (!block_table || max_blocks_per_seq < 1)) return KVQ_ERR_INVALID_ARG;
-  }
-  if (!rope_pos && !pos) return KVQ_ERR_INVALID_ARG;
-  if (n * (int64_t(q_heads) + 2ll * cache->num_kv_heads) > (1ll << 33)) return KVQ_ERR_UNSUPPORTED;  // grid limit
-  kvq::RopeArgs a;
-  a.ap.c = view(cache);
-  a.ap.k_new = static_cast<const uint16_t*>(k_new);
-  a.ap.v_new = static_cast<const uint16_t*>(v_new);
-  a.ap.n = n;
-  a.ap.seq_idx = seq_idx;
-  a.ap.pos = pos;
-  a.ap.mode = mode;
-  a.ap.table = block_table;
-  a.ap.batch = batch;
-  a.ap.mbps = max_blocks_per_seq > 0 ? max_blocks_per_seq : 1;
-  a.ap.err = err_word;
-  a.write = write;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_out = static_cast<uint16_t*>(q_out);
-  a.Hq = q_heads;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.table = rope->table;
-  a.R = rope->rotary_dim;
-  a.max_pos = rope->max_pos;
-  a.interleaved = rope->interleaved != 0;
-  a.rope_pos = rope_pos ? rope_pos : pos;
-  if (kvq::launch_rope_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
-  return KVQ_OK;
+  return rope_call(cache, rope, nullptr, q, q_heads, q_stride, q_out, k_new, k_stride, v_new, v_stride, n, rope_pos, seq_idx,
+                   pos, mode, block_table, batch, max_blocks_per_seq, err_word, stream);
+}
+
+kvq_status kvq_norm_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const kvq_norm_desc* norm,
+                                const void* q, int32_t q_heads, int64_t q_stride, void* q_out, const void* k_new,
+                                int64_t k_stride, const void* v_new, int64_t v_stride, int32_t n,
+                                const int32_t* rope_pos, const int32_t* seq_idx, const int32_t* pos, int32_t mode,
+                                const int32_t* block_table, int32_t batch, int32_t max_blocks_per_seq,
+                                uint32_t* err_word, void* stream) {
+  if (!norm) return KVQ_ERR_INVALID_ARG;
+  return rope_call(cache, rope, norm, q, q_heads, q_stride, q_out, k_new, k_stride, v_new, v_stride, n, rope_pos, seq_idx,
+                   pos, mode, block_table, batch, max_blocks_per_seq, err_word, stream);
 }
 
 kvq_status kvq_decode_shared_workspace_size(const kvq_cache_desc* cache, int32_t batch, int32_t q_heads,

@@ -52,6 +52,11 @@ struct RopeArgs {
   int R, max_pos;
   bool interleaved;
   const int* rope_pos;
+  // kvq_norm_rope_append: weights of the heads' norms, [128] or one for each head, or null
+  const float* q_weight = nullptr;
+  const float* k_weight = nullptr;
+  bool per_head = false;
+  float eps = 0.f;
 };
 
 struct RopeFreqs {
@@ -221,6 +226,7 @@ DecodeLayout decode_layout(int B, int Hq, int H, int window, int stream_ctas, in
 // may be that of an earlier call that the caller has dealt with.
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeArgs& a, cudaStream_t s);
+cudaError_t launch_norm_rope_append(const RopeArgs& a, cudaStream_t s);
 cudaError_t launch_rope_table(const RopeFreqs& f, int pairs, int max_pos, float* table, cudaStream_t s);
 cudaError_t launch_mass(const MassArgs& a, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
