@@ -124,6 +124,9 @@ typedef enum {
 /* kvq_prefill: stream_ctas value that selects the query-tile path */
 #define KVQ_PREFILL_TILES (-1)
 
+/* kvq_prefill_sinks: and the one that selects units of 256 query vectors */
+#define KVQ_PREFILL_UNITS (-2)
+
 /* Description of one layer's cache.  Every pointer is caller-owned device memory. */
 typedef struct {
   int32_t num_kv_heads;   /* H_kv >= 1                                              */

@@ -32,6 +32,7 @@ APPEND_QUANT = 0
 APPEND_RING = 1
 APPEND_STEP = 2
 PREFILL_TILES = -1  # kvq_prefill stream_ctas: the query-tile path
+PREFILL_UNITS = -2  # kvq_prefill_sinks stream_ctas: units of 256 query vectors
 ROPE_PLAIN = 0
 ROPE_LINEAR = 1
 ROPE_NTK = 2

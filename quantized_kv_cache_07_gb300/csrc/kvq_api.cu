@@ -119,6 +119,9 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
   return (long long)((n + TR - 1) / TR) * kv_heads;
 }
 
+// Units of 256 query vectors for a chunk with sinks: where a sequence of the batch has 64 of them on average.
+bool prefill_units(int n, int q_heads, int batch) { return (long long)n * q_heads >= 64ll * batch * 0x7fffffff; }
+
 // The cache as the kernels of kvq_decode_shared see it: under a key factor the query times the factor
 // needs more than fp16's 11 bits (one part: the log-sum-exp is off by 1.3e-5 of it on 33 sequences of 8k
 // tokens, two: 1e-7), so it goes in two parts.
@@ -301,12 +304,17 @@ kvq_status prefill_call(const kvq_cache_desc* cache, const void* q, int n, int q
     return KVQ_ERR_INVALID_ARG;
   if ((k_new == nullptr) != (v_new == nullptr)) return KVQ_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return KVQ_ERR_ALIGNMENT;
-  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES) return KVQ_ERR_INVALID_ARG;
+  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES && !(sinks && stream_ctas == KVQ_PREFILL_UNITS))
+    return KVQ_ERR_INVALID_ARG;
   const kvq::CacheView v = sinks ? shared_view(cache) : view(cache);
   const bool tiles_ok = kvq::prefill_tiles_supported(v);
   if (stream_ctas == KVQ_PREFILL_TILES && !tiles_ok) return KVQ_ERR_UNSUPPORTED;
-  bool tiles = stream_ctas == KVQ_PREFILL_TILES;
-  if (stream_ctas == 0 && tiles_ok) {
+  // units carry the weights in one part: not for the two-part mode
+  const bool units_ok = tiles_ok && cache->q_bits != 32;
+  if (stream_ctas == KVQ_PREFILL_UNITS && !units_ok) return KVQ_ERR_UNSUPPORTED;
+  const bool units = stream_ctas == KVQ_PREFILL_UNITS || (sinks && stream_ctas == 0 && units_ok && prefill_units(n, q_heads, batch));
+  bool tiles = stream_ctas == KVQ_PREFILL_TILES || units;
+  if (stream_ctas == 0 && tiles_ok && !units) {
     // Tiles once their CTAs fill at least 9/16 of the SMs; fewer tiles leave
     // the long prefixes to too few CTAs and split rows (every row one query
     // group of the decode split over all SMs) are faster.  Measured crossover
@@ -356,7 +364,7 @@ kvq_status prefill_call(const kvq_cache_desc* cache, const void* q, int n, int q
   if (sinks) {
     a.sinks = sinks->sinks;
     a.span = sinks->span;
-    e = tiles ? kvq::launch_sinks_tiles(a, cs) : kvq::launch_sinks(a, cs);
+    e = units ? kvq::launch_sinks_tc(a, cs) : tiles ? kvq::launch_sinks_tiles(a, cs) : kvq::launch_sinks(a, cs);
   } else {
     e = tiles ? kvq::launch_prefill_tiles(a, cs) : kvq::launch_decode(a, cs);
   }

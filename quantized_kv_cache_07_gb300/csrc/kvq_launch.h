@@ -272,5 +272,7 @@ cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t s);
 bool prefill_tiles_supported(const CacheView& c);
 cudaError_t launch_prefill_tiles(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_sinks_tiles(const DecodeArgs& a, cudaStream_t s);
+// The same on tcgen05, 256 query vectors a unit (kvq_sinks_tc.cu); not for bf16 caches.
+cudaError_t launch_sinks_tc(const DecodeArgs& a, cudaStream_t s);
 
 }  // namespace kvq

@@ -168,7 +168,7 @@ def prefill(run, seq, pos, qbits, sinks, span, stream_ctas=0, table=None, fused_
     t = lambda bits: torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
     out = torch.full((n, w.q_heads, 128), float("nan"), dtype=torch.float32 if out_fp32 else torch.bfloat16, device="cuda")
     lse = torch.full((n, w.q_heads), float("nan"), device="cuda")
-    nb = lib.kvq_prefill_workspace_size(run.cache.desc, n, w.q_heads, stream_ctas)
+    nb = lib.kvq_prefill_workspace_size(run.cache.desc, n, w.q_heads, max(stream_ctas, 0))
     ws = torch.zeros(max(nb, 16), dtype=torch.uint8, device="cuda")
     new = {} if fused_rows is None else dict(k_new=t(run.inp.k[fused_rows]), v_new=t(run.inp.v[fused_rows]))
     lib.kvq_prefill_sinks(run.cache.desc, t(qbits), w.q_heads, i(seq), i(pos), run.table if table is None else table,
@@ -203,12 +203,12 @@ def test_prefill_matches_the_oracle(fmt, order):
             for h in range(w.kv_heads):
                 g = slice(h * G, (h + 1) * G)
                 o[r, g], l[r, g] = ref(b, h, q[g], p + 1, sinks, span)
-        for ctas in (0, 5) if w.k_bits == 16 else (0, -1, 5):
+        for ctas in (0, 5) if w.k_bits == 16 else (0, -1, 5) if w.q_bits == 32 else (0, -1, -2, 5):
             assert worst(*prefill(run, seq, pos, qbits, sinks, span, ctas, table), o, l) <= 1.0, (sinks, span, ctas)
     assert run.err_bits() == 0
 
 
-@pytest.mark.parametrize("ctas", [-1, 3])
+@pytest.mark.parametrize("ctas", [-1, -2, 3])
 @pytest.mark.parametrize("fmt", ["int8_g4", "int4_factor_g8", "asym_int8", "bf16_g7"])
 def test_prefill_rows_that_hide_a_token(fmt, ctas):
     """A token that is no number, or infinite, changes the rows that see it and no others of their tile."""
@@ -228,6 +228,39 @@ def test_prefill_rows_that_hide_a_token(fmt, ctas):
         np.testing.assert_array_equal(before[0][hidden], after[0][hidden])
         np.testing.assert_array_equal(before[1][hidden], after[1][hidden])
         assert np.all(~np.isfinite(after[0][~hidden]).all(axis=(1, 2)))
+
+
+@pytest.mark.parametrize("fmt", ["int8_g4", "int4_factor_g8", "asym_int8", "k4v8_g3", "int8_g1_paged", "asym_int2_g8"])
+@pytest.mark.parametrize("case", ["one long", "ragged", "few rows", "many sequences"])
+def test_units_of_many_rows(fmt, case):
+    """Units with several tiles, several units, sequences that share a unit, empty and invalid rows among them."""
+    B, lo, hi = {"one long": (1, 900, 900), "ragged": (4, 150, 500), "few rows": (2, 700, 800),
+                 "many sequences": (20, 1, 90)}[case]
+    w = small_workload(fmt, **dict(dict(batch=B, len_range=(lo, hi)), **FORMATS[fmt]))
+    inp = make_inputs(w, 9)
+    run, ref, G = DeviceRun(inp), Oracle(inp), w.group
+    start = [0] * B if case != "few rows" else [int(L) - 3 for L in inp.lengths]
+    seq, pos = _rows("seq", inp.lengths, start)
+    bad = np.zeros(len(seq), bool)
+    if case in ("ragged", "many sequences"):
+        seq, pos = seq.copy(), pos.copy()
+        bad[5::41] = True
+        pos[5::41] = -1          # nothing to attend to
+        seq[46::82], bad[46::82] = B + 3, True
+    qbits = query_rows(len(seq), w.q_heads, 11)
+    for sinks, span in ((4, 130), (70, 1), (0, 333)):
+        table = freed(run.table, inp.lengths, [s + 1 - span for s in start], sinks)
+        out, lse = prefill(run, seq, pos, qbits, sinks, span, -2, table)
+        assert run.err_bits() & ~run.lib.KVQ_DEVERR_POSITION == 0
+        assert np.all(out[bad] == 0) and np.all(np.isneginf(lse[bad]))
+        bf, _ = prefill(run, seq, pos, qbits, sinks, span, -2, table, out_fp32=False)
+        for r in np.nonzero(~bad)[0][::7]:
+            q = O.bf16_to_f64(qbits[r])
+            for h in range(w.kv_heads):
+                g = slice(h * G, (h + 1) * G)
+                o, l = ref(seq[r], h, q[g], pos[r] + 1, sinks, span)
+                assert worst(out[r, g], lse[r, g], o, l) <= 1.0, (r, h, sinks, span)
+                assert worst(bf[r, g], None, o, l, True) <= 1.0
 
 
 def test_prefill_writes_its_chunk_first():
@@ -276,6 +309,10 @@ def test_refusals():
         with pytest.raises(lib.KvqError) as e:
             decode(run, sinks, span)
         assert e.value.status == status
+    q32 = DeviceRun(make_inputs(small_workload("q", batch=1, q_bits=32, len_range=(50, 60)), 7))
+    with pytest.raises(lib.KvqError) as e:  # units carry the weights in one part
+        prefill(q32, [0], [3], query_rows(1, 8, 0), 4, 64, lib.PREFILL_UNITS)
+    assert e.value.status == lib.KVQ_ERR_UNSUPPORTED
     with pytest.raises(lib.KvqError) as e:  # a chunk needs its positions in blocks
         prefill(run, [0], [3], query_rows(1, w.q_heads, 0), 4, 64)
     assert e.value.status == lib.KVQ_ERR_UNSUPPORTED
