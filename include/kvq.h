@@ -563,8 +563,12 @@ kvq_status kvq_decode_sinks(const kvq_cache_desc* cache, const void* q, int32_t 
 /*
  * kvq_prefill_sinks -- kvq_prefill with a sliding window and sinks: the row at position p attends to
  * tokens i <= p with i < sinks or i > p - span (a chunk of single rows is kvq_decode_sinks).  Every
- * row sees its own tokens alone, whatever the others hold.  Everything else as kvq_prefill (both attention
+ * row sees its own tokens alone, whatever the others hold.  Everything else as kvq_prefill (its attention
  * paths, kvq_prefill_workspace_size, the chunk's own write), block table and key factor as kvq_decode_sinks.
+ * One more path, stream_ctas = KVQ_PREFILL_UNITS (-2), on tcgen05: 256 / G consecutive rows x the G query heads of
+ * a KV head meet every tile of 64 tokens, once for each sequence among the rows.  Quantized caches, not q_bits 32
+ * (KVQ_ERR_UNSUPPORTED); no workspace.  0 takes it where the rows are 128 query vectors (of a KV head) for
+ * every sequence of the batch on average, 64 for a batch of one.
  */
 kvq_status kvq_prefill_sinks(const kvq_cache_desc* cache, const void* q, int32_t n, int32_t q_heads,
                              const int32_t* seq_idx, const int32_t* pos, const void* k_new, const void* v_new,

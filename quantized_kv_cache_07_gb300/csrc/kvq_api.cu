@@ -119,8 +119,10 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
   return (long long)((n + TR - 1) / TR) * kv_heads;
 }
 
-// Units of 256 query vectors for a chunk with sinks: where a sequence of the batch has 64 of them on average.
-bool prefill_units(int n, int q_heads, int batch) { return (long long)n * q_heads >= 64ll * batch * 0x7fffffff; }
+// Units of 256 query vectors for a chunk with sinks: where a sequence of the batch has 128 of them on average, as each
+// sequence in a unit is a pass over its own tokens (one sequence: 64).  Units / the other paths' best, us, 32 / 8 heads on
+// windows of 4096: 4 sequences of 16 / 32 / 64 rows 129 / 84, 83 / 88, 47 / 140; one of 16 / 64 / 2048 rows 27 / 32, 37 / 83, 196 / 752.
+bool prefill_units(int n, int group, int batch) { return (long long)n * group >= (batch == 1 ? 64ll : 128ll * batch); }
 
 // The cache as the kernels of kvq_decode_shared see it: under a key factor the query times the factor
 // needs more than fp16's 11 bits (one part: the log-sum-exp is off by 1.3e-5 of it on 33 sequences of 8k
@@ -312,7 +314,7 @@ kvq_status prefill_call(const kvq_cache_desc* cache, const void* q, int n, int q
   // units carry the weights in one part: not for the two-part mode
   const bool units_ok = tiles_ok && cache->q_bits != 32;
   if (stream_ctas == KVQ_PREFILL_UNITS && !units_ok) return KVQ_ERR_UNSUPPORTED;
-  const bool units = stream_ctas == KVQ_PREFILL_UNITS || (sinks && stream_ctas == 0 && units_ok && prefill_units(n, q_heads, batch));
+  const bool units = stream_ctas == KVQ_PREFILL_UNITS || (sinks && stream_ctas == 0 && units_ok && prefill_units(n, q_heads / cache->num_kv_heads, batch));
   bool tiles = stream_ctas == KVQ_PREFILL_TILES || units;
   if (stream_ctas == 0 && tiles_ok && !units) {
     // Tiles once their CTAs fill at least 9/16 of the SMs; fewer tiles leave

@@ -274,5 +274,8 @@ cudaError_t launch_prefill_tiles(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_sinks_tiles(const DecodeArgs& a, cudaStream_t s);
 // The same on tcgen05, 256 query vectors a unit (kvq_sinks_tc.cu); not for bf16 caches.
 cudaError_t launch_sinks_tc(const DecodeArgs& a, cudaStream_t s);
+// A cluster of 2^c CTAs a unit, and how many run at once (kvq_sinks_tc_shared.cu).
+cudaError_t launch_sinks_tc_shared(const DecodeArgs& a, int units, int rows, int c, cudaStream_t s);
+cudaError_t sinks_tc_clusters(const CacheView& v, int ctas, int c, int* n);
 
 }  // namespace kvq

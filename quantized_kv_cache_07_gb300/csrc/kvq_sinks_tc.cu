@@ -1,728 +1,53 @@
-// Chunked prefill with sinks and a sliding window on tcgen05 (kvq_prefill_sinks, KVQ_PREFILL_UNITS).
-//
-// A unit is up to 256 query vectors: 256 / G consecutive rows of the call x the G query heads of one KV head.  A
-// CTA takes units in turn and, for every sequence among a unit's rows (a "pass", mostly one), streams the tiles of
-// 64 tokens that one row at least sees: those of the sinks, then from the shortest row's window on.  The products, the
-// softmax and the conversion of codes are those of kvq_shared_tc.cu, which has the layouts and the roles:
-//   warpgroups 0 and 1 softmax (thread v = vector v), warpgroup 2 converts, warp 12 issues the products,
-// and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while this one runs.
-//
-// Masks.  Row of length L sees token i < L if i < sinks or i >= L - span.  Tiles are aligned to 64 tokens; a
-// tile that every row of a warp sees whole skips the mask, so it costs the tiles at the window's start and at the chunk itself.
-// Blocks that no row sees are not read (their table entries may be gone); of blocks that are read, hidden tokens have no
-// say: scores -inf, value scales by row (as sequences stand apart in kvq_shared_tc.cu).
-#include "kvq_tc_tiles.cuh"
+// Chunked prefill with sinks on tcgen05 (kvq_sinks_tc.cuh): one CTA a unit, and the choice between that and clusters.
+#include "kvq_sinks_tc.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kPlanRows = 2 * kQ;  // G = 1
-
-struct Pass {
-  int seq, least, most;  // shortest and longest row
+// SMs of the current device, and how many clusters of 2, 4 and 8 CTAs run on it at once (they take the same
+// shared memory and threads whatever the format).
+struct Room {
+  int sms, clusters[4];
 };
 
-struct Plan {
-  int passes, h, r0, nrows;
-  Pass pass[kPlanRows];
-  int seq[kPlanRows], len[kPlanRows];  // by row; an empty one has sequence -1
-};
-
-struct UnitSmem {
-  alignas(1024) uint8_t q[2][2][kQ * 128];  // [warpgroup][half]
-  alignas(1024) TcStage st[kRing];
-  float sk[kRing][kTok], sv[kRing][kTok], mk[kRing][kTok], mv[kRing][kTok];
-  float svmax[kRing][4];
-  float qs[2 * kQ], qz[2 * kQ];  // after a pass of one half: the second warpgroup's m and l
-  int qlen[2 * kQ];
-  // full: a stage's 128 converting threads; empty: its products are done; q_full: the softmax threads have staged a
-  // pass's queries; s_full, p_full, o_done [warpgroup][S buffer]: scores, weights, P . V done; plan_full, plan_empty
-  // [plan buffer]; meet: both softmax warpgroups
-  uint64_t full[kRing], empty[kRing], q_full, meet, s_full[2][2], p_full[2][2], o_done[2][2], plan_full[2], plan_empty[2];
-  uint32_t tmem;
-  Plan plan[2];
-};
-
-// A pass, walked alike by every role: tile i of it is tile i of the sequence, or i + skip from `front` on.
-struct Walk {
-  int seq, h, nt, front, skip;
-  int from, most;  // no row sees the tokens between the sinks and `from`, nor those from `most` on
-  int nv;
-  bool both;  // more than 128 vectors: both warpgroups meet every tile
-  __device__ __forceinline__ int tile(int i) const { return i < front ? i : i + skip; }
-};
-__device__ __forceinline__ Walk walk_of(const DecodeArgs& a, const Plan& p, int i) {
-  Walk w;
-  const Pass ps = p.pass[i];
-  const int all = (ps.most + kTok - 1) / kTok;
-  w.seq = ps.seq;
-  w.h = p.h;
-  w.most = ps.most;
-  w.from = max(ps.least - a.span, 0);
-  w.front = (min(a.sinks, ps.most) + kTok - 1) / kTok;
-  w.skip = max(w.from / kTok - w.front, 0);
-  w.nt = all - w.skip;
-  w.nv = p.nrows * a.G;
-  w.both = w.nv > kQ;
-  return w;
-}
-// Tiles of a pass that warpgroup j takes.
-__device__ __forceinline__ int jobs_of(const Walk& g, int j) { return g.both ? g.nt : (g.nt + 1 - j) / 2; }
-
-// The rows of unit u by one warp.
-__device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, int rows_per, int lane) {
-  const int H = a.c.H, h = u % H, r0 = (u / H) * rows_per, nrows = min(rows_per, a.B - r0);
-  int passes = 0;
-  for (int base = 0; base < nrows; base += 32) {
-    const int i = base + lane;
-    int seq = -1, len = 0;
-    if (i < nrows) {
-      seq = a.seq_of[r0 + i];
-      if (seq < 0 || seq >= a.nseq) {
-        if (h == 0) flag(a.err, KVQ_DEVERR_POSITION);
-        seq = -1;
-      } else {
-        const int most = table_tokens(a.mbps, 0), pos = a.pos[r0 + i];
-        len = pos < 0x7fffffff ? pos + 1 : -1;
-        if (len < 0 || len > most) {
-          if (h == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
-          len = len < 0 && pos < 0 ? 0 : most;
-        }
-        if (len == 0) seq = -1;
-      }
-      p->seq[i] = seq;
-      p->len[i] = len;
-    }
-    uint32_t left = __ballot_sync(kFull, seq >= 0);
-    while (left) {  // the sequences among these 32 rows
-      const int s = __shfl_sync(kFull, seq, __ffs(left) - 1);
-      const uint32_t who = __ballot_sync(kFull, seq == s);
-      const int least = __reduce_min_sync(kFull, seq == s ? len : 0x7fffffff);
-      const int most = __reduce_max_sync(kFull, seq == s ? len : 0);
-      int at = -1;
-      for (int k = 0; k < passes; k += 32) {
-        const uint32_t hit = __ballot_sync(kFull, k + lane < passes && p->pass[k + lane].seq == s);
-        if (hit) {
-          at = k + __ffs(hit) - 1;
-          break;
-        }
-      }
-      if (lane == 0) {
-        Pass& ps = p->pass[at < 0 ? passes : at];
-        ps = at < 0 ? Pass{s, least, most} : Pass{s, min(ps.least, least), max(ps.most, most)};
-      }
-      passes += at < 0;
-      left &= ~who;
-      __syncwarp();
-    }
-    // rows that attend to nothing
-    for (uint32_t none = __ballot_sync(kFull, i < nrows && seq < 0); none; none &= none - 1) {
-      const size_t row = size_t(r0 + base + __ffs(none) - 1) * a.Hq + h * a.G;
-      for (int e = lane; e < a.G * kHeadDim; e += 32) {
-        if (a.out_fp32) reinterpret_cast<float*>(a.out)[row * kHeadDim + e] = 0.f;
-        else reinterpret_cast<__nv_bfloat16*>(a.out)[row * kHeadDim + e] = __float2bfloat16_rn(0.f);
-      }
-      if (a.lse && lane < a.G) a.lse[row + lane] = kNegInf;
-    }
-  }
-  if (lane == 0) {
-    p->passes = passes;
-    p->h = h;
-    p->r0 = r0;
-    p->nrows = nrows;
-  }
-}
-
-// Four outputs of a row.
-__device__ __forceinline__ void put_out(const DecodeArgs& a, size_t at, float4 o) {
-  if (a.out_fp32) {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = o;
-  } else {
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at) =
-        make_uint2(pack_bf162(o.x, o.y), pack_bf162(o.z, o.w));
-  }
-}
-
-// TWO: queries as an fp16 high and low part, the low ones in the second query tile; units of 128 vectors.
-template <int KB, int VB, bool ASYM, bool TWO>
-__global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArgs a, int units, int rows_per) {
-  using F = Fmt<KB, VB, ASYM>;
-  constexpr int kStep = kTok / kBlock;
-  constexpr float kKC = KB == 8 ? 128.f : (KB == 4 ? 8.f : 2.f), kVC = VB == 8 ? 128.f : (VB == 4 ? 8.f : 2.f);
-  extern __shared__ uint8_t raw_smem[];
-  UnitSmem* sm = reinterpret_cast<UnitSmem*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sm->full[i], 128);
-      mbar_init(&sm->empty[i], 1);
-    }
-    mbar_init(&sm->q_full, 2 * kQ);
-    mbar_init(&sm->meet, 2 * kQ);
-    for (int j = 0; j < 2; ++j) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sm->s_full[j][i], 1);
-        mbar_init(&sm->p_full[j][i], kQ);
-        mbar_init(&sm->o_done[j][i], 1);
-      }
-      mbar_init(&sm->plan_full[j], 1);
-      mbar_init(&sm->plan_empty[j], 2 * kQ + 128 + 1);
-    }
-    fence_mbar_init();
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 12) tmem_alloc(&sm->tmem, kTmemCols);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = __shfl_sync(kFull, sm->tmem, 0);
-  const int P = gridDim.x, ci = blockIdx.x;
-  // Every wait is bounded; a role that gives up leaves its loop, the others follow when their own waits run out.
-  bool ok = true;
-  auto ring_wait = [&](uint64_t* bars, int n) { return mbar_wait(&bars[n & (kRing - 1)], uint32_t(n / kRing) & 1u); };
-  auto pair_wait = [&](uint64_t* bars, int c) { return mbar_wait(&bars[c & 1], uint32_t(c >> 1) & 1u); };
-
-  if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 13) {
-      // -------------------------------------------------------------- plans
-      for (int u = ci, k = 0; u < units; u += P, ++k) {
-        if (k >= 2) ok = __all_sync(kFull, pair_wait(sm->plan_empty, k - 2));
-        if (!ok) break;
-        plan_unit(a, &sm->plan[k & 1], u, rows_per, lane);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->plan_full[k & 1]);
-      }
-    } else if (warp == 12) {
-      // -------------------------------------------------------------- products
-      const bool leader = elect_one();
-      const uint32_t q_addr = smem_u32(sm->q), st_addr = smem_u32(sm->st);
-      int n0 = 0, c0 = 0, c1 = 0, seg = 0;  // tiles and jobs before this pass
-      for (int u = ci, k = 0; u < units && ok; u += P, ++k) {
-        ok = pair_wait(sm->plan_full, k);
-        const Plan& plan = sm->plan[k & 1];
-        for (int ps = 0; ok && ps < plan.passes; ++ps, ++seg) {
-          const Walk g = walk_of(a, plan, ps);
-          ok = mbar_wait(&sm->q_full, uint32_t(seg) & 1u);
-          // P . V runs one tile behind the scores, two where the warpgroups take turns
-          const int lag = g.both ? 1 : 2;
-          for (int i = 0; i < g.nt + lag && ok; ++i) {
-            if (i < g.nt) {
-              const int n = n0 + i;
-              ok = ring_wait(sm->full, n);
-              tc_fence_after();
-              const uint64_t kd = tile_desc(st_addr + uint32_t(n & (kRing - 1)) * uint32_t(sizeof(TcStage)));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!g.both && (i & 1) != j) continue;
-                const int c = (j ? c1 : c0) + (g.both ? i : i >> 1);
-                if (c >= 2) ok = ok && pair_wait(sm->o_done[j], c - 2);  // S's buffer: its weights have been read
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t qd = tile_desc(q_addr + (g.both ? j : 0) * uint32_t(sizeof(sm->q[0])));
-                const uint32_t d = tmem + 256 + 128 * j + 64 * (c & 1);
-                if (leader) {
-#pragma unroll
-                  for (int e = 0; e < kHeadDim / 16; ++e)
-                    tc_mma_ss(d, qd + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
-                              kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), e > 0);
-                  if constexpr (TWO) {
-#pragma unroll
-                    for (int e = 0; e < kHeadDim / 16; ++e)
-                      tc_mma_ss(d, qd + (sizeof(sm->q[0]) >> 4) + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
-                                kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), true);
-                  }
-                  tc_commit(&sm->s_full[j][c & 1]);
-                }
-                __syncwarp();
-              }
-            }
-            const int p = i - lag;
-            if (p >= 0 && ok) {
-              const int n = n0 + p, s = n & (kRing - 1);
-              const uint64_t vd =
-                  tile_desc(st_addr + uint32_t(s) * uint32_t(sizeof(TcStage)) + uint32_t(sizeof(sm->st[0].k)));
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!g.both && (p & 1) != j) continue;
-                const int job = g.both ? p : p >> 1, c = (j ? c1 : c0) + job;
-                ok = ok && pair_wait(sm->p_full[j], c);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tmem + 128 * j, w = tmem + 256 + 128 * j + 64 * (c & 1);
-                if (leader) {
-#pragma unroll
-                  for (int e = 0; e < kTok / 16; ++e)
-                    tc_mma_ts(d, w + 8 * e, vd + 2 * e, f16_idesc(kQ, kHeadDim), job > 0 || e > 0);
-                  tc_commit(&sm->o_done[j][c & 1]);
-                  if (j == 1 || !g.both) tc_commit(&sm->empty[s]);
-                }
-                __syncwarp();
-              }
-            }
-          }
-          n0 += g.nt;
-          c0 += jobs_of(g, 0);
-          c1 += jobs_of(g, 1);
-        }
-        if (lane == 0) mbar_arrive(&sm->plan_empty[k & 1]);
-      }
-    }
-  } else if (warp >= 8) {
-    // ---------------------------------------------------------------- conversion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
-    const int w = warp - 8;
-    const uint32_t km = magic_f16x2(a.B);
-    const uint32_t c64 = 0x64646464u | (uint32_t(a.B) >> 16);  // a.B <= 4096: the constant itself
-    int n = 0;
-    for (int u = ci, k = 0; u < units && ok; u += P, ++k) {
-      ok = __all_sync(kFull, pair_wait(sm->plan_full, k));
-      if (!ok) break;
-      const Plan& plan = sm->plan[k & 1];
-      for (int ps = 0; ok && ps < plan.passes; ++ps) {
-        const Walk g = walk_of(a, plan, ps);
-        const int* table = a.table + size_t(g.seq) * a.mbps;
-        int ids = -1, ids_next = -1;  // this warp's table entries of 32 tiles, and of the next 32
-        auto load_ids = [&](int i) {
-          const int blk = g.tile(i + lane) * kStep + w;
-          int id = -1;
-          if (i + lane < g.nt && blk * kBlock < g.most && (blk * kBlock < a.sinks || (blk + 1) * kBlock > g.from)) {
-            id = __ldcg(table + blk);
-            if (id < 0 || id >= a.c.num_blocks) {
-              flag(a.err, KVQ_DEVERR_BLOCK_ID);
-              id = 0;
-            }
-          }
-          return id;
-        };
-        ids_next = load_ids(0);
-        // this warp's block of the tile: codes, and the record entries of token `lane` (lanes 0..15)
-        Raw<KB> rk;
-        Raw<VB> rv;
-        float ks = 0.f, vs = 0.f, ko = 0.f, vo = 0.f;
-        auto block_of = [&](int i) {  // called once per tile, in order
-          if ((i & 31) == 0) {
-            ids = ids_next;
-            ids_next = load_ids(i + 32);
-          }
-          return i < g.nt ? __shfl_sync(kFull, ids, i & 31) : -1;
-        };
-        auto fetch_keys = [&](int phys) {
-          ks = vs = ko = vo = 0.f;
-          rk.clear();
-          if (phys < 0) return;
-          const size_t hb = size_t(g.h) * a.c.num_blocks + phys;
-          rk.load(a.c.k_codes + hb * F::kKBB, lane);
-          const float* rec = a.c.meta + hb * F::kMF + (F::kGroup ? 0 : (lane & 15));
-          ks = a.c.k_chan ? 1.f : __ldcg(rec + F::kKS);
-          vs = __ldcg(rec + F::kVS);
-          if constexpr (ASYM) {
-            ko = __ldcg(rec + F::kKO);
-            vo = __ldcg(rec + F::kVO);
-          }
-        };
-        auto fetch_values = [&](int phys) {
-          rv.clear();
-          if (phys >= 0) rv.load(a.c.v_codes + (size_t(g.h) * a.c.num_blocks + phys) * F::kVBB, lane);
-        };
-        {
-          const int phys = block_of(0);
-          fetch_keys(phys);
-          fetch_values(phys);
-        }
-#pragma unroll 1
-        for (int i = 0; i < g.nt; ++i, ++n) {
-          const int s = n & (kRing - 1);
-          ok = __all_sync(kFull, n < kRing || ring_wait(sm->empty, n - kRing));
-          if (!ok) break;
-          put_keys<KB>(rk, sm->st[s].k[0], sm->st[s].k[1], w, lane, km, c64);
-          const int pos = (g.tile(i) * kStep + w) * kBlock + lane;
-          const bool data = pos < g.most && (pos < a.sinks || pos >= g.from);
-          if (!data) vs = 0.f;
-          if (lane < kBlock) {
-            const int col = tile_col(w, lane);
-            sm->sk[s][col] = ks;
-            sm->sv[s][col] = vs;
-            if constexpr (ASYM) {
-              sm->mk[s][col] = fmaf(kKC, ks, ko);
-              sm->mv[s][col] = data ? fmaf(kVC, vs, vo) : 0.f;
-            }
-          }
-          // value scales are positive: they order as their bits
-          const uint32_t vm = __reduce_max_sync(kFull, lane < kBlock ? __float_as_uint(vs) : 0u);
-          if (lane == 0) sm->svmax[s][w] = __uint_as_float(vm);
-          const int phys = block_of(i + 1);
-          fetch_keys(phys);
-          put_values<VB>(rv, sm->st[s].v, w, lane, km, c64);
-          fetch_values(phys);
-          fence_async_smem();
-          mbar_arrive(&sm->full[s]);
-        }
-      }
-      mbar_arrive(&sm->plan_empty[k & 1]);
-    }
-  } else {
-    // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-    const int j = warp >> 2, v = tid & (kQ - 1);  // warpgroup, its vector
-    const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t o_cols = lanes + 128 * j, s_cols = lanes + 256 + 128 * j;
-    int n0 = 0, c = 0, seg = 0;  // tiles before this pass; this warpgroup's jobs so far
-    uint32_t meets = 0;
-    auto meet = [&]() {  // both warpgroups
-      mbar_arrive(&sm->meet);
-      return __all_sync(kFull, mbar_wait(&sm->meet, meets++ & 1u)) != 0;
-    };
-    for (int u = ci, k = 0; u < units && ok; u += P, ++k) {
-      ok = __all_sync(kFull, pair_wait(sm->plan_full, k));
-      if (!ok) break;
-      const Plan& plan = sm->plan[k & 1];
-      for (int ps = 0; ok && ps < plan.passes; ++ps, ++seg) {
-        const Walk g = walk_of(a, plan, ps);
-        if (seg > 0 && !(ok = meet())) break;  // both are done with the previous pass's queries
-        const int G = a.G;
-        {
-          // this warp's 32 vectors (16 of the shared 128), 4 a step
-          const int per = g.both ? 32 : 16, v0 = (g.both ? warp : 2 * (warp & 3) + j) * per, sub = lane & 7;
-          const uint16_t* src = a.q + (size_t(plan.r0) * a.Hq + g.h * G) * kHeadDim + 16 * sub;
-          float f[16];
-          if (a.c.factor) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(f + e) =
-                  __ldcg(reinterpret_cast<const float4*>(a.c.factor + g.h * kHeadDim + 16 * sub + e));
-          }
-          uint8_t* half = sm->q[g.both ? j : 0][sub & 1];
-          int r = (v0 + (lane >> 3)) / G, hj = (v0 + (lane >> 3)) % G;
-          uint4 raw[8][2];  // all loads before the first conversion: one latency
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (4 * i < per && r < plan.nrows) {
-              const uint4* p = reinterpret_cast<const uint4*>(src + (size_t(r) * a.Hq + hj) * kHeadDim);
-              raw[i][0] = __ldcg(p);
-              raw[i][1] = __ldcg(p + 1);
-            }
-            hj += 4;
-            while (hj >= G) {
-              hj -= G;
-              ++r;
-            }
-          }
-          if (lane < per) {
-            const int row = (v0 + lane) / G;
-            sm->qlen[v0 + lane] = row < plan.nrows && plan.seq[row] == g.seq ? plan.len[row] : 0;
-          }
-#pragma unroll 1
-          for (int b = 0; b < per; b += 4) {
-            const uint4 cur[2] = {raw[0][0], raw[0][1]};
-#pragma unroll
-            for (int e = 0; e < 7; ++e) {  // rotate: the loop stays short and every index is known
-              raw[e][0] = raw[e + 1][0];
-              raw[e][1] = raw[e + 1][1];
-            }
-            const int at = v0 + b + (lane >> 3);
-            float qs, sum;
-            put_query<ASYM, TWO>(a, cur, f, half, int(sizeof(sm->q[0])), at & (kQ - 1), sub, qs, sum);
-            if (sub == 0) {
-              sm->qs[at] = qs;
-              sm->qz[at] = sum;
-            }
-          }
-        }
-        fence_async_smem();
-        mbar_arrive(&sm->q_full);
-        ok = __all_sync(kFull, mbar_wait(&sm->q_full, uint32_t(seg) & 1u));
-        if (!ok) break;
-        const int at = g.both ? tid : v;
-        const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] : 0.f;
-        const int len = sm->qlen[at], lo = len - a.span;
-        const int hidden = max(lo - a.sinks, 0);  // tokens from the sinks on that the row does not see
-        // the warp's shortest row and latest window decide whether a tile needs the mask at all (vectors that are not of
-        // this pass do not count)
-        const int minlen = __reduce_min_sync(kFull, len > 0 ? len : 0x7fffffff);
-        const int maxlo = __reduce_max_sync(kFull, len > 0 ? lo : -0x7fffffff);
-        float m = kNegInf, l = 0.f, z = 0.f, sg = float(kSigma0);
-        float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
-        const int jobs = jobs_of(g, j);
-#pragma unroll 1
-        for (int i = 0; i < jobs; ++i, ++c) {
-          const int tile = g.both ? i : 2 * i + j, sc = (n0 + tile) & (kRing - 1);
-          ok = __all_sync(kFull, ring_wait(sm->full, n0 + tile) && pair_wait(sm->s_full[j], c));  // scales, scores
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t st = s_cols + 64 * (c & 1);
-          uint32_t r[kTok];
-          tmem_ld32(st, r);
-          tmem_ld32(st + 32, r + 32);
-          tc_wait_ld();
-          const int tok0 = g.tile(tile) * kTok;
-          auto sees = [&](int pos) { return pos < len && (pos < a.sinks || pos >= lo); };
-#pragma unroll
-          for (int e = 0; e < kTok; e += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&sm->sk[sc][e]);
-            if constexpr (ASYM) {
-              const float4 ko = *reinterpret_cast<const float4*>(&sm->mk[sc][e]);
-              fma2(r[e], r[e + 1], ks.x, ks.y, ko.x * qz, ko.y * qz);
-              fma2(r[e + 2], r[e + 3], ks.z, ks.w, ko.z * qz, ko.w * qz);
-            } else {
-              mul2(r[e], r[e + 1], ks.x, ks.y);
-              mul2(r[e + 2], r[e + 3], ks.z, ks.w);
-            }
-          }
-          // a row of the warp that ends inside this tile or before it, or hides tokens of it
-          if (tok0 + kTok > minlen || (tok0 < maxlo && tok0 + kTok > a.sinks)) {
-            const int left = len - tok0, first = a.sinks - tok0;
-#pragma unroll
-            for (int e = 0; e < kTok; ++e)
-              if (tile_token(e) >= left || unsigned(tile_token(e) - first) < unsigned(hidden)) r[e] = __float_as_uint(kNegInf);
-          }
-          float x4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-          for (int e = 0; e < kTok; e += 8)
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              x4[b] = fmaxf(x4[b], fmaxf(__uint_as_float(r[e + 2 * b]), __uint_as_float(r[e + 2 * b + 1])));
-          const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * qs;
-          const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
-          const float svm = max_nan(max_nan(sm4.x, sm4.y), max_nan(sm4.z, sm4.w));  // the same in every thread
-          if (__any_sync(kFull, mx > m + kMaxSlack || !(svm <= svlim))) {
-            float f = 1.f;
-            if (__any_sync(kFull, mx > m + kMaxSlack)) {
-              const float mn = fmaxf(m, mx);
-              f = mn == kNegInf ? 1.f : ex2(m - mn);
-              m = mn;
-            }
-            float sv = svm;
-            if (!(svm <= kFloatMax)) {
-              // A value scale that is not finite: -1 stands for it, as in rows that do not see its token 0 x inf would be
-              // no number.  Every warp that goes on to use the scales writes the same.
-              for (int e = lane; e < kTok; e += 32)
-                if (!(fabsf(sm->sv[sc][e]) <= kFloatMax)) {
-                  sm->sv[sc][e] = -1.f;
-                  if constexpr (ASYM) sm->mv[sc][e] = 0.f;
-                }
-              __syncwarp();
-            }
-            // by the scales that this row sees
-            const bool none = tok0 >= len || (tok0 >= a.sinks && tok0 + kTok <= lo);
-            const bool all = tok0 + kTok <= len && (tok0 >= lo || tok0 + kTok <= a.sinks);
-            if (none) {
-              sv = 0.f;
-              if (tok0 >= len) svlim = fmaxf(svlim, kFloatMax);  // the row has ended, or is not of this pass
-            } else if (!(svm <= svlim) && (!all || !(svm <= kFloatMax))) {
-              float least = 0.f;
-              sv = 0.f;
-#pragma unroll 1
-              for (int e = 0; e < kTok; ++e) {
-                const float own = sees(tok0 + tile_token(e)) ? sm->sv[sc][e] : 0.f;
-                sv = fmaxf(sv, own);
-                least = fminf(least, own);
-              }
-              if (least < 0.f) svlim = -kNegInf;  // the row's outputs are no numbers
-            }
-            if (sv > svlim) {
-              int e;
-              frexpf(sv, &e);
-              const int sn = min(int(sg), kWeightExp - int(kMaxSlack) - e);
-              f *= ldexpf(1.f, sn - int(sg));
-              sg = float(sn);
-              svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - sn);
-            }
-            l *= f;
-            z *= f;
-            if (i > 0) {  // O too, once the products so far are complete
-              ok = __all_sync(kFull, pair_wait(sm->o_done[j], c - 1));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int e = 0; e < kHeadDim; e += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_cols + e, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int b = 0; b < 32; ++b) o[b] = __float_as_uint(__uint_as_float(o[b]) * f);
-                tmem_st32(o_cols + e, o);
-              }
-              tc_wait_st();
-            }
-          }
-          const float base = m == kNegInf ? 0.f : m - sg;
-          uint32_t la[4] = {0u, 0u, 0u, 0u};  // four partial sums of the weights
-#pragma unroll
-          for (int half = 0; half < kTok; half += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = half; e < half + 32; e += 4) {
-              const float4 vs = *reinterpret_cast<const float4*>(&sm->sv[sc][e]);
-              fma2(r[e], r[e + 1], qs, qs, -base, -base);
-              fma2(r[e + 2], r[e + 3], qs, qs, -base, -base);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) r[e + b] = __float_as_uint(ex2(__uint_as_float(r[e + b])));
-              add2(la[0], la[1], r[e], r[e + 1]);
-              add2(la[2], la[3], r[e + 2], r[e + 3]);
-              if constexpr (ASYM) {
-                const float4 vo = *reinterpret_cast<const float4*>(&sm->mv[sc][e]);
-                z = fmaf(__uint_as_float(r[e]), vo.x, fmaf(__uint_as_float(r[e + 1]), vo.y, z));
-                z = fmaf(__uint_as_float(r[e + 2]), vo.z, fmaf(__uint_as_float(r[e + 3]), vo.w, z));
-              }
-              mul2(r[e], r[e + 1], vs.x, vs.y);
-              mul2(r[e + 2], r[e + 3], vs.z, vs.w);
-              p[(e - half) / 2] = pack_half2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-              p[(e - half) / 2 + 1] = pack_half2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-            }
-            tmem_st16(st + half / 2, p);  // over S, which has been read
-          }
-          l += (__uint_as_float(la[0]) + __uint_as_float(la[1])) + (__uint_as_float(la[2]) + __uint_as_float(la[3]));
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(&sm->p_full[j][c & 1]);
-        }
-        if (!ok) break;
-        // ---- the pass's outputs
-        if (jobs > 0) {
-          ok = __all_sync(kFull, pair_wait(sm->o_done[j], c - 1));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const float add = svlim == -kNegInf ? __int_as_float(0x7fffffff) : z;
-        // row i of the warp: its place, or -1 (its own thread's length)
-        const size_t out0 = size_t(plan.r0) * a.Hq + g.h * G;
-        auto place = [&](int vec) { return (out0 + size_t(vec / G) * a.Hq + vec % G) * kHeadDim; };
-        const uint32_t used = __ballot_sync(kFull, len > 0);
-        float4* buf;
-        if (g.both) {
-          // by way of 4 KB of this warp's in its own Q, which no product reads any more
-          buf = reinterpret_cast<float4*>(sm->q[j][0]) + (warp & 3) * 256;
-          const float inv = 1.f / l;
-          if (len > 0 && a.lse) a.lse[place(tid) / kHeadDim] = (m - sg + log2f(l)) * kLn2;
-#pragma unroll 1
-          for (int e = 0; e < kHeadDim; e += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_cols + e, o);
-            tc_wait_ld();
-#pragma unroll
-            for (int b = 0; b < 8; ++b)
-              buf[lane * 8 + (b ^ (lane & 7))] =
-                  make_float4((__uint_as_float(o[4 * b]) + add) * inv, (__uint_as_float(o[4 * b + 1]) + add) * inv,
-                              (__uint_as_float(o[4 * b + 2]) + add) * inv, (__uint_as_float(o[4 * b + 3]) + add) * inv);
-            __syncwarp();
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-              const int row = 4 * b + (lane >> 3);
-              if (used >> row & 1u)
-                put_out(a, place(warp * 32 + row) + e + 4 * (lane & 7), buf[row * 8 + ((lane & 7) ^ (row & 7))]);
-            }
-            __syncwarp();
-          }
-        } else {
-          // both hold the same vectors: the second one's state goes through Q once every product of the pass is done
-          ok = meet();
-          if (!ok) break;
-          buf = reinterpret_cast<float4*>(sm->q[0][0]) + v * 32;  // this vector's 128 values, chunks by its lane
-          if (j == 1) {
-            sm->qs[v] = jobs > 0 && m != kNegInf ? m - sg : kNegInf;
-            sm->qz[v] = l;
-            if (jobs > 0) {
-#pragma unroll 1
-              for (int e = 0; e < kHeadDim; e += 32) {
-                uint32_t o[32];
-                tmem_ld32(o_cols + e, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int b = 0; b < 8; ++b)
-                  buf[(e / 4 + b) ^ lane] =
-                      make_float4(__uint_as_float(o[4 * b]) + add, __uint_as_float(o[4 * b + 1]) + add,
-                                  __uint_as_float(o[4 * b + 2]) + add, __uint_as_float(o[4 * b + 3]) + add);
-              }
-            }
-          }
-          ok = meet();
-          if (!ok) break;
-          if (j == 0) {
-            const float m0 = m == kNegInf ? kNegInf : m - sg, m1 = sm->qs[v];
-            const float M = fmaxf(m0, m1);
-            const float w0 = m0 == kNegInf ? 0.f : exp2f(m0 - M), w1 = m1 == kNegInf ? 0.f : exp2f(m1 - M);
-            const float L = w0 * l + w1 * sm->qz[v], inv = 1.f / L;
-            // a warpgroup without a tile has left no values; one that is no number stays none
-            const bool other = jobs_of(g, 1) > 0;
-            if (len > 0 && a.lse) a.lse[place(v) / kHeadDim] = (M + log2f(L)) * kLn2;
-#pragma unroll 1
-            for (int e = 0; e < kHeadDim; e += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_cols + e, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                float4& x = buf[(e / 4 + b) ^ lane];
-                const float4 y = other ? x : make_float4(0.f, 0.f, 0.f, 0.f);
-                x = make_float4((w0 * (__uint_as_float(o[4 * b]) + add) + w1 * y.x) * inv,
-                                (w0 * (__uint_as_float(o[4 * b + 1]) + add) + w1 * y.y) * inv,
-                                (w0 * (__uint_as_float(o[4 * b + 2]) + add) + w1 * y.z) * inv,
-                                (w0 * (__uint_as_float(o[4 * b + 3]) + add) + w1 * y.w) * inv);
-              }
-            }
-            __syncwarp();
-            const float4* rows = reinterpret_cast<const float4*>(sm->q[0][0]) + warp * 32 * 32;
-            for (int row = 0; row < 32; ++row)
-              if (used >> row & 1u) put_out(a, place(warp * 32 + row) + 4 * lane, rows[row * 32 + (lane ^ row)]);
-          }
-        }
-        tc_fence_before();
-        n0 += g.nt;
-      }
-      mbar_arrive(&sm->plan_empty[k & 1]);
-    }
-  }
-  if (!ok) flag(a.err, KVQ_DEVERR_TIMEOUT);
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  if (warp == 12) tmem_free(tmem, kTmemCols);
-}
-
-template <int KB, int VB, bool ASYM, bool TWO>
-cudaError_t launch_units(const DecodeArgs& a, cudaStream_t s) {
-  const auto k = sinks_tc_kernel<KB, VB, ASYM, TWO>;
-  constexpr int smem = int(sizeof(UnitSmem)) + 1024;
-  static_assert(smem <= 232448, "shared memory of an SM");
-  int dev = 0, sms = 0;
+cudaError_t room_of_device(const CacheView& v, Room* room) {
+  static std::mutex mu;
+  static std::map<int, Room> done;
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
-  const int rows = (TWO ? kQ : 2 * kQ) / a.G;
-  const int units = (a.B + rows - 1) / rows * a.c.H;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(units < sms ? units : sms));  // one CTA an SM: its shared memory and all of its tensor memory
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a, units, rows);
-}
-
-template <bool TWO>
-cudaError_t launch_format(const DecodeArgs& a, cudaStream_t s) {
-  const int kb = a.c.k_bits, vb = a.c.v_bits;
-  const bool as = a.c.asym != 0;
-  if (kb == 8 && vb == 8) return as ? launch_units<8, 8, true, TWO>(a, s) : launch_units<8, 8, false, TWO>(a, s);
-  if (kb == 4 && vb == 4) return as ? launch_units<4, 4, true, TWO>(a, s) : launch_units<4, 4, false, TWO>(a, s);
-  if (kb == 4 && vb == 8) return as ? launch_units<4, 8, true, TWO>(a, s) : launch_units<4, 8, false, TWO>(a, s);
-  if (kb == 8 && vb == 4) return as ? launch_units<8, 4, true, TWO>(a, s) : launch_units<8, 4, false, TWO>(a, s);
-  return as ? launch_units<2, 2, true, TWO>(a, s) : launch_units<2, 2, false, TWO>(a, s);
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = done.find(dev);
+  if (it == done.end()) {
+    Room r{};
+    if ((e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    for (int c = 1; c < 4; ++c)
+      if ((e = sinks_tc_clusters(v, r.sms >> c << c, c, &r.clusters[c])) != cudaSuccess) return e;
+    it = done.emplace(dev, r).first;
+  }
+  *room = it->second;
+  return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_sinks_tc(const DecodeArgs& a, cudaStream_t s) {
-  return a.c.q_bits == 32 ? launch_format<true>(a, s) : launch_format<false>(a, s);
+  Room room;
+  const cudaError_t e = room_of_device(a.c, &room);
+  if (e != cudaSuccess) return e;
+  const int rows = (a.c.q_bits == 32 ? kQ : 2 * kQ) / a.G;
+  const int units = (a.B + rows - 1) / rows * a.c.H;
+  // The largest cluster of which all units' run at once (one CTA an SM: its shared memory and all of its tensor
+  // memory), of 4 tiles a CTA at least
+  const long long reach = (long long)a.sinks + a.span + rows, held = (long long)a.mbps * kBlock;
+  const long long tiles = (reach < held ? reach : held) / kTok;
+  int c = 3;
+  while (c > 0 && (units > room.clusters[c] || tiles < (4 << c))) --c;
+  if (c > 0) return launch_sinks_tc_shared(a, units, rows, c, s);
+  return by_format<false>(a.c, [&](auto k) {
+    const cudaError_t p = k.prepare();
+    return p != cudaSuccess ? p : k.launch(a, units, rows, units < room.sms ? units : room.sms, 0, s);
+  });
 }
 
 }  // namespace kvq
