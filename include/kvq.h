@@ -313,9 +313,10 @@ typedef struct {
 /*
  * kvq_norm_rope_append -- kvq_rope_append of queries and keys whose heads are normed first:
  *   z_j = x_j / sqrt(mean(x^2) + eps) * weight_j over the head's 128 dimensions,
- * then turned (dimensions behind rotary_dim are normed too).  Computed as the exact value rounded to float32 and
- * then to bf16, once, up to one case in about 2^30 (weights that differ from one are float32: 1 + w of a
- * model that stores w is added by the caller).  Values are stored as they come.  Everything else as kvq_rope_append.
+ * then turned (dimensions behind rotary_dim are normed too).  Keys are computed as the exact value rounded to
+ * float32 and then to bf16, up to one case in about 2^30, and written as kvq_append writes them; queries in float32
+ * (within 2^-20 of the two terms of a turn), rounded to bf16 once.  Weights are float32: 1 + w of a model that
+ * stores w is added by the caller.  Values are stored as they come.  Everything else as kvq_rope_append.
  */
 kvq_status kvq_norm_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const kvq_norm_desc* norm,
                                 const void* q, int32_t q_heads, int64_t q_stride, void* q_out, const void* k_new,

@@ -225,12 +225,14 @@ class _Args:
     """Pointers of one call's tensor arguments; None and raw pointers pass through.  The library cannot see a
     tensor's type, layout or device: they are checked here, and a mismatch is an invalid argument."""
 
-    __slots__ = ("where", "device", "bf16", "f32", "i32", "u8")
+    __slots__ = ("where", "device")
+    bf16 = f32 = i32 = u8 = None  # torch's, from the first call on
 
     def __init__(self, where: str):
-        torch = _torch or _need_torch()
+        if _torch is None or _Args.u8 is None:
+            torch = _need_torch()
+            _Args.bf16, _Args.f32, _Args.i32, _Args.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
         self.where, self.device = where, _current_device()
-        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
     def stream(self, stream):
         return _stream(stream, self.device)

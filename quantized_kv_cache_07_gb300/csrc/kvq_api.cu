@@ -933,6 +933,9 @@ kvq_status kvq_copy_blocks(const kvq_cache_desc* caches, int32_t num_caches, con
         break;
       a.pools[a.layers++] = {l.k_codes, l.v_codes, reinterpret_cast<uint8_t*>(l.meta)};
     }
+    // items, and blocks of a pool, are counted in 32 bits
+    if ((long long)a.H * a.num_blocks > 0x7fffffffll || (long long)max_copies * a.H * a.layers > 0x7fffffffll)
+      return KVQ_ERR_UNSUPPORTED;
     if (kvq::launch_copy_blocks(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return KVQ_ERR_CUDA;
   }
   return KVQ_OK;

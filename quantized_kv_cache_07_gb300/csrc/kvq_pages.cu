@@ -18,15 +18,17 @@ namespace {
 constexpr int kPageThreads = 1024;
 constexpr int kPageCtas = 8;  // of the cluster
 constexpr int kPageWarps = kPageCtas * kPageThreads / 32;
+constexpr int kKeep = 16;  // pages of a thread whose counts stay in registers (pools of 131072)
+constexpr int kCols = 8;  // table entries of a lane in flight (4: 18.5 us for 64 rows of 2048, 16: 15)
 
 __device__ __forceinline__ int cluster_cta() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return int(r);
 }
-// All threads of the cluster; global writes before it are seen behind it (reads go to L2: __ldcg).
+// All threads of the cluster; the cluster's global writes before it are seen behind it (release and acquire at cluster
+// scope; what other CTAs write is read from L2, __ldcg).
 __device__ __forceinline__ void cluster_sync() {
-  __threadfence();
   __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -156,23 +158,23 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
 
   // ---- every row takes its parent's pages: those that hold tokens, but for those between the sinks and the window,
   // and its own that were kept for coming ones
-  const int chunks = (width + 127) / 128, front = (a.sinks + kBlock - 1) / kBlock;
+  const int chunks = (width + 32 * kCols - 1) / (32 * kCols), front = (a.sinks + kBlock - 1) / kBlock;
   for (int w = gwarp; w < B * chunks; w += kPageWarps) {
-    const int r = w / chunks, j0 = (w % chunks) * 128 + lane;
+    const int r = w / chunks, j0 = (w % chunks) * 32 * kCols + lane;
     const Row x = rows[r];
     const int* mine = a.table + size_t(r) * width;
     const int* theirs = a.table + size_t(max(x.parent, 0)) * width;
-    int old[4], now[4];
+    int old[kCols], now[kCols];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kCols; ++k) {
       const int j = j0 + 32 * k;
       old[k] = j < width ? mine[j] : -1;
       now[k] = j < width && x.parent >= 0 ? theirs[j] : -1;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kCols; ++k) {
       const int j = j0 + 32 * k;
-      if (j >= width) continue;
+      if (j >= width) break;
       const bool held = j < x.count ? a.span == 0 || j < front || (j + 1) * kBlock > x.len - a.span
                                     : x.parent == r && j < x.need;
       if (!page_ok(a, old[k], bad)) old[k] = -1;
@@ -208,6 +210,24 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
   }
   if (any) ws[kWsAny] = 1;
   cluster_sync();
+  // what is read next, on its way together with the word that says whether it is final
+  constexpr int kPer = kMaxBatch / kPageThreads;  // rows a thread: tid * per ..
+  const int per = (B + kPageThreads - 1) / kPageThreads;
+  int last[kPer], held[kPer], gone[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = tid * per + i;
+    last[i] = -1;
+    gone[i] = 0;
+    if (i < per && r < B) {
+      const Row x = rows[r];
+      gone[i] = __ldcg(&ws[kWsMissing + r]);
+      if (x.parent >= 0 && (max(x.len - a.window, 0) & (kBlock - 1)) != 0) {
+        last[i] = __ldcg(&a.table_out[size_t(r) * width + x.count - 1]);
+        if (last[i] < 0) bad |= KVQ_DEVERR_BLOCK_ID;
+      }
+    }
+  }
   if (__ldcg(&ws[kWsAny])) {
     for (int r = gwarp; r < B; r += kPageWarps) {
       const Row x = rows[r];
@@ -222,29 +242,27 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
 
   // ---- each row's last page, where it has room left: its own alone, or to be copied.  Of the rows that write to it the
   // lowest keeps it, if no one else holds it.  Every CTA finds this for all rows
-  auto last_of = [&](int r, int& refs) {
-    const Row x = rows[r];
-    refs = 0;
-    if (x.parent < 0 || (max(x.len - a.window, 0) & (kBlock - 1)) == 0) return -1;
-    const int e = __ldcg(&a.table_out[size_t(r) * width + x.count - 1]);
-    if (e < 0) {
-      bad |= KVQ_DEVERR_BLOCK_ID;
-      return -1;
-    }
-    refs = __ldcg(&a.refs_out[e]);
-    return e;
-  };
-  constexpr int kPer = kMaxBatch / kPageThreads;  // rows a thread: tid * per ..
-  const int per = (B + kPageThreads - 1) / kPageThreads;
-  int last[kPer], held[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = tid * per + i;
-    last[i] = -1;
-    if (i < per && r < B) {
-      last[i] = last_of(r, held[i]);
-      if (last[i] >= 0 && held[i] > 1) wr.add(last[i], r);
+  for (int i = 0; i < kPer; ++i)
+    if (last[i] >= 0) {
+      held[i] = __ldcg(&a.refs_out[last[i]]);
+      if (held[i] > 1) wr.add(last[i], tid * per + i);
     }
+  // ---- free pages of this CTA's part of the pool: a small part's counts stay in registers
+  const int part = ((n + kPageCtas - 1) / kPageCtas + 31) / 32 * 32;
+  const int p0 = min(cta * part, n), p1 = min(p0 + part, n);
+  const bool kept = part <= kKeep * kPageThreads;
+  uint32_t free_bits = 0;
+  int free_here = 0, free_cta;
+  if (kept) {
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k) {
+      const int i = p0 + k * kPageThreads + tid;
+      if (i < p1 && __ldcg(&a.refs_out[i]) == 0) free_bits |= 1u << k;
+    }
+    free_here = __popc(free_bits);
+  } else {
+    for (int i = p0 + tid; i < p1; i += kPageThreads) free_here += __ldcg(&a.refs_out[i]) == 0;
   }
   __syncthreads();
   int asks = 0, copies = 0, ask[kPer], copy[kPer];
@@ -257,7 +275,7 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
         const int s = wr.find(last[i]);
         copy[i] = !(wr.rows[s] == held[i] && wr.first[s] == r);
       }
-      ask[i] = __ldcg(&ws[kWsMissing + r]) + copy[i];
+      ask[i] = gone[i] + copy[i];
       asks += ask[i];
       copies += copy[i];
     }
@@ -279,11 +297,6 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
     pages_before[B] = all_asks;
     copies_before[B] = all_copies;
   }
-  // ---- free pages of this CTA's part of the pool
-  const int part = ((n + kPageCtas - 1) / kPageCtas + 31) / 32 * 32;
-  const int p0 = min(cta * part, n), p1 = min(p0 + part, n);
-  int free_here = 0, free_cta;
-  for (int i = p0 + tid; i < p1; i += kPageThreads) free_here += __ldcg(&a.refs_out[i]) == 0;
   cta_scan(free_here, warp_sum, free_cta, warp, lane);
   if (tid == 0) ws[kWsCounts + cta] = free_cta;
   cluster_sync();
@@ -298,8 +311,8 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
   if (all_asks > free_all) {
     // ---- too few: all is as it was before
     for (int w = gwarp; w < B * chunks; w += kPageWarps) {
-      const int r = w / chunks;
-      for (int j = (w % chunks) * 128 + lane; j < min(width, (w % chunks) * 128 + 128); j += 32) {
+      const int r = w / chunks, j0 = (w % chunks) * 32 * kCols;
+      for (int j = j0 + lane; j < min(width, j0 + 32 * kCols); j += 32) {
         const size_t at = size_t(r) * width + j;
         const int was = a.table[at], now = __ldcg(&a.table_out[at]);
         a.table_out[at] = was;
@@ -323,7 +336,8 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
     // ---- the k-th free page goes to the k-th place that asks
     for (int base = p0; base < p1 && free_before < all_asks; base += kPageThreads) {
       const int i = base + tid;
-      const bool is_free = i < p1 && __ldcg(&a.refs_out[i]) == 0;
+      const bool is_free = kept ? (free_bits & 1u) != 0 : i < p1 && __ldcg(&a.refs_out[i]) == 0;
+      free_bits >>= 1;
       int here;
       const int k = free_before + cta_scan(is_free ? 1 : 0, warp_sum, here, warp, lane) - 1;
       free_before += here;
@@ -436,40 +450,91 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
   if (bad) flag(a.err, bad);
 }
 
-// ---- copies of pages: a warp per (layer, pair, head)
-__device__ __forceinline__ void copy_lines(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
-  const uint4* s = reinterpret_cast<const uint4*>(src) + lane;
-  uint4* d = reinterpret_cast<uint4*>(dst) + lane;
-  uint4 v[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k * 512 < bytes) v[k] = s[k * 32];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k * 512 < bytes) d[k * 32] = v[k];
+// ---- copies of pages: a warp takes (layer, pair, head) in turn, and its lane 0 moves each by bulk copies
+// through shared memory: keys, values and metadata in, and out as soon as they have landed, kCopySlots of them on their way.
+constexpr int kCopyWarps = 8, kCopySlots = 6;
+
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
 }
 
-__global__ void __launch_bounds__(256) copy_blocks_kernel(const CopyArgs a) {
+__global__ void __launch_bounds__(kCopyWarps * 32) copy_blocks_kernel(const CopyArgs a, int slots) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kCopyWarps][kCopySlots];
+  __shared__ int2 places[kCopyWarps][kCopySlots];  // where a slot's page goes: layer, block in its pool
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (lane == 0) {
+    for (int s = 0; s < kCopySlots; ++s) mbar_init(&bars[warp][s], 1);
+    fence_mbar_init();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int n = min(max(*a.num_copies, 0), a.max_copies), H = a.H, per = n * H;
-  const long long all = (long long)per * a.layers;
-  for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < all; w += (long long)gridDim.x * 8) {
-    const int layer = int(w / per), rest = int(w % per), pair = rest / H, h = rest % H;
+  const int n = min(max(*a.num_copies, 0), a.max_copies), H = a.H;
+  const uint32_t per = uint32_t(n) * H, all = per * a.layers, step = gridDim.x * kCopyWarps;
+  const uint32_t kb = a.k_bytes, vb = a.v_bytes, mb = a.meta_bytes;
+  uint8_t* buf = smem + size_t(warp) * slots * (kb + vb + mb);
+  const uint64_t pol = l2_evict_first_policy();
+  const uint32_t first = blockIdx.x * kCopyWarps + warp;
+  const int mine = first < all ? int((all - 1 - first) / step) + 1 : 0;  // items of this warp
+  // lane l: item base + l of the warp's; its layer, or -1 for a pair out of range, and its blocks in a pool
+  int layer = -1;
+  uint32_t src = 0, dst = 0;
+  auto look_up = [&](int base) {
+    if (base + lane >= mine) return;
+    const uint32_t w = first + uint32_t(base + lane) * step, rest = w % per, pair = rest % uint32_t(n), h = rest / uint32_t(n);
     const int2 m = reinterpret_cast<const int2*>(a.copies)[pair];
-    if (m.x < 0 || m.y < 0 || m.x >= a.num_blocks || m.y >= a.num_blocks) {
-      if (lane == 0) flag(a.err, KVQ_DEVERR_BLOCK_ID);
-      continue;
+    layer = m.x >= 0 && m.y >= 0 && m.x < a.num_blocks && m.y < a.num_blocks ? int(w / per) : -1;
+    src = h * a.num_blocks + m.x;
+    dst = h * a.num_blocks + m.y;
+  };
+  // the loads run slots - 1 items ahead of the stores; a slot is loaded again once its store has read it
+  bool ok = true;
+  int in = 0;
+  for (int out = 0; out < mine && ok; ++out) {
+    while (in < mine && in - out < slots - 1) {
+      if (in % 32 == 0) look_up(in);
+      const int s = in % slots, l = __shfl_sync(kFull, layer, in & 31);
+      const uint32_t from = __shfl_sync(kFull, src, in & 31), to = __shfl_sync(kFull, dst, in & 31);
+      if (lane == 0) {
+        // the slot's last store has read it: at most the one after it is still on its way (in - out is slots - 2 at most)
+        if (in >= slots) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        places[warp][s] = make_int2(l, int(to));
+        uint8_t* at = buf + s * (kb + vb + mb);
+        if (l >= 0) {
+          const CopyPools& p = a.pools[l];
+          mbar_arrive_expect_tx(&bars[warp][s], kb + vb + mb);
+          bulk_g2s(at, p.k + size_t(from) * kb, kb, &bars[warp][s], pol);
+          bulk_g2s(at + kb, p.v + size_t(from) * vb, vb, &bars[warp][s], pol);
+          if (mb) bulk_g2s(at + kb + vb, p.meta + size_t(from) * mb, mb, &bars[warp][s], pol);
+        } else {
+          flag(a.err, KVQ_DEVERR_BLOCK_ID);
+          mbar_arrive(&bars[warp][s]);
+        }
+      }
+      __syncwarp();
+      ++in;
     }
-    const size_t src = size_t(h) * a.num_blocks + m.x, dst = size_t(h) * a.num_blocks + m.y;
-    const CopyPools& p = a.pools[layer];
-    copy_lines(p.k + dst * a.k_bytes, p.k + src * a.k_bytes, a.k_bytes, lane);
-    copy_lines(p.v + dst * a.v_bytes, p.v + src * a.v_bytes, a.v_bytes, lane);
-    if (lane * 16 < a.meta_bytes)
-      *reinterpret_cast<uint4*>(p.meta + dst * a.meta_bytes + lane * 16) =
-          *reinterpret_cast<const uint4*>(p.meta + src * a.meta_bytes + lane * 16);
+    if (lane == 0) {
+      const int s = out % slots;
+      ok = mbar_wait(&bars[warp][s], uint32_t(out / slots) & 1u);
+      const int2 to = places[warp][s];
+      if (ok && to.x >= 0) {
+        const CopyPools& p = a.pools[to.x];
+        const uint8_t* at = buf + s * (kb + vb + mb);
+        bulk_s2g(p.k + size_t(uint32_t(to.y)) * kb, at, kb);
+        bulk_s2g(p.v + size_t(uint32_t(to.y)) * vb, at + kb, vb);
+        if (mb) bulk_s2g(p.meta + size_t(uint32_t(to.y)) * mb, at + kb + vb, mb);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      if (!ok) {  // the other loads on their way land first
+        flag(a.err, KVQ_DEVERR_TIMEOUT);
+        for (int k = out + 1; k < in; ++k) mbar_wait(&bars[warp][k % slots], uint32_t(k / slots) & 1u);
+      }
+    }
+    ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
   }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // ---- rings of a bf16 window: row r becomes its parent's, in place.  A CTA holds a slice of every row that changes in
@@ -495,16 +560,18 @@ __global__ void __launch_bounds__(256) fork_windows_kernel(const RingArgs a) {
     }
   }
   __syncthreads();
-  const int lines = a.slice_bytes / 16, all = moved_s * lines;
+  const int lines = a.slice_bytes / 16, log_lines = 31 - __clz(lines), all = moved_s * lines;  // a power of two
   const int slices = a.row_bytes / a.slice_bytes;
   for (int u = blockIdx.x; u < 2 * a.layers * slices; u += gridDim.x) {
     uint8_t* ring = (u / slices % 2 ? a.rings[u / slices / 2].v : a.rings[u / slices / 2].k) +
                     size_t(u % slices) * a.slice_bytes;
     for (int i = threadIdx.x; i < all; i += blockDim.x)
-      slice[i] = reinterpret_cast<const uint4*>(ring + size_t(from[i / lines]) * a.row_bytes)[i % lines];
+      cp_async16(&slice[i], reinterpret_cast<const uint4*>(ring + size_t(from[i >> log_lines]) * a.row_bytes) + (i & (lines - 1)));
+    cp_async_commit();
+    cp_async_wait<0>();
     __syncthreads();
     for (int i = threadIdx.x; i < all; i += blockDim.x)
-      reinterpret_cast<uint4*>(ring + size_t(to[i / lines]) * a.row_bytes)[i % lines] = slice[i];
+      reinterpret_cast<uint4*>(ring + size_t(to[i >> log_lines]) * a.row_bytes)[i & (lines - 1)] = slice[i];
     __syncthreads();
   }
 }
@@ -549,12 +616,19 @@ cudaError_t launch_pages_compact(PagesArgs a, cudaStream_t s) {
 
 cudaError_t launch_copy_blocks(CopyArgs a, cudaStream_t s) {
   int sms = 0;
-  const cudaError_t e = sm_count(&sms);
+  cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const long long ctas = ((long long)a.max_copies * a.H * a.layers + 7) / 8;
-  void* args[] = {&a};
-  return launch(reinterpret_cast<const void*>(copy_blocks_kernel), dim3(unsigned(ctas < 4ll * sms ? ctas : 4ll * sms)), 256,
-                0, s, args);
+  const void* k = reinterpret_cast<const void*>(copy_blocks_kernel);
+  const int item = a.k_bytes + a.v_bytes + a.meta_bytes;
+  int slots = kCopySlots;  // fewer of larger pages: three of 8 KB (bf16)
+  while (kCopyWarps * slots * item > 208 * 1024) --slots;
+  const int smem = kCopyWarps * slots * item;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - 1024)) != cudaSuccess) return e;
+  const long long ctas = ((long long)a.max_copies * a.H * a.layers + kCopyWarps - 1) / kCopyWarps;
+  // int8 pages: 203 KB of shared memory, one CTA an SM; smaller ones several
+  const int room = 227 * 1024 / (smem + 1024), most = sms * (room < 1 ? 1 : room > 3 ? 3 : room);
+  void* args[] = {&a, &slots};
+  return launch(k, dim3(unsigned(ctas < most ? ctas : most)), kCopyWarps * 32, smem, s, args);
 }
 
 cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s) {
@@ -569,7 +643,8 @@ cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s) {
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
   const long long units = 2ll * a.layers * (a.row_bytes / a.slice_bytes);
   void* args[] = {&a};
-  return launch(k, dim3(unsigned(units < 2ll * sms ? units : 2ll * sms)), 256, smem, s, args);
+  const int room = 220 * 1024 / (smem + 1024), most = sms * (room > 4 ? 4 : room);  // CTAs that load while others store
+  return launch(k, dim3(unsigned(units < most ? units : most)), 256, smem, s, args);
 }
 
 }  // namespace kvq

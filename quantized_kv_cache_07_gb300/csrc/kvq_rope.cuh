@@ -116,9 +116,9 @@ __device__ __forceinline__ uint2 rotate4(uint2 raw, const Turn& t, int R, bool i
 // ---- norms of the heads (kvq_norm_rope_append)
 //
 // z_j = x_j w_j r, r = (mean(x^2) + eps)^-1/2, then turned: y_j = r (x_j (w_j c_j) + m_j (w'_j s_j)) with w' the mate's
-// weights, so the weights are folded into the turn, once for all heads that share them.  Rounding is the
-// rotation's: the exact value rounded to float32 and then to bf16, so that 4-bit codes do not depend on how the norm was
-// summed.  In float32 r is off by 5 x 2^-24 at most (the sum of squares, which are exact, by 8 roundings of which the
+// weights, so the weights are folded into the turn, once for all heads that share them.  Queries are what float32 gives,
+// rounded to bf16 (off by 2^-20 of the terms before that).  Keys are the rotation's: the exact value rounded to
+// float32 and then to bf16, so that 4-bit codes do not depend on how the norm was summed.  In float32 r is off by 5 x 2^-24 at most (the sum of squares, which are exact, by 8 roundings of which the
 // root leaves half, eps, the root), the folded factors and the products by one each, y r and the bounds
 // themselves by one: 12 x 2^-24 of the terms covers it.  Where both ends round to the same bf16 values that is the exact
 // one; otherwise (one vector in 20) the warp takes it again in pairs of floats (about 2^-44).
@@ -221,6 +221,9 @@ static __device__ __noinline__ uint2 norm_exact(uint2 raw, uint2 other, const Tu
 }
 
 // One lane's four bf16 values normed over the warp's vector, weighted, turned and rounded; f: the turn with the weights.
+// Queries (EXACT false) stop at float32: what decides a rounding is 14 instructions a value and the far way of one vector
+// in 20, 75 us for 4099 rows of 48 vectors where the queries' 32 without it take 52.
+template <bool EXACT>
 __device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Turn& f, const float* weight, float eps,
                                               int R, bool interleaved, int lane) {
   uint2 other;
@@ -240,6 +243,14 @@ __device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Tu
   float ss = __fmaf_rn(x[3], x[3], __fmaf_rn(x[2], x[2], __fmaf_rn(x[1], x[1], __fmul_rn(x[0], x[0]))));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(kFull, ss, o));
+  if constexpr (!EXACT) {
+    const float r = rsqrtf(__fmaf_rn(ss, 1.f / kHeadDim, eps));
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(__fmaf_rn(x[j], f.c[j], __fmul_rn(m[j], f.s[j])), r);
+    if (!(ss < 0x1p100f)) return norm_exact(raw, other, t, weight, eps, ss, R, interleaved, lane);
+    return make_uint2(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]));
+  }
   const float r = __frsqrt_rn(__fmaf_rn(ss, 1.f / kHeadDim, eps)), re = __fmul_rn(r, 12.f * 0x1p-24f);
   const float ra = __fmaf_rn(r, 0x1p-148f, 0x1p-148f);  // roundings below the normal range
   float hi[4], lo[4];
@@ -263,12 +274,12 @@ __device__ __forceinline__ const float* weight_of(const float* w, bool per_head,
 }
 
 // A key's or query's four values of a lane, head h, by its row's turn.
-template <bool NORM>
+template <bool NORM, bool KEY>
 __device__ __forceinline__ uint2 turn_head(const RopeArgs& a, uint2 raw, const Turn& t, const float* weights, int h,
                                            int lane) {
   if constexpr (NORM) {
     const float* w = weight_of(weights, a.per_head, h);
-    return norm_rotate4(raw, t, fold(t, w, a.R, a.interleaved, lane), w, a.eps, a.R, a.interleaved, lane);
+    return norm_rotate4<KEY>(raw, t, fold(t, w, a.R, a.interleaved, lane), w, a.eps, a.R, a.interleaved, lane);
   } else {
     return rotate4(raw, t, a.R, a.interleaved, lane);
   }
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
   if (i < a.Hq) {
     const uint2 x = *reinterpret_cast<const uint2*>(a.q + r * a.q_stride + i * kHeadDim + 4 * lane);
     *reinterpret_cast<uint2*>(a.q_out + (size_t(r) * a.Hq + i) * kHeadDim + 4 * lane) =
-        turn_head<NORM>(a, x, load_turn(cs, a.R, a.interleaved, lane), a.q_weight, i, lane);
+        turn_head<NORM, false>(a, x, load_turn(cs, a.R, a.interleaved, lane), a.q_weight, i, lane);
     return;
   }
   const bool is_key = i < a.Hq + H;
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeArgs a) {
     if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
     return;
   }
-  if (is_key) v = turn_head<NORM>(a, v, load_turn(cs, a.R, a.interleaved, lane), a.k_weight, h, lane);
+  if (is_key) v = turn_head<NORM, true>(a, v, load_turn(cs, a.R, a.interleaved, lane), a.k_weight, h, lane);
   const uint16_t xb[4] = {uint16_t(v.x & 0xFFFF), uint16_t(v.x >> 16), uint16_t(v.y & 0xFFFF), uint16_t(v.y >> 16)};
   append_vector(a.ap, is_key, b, p, h, xb, lane);
 }
@@ -343,7 +354,7 @@ __global__ void __launch_bounds__(kGroupWarps * 32) rope_append_group_kernel(con
             (is_key ? a.ap.k_new + row * a.k_stride : a.ap.v_new + row * a.v_stride) + h * kHeadDim + 4 * lane);
         if (is_key) {
           const Turn t = load_turn(a.table + size_t(rope_row(a, row)) * a.R, a.R, a.interleaved, lane);
-          v = turn_head<NORM>(a, v, t, a.k_weight, h, lane);
+          v = turn_head<NORM, true>(a, v, t, a.k_weight, h, lane);
         }
         unpack4(v, x);
       });
@@ -449,7 +460,7 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
       const int tok = token(t, k);
       uint2 bits = raw[k];
       if constexpr (KEY)
-        bits = turn_head<NORM>(a, bits, load_turn(sm->cs[kRows + tok], a.R, a.interleaved, lane), a.k_weight, h, lane);
+        bits = turn_head<NORM, true>(a, bits, load_turn(sm->cs[kRows + tok], a.R, a.interleaved, lane), a.k_weight, h, lane);
       float x[4];
       unpack4(bits, x);
       if constexpr (BITS == 16) {
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
         uint2 v = *reinterpret_cast<const uint2*>(
             (is_key ? a.ap.k_new + (long long)r * a.k_stride : a.ap.v_new + (long long)r * a.v_stride) + h * kHeadDim +
             4 * lane);
-        if (is_key) v = turn_head<NORM>(a, v, load_turn(sm->cs[i], a.R, a.interleaved, lane), a.k_weight, h, lane);
+        if (is_key) v = turn_head<NORM, true>(a, v, load_turn(sm->cs[i], a.R, a.interleaved, lane), a.k_weight, h, lane);
         append_single(a.ap, is_key, b, p, h, v, lane);
       }
       continue;
@@ -620,7 +631,7 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
         if constexpr (NORM) {
           const float* w = weight_of(a.q_weight, a.per_head, min(h0 + k + e, a.Hq - 1));
           if (a.per_head) f = fold(t, w, a.R, a.interleaved, lane);
-          y = norm_rotate4(raw[e], t, f, w, a.eps, a.R, a.interleaved, lane);
+          y = norm_rotate4<false>(raw[e], t, f, w, a.eps, a.R, a.interleaved, lane);
         } else {
           y = rotate4(raw[e], t, a.R, a.interleaved, lane);
         }

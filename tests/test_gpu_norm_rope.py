@@ -1,7 +1,8 @@
 """Norms of the heads and rotary positions with the cache write (kvq_norm_rope_append).
 
-The definition is evaluated in float64 and rounded to float32 and then to bf16: queries are compared bit for bit,
-and the stored cache, bit for bit, with kvq_append of the keys so computed.
+The definition is evaluated in float64.  Keys are that rounded to float32 and then to bf16: the stored cache is compared,
+bit for bit, with kvq_append of the keys so computed.  Queries are float32 rounded once: half a bf16 step, and before
+that 2^-20 of the two terms of a turn (float32's 12 roundings of 2^-24 at most, and 2^-22 of the root).
 """
 import numpy as np
 import pytest
@@ -17,8 +18,9 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 
-def normed(bits, weight, eps, cs, interleaved):
-    """bf16 bits [n, heads, 128]: each head over the root of its mean square, weighted, turned by cs [n, pairs, 2]."""
+def normed(bits, weight, eps, cs, interleaved, rounded=True):
+    """bf16 bits [n, heads, 128]: each head over the root of its mean square, weighted, turned by cs [n, pairs, 2].  As
+    bf16 bits, or in float64 with the sum of the terms' sizes."""
     x = O.bf16_to_f64(bits)
     eps = float(np.float32(eps))
     with np.errstate(all="ignore"):
@@ -29,10 +31,22 @@ def normed(bits, weight, eps, cs, interleaved):
         j = np.arange(pairs)
         a, b = (2 * j, 2 * j + 1) if interleaved else (j, j + pairs)
         c, s = cs[:, None, :, 0], cs[:, None, :, 1]
-        y = x.copy()
+        y, size = x.copy(), np.abs(x)
         y[..., a] = x[..., a] * c - x[..., b] * s
         y[..., b] = x[..., a] * s + x[..., b] * c
-        return f32_to_bf16_bits(y.astype(np.float32))
+        size[..., a] = np.abs(x[..., a] * c) + np.abs(x[..., b] * s)
+        size[..., b] = np.abs(x[..., a] * s) + np.abs(x[..., b] * c)
+        return f32_to_bf16_bits(y.astype(np.float32)) if rounded else (y, size)
+
+
+def check_queries(got, bits, weight, eps, cs, interleaved):
+    """Half a bf16 step of the largest value it can be (2^-8 of it, and subnormals' 2^-134), and 2^-20 of the terms."""
+    want, size = normed(bits, weight, eps, cs, interleaved, rounded=False)
+    early = size * 2.0 ** -20 + 2.0 ** -134
+    ok = np.isfinite(want) & (np.abs(want) < 3e38)
+    y = O.bf16_to_f64(got)
+    assert np.all(np.isnan(y) == np.isnan(want))
+    assert np.all((np.abs(y - want) <= early + (np.abs(want) + early) * 2.0 ** -8)[ok])
 
 
 def heads_of(rng, n, heads, spread=3.0):
@@ -84,7 +98,7 @@ def test_bits_and_codes_of_the_definition(n, Hq, H, R, inter, fmt, kind, eps):
                               err_word=err)
     cs = rope.table.cpu().numpy().astype(np.float64)[pos]
     got = out.view(torch.int16).cpu().numpy().view(np.uint16)
-    np.testing.assert_array_equal(got, normed(q, wq, eps, cs, inter))
+    check_queries(got, q, wq, eps, cs, inter)
     key = normed(k, wk, eps, cs, inter)
     _lib.kvq_append(ref.desc, _t(key), _t(v), _i(seq), _i(slot), _lib.APPEND_QUANT, table, seqs, mb)
     torch.cuda.synchronize()
@@ -94,7 +108,7 @@ def test_bits_and_codes_of_the_definition(n, Hq, H, R, inter, fmt, kind, eps):
 
 @pytest.mark.parametrize("n", [3, 1300])
 def test_sizes_beyond_float32_squares_and_no_numbers(n):
-    """Heads whose squares overflow or vanish in float32, infinities and NaN: the definition's bits, where it has any."""
+    """Heads whose squares overflow or vanish in float32, infinities and NaN, as queries and (bf16 cache) as keys."""
     from quantized_kv_cache_07_gb300 import _lib
     from quantized_kv_cache_07_gb300.cache import HeadNorm, KVCache, RopeTable
     rng = np.random.default_rng(n)
@@ -110,10 +124,21 @@ def test_sizes_beyond_float32_squares_and_no_numbers(n):
     _lib.kvq_norm_rope_append(c.desc, rope.desc, norm.desc, _t(q), Hq, out, None, None, _i(pos), None, None,
                               _lib.APPEND_QUANT, None, 0, 0)
     cs = rope.table.cpu().numpy().astype(np.float64)[pos]
-    want = normed(q, norm.q_weight.cpu().numpy(), 1e-6, cs, False)
+    w = norm.q_weight.cpu().numpy()
+    want = normed(q, w, 1e-6, cs, False)
     got = out.view(torch.int16).cpu().numpy().view(np.uint16)
     none = np.isnan(O.bf16_to_f64(want))
-    assert np.all(np.isnan(O.bf16_to_f64(got))[none]) and none.sum() >= 128
+    assert none.sum() >= 128
+    check_queries(got, q, w, 1e-6, cs, False)
+    # the same as keys: the definition's bits, where it has any
+    cache = KVCache(n // 16 + 1, Hq, 16, 16)
+    at = np.arange(n)
+    _lib.kvq_norm_rope_append(cache.desc, rope.desc, HeadNorm(None, w).desc, None, 0, None, _t(q), _t(q), _i(pos), _i(at * 0),
+                              _i(at), _lib.APPEND_QUANT, _i([np.arange(n // 16 + 1)]), 1, n // 16 + 1)
+    k, v = torch.empty(n, Hq, 128, device="cuda"), torch.empty(n, Hq, 128, device="cuda")
+    _lib.kvq_dequant(cache.desc, _i(at), k, v)
+    got = f32_to_bf16_bits(k.cpu().numpy())
+    assert np.all(np.isnan(k.cpu().numpy()) == none)
     np.testing.assert_array_equal(got[~none], want[~none])
 
 
