@@ -220,12 +220,9 @@ static __device__ __noinline__ uint2 norm_exact(uint2 raw, uint2 other, const Tu
   return make_uint2(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]));
 }
 
-// One lane's four bf16 values normed over the warp's vector, weighted, turned and rounded; f: the turn with the weights.
-// Queries (EXACT false) stop at float32: what decides a rounding is 14 instructions a value and the far way of one vector
-// in 20, 75 us for 4099 rows of 48 vectors where the queries' 32 without it take 52.
-template <bool EXACT>
-__device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Turn& f, const float* weight, float eps,
-                                              int R, bool interleaved, int lane) {
+// The mates of a lane's four bf16 values.  Behind R they count as -0, which as the second term leaves any first one as it
+// is, zeros' signs too.
+__device__ __forceinline__ uint2 mates_of(uint2 raw, int R, bool interleaved, int lane) {
   uint2 other;
   if (interleaved) {
     other = make_uint2(__byte_perm(raw.x, 0, 0x1032), __byte_perm(raw.y, 0, 0x1032));
@@ -234,8 +231,15 @@ __device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Tu
     const int mate = d < R ? (d < (R >> 1) ? lane + step : lane - step) : lane;
     other = make_uint2(__shfl_sync(kFull, raw.x, mate), __shfl_sync(kFull, raw.y, mate));
   }
-  // behind R the mate counts as -0, which as the second term leaves any first one as it is, zeros' signs too
   if (4 * lane >= R) other = make_uint2(0x80008000u, 0x80008000u);
+  return other;
+}
+
+// One lane's four bf16 values of a key normed over the warp's vector, weighted, turned and rounded; f: the turn with the
+// weights.
+__device__ __forceinline__ uint2 norm_key4(uint2 raw, const Turn& t, const Turn& f, const float* weight, float eps, int R,
+                                           bool interleaved, int lane) {
+  const uint2 other = mates_of(raw, R, interleaved, lane);
   const float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u), __uint_as_float(raw.y << 16),
                       __uint_as_float(raw.y & 0xFFFF0000u)};
   const float m[4] = {__uint_as_float(other.x << 16), __uint_as_float(other.x & 0xFFFF0000u),
@@ -243,14 +247,6 @@ __device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Tu
   float ss = __fmaf_rn(x[3], x[3], __fmaf_rn(x[2], x[2], __fmaf_rn(x[1], x[1], __fmul_rn(x[0], x[0]))));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss = __fadd_rn(ss, __shfl_xor_sync(kFull, ss, o));
-  if constexpr (!EXACT) {
-    const float r = rsqrtf(__fmaf_rn(ss, 1.f / kHeadDim, eps));
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(__fmaf_rn(x[j], f.c[j], __fmul_rn(m[j], f.s[j])), r);
-    if (!(ss < 0x1p100f)) return norm_exact(raw, other, t, weight, eps, ss, R, interleaved, lane);
-    return make_uint2(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]));
-  }
   const float r = __frsqrt_rn(__fmaf_rn(ss, 1.f / kHeadDim, eps)), re = __fmul_rn(r, 12.f * 0x1p-24f);
   const float ra = __fmaf_rn(r, 0x1p-148f, 0x1p-148f);  // roundings below the normal range
   float hi[4], lo[4];
@@ -268,6 +264,70 @@ __device__ __forceinline__ uint2 norm_rotate4(uint2 raw, const Turn& t, const Tu
   return y;
 }
 
+static __device__ __noinline__ uint2 norm_large(uint2 raw, const Turn t, const float* weight, float eps, float ss, int R,
+                                               bool interleaved, int lane) {
+  return norm_exact(raw, mates_of(raw, R, interleaved, lane), t, weight, eps, ss, R, interleaved, lane);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+// A query's: float32, two values an instruction, rounded to bf16 once (what decides a key's rounding is 14 instructions a
+// value and the far way of one vector in 20).  Weights of each head (PER) multiply the values before they turn, f is the plain turn then.
+template <bool PER>
+__device__ __forceinline__ uint2 norm_query4(uint2 raw, const Turn& f, const float* weight, float eps, int R,
+                                             bool interleaved, int lane) {
+  float2 x0 = unpack2(raw.x), x1 = unpack2(raw.y);
+  float2 sq = fma2(x1, x1, mul2(x0, x0));
+  float ss = sq.x + sq.y;
+  float2 m0, m1;
+  if constexpr (PER) {
+    const float4 w = weight ? *reinterpret_cast<const float4*>(weight + 4 * lane) : make_float4(1.f, 1.f, 1.f, 1.f);
+    x0 = mul2(x0, make_float2(w.x, w.y));
+    x1 = mul2(x1, make_float2(w.z, w.w));
+    if (interleaved) {
+      m0 = make_float2(x0.y, x0.x);
+      m1 = make_float2(x1.y, x1.x);
+    } else {
+      const int d = 4 * lane, mate = d < R ? (d < (R >> 1) ? lane + (R >> 3) : lane - (R >> 3)) : lane;
+      m0 = make_float2(__shfl_sync(kFull, x0.x, mate), __shfl_sync(kFull, x0.y, mate));
+      m1 = make_float2(__shfl_sync(kFull, x1.x, mate), __shfl_sync(kFull, x1.y, mate));
+    }
+  } else {
+    const uint2 other = mates_of(raw, R, interleaved, lane);
+    m0 = unpack2(other.x);
+    m1 = unpack2(other.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+  if (!(ss < 0x1p100f)) {  // the same in the whole warp
+    Turn t = f;
+    if constexpr (!PER) {  // the weights are in the turn: norm_exact takes them from there
+      return norm_large(raw, t, nullptr, eps, ss, R, interleaved, lane);
+    }
+    return norm_large(raw, t, weight, eps, ss, R, interleaved, lane);
+  }
+  const float r = rsqrtf(fmaf(ss, 1.f / kHeadDim, eps));
+  const float2 rr = make_float2(r, r);
+  const float2 y0 = mul2(fma2(x0, make_float2(f.c[0], f.c[1]), mul2(m0, make_float2(f.s[0], f.s[1]))), rr);
+  const float2 y1 = mul2(fma2(x1, make_float2(f.c[2], f.c[3]), mul2(m1, make_float2(f.s[2], f.s[3]))), rr);
+  return make_uint2(pack_bf162(y0.x, y0.y), pack_bf162(y1.x, y1.y));
+}
+
 // Head h's weights, or null.
 __device__ __forceinline__ const float* weight_of(const float* w, bool per_head, int h) {
   return w && per_head ? w + h * kHeadDim : w;
@@ -279,7 +339,10 @@ __device__ __forceinline__ uint2 turn_head(const RopeArgs& a, uint2 raw, const T
                                            int lane) {
   if constexpr (NORM) {
     const float* w = weight_of(weights, a.per_head, h);
-    return norm_rotate4<KEY>(raw, t, fold(t, w, a.R, a.interleaved, lane), w, a.eps, a.R, a.interleaved, lane);
+    if constexpr (KEY)
+      return norm_key4(raw, t, fold(t, w, a.R, a.interleaved, lane), w, a.eps, a.R, a.interleaved, lane);
+    else
+      return norm_query4<true>(raw, t, w, a.eps, a.R, a.interleaved, lane);
   } else {
     return rotate4(raw, t, a.R, a.interleaved, lane);
   }
@@ -422,17 +485,21 @@ __device__ __forceinline__ void put_tokens(uint8_t* img, int t, const uint32_t (
   }
 }
 
-// One full block of head h: tokens r .. r + 15 of the call, four at a time in a loop: unrolled over the 16
+// One full block of head h, or with norms half of one (part 0 or 1: of every eight tokens the lower or the upper four; a
+// warp's task is half as long then: 4099 rows of 8 heads, keys and values alone, 36 us in blocks and 31 in halves): tokens
+// r .. r + 15 of the call, four at a time in a loop: unrolled over the 16
 // tokens the kernel waited on instruction fetches (6.6 of 12 stalled warps; 209 us for 8192 rows).
 template <int BITS, bool KEY, bool NORM>
-__device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int r, int h, uint8_t* img, int lane) {
+__device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int r, int h, uint8_t* img, int lane,
+                                            int part) {
   const CacheView& c = a.ap.c;
   const long long stride = KEY ? a.k_stride : a.v_stride;
   const uint16_t* src = (KEY ? a.ap.k_new : a.ap.v_new) + r * stride + h * kHeadDim + 4 * lane;
   auto token = [](int t, int k) { return 2 * t + (k >> 1) + 8 * (k & 1); };
+  const int t0 = NORM ? 2 * part : 0, t1 = NORM ? t0 + 2 : 4;
   uint2 next[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint2*>(src + token(0, k) * stride);
+  for (int k = 0; k < 4; ++k) next[k] = *reinterpret_cast<const uint2*>(src + token(t0, k) * stride);
   const int b = sm->seq[r - blockIdx.x * kRows + kRows - 1], p = sm->pos[r - blockIdx.x * kRows + kRows - 1];
   if (p / kBlock >= a.ap.mbps) {
     if (lane == 0) flag(a.ap.err, KVQ_DEVERR_POSITION);
@@ -447,12 +514,12 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
   if (KEY && c.factor) f = *reinterpret_cast<const float4*>(c.factor + h * kHeadDim + 4 * lane);
   float s_of = 1.f, z_of = 0.f;  // lane i < 16: token i's scale and zero point
 #pragma unroll 1
-  for (int t = 0; t < 4; ++t) {
+  for (int t = t0; t < t1; ++t) {
     uint2 raw[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       raw[k] = next[k];
-      if (t < 3) next[k] = *reinterpret_cast<const uint2*>(src + token(t + 1, k) * stride);
+      if (t < t1 - 1) next[k] = *reinterpret_cast<const uint2*>(src + token(t + 1, k) * stride);
     }
     uint32_t u[4][4];
 #pragma unroll
@@ -507,10 +574,12 @@ __device__ __forceinline__ void write_block(const RopeArgs& a, RopeSmem* sm, int
   __syncwarp();
   constexpr int kBytes = block_bytes(BITS);
   uint8_t* blk = (KEY ? c.k_codes : c.v_codes) + (size_t(h) * c.num_blocks + phys) * kBytes;
+  // a half is the 16-byte pieces of its tokens: keys by token, values by token pair
+  if (!NORM || (KEY ? lane >> 4 : (lane & 3) >> 1) == part)
 #pragma unroll
-  for (int i = 0; i < kBytes / 512; ++i)
-    reinterpret_cast<uint4*>(blk)[i * 32 + lane] = reinterpret_cast<const uint4*>(img)[i * 32 + lane];
-  if (BITS != 16 && lane < kBlock && !(KEY && c.k_chan)) {
+    for (int i = 0; i < kBytes / 512; ++i)
+      reinterpret_cast<uint4*>(blk)[i * 32 + lane] = reinterpret_cast<const uint4*>(img)[i * 32 + lane];
+  if (BITS != 16 && lane < kBlock && !(KEY && c.k_chan) && (!NORM || (lane & 7) >> 2 == part)) {
     float* rec = c.meta + (size_t(h) * c.num_blocks + phys) * c.meta_floats + (KEY ? 0 : c.meta_floats / 2);
     rec[lane] = s_of;
     if (c.asym) rec[kBlock + lane] = z_of;
@@ -585,13 +654,15 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
   __syncthreads();
 
   // ---- tasks: the run's blocks, the single rows' vectors, the queries 8 at a time
-  const int blocks = lead >= 0 ? 2 * H : 0, singles = sm->single ? 2 * H : 0;
+  constexpr int kHalves = NORM ? 2 : 1;
+  const int blocks = lead >= 0 ? kHalves * 2 * H : 0, singles = sm->single ? 2 * H : 0;
   const int q8 = (a.Hq + 7) / 8, queries = kRows * q8;
   const int step = 8 * gridDim.y;
   for (int task = blockIdx.y * 8 + warp; task < blocks + singles + queries; task += step) {
     if (task < blocks) {
-      if (task < H) write_block<KB, true, NORM>(a, sm, lead, task, sm->img[warp], lane);
-      else write_block<VB, false, NORM>(a, sm, lead, task - H, sm->img[warp], lane);
+      const int th = task / kHalves, part = task % kHalves;
+      if (th < H) write_block<KB, true, NORM>(a, sm, lead, th, sm->img[warp], lane, part);
+      else write_block<VB, false, NORM>(a, sm, lead, th - H, sm->img[warp], lane, part);
       continue;
     }
     if (task < blocks + singles) {
@@ -612,6 +683,7 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
       }
       continue;
     }
+    if constexpr (NORM) continue;  // norm_queries_kernel
     const int qt = task - blocks - singles, i = qt / q8, h0 = (qt % q8) * 8, r = r0 + i;
     if (r >= n || sm->rope[i + kRows - 1] < 0) continue;
     const uint16_t* src = a.q + (long long)r * a.q_stride + h0 * kHeadDim + 4 * lane;
@@ -621,20 +693,11 @@ __global__ void __launch_bounds__(256, 3) rope_rows_kernel(const RopeArgs a) {
       raw[k] = h0 + k < a.Hq ? *reinterpret_cast<const uint2*>(src + k * kHeadDim) : make_uint2(0u, 0u);
     uint16_t* dst = a.q_out + ((size_t)r * a.Hq + h0) * kHeadDim + 4 * lane;
     const Turn t = load_turn(sm->cs[i], a.R, a.interleaved, lane);
-    Turn f{};
-    if constexpr (NORM) f = fold(t, a.per_head ? nullptr : a.q_weight, a.R, a.interleaved, lane);
 #pragma unroll 1
     for (int k = 0; k < 8; k += 2) {  // a short loop; the registers rotate, so that every index is known
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        uint2 y;
-        if constexpr (NORM) {
-          const float* w = weight_of(a.q_weight, a.per_head, min(h0 + k + e, a.Hq - 1));
-          if (a.per_head) f = fold(t, w, a.R, a.interleaved, lane);
-          y = norm_rotate4<false>(raw[e], t, f, w, a.eps, a.R, a.interleaved, lane);
-        } else {
-          y = rotate4(raw[e], t, a.R, a.interleaved, lane);
-        }
+        const uint2 y = rotate4(raw[e], t, a.R, a.interleaved, lane);
         if (h0 + k + e < a.Hq) *reinterpret_cast<uint2*>(dst + (k + e) * kHeadDim) = y;
       }
 #pragma unroll
@@ -650,7 +713,7 @@ cudaError_t launch_rows(const RopeArgs& a, int sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int windows = (a.ap.n + kRows - 1) / kRows;
-  const int tasks = (a.write ? 4 * a.ap.c.H : 0) + kRows * ((a.Hq + 7) / 8);
+  const int tasks = NORM ? 8 * a.ap.c.H : (a.write ? 4 * a.ap.c.H : 0) + kRows * ((a.Hq + 7) / 8);
   // few windows: their tasks over several CTAs, up to two tasks a warp
   int y = (8 * sms + windows - 1) / windows;
   y = y > (tasks + 15) / 16 ? (tasks + 15) / 16 : y;
@@ -680,6 +743,52 @@ cudaError_t launch_pdl(void (*kernel)(const RopeArgs), const RopeArgs& a, long l
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// ---- queries of many rows with their norms: a warp takes 8 heads of a row, all its loads in flight.
+// It runs beside the keys' and values' kernel, which has let it start after its own wait for what is before both on the
+// stream, so its queries are complete and are read from L2; it waits for that kernel only before it ends, so that what
+// follows on the stream follows both (as in kvq_shared.cuh).
+template <bool PER>
+__global__ void __launch_bounds__(256, 4) norm_queries_kernel(const RopeArgs a, bool beside) {
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, Hq = a.Hq, q8 = (Hq + 7) / 8;
+  const uint32_t task = blockIdx.x * 8 + (threadIdx.x >> 5), r = task / q8, h0 = (task % q8) * 8;
+  const int rp = r < uint32_t(a.ap.n) ? __ldcg(a.rope_pos + r) : -1;
+  if (rp >= 0 && rp < a.max_pos) {
+    const uint16_t* src = a.q + (long long)r * a.q_stride + h0 * kHeadDim + 4 * lane;
+    uint2 raw[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      raw[k] = h0 + k < Hq ? __ldcg(reinterpret_cast<const uint2*>(src + k * kHeadDim)) : make_uint2(0u, 0u);
+    uint16_t* dst = a.q_out + ((size_t)r * Hq + h0) * kHeadDim + 4 * lane;
+    const Turn t = load_turn(a.table + size_t(rp) * a.R, a.R, a.interleaved, lane);
+    const Turn f = PER ? t : fold(t, a.q_weight, a.R, a.interleaved, lane);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* w = PER ? weight_of(a.q_weight, true, min(int(h0) + k, Hq - 1)) : nullptr;
+      const uint2 y = norm_query4<PER>(raw[k], f, w, a.eps, a.R, a.interleaved, lane);
+      if (int(h0) + k < Hq) *reinterpret_cast<uint2*>(dst + k * kHeadDim) = y;
+    }
+  } else if (r < uint32_t(a.ap.n) && lane == 0 && h0 == 0) {
+    flag(a.ap.err, KVQ_DEVERR_POSITION);
+  }
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+cudaError_t launch_norm_queries(const RopeArgs& a, bool beside, cudaStream_t s) {
+  const long long tasks = (long long)a.ap.n * ((a.Hq + 7) / 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned((tasks + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, a.per_head ? norm_queries_kernel<true> : norm_queries_kernel<false>, a, beside);
+}
+
 template <bool NORM>
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const int kb = a.ap.c.k_bits, vb = a.ap.c.v_bits;
@@ -690,6 +799,13 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   constexpr long long kRowsVectors = 3ll * 152 * 64;
   const long long vectors = (long long)a.ap.n * (a.Hq + (a.write ? 2 * a.ap.c.H : 0));
   if (vectors >= kRowsVectors && (!a.write || (a.ap.mode == KVQ_APPEND_QUANT && !group))) {
+    if (NORM && a.Hq > 0) {
+      if (!a.write) return launch_norm_queries(a, false, s);
+      RopeArgs kv = a;
+      kv.Hq = 0;
+      const cudaError_t e = launch_rope<NORM>(kv, s);  // by windows or one by one, as many as they are
+      return e != cudaSuccess ? e : launch_norm_queries(a, true, s);
+    }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
