@@ -1235,7 +1235,11 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
   // Effective stream split: never more CTAs than blocks / kMinBlocksPerCta, so
   // every CTA below Pe owns blocks and a unit's owners are exactly c0..c1.
   const long long cap_ctas = (T + kMinBlocksPerCta - 1) / kMinBlocksPerCta;
-  const int Pe = int(cap_ctas < (long long)P ? cap_ctas : (long long)P);
+  int Pe = int(cap_ctas < (long long)P ? cap_ctas : (long long)P);
+  // Windows make the units alike: a multiple of their number leaves no CTA with parts of two, where that gives up
+  // an eighth of the CTAs at most (one sequence of 4 heads of 700 tokens: 9 CTAs 16.5 us, 8 12.4; 8 heads on a window
+  // of 4096: 129 20.5, 128 16.5; but 128 units of 2000: 456 24.6, 384 26.7)
+  if (SPAN && Pe > U && Pe % U <= Pe / 8) Pe -= Pe % U;
   uint32_t cphase = 0;
 
   // ==================================================================== window CTAs
