@@ -659,7 +659,7 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
  *   - its last block, if there is room left in it, is its own: of the rows that share it the lowest keeps it
  *     unless other entries or claims hold it too, the others get a new block and a pair (source,
  *     destination) in `copies`, in the order of rows
- *   - it has a block of its own for each of the next `room` tokens
+ *   - it has blocks of its own for the next `room` tokens, or rooms[r] (device int32 [batch], NULL: room for all)
  * New blocks are the free ones from the lowest number on, in the order of rows and their entries.
  * Blocks that no entry holds any more are free at once, for this call's rows as well.
  *   block_table  : device int32 [batch][max_blocks_per_seq], -1 where there is no block
@@ -667,21 +667,24 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
  *                  (KVQ_ERR_UNSUPPORTED)
  *   refs_out     : may be refs itself; table_out and lens_out are not block_table and seq_lens
  *                  (KVQ_ERR_INVALID_ARG): a program keeps two of each and uses them in turn
+ *   parent_out   : device int32 [batch] or NULL: what each row became, itself where nothing changed (too few blocks,
+ *                  a parent out of range)
  *   copies       : device int32 [batch][2], 8-byte aligned; num_copies: device int32.  kvq_copy_blocks next on
- *                  the stream, in every layer; kvq_fork_windows too, where there is a bf16 window
+ *                  the stream, in every layer; kvq_fork_windows by parent_out too, where there is a bf16 window
  *   workspace    : >= kvq_pages_workspace_size bytes; what it holds does not matter, one per
  *                  concurrently running call
  * Errors: NO_BLOCKS: the free blocks do not suffice, and nothing changes (the outputs are the inputs, no copies);
- * POSITION: a parent outside [-1, batch), the row stays itself; SEQ_LEN: a length (or length and room) < 0
- * or beyond the table's capacity: cut; BLOCK_ID: an entry outside [-1, num_blocks), or a last block that is missing: -1.
+ * POSITION: a parent outside [-1, batch), the row stays itself; SEQ_LEN: a length, a room (or both together) < 0 or beyond
+ * the table's capacity: cut; BLOCK_ID: an entry outside [-1, num_blocks), or a last block that is missing: -1.
  * refs that are less than the entries in the table are the caller's mistake: blocks in use may be handed out.
  * Requirements: batch in 1..4096.
  */
 kvq_status kvq_pages_update(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
                             const int32_t* parent, int32_t batch, int32_t max_blocks_per_seq, int32_t window,
-                            int32_t room, int32_t sinks, int32_t span, int32_t* refs_out, int32_t* table_out,
-                            int32_t* lens_out, int32_t* copies, int32_t* num_copies, void* workspace,
-                            size_t workspace_bytes, uint32_t* err_word, void* stream);
+                            int32_t room, const int32_t* rooms, int32_t sinks, int32_t span, int32_t* refs_out,
+                            int32_t* table_out, int32_t* lens_out, int32_t* parent_out, int32_t* copies,
+                            int32_t* num_copies, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                            void* stream);
 
 /*
  * kvq_pages_compact -- the blocks in use (refs > 0) to the front of their pools, so that the pools can be cut to

@@ -120,8 +120,8 @@ SIGNATURES = {
                             c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
                             c_void_p]),
     "kvq_pages_update": (c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
-                                   c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
-                                   c_size_t, c_void_p, c_void_p]),
+                                   c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "kvq_pages_compact": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p,
                                     c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "kvq_pages_workspace_size": (c_int32, [c_int32, POINTER(c_size_t)]),
@@ -184,12 +184,20 @@ def _ptr(t) -> int | None:
 _torch = _current_device = _raw_stream = None
 
 
+def _first_device() -> int:
+    """The current device; later calls take it without torch's look at whether CUDA has been started."""
+    global _current_device
+    device = _torch.cuda.current_device()
+    _current_device = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
+    return device
+
+
 def _need_torch():
     """torch, imported by the first call that needs it."""
     global _torch, _current_device, _raw_stream
     if _torch is None:
         import torch
-        _current_device = torch.cuda.current_device
+        _current_device = _first_device
         # the raw handle without a Stream object per call, where this torch has it
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -411,15 +419,20 @@ def kvq_pages_workspace_size(num_blocks: int) -> int:
 
 
 def kvq_pages_update(refs, block_table, seq_lens, refs_out, table_out, lens_out, copies, num_copies, parent=None,
-                     room: int = 0, window: int = 0, sinks: int = 0, span: int = 0, workspace=None, err_word=None,
-                     stream=None):
-    """kvq_pages_update; refs are int32 [num_blocks], tables [batch, max_blocks_per_seq], copies [batch, 2]."""
+                     room=0, window: int = 0, sinks: int = 0, span: int = 0, parent_out=None, workspace=None,
+                     err_word=None, stream=None):
+    """kvq_pages_update; refs are int32 [num_blocks], tables [batch, max_blocks_per_seq], copies [batch, 2]; room is a
+    number for all rows or an int32 tensor [batch] (the C argument rooms)."""
     arg = _Args("kvq_pages_update")
     n, (batch, width) = int(refs.shape[0]), block_table.shape
+    rooms = None
+    if not isinstance(room, int):
+        room, rooms = 0, arg(room, arg.i32, (batch,))
     _check(load().kvq_pages_update(arg(refs, arg.i32, (n,)), n, arg(block_table, arg.i32, (batch, width)),
                                    arg(seq_lens, arg.i32, (batch,)), arg(parent, arg.i32, (batch,)), batch, width, window,
-                                   room, sinks, span, arg(refs_out, arg.i32, (n,)), arg(table_out, arg.i32, (batch, width)),
-                                   arg(lens_out, arg.i32, (batch,)), arg.room(copies, arg.i32, 2 * batch),
+                                   room, rooms, sinks, span, arg(refs_out, arg.i32, (n,)),
+                                   arg(table_out, arg.i32, (batch, width)), arg(lens_out, arg.i32, (batch,)),
+                                   arg(parent_out, arg.i32, (batch,)), arg.room(copies, arg.i32, 2 * batch),
                                    arg.room(num_copies, arg.i32, 1), arg.room(workspace, arg.u8, 0),
                                    0 if workspace is None else workspace.numel(), arg.word(err_word),
                                    arg.stream(stream)), arg.where)

@@ -150,18 +150,20 @@ class Pages:
         self.refs = zeros(first.num_blocks)
         self.table, self._table = zeros(batch, max_blocks) - 1, zeros(batch, max_blocks)
         self.lens, self._lens = zeros(batch), zeros(batch)
+        self.parents = zeros(batch)  # what each row of the last update became
         self.copies, self.counts = zeros(max(batch, first.num_blocks // 2, 1), 2), zeros(2)
         self.workspace = torch.empty(_lib.kvq_pages_workspace_size(first.num_blocks), dtype=torch.uint8, device=first.device)
 
-    def update(self, parent=None, room: int = 1, err_word=None, stream=None):
-        """kvq_pages_update: rows become their parents' sequences (-1 ends one), with room for the next ``room`` tokens."""
+    def update(self, parent=None, room=1, err_word=None, stream=None):
+        """kvq_pages_update: rows become their parents' sequences (-1 ends one), with room for the next ``room`` tokens (a
+        number, or an int32 tensor [batch])."""
         _lib.kvq_pages_update(self.refs, self.table, self.lens, self.refs, self._table, self._lens, self.copies, self.counts,
                               parent=parent, room=room, window=self.window, sinks=self.sinks, span=self.span,
-                              workspace=self.workspace, err_word=err_word, stream=stream)
+                              parent_out=self.parents, workspace=self.workspace, err_word=err_word, stream=stream)
         self.table, self._table, self.lens, self._lens = self._table, self.table, self._lens, self.lens
         _lib.kvq_copy_blocks(self.caches, self.copies[: len(self.lens)], self.counts, err_word=err_word, stream=stream)
         if self.window and parent is not None:
-            _lib.kvq_fork_windows(self.caches, parent, len(self.lens), err_word=err_word, stream=stream)
+            _lib.kvq_fork_windows(self.caches, self.parents, len(self.lens), err_word=err_word, stream=stream)
 
     def compact(self, err_word=None, stream=None):
         """kvq_pages_compact; ``counts[1]`` is then the number of blocks in use, all of them in front."""

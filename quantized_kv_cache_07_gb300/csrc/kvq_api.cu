@@ -13,6 +13,7 @@ namespace {
 
 using kvq::kHeadDim;
 
+constexpr int kMaxPages = 1 << 30;  // of a pool whose pages are managed here: counts and ranks stay in 32 bits
 constexpr int kMaxWindow = 128;  // window ring: at most 8 bf16 blocks per (sequence, kv head)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -622,9 +623,11 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, in
   if (cache->window != 0) return KVQ_ERR_UNSUPPORTED;
   st = check_decode_shape(cache, n, q_heads);
   if (st != KVQ_OK) return st;
-  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES) return KVQ_ERR_INVALID_ARG;
-  if (stream_ctas == KVQ_PREFILL_TILES) {  // the tile path needs no workspace
-    if (!kvq::prefill_tiles_supported(view(cache))) return KVQ_ERR_UNSUPPORTED;
+  if (stream_ctas < 0 && stream_ctas != KVQ_PREFILL_TILES && stream_ctas != KVQ_PREFILL_UNITS)
+    return KVQ_ERR_INVALID_ARG;
+  if (stream_ctas < 0) {  // tiles and units need no workspace
+    if (!kvq::prefill_tiles_supported(view(cache)) || (stream_ctas == KVQ_PREFILL_UNITS && cache->q_bits == 32))
+      return KVQ_ERR_UNSUPPORTED;
     *bytes = 0;
     return KVQ_OK;
   }
@@ -842,18 +845,20 @@ kvq_status kvq_pages_workspace_size(int32_t num_blocks, size_t* bytes) {
 
 kvq_status kvq_pages_update(const int32_t* refs, int32_t num_blocks, const int32_t* block_table, const int32_t* seq_lens,
                             const int32_t* parent, int32_t batch, int32_t max_blocks_per_seq, int32_t window,
-                            int32_t room, int32_t sinks, int32_t span, int32_t* refs_out, int32_t* table_out,
-                            int32_t* lens_out, int32_t* copies, int32_t* num_copies, void* workspace,
-                            size_t workspace_bytes, uint32_t* err_word, void* stream) {
+                            int32_t room, const int32_t* rooms, int32_t sinks, int32_t span, int32_t* refs_out,
+                            int32_t* table_out, int32_t* lens_out, int32_t* parent_out, int32_t* copies,
+                            int32_t* num_copies, void* workspace, size_t workspace_bytes, uint32_t* err_word,
+                            void* stream) {
   if (num_blocks < 1 || batch < 1 || max_blocks_per_seq < 1 || window < 0 || room < 0 || sinks < 0 || span < 0)
     return KVQ_ERR_INVALID_ARG;
-  if (batch > kvq::kMaxBatch || window > kMaxWindow || window % 16 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (batch > kvq::kMaxBatch || window > kMaxWindow || window % 16 != 0 || num_blocks > kMaxPages)
+    return KVQ_ERR_UNSUPPORTED;
   if (span > 0 && span < window) return KVQ_ERR_UNSUPPORTED;
   if ((long long)batch * max_blocks_per_seq > 0x7fffffffll) return KVQ_ERR_UNSUPPORTED;  // entries are counted in 32 bits
   if (!refs || !block_table || !seq_lens || !refs_out || !table_out || !lens_out || !copies || !num_copies)
     return KVQ_ERR_INVALID_ARG;
   // rows read one another's entries
-  if (table_out == block_table || lens_out == seq_lens) return KVQ_ERR_INVALID_ARG;
+  if (table_out == block_table || lens_out == seq_lens || (parent_out && parent_out == parent)) return KVQ_ERR_INVALID_ARG;
   if (!aligned8(copies)) return KVQ_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < kvq::pages_workspace_bytes(num_blocks)) return KVQ_ERR_WORKSPACE;
   if (!aligned16(workspace)) return KVQ_ERR_ALIGNMENT;
@@ -867,6 +872,8 @@ kvq_status kvq_pages_update(const int32_t* refs, int32_t num_blocks, const int32
   a.width = max_blocks_per_seq;
   a.window = window;
   a.room = room;
+  a.rooms = rooms;
+  a.parent_out = parent_out;
   a.sinks = sinks;
   a.span = span;
   a.refs_out = refs_out;
@@ -884,6 +891,7 @@ kvq_status kvq_pages_compact(const int32_t* refs, int32_t num_blocks, const int3
                              int32_t* counts, void* workspace, size_t workspace_bytes, uint32_t* err_word,
                              void* stream) {
   if (num_blocks < 1 || batch < 0 || (batch > 0 && max_blocks_per_seq < 1)) return KVQ_ERR_INVALID_ARG;
+  if (num_blocks > kMaxPages) return KVQ_ERR_UNSUPPORTED;
   if (!refs || !refs_out || !moves || !counts || (batch > 0 && (!block_table || !table_out))) return KVQ_ERR_INVALID_ARG;
   if (!aligned8(moves)) return KVQ_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < kvq::pages_workspace_bytes(num_blocks)) return KVQ_ERR_WORKSPACE;
@@ -949,6 +957,7 @@ kvq_status kvq_fork_windows(const kvq_cache_desc* caches, int32_t num_caches, co
     const kvq_status st = check_cache(&caches[i]);
     if (st != KVQ_OK) return st;
     if (caches[i].window == 0 || caches[i].window_batch < batch) return KVQ_ERR_INVALID_ARG;
+    if ((long long)caches[i].num_kv_heads * caches[i].window > (1ll << 22)) return KVQ_ERR_UNSUPPORTED;  // a row of 1 GB
   }
   if (num_caches == 0 || batch == 0) return KVQ_OK;
   if (!parent) return KVQ_ERR_INVALID_ARG;

@@ -106,6 +106,8 @@ struct PagesArgs {
   const int* parent;  // [B] or null: every row its own
   int num_blocks, B, width;
   int window, room, sinks, span;
+  const int* rooms;  // [B] or null: room for all
+  int* parent_out;   // [B] or null
   int* refs_out;
   int* table_out;
   int* lens_out;

@@ -76,7 +76,12 @@ __device__ __forceinline__ Row row_of(const PagesArgs& a, int r, uint32_t& bad) 
     bad |= KVQ_DEVERR_SEQ_LEN;
     x.len = x.len < 0 ? 0 : most;
   }
-  long long wanted = (long long)x.len + a.room;
+  int room = a.rooms ? a.rooms[r] : a.room;
+  if (room < 0) {
+    bad |= KVQ_DEVERR_SEQ_LEN;
+    room = 0;
+  }
+  long long wanted = (long long)x.len + room;
   if (wanted > most) {
     bad |= KVQ_DEVERR_SEQ_LEN;
     wanted = most;
@@ -322,7 +327,10 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
       }
     }
     if (cta == 0) {
-      for (int r = tid; r < B; r += kPageThreads) a.lens_out[r] = a.lens[r];
+      for (int r = tid; r < B; r += kPageThreads) {
+        a.lens_out[r] = a.lens[r];
+        if (a.parent_out) a.parent_out[r] = r;
+      }
       if (tid == 0) {
         *a.num_copies = 0;
         flag(a.err, KVQ_DEVERR_NO_BLOCKS);
@@ -330,7 +338,10 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
     }
   } else {
     if (cta == 0) {
-      for (int r = tid; r < B; r += kPageThreads) a.lens_out[r] = rows[r].len;
+      for (int r = tid; r < B; r += kPageThreads) {
+        a.lens_out[r] = rows[r].len;
+        if (a.parent_out) a.parent_out[r] = rows[r].parent;
+      }
       if (tid == 0) *a.num_copies = all_copies;
     }
     // ---- the k-th free page goes to the k-th place that asks
@@ -562,9 +573,9 @@ __global__ void __launch_bounds__(256) fork_windows_kernel(const RingArgs a) {
   __syncthreads();
   const int lines = a.slice_bytes / 16, log_lines = 31 - __clz(lines), all = moved_s * lines;  // a power of two
   const int slices = a.row_bytes / a.slice_bytes;
-  for (int u = blockIdx.x; u < 2 * a.layers * slices; u += gridDim.x) {
-    uint8_t* ring = (u / slices % 2 ? a.rings[u / slices / 2].v : a.rings[u / slices / 2].k) +
-                    size_t(u % slices) * a.slice_bytes;
+  for (long long u = blockIdx.x; u < 2ll * a.layers * slices; u += gridDim.x) {
+    const int pool = int(u / slices);
+    uint8_t* ring = (pool % 2 ? a.rings[pool / 2].v : a.rings[pool / 2].k) + size_t(u % slices) * a.slice_bytes;
     for (int i = threadIdx.x; i < all; i += blockDim.x)
       cp_async16(&slice[i], reinterpret_cast<const uint4*>(ring + size_t(from[i >> log_lines]) * a.row_bytes) + (i & (lines - 1)));
     cp_async_commit();

@@ -45,7 +45,11 @@ static __device__ __noinline__ float turn_exact(float a, float c, float b, float
 struct Turn {
   float c[4], s[4];
 };
+template <bool L2 = false>  // read past L1 (norm_queries_kernel)
 __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleaved, int lane) {
+  auto get = [](const float* p) {
+    return L2 ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
+  };
   const int d = 4 * lane;
   Turn t;
 #pragma unroll
@@ -55,7 +59,7 @@ __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleav
   }
   if (d >= R) return t;
   if (interleaved) {
-    const float4 v = *reinterpret_cast<const float4*>(cs + d);
+    const float4 v = get(cs + d);
     t.c[0] = t.c[1] = v.x;
     t.c[2] = t.c[3] = v.z;
     t.s[0] = -v.y;
@@ -64,8 +68,8 @@ __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleav
     t.s[3] = v.w;
   } else {
     const bool low = d < (R >> 1);
-    const float4* p = reinterpret_cast<const float4*>(cs + 2 * (low ? d : d - (R >> 1)));
-    const float4 a = p[0], b = p[1];
+    const float* p = cs + 2 * (low ? d : d - (R >> 1));
+    const float4 a = get(p), b = get(p + 4);
     const float f = low ? -1.f : 1.f;
     t.c[0] = a.x;
     t.c[1] = a.z;
@@ -132,7 +136,7 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
 // A lane's own four weights and its mates' (ones behind R, where nothing is added).
 __device__ __forceinline__ void load_weights(const float* w, int R, bool interleaved, int lane, float (&own)[4],
                                              float (&mate)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(w + 4 * lane);
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(w + 4 * lane));
   own[0] = a.x;
   own[1] = a.y;
   own[2] = a.z;
@@ -141,7 +145,7 @@ __device__ __forceinline__ void load_weights(const float* w, int R, bool interle
   float4 b = make_float4(1.f, 1.f, 1.f, 1.f);
   if (d < R) {
     if (interleaved) b = make_float4(a.y, a.x, a.w, a.z);
-    else b = *reinterpret_cast<const float4*>(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1)));
+    else b = __ldcg(reinterpret_cast<const float4*>(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1))));
   }
   mate[0] = b.x;
   mate[1] = b.y;
@@ -296,7 +300,7 @@ __device__ __forceinline__ uint2 norm_query4(uint2 raw, const Turn& f, const flo
   float ss = sq.x + sq.y;
   float2 m0, m1;
   if constexpr (PER) {
-    const float4 w = weight ? *reinterpret_cast<const float4*>(weight + 4 * lane) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 w = weight ? __ldcg(reinterpret_cast<const float4*>(weight + 4 * lane)) : make_float4(1.f, 1.f, 1.f, 1.f);
     x0 = mul2(x0, make_float2(w.x, w.y));
     x1 = mul2(x1, make_float2(w.z, w.w));
     if (interleaved) {
@@ -761,7 +765,7 @@ __global__ void __launch_bounds__(256, 4) norm_queries_kernel(const RopeArgs a, 
     for (int k = 0; k < 8; ++k)
       raw[k] = h0 + k < Hq ? __ldcg(reinterpret_cast<const uint2*>(src + k * kHeadDim)) : make_uint2(0u, 0u);
     uint16_t* dst = a.q_out + ((size_t)r * Hq + h0) * kHeadDim + 4 * lane;
-    const Turn t = load_turn(a.table + size_t(rp) * a.R, a.R, a.interleaved, lane);
+    const Turn t = load_turn<true>(a.table + size_t(rp) * a.R, a.R, a.interleaved, lane);
     const Turn f = PER ? t : fold(t, a.q_weight, a.R, a.interleaved, lane);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {

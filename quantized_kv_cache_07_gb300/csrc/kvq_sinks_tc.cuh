@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         const int at = g.both ? tid : v;
         const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] : 0.f;
         const int len = sm->qlen[at], lo = len - a.span;
-        const int hidden = max(lo - a.sinks, 0);  // tokens from the sinks on that the row does not see
+        const int hidden = lo > a.sinks ? lo - a.sinks : 0;  // tokens from the sinks on that the row does not see
         // the warp's shortest row and latest window decide whether a tile needs the mask at all (vectors that are not of
         // this pass do not count)
         const int minlen = __reduce_min_sync(kFull, len > 0 ? len : 0x7fffffff);

@@ -18,8 +18,10 @@ def _i(x):
 
 
 def update_rule(refs, table, lens, parent, room=0, window=0, sinks=0, span=0):
-    """(refs, table, lens, copies) after kvq_pages_update, or None where the free pages do not suffice."""
+    """(refs, table, lens, copies) after kvq_pages_update, or None where the free pages do not suffice; room: of all rows,
+    or of each."""
     refs = list(map(int, refs))
+    rooms = np.broadcast_to(room, len(lens))
     B, width = table.shape
     most = 16 * width + window
     rows = []
@@ -28,7 +30,7 @@ def update_rule(refs, table, lens, parent, room=0, window=0, sinks=0, span=0):
         L = int(lens[s]) if s >= 0 else 0
         L = min(max(L, 0), most)
         count = -(-max(L - window, 0) // 16)
-        need = -(-max(min(L + room, most) - window, 0) // 16) if s >= 0 else 0
+        need = -(-max(min(L + int(rooms[r]), most) - window, 0) // 16) if s >= 0 else 0
         row = [-1] * width
         for j in range(width if s >= 0 else 0):
             if j < count:
@@ -85,6 +87,8 @@ class Run:
 
     def __call__(self, refs, table, lens, parent, in_place=False, **kw):
         refs_d = _i(refs)
+        if isinstance(kw.get("room"), np.ndarray):
+            kw["room"] = _i(kw["room"])
         refs_out, table_out, lens_out, copies, num = self.out
         if in_place:
             refs_out = refs_d
@@ -143,9 +147,12 @@ def test_update_follows_the_rules(B, width, blocks, seed):
         kind = rng.integers(0, 4)
         parent = [None, rng.integers(-1, B, B), rng.integers(0, B, B), np.full(B, rng.integers(0, B))][kind]
         span = int(rng.choice([0, 0, max(window, 1), window + 37, 500]))
-        kw = dict(room=int(rng.choice([0, 1, 16, 40])), window=window, sinks=int(rng.integers(0, 40)), span=span)
+        room = int(rng.choice([0, 1, 16, 40]))
+        if rng.random() < 0.3:
+            room = rng.integers(0, 50, B)
+        kw = dict(room=room, window=window, sinks=int(rng.integers(0, 40)), span=span)
         if rng.random() < 0.8:
-            lens = np.minimum(lens, 16 * width + window - kw["room"]).clip(0)
+            lens = np.minimum(lens, 16 * width + window - np.max(room)).clip(0)
         want = update_rule(refs, table, lens, parent, **kw)
         got = run(refs, table, lens, parent, in_place=bool(rng.integers(0, 2)), **kw)
         err = int(run.err.item())
@@ -156,8 +163,8 @@ def test_update_follows_the_rules(B, width, blocks, seed):
             lens = lens // 2  # and go on with shorter rows
             continue
         # a last page that a window has freed is reported, and a row that its table has no room for
-        going = lens if parent is None else lens[parent[parent >= 0]]
-        full = bool(np.any(going + kw["room"] > 16 * width + window))
+        whose = np.arange(B) if parent is None else parent
+        full = bool(np.any((lens[whose] + room > 16 * width + window) & (whose >= 0)))
         assert err & ~run.lib.KVQ_DEVERR_BLOCK_ID == (run.lib.KVQ_DEVERR_SEQ_LEN if full else 0)
         same(got, want)
         refs, table, lens = (np.asarray(x) for x in want[:3])
