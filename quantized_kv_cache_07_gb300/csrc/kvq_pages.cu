@@ -19,7 +19,7 @@ constexpr int kPageThreads = 1024;
 constexpr int kPageCtas = 8;  // of the cluster
 constexpr int kPageWarps = kPageCtas * kPageThreads / 32;
 constexpr int kKeep = 16;  // pages of a thread whose counts stay in registers (pools of 131072)
-constexpr int kCols = 8;  // table entries of a lane in flight (4: 18.5 us for 64 rows of 2048, 16: 15)
+constexpr int kCols = 8;  // table entries of a lane in flight (64 rows of 2048: 4 18.2 us, 8 and 16 16.5; 48 rows of 300: 16.4, 16.5, 18.6)
 
 __device__ __forceinline__ int cluster_cta() {
   uint32_t r;
@@ -549,18 +549,26 @@ __global__ void __launch_bounds__(kCopyWarps * 32) copy_blocks_kernel(const Copy
 }
 
 // ---- rings of a bf16 window: row r becomes its parent's, in place.  A CTA holds a slice of every row that changes in
-// shared memory before it writes any
+// shared memory before it writes any: bulk copies of a row each, the next slice on its way in while one goes out.
+// (48 rows, 36 of them changed, of 8 layers, 240 MB: 16 bytes a thread by cp.async 61 us, one at a time 112.)
 __global__ void __launch_bounds__(256) fork_windows_kernel(const RingArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int moved_s;
+  __shared__ uint64_t bars[2];
   uint16_t* to = reinterpret_cast<uint16_t*>(smem);  // [B] rows that change, and their parents
   uint16_t* from = to + a.B;
-  uint4* slice = reinterpret_cast<uint4*>(smem + (a.B * 4 + 15) / 16 * 16);
+  uint8_t* slices = smem + (a.B * 4 + 15) / 16 * 16;  // two of [B][slice_bytes]
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    moved_s = 0;
+    mbar_init(&bars[0], 1);
+    mbar_init(&bars[1], 1);
+    fence_mbar_init();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (threadIdx.x == 0) moved_s = 0;
   __syncthreads();
-  for (int r = threadIdx.x; r < a.B; r += blockDim.x) {
+  for (int r = tid; r < a.B; r += blockDim.x) {
     const int p = a.parent[r];
     if (p < -1 || p >= a.B) {
       if (blockIdx.x == 0) flag(a.err, KVQ_DEVERR_POSITION);
@@ -571,20 +579,44 @@ __global__ void __launch_bounds__(256) fork_windows_kernel(const RingArgs a) {
     }
   }
   __syncthreads();
-  const int lines = a.slice_bytes / 16, log_lines = 31 - __clz(lines), all = moved_s * lines;  // a power of two
-  const int slices = a.row_bytes / a.slice_bytes;
-  for (long long u = blockIdx.x; u < 2ll * a.layers * slices; u += gridDim.x) {
-    const int pool = int(u / slices);
-    uint8_t* ring = (pool % 2 ? a.rings[pool / 2].v : a.rings[pool / 2].k) + size_t(u % slices) * a.slice_bytes;
-    for (int i = threadIdx.x; i < all; i += blockDim.x)
-      cp_async16(&slice[i], reinterpret_cast<const uint4*>(ring + size_t(from[i >> log_lines]) * a.row_bytes) + (i & (lines - 1)));
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    for (int i = threadIdx.x; i < all; i += blockDim.x)
-      reinterpret_cast<uint4*>(ring + size_t(to[i >> log_lines]) * a.row_bytes)[i & (lines - 1)] = slice[i];
-    __syncthreads();
+  const int moved = moved_s, per_pool = a.row_bytes / a.slice_bytes;
+  if (moved == 0) return;
+  const long long units = 2ll * a.layers * per_pool;
+  const uint64_t pol = l2_evict_first_policy();
+  auto ring_of = [&](long long u) {
+    const int pool = int(u / per_pool);
+    return (pool % 2 ? a.rings[pool / 2].v : a.rings[pool / 2].k) + size_t(u % per_pool) * a.slice_bytes;
+  };
+  auto load = [&](long long u, int at) {
+    const uint8_t* ring = ring_of(u);
+    uint8_t* slice = slices + size_t(at) * a.B * a.slice_bytes;
+    if (tid == 0) mbar_arrive_expect_tx(&bars[at], uint32_t(moved) * a.slice_bytes);
+    for (int i = tid; i < moved; i += blockDim.x)
+      bulk_g2s(slice + size_t(i) * a.slice_bytes, ring + size_t(from[i]) * a.row_bytes, a.slice_bytes, &bars[at], pol);
+  };
+  int k = 0;
+  if ((long long)blockIdx.x < units) load(blockIdx.x, 0);
+  for (long long u = blockIdx.x; u < units; u += gridDim.x, ++k) {
+    const int at = k & 1;
+    if (u + gridDim.x < units) {
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // this thread's stores have read the other slice,
+      __syncthreads();                                               // and so have all threads'
+      load(u + gridDim.x, at ^ 1);
+    }
+    // every row's slice is here before any is written
+    if (__syncthreads_or(!mbar_wait(&bars[at], uint32_t(k >> 1) & 1u))) {
+      if (tid == 0) flag(a.err, KVQ_DEVERR_TIMEOUT);
+      mbar_wait(&bars[at], uint32_t(k >> 1) & 1u);  // what is on its way lands first
+      if (u + gridDim.x < units) mbar_wait(&bars[at ^ 1], uint32_t((k + 1) >> 1) & 1u);
+      break;
+    }
+    uint8_t* ring = ring_of(u);
+    const uint8_t* slice = slices + size_t(at) * a.B * a.slice_bytes;
+    for (int i = tid; i < moved; i += blockDim.x)
+      bulk_s2g(ring + size_t(to[i]) * a.row_bytes, slice + size_t(i) * a.slice_bytes, a.slice_bytes);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 cudaError_t launch(const void* kernel, dim3 grid, int threads, int smem, cudaStream_t s, void** args) {
@@ -646,15 +678,15 @@ cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // slices as wide as 64 KB of shared memory hold for every row, from 16 bytes (4096 rows) to 4 KB
+  // two slices as wide as 52 KB each hold for every row, from 16 bytes (above 1664 rows: 64 KB at 4096) to 4 KB
   a.slice_bytes = 4096;
-  while (a.slice_bytes > 16 && a.slice_bytes * a.B > 65536) a.slice_bytes /= 2;
+  while (a.slice_bytes > 16 && a.slice_bytes * a.B > 53248) a.slice_bytes /= 2;
   const void* k = reinterpret_cast<const void*>(fork_windows_kernel);
-  const int smem = (a.B * 4 + 15) / 16 * 16 + a.B * a.slice_bytes;
+  const int smem = (a.B * 4 + 15) / 16 * 16 + 2 * a.B * a.slice_bytes;
   if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
   const long long units = 2ll * a.layers * (a.row_bytes / a.slice_bytes);
   void* args[] = {&a};
-  const int room = 220 * 1024 / (smem + 1024), most = sms * (room > 4 ? 4 : room);  // CTAs that load while others store
+  const int room = 224 * 1024 / (smem + 1024), most = sms * (room < 1 ? 1 : room > 4 ? 4 : room);
   return launch(k, dim3(unsigned(units < most ? units : most)), 256, smem, s, args);
 }
 

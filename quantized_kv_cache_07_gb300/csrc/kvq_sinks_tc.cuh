@@ -4,12 +4,26 @@
 // CTA takes units in turn and, for every sequence among a unit's rows (a "pass", mostly one), streams the tiles of
 // 64 tokens that one row at least sees: those of the sinks, then from the shortest row's window on.  The products, the
 // softmax and the conversion of codes are those of kvq_shared_tc.cu, which has the layouts and the roles:
-//   warpgroups 0 and 1 softmax (thread v = vector v), warpgroup 2 converts, warp 12 issues the products,
-// and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while this one runs.
+//   warpgroups 0 and 1 softmax (thread v = vector v), warpgroup 2 converts, warps 12 and 14 issue the products of one
+// softmax warpgroup each, and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while
+// this one runs.
 //
 // Few units: a cluster of 2, 4 or 8 CTAs takes each, every one an equal share of a pass's tiles, and they join their
 // states through the cluster's shared memory (the ring's place, once the pass has drained it), each writing its share of the
 // vectors.
+//
+// Scores.  Queries of ordinary size are scaled by one power of two, so that what turns a code product into an exponent is
+// the token's alone: the converting warps store its key scale times log2(e) / sqrt(D) times that power, and an exponent
+// is one fused product and sum, S s_k - (m - sigma); rows of other sizes are brought to it first.
+//
+// Measured: 2048 rows of 32 / 8 heads on windows of 4096 (256 units of 66 tiles, int8): 187 us, where the products alone
+// would take 72 on all SMs; 752 on 16-vector tiles.  A tile of 256 vectors takes 2500 cycles: 1024 of the tensor
+// core's, and a softmax thread's 64 columns cost about 260 instructions that two warps a scheduler do not overlap better.
+// One warp that issued both warpgroups' products was itself what they waited for (195 us).  A unit's start and
+// end take 25,000 cycles (queries 9,500, the first tiles with their maximum and scales 5,000, outputs 11,000), and 256 units are
+// two rounds of 152 SMs.  Reading the scales in fragments (a thread four rows, two columns of eight) took the shared-memory
+// wavefronts of a tile from 2640 to 1870 and no time; leaving out the maximum of a tile until a sum passes
+// its bound takes too many tiles twice (255 us).
 //
 // Masks.  Row of length L sees token i < L if i < sinks or i >= L - span.  Tiles are aligned to 64 tokens; a
 // tile that every row of a warp sees whole skips the mask, so it costs the tiles at the window's start and at the chunk itself.
@@ -42,7 +56,7 @@ struct UnitSmem {
   float qs[2 * kQ], qz[2 * kQ];  // after a pass of one half: the second warpgroup's m and l
   int qlen[2 * kQ];
   float rm[2 * kQ], rl[2 * kQ];  // a share's m and l, for the cluster
-  // full: a stage's 128 converting threads; empty: its products are done; q_full: the softmax threads have staged a
+  // full: a stage's 128 converting threads; empty: its products are done, of both warpgroups; q_full: the softmax threads have staged a
   // pass's queries; s_full, p_full, o_done [warpgroup][S buffer]: scores, weights, P . V done; plan_full, plan_empty
   // [plan buffer]; meet: both softmax warpgroups; gather, release: the cluster's softmax threads have left their states, and
   // have read them
@@ -145,6 +159,15 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
   }
 }
 
+// What a code product times its key scale is multiplied by for queries scaled by 2^kFixedExp: log2(e) / sqrt(D) / 2^kFixedExp.
+constexpr float kUnitScale = kLog2e * kInvSqrtD / float(1 << kFixedExp);
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Four outputs of a row.
 __device__ __forceinline__ void put_out(const DecodeArgs& a, size_t at, float4 o) {
   if (a.out_fp32) {
@@ -207,7 +230,7 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 // TWO: queries as an fp16 high and low part, the low ones in the second query tile; units of 128 vectors.
-// SHARED: a cluster takes each unit (its own kernel: the join's code cost the others 7 %, 239 us for 222).
+// SHARED: a cluster takes each unit (its own kernel: the join's code cost the others 7 %).
 template <int KB, int VB, bool ASYM, bool TWO, bool SHARED>
 __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArgs a, int units, int rows_per) {
   using F = Fmt<KB, VB, ASYM>;
@@ -219,7 +242,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&sm->full[i], 128);
-      mbar_init(&sm->empty[i], 1);
+      mbar_init(&sm->empty[i], 2);
     }
     mbar_init(&sm->q_full, 2 * kQ);
     mbar_init(&sm->meet, 2 * kQ);
@@ -232,7 +255,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         mbar_init(&sm->o_done[j][i], 1);
       }
       mbar_init(&sm->plan_full[j], 1);
-      mbar_init(&sm->plan_empty[j], 2 * kQ + 128 + 1);
+      mbar_init(&sm->plan_empty[j], 2 * kQ + 128 + 2);
     }
     fence_mbar_init();
   }
@@ -262,77 +285,66 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->plan_full[k & 1]);
       }
-    } else if (warp == 12) {
-      // -------------------------------------------------------------- products
+    } else if (warp != 15) {
+      // -------------------------------------------------------------- products: of warpgroup j's scores
+      const int j = warp == 14;
       const bool leader = elect_one();
       const uint32_t q_addr = smem_u32(sm->q), st_addr = smem_u32(sm->st);
-      int n0 = 0, c0 = 0, c1 = 0, seg = 0;  // tiles and jobs before this pass
+      int n0 = 0, c0 = 0, seg = 0;  // tiles and jobs before this pass
       for (int u = ci, k = 0; u < units && ok; u += P, ++k) {
         ok = pair_wait(sm->plan_full, k);
         const Plan& plan = sm->plan[k & 1];
         for (int ps = 0; ok && ps < plan.passes; ++ps, ++seg) {
           const Walk g = walk_of(a, plan, ps, part, parts);
           ok = mbar_wait(&sm->q_full, uint32_t(seg) & 1u);
-          // P . V runs one tile behind the scores, two where the warpgroups take turns
-          const int lag = g.both ? 1 : 2;
-          for (int i = 0; i < g.nt + lag && ok; ++i) {
-            if (i < g.nt) {
-              const int n = n0 + i;
+          const int jobs = jobs_of(g, j);
+          const uint64_t qd = tile_desc(q_addr + (g.both ? j : 0) * uint32_t(sizeof(sm->q[0])));
+          // P . V runs one job behind the scores
+          for (int i = 0; i <= jobs && ok; ++i) {
+            if (i < jobs) {
+              const int n = n0 + (g.both ? i : 2 * i + j), c = c0 + i;
               ok = ring_wait(sm->full, n);
+              if (c >= 2) ok = ok && pair_wait(sm->o_done[j], c - 2);  // S's buffer: its weights have been read
+              if (!ok) break;
               tc_fence_after();
               const uint64_t kd = tile_desc(st_addr + uint32_t(n & (kRing - 1)) * uint32_t(sizeof(TcStage)));
+              const uint32_t d = tmem + 256 + 128 * j + 64 * (c & 1);
+              if (leader) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!g.both && (i & 1) != j) continue;
-                const int c = (j ? c1 : c0) + (g.both ? i : i >> 1);
-                if (c >= 2) ok = ok && pair_wait(sm->o_done[j], c - 2);  // S's buffer: its weights have been read
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t qd = tile_desc(q_addr + (g.both ? j : 0) * uint32_t(sizeof(sm->q[0])));
-                const uint32_t d = tmem + 256 + 128 * j + 64 * (c & 1);
-                if (leader) {
+                for (int e = 0; e < kHeadDim / 16; ++e)
+                  tc_mma_ss(d, qd + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
+                            kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), e > 0);
+                if constexpr (TWO) {
 #pragma unroll
                   for (int e = 0; e < kHeadDim / 16; ++e)
-                    tc_mma_ss(d, qd + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
-                              kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), e > 0);
-                  if constexpr (TWO) {
-#pragma unroll
-                    for (int e = 0; e < kHeadDim / 16; ++e)
-                      tc_mma_ss(d, qd + (sizeof(sm->q[0]) >> 4) + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
-                                kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), true);
-                  }
-                  tc_commit(&sm->s_full[j][c & 1]);
+                    tc_mma_ss(d, qd + (sizeof(sm->q[0]) >> 4) + (e >> 2) * (sizeof(sm->q[0][0]) >> 4) + 2 * (e & 3),
+                              kd + (e >> 2) * (sizeof(sm->st[0].k[0]) >> 4) + 2 * (e & 3), f16_idesc(kQ, kTok), true);
                 }
-                __syncwarp();
+                tc_commit(&sm->s_full[j][c & 1]);
               }
+              __syncwarp();
             }
-            const int p = i - lag;
-            if (p >= 0 && ok) {
-              const int n = n0 + p, s = n & (kRing - 1);
+            if (i > 0) {
+              const int n = n0 + (g.both ? i - 1 : 2 * (i - 1) + j), s = n & (kRing - 1), c = c0 + i - 1;
               const uint64_t vd =
                   tile_desc(st_addr + uint32_t(s) * uint32_t(sizeof(TcStage)) + uint32_t(sizeof(sm->st[0].k)));
+              const uint32_t d = tmem + 128 * j, w = tmem + 256 + 128 * j + 64 * (c & 1);
+              ok = pair_wait(sm->p_full[j], c);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if (!g.both && (p & 1) != j) continue;
-                const int job = g.both ? p : p >> 1, c = (j ? c1 : c0) + job;
-                ok = ok && pair_wait(sm->p_full[j], c);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t d = tmem + 128 * j, w = tmem + 256 + 128 * j + 64 * (c & 1);
-                if (leader) {
-#pragma unroll
-                  for (int e = 0; e < kTok / 16; ++e)
-                    tc_mma_ts(d, w + 8 * e, vd + 2 * e, f16_idesc(kQ, kHeadDim), job > 0 || e > 0);
-                  tc_commit(&sm->o_done[j][c & 1]);
-                  if (j == 1 || !g.both) tc_commit(&sm->empty[s]);
-                }
-                __syncwarp();
+                for (int e = 0; e < kTok / 16; ++e)
+                  tc_mma_ts(d, w + 8 * e, vd + 2 * e, f16_idesc(kQ, kHeadDim), i > 1 || e > 0);
+                tc_commit(&sm->o_done[j][c & 1]);
+                tc_commit(&sm->empty[s]);
+                if (!g.both) tc_commit(&sm->empty[s]);  // for the other warpgroup, which this tile passes by
               }
+              __syncwarp();
             }
           }
           n0 += g.nt;
-          c0 += jobs_of(g, 0);
-          c1 += jobs_of(g, 1);
+          c0 += jobs;
         }
         if (lane == 0) mbar_arrive(&sm->plan_empty[k & 1]);
       }
@@ -414,10 +426,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           if (!data) vs = 0.f;
           if (lane < kBlock) {
             const int col = tile_col(w, lane);
-            sm->sk[s][col] = ks;
+            sm->sk[s][col] = ks * kUnitScale;
             sm->sv[s][col] = vs;
             if constexpr (ASYM) {
-              sm->mk[s][col] = fmaf(kKC, ks, ko);
+              sm->mk[s][col] = fmaf(kKC, ks, ko) * kUnitScale;
               sm->mv[s][col] = data ? fmaf(kVC, vs, vo) : 0.f;
             }
           }
@@ -500,7 +512,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
             }
             const int at = v0 + b + (lane >> 3);
             float qs, sum;
-            put_query<ASYM, TWO>(a, cur, f, half, int(sizeof(sm->q[0])), at & (kQ - 1), sub, qs, sum);
+            put_query<ASYM, TWO, true>(a, cur, f, half, int(sizeof(sm->q[0])), at & (kQ - 1), sub, qs, sum);
             if (sub == 0) {
               sm->qs[at] = qs;
               sm->qz[at] = sum;
@@ -512,14 +524,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         ok = __all_sync(kFull, mbar_wait(&sm->q_full, uint32_t(seg) & 1u));
         if (!ok) break;
         const int at = g.both ? tid : v;
-        const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] : 0.f;
+        const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] * qs : 0.f;
         const int len = sm->qlen[at], lo = len - a.span;
         const int hidden = lo > a.sinks ? lo - a.sinks : 0;  // tokens from the sinks on that the row does not see
         // the warp's shortest row and latest window decide whether a tile needs the mask at all (vectors that are not of
         // this pass do not count)
         const int minlen = __reduce_min_sync(kFull, len > 0 ? len : 0x7fffffff);
         const int maxlo = __reduce_max_sync(kFull, len > 0 ? lo : -0x7fffffff);
+        const bool scaled = __any_sync(kFull, qs != 1.f);
         float m = kNegInf, l = 0.f, z = 0.f, sg = float(kSigma0);
+        float nb = 0.f, thr = kNegInf;  // sigma - m; the exponent from which on the maximum has to move
         float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
         const int jobs = jobs_of(g, j);
 #pragma unroll 1
@@ -534,16 +548,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           tmem_ld32(st + 32, r + 32);
           tc_wait_ld();
           const int tok0 = g.tile(tile) * kTok;
+          if (scaled) {
+#pragma unroll
+            for (int e = 0; e < kTok; e += 2) mul2(r[e], r[e + 1], qs, qs);
+          }
 #pragma unroll
           for (int e = 0; e < kTok; e += 4) {
             const float4 ks = *reinterpret_cast<const float4*>(&sm->sk[sc][e]);
             if constexpr (ASYM) {
               const float4 ko = *reinterpret_cast<const float4*>(&sm->mk[sc][e]);
-              fma2(r[e], r[e + 1], ks.x, ks.y, ko.x * qz, ko.y * qz);
-              fma2(r[e + 2], r[e + 3], ks.z, ks.w, ko.z * qz, ko.w * qz);
+              fma2(r[e], r[e + 1], ks.x, ks.y, fmaf(ko.x, qz, nb), fmaf(ko.y, qz, nb));
+              fma2(r[e + 2], r[e + 3], ks.z, ks.w, fmaf(ko.z, qz, nb), fmaf(ko.w, qz, nb));
             } else {
-              mul2(r[e], r[e + 1], ks.x, ks.y);
-              mul2(r[e + 2], r[e + 3], ks.z, ks.w);
+              fma2(r[e], r[e + 1], ks.x, ks.y, nb, nb);
+              fma2(r[e + 2], r[e + 3], ks.z, ks.w, nb, nb);
             }
           }
           // a row of the warp that ends inside this tile or before it, or hides tokens of it
@@ -557,15 +575,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
 #pragma unroll
           for (int e = 0; e < kTok; e += 8)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-              x4[b] = fmaxf(x4[b], fmaxf(__uint_as_float(r[e + 2 * b]), __uint_as_float(r[e + 2 * b + 1])));
-          const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3])) * qs;
+            for (int b = 0; b < 4; ++b) x4[b] = max3(x4[b], __uint_as_float(r[e + 2 * b]), __uint_as_float(r[e + 2 * b + 1]));
+          const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
           const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
           const float svm = max_nan(max_nan(sm4.x, sm4.y), max_nan(sm4.z, sm4.w));  // the same in every thread
-          if (__any_sync(kFull, mx > m + kMaxSlack || !(svm <= svlim))) {
+          if (__any_sync(kFull, mx > thr || !(svm <= svlim))) {
             float f = 1.f;
-            if (__any_sync(kFull, mx > m + kMaxSlack)) {
-              const float mn = fmaxf(m, mx);
+            if (__any_sync(kFull, mx > thr)) {
+              const float mn = fmaxf(m, mx - nb);
               f = mn == kNegInf ? 1.f : ex2(m - mn);
               m = mn;
             }
@@ -614,6 +631,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
               sg = float(sn);
               svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - sn);
             }
+            const float nb_was = nb;
+            nb = m == kNegInf ? 0.f : sg - m;
+            thr = m == kNegInf ? kNegInf : kMaxSlack + sg;
+#pragma unroll
+            for (int e = 0; e < kTok; e += 2)
+              add2(r[e], r[e + 1], __float_as_uint(nb - nb_was), __float_as_uint(nb - nb_was));
             l *= f;
             z *= f;
             if (i > 0) {  // O too, once the products so far are complete
@@ -632,7 +655,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
               tc_wait_st();
             }
           }
-          const float base = m == kNegInf ? 0.f : m - sg;
           uint32_t la[4] = {0u, 0u, 0u, 0u};  // four partial sums of the weights
 #pragma unroll
           for (int half = 0; half < kTok; half += 32) {
@@ -640,8 +662,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
 #pragma unroll
             for (int e = half; e < half + 32; e += 4) {
               const float4 vs = *reinterpret_cast<const float4*>(&sm->sv[sc][e]);
-              fma2(r[e], r[e + 1], qs, qs, -base, -base);
-              fma2(r[e + 2], r[e + 3], qs, qs, -base, -base);
 #pragma unroll
               for (int b = 0; b < 4; ++b) r[e + b] = __float_as_uint(ex2(__uint_as_float(r[e + b])));
               add2(la[0], la[1], r[e], r[e + 1]);

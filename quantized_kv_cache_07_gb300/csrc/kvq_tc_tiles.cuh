@@ -163,7 +163,10 @@ __device__ __forceinline__ void put_values(const Raw<VB>& raw, uint8_t* const ti
 // Four vectors a step in a loop, not unrolled: code that runs once is fetched at memory speed (unrolled over the
 // 32 vectors of a warp the staging took 13 us).
 // TWO: what the fp16 rounding leaves goes to a second tile `lo` bytes behind.
-template <bool ASYM, bool TWO>
+// FIXED: vectors of ordinary size (up to 250) are all scaled by 2^kFixedExp, exact in fp16 for bf16 values from 2^-22 on; the
+// scale that comes back is relative to that one's, 1 for them.
+constexpr int kFixedExp = 8;
+template <bool ASYM, bool TWO, bool FIXED = false>
 __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw)[2], const float (&f)[16], uint8_t* half,
                                           int lo, int row, int sub, float& scale, float& sum) {
   float x[16];
@@ -198,14 +201,16 @@ __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[12 + e] = c[e];
     }
-    scale *= s;
+    scale = FIXED ? s * float(1 << kFixedExp) : scale * s;
   } else {
     // exact powers of two: am * 2^(14 - e) in [2^14, 2^15); below 2^-112 the scores are zero to any precision
     const uint32_t e = max(__float_as_uint(am) >> 23, 15u);
-    const float f2 = __uint_as_float((268u - e) << 23);
+    const bool fixed = FIXED && am <= 250.f;
+    const float f2 = fixed ? float(1 << kFixedExp) : __uint_as_float((268u - e) << 23);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] *= f2;
-    scale *= __uint_as_float((e - 14u) << 23);
+    if constexpr (FIXED) scale = fixed ? 1.f : __uint_as_float((e - 14u) << 23) * float(1 << kFixedExp);
+    else scale *= __uint_as_float((e - 14u) << 23);
   }
   scale = fmaxf(scale, 1.17549435e-38f);  // positive, so that a masked score stays -inf
   sum = 0.f;
