@@ -552,7 +552,8 @@ kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, in
  *           (KVQ_ERR_UNSUPPORTED otherwise)
  * Only blocks that hold such a token are read; the other entries of the block table may be anything
  * (kvq_pages_update frees their blocks and sets them to -1).  Hidden tokens that share a block with
- * seen ones have no effect, whatever they hold.  Everything else as kvq_decode, with
+ * seen ones have no effect, whatever they hold.  (kvq_attn_mass takes every cached token for
+ * visible: not with this call's lse.)  Everything else as kvq_decode, with
  * kvq_decode_workspace_size and the same workspace; under a key factor the query times the factor
  * is carried in two fp16 parts (as with q_bits 32), so that lse holds float32's precision.
  */

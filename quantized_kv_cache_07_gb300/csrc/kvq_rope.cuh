@@ -45,7 +45,11 @@ static __device__ __noinline__ float turn_exact(float a, float c, float b, float
 struct Turn {
   float c[4], s[4];
 };
+template <bool L2 = false>  // read past L1 (norm_queries_kernel)
 __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleaved, int lane) {
+  auto get = [](const float* p) {
+    return L2 ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
+  };
   const int d = 4 * lane;
   Turn t;
 #pragma unroll
@@ -55,7 +59,7 @@ __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleav
   }
   if (d >= R) return t;
   if (interleaved) {
-    const float4 v = *reinterpret_cast<const float4*>(cs + d);
+    const float4 v = get(cs + d);
     t.c[0] = t.c[1] = v.x;
     t.c[2] = t.c[3] = v.z;
     t.s[0] = -v.y;
@@ -64,8 +68,8 @@ __device__ __forceinline__ Turn load_turn(const float* cs, int R, bool interleav
     t.s[3] = v.w;
   } else {
     const bool low = d < (R >> 1);
-    const float4* p = reinterpret_cast<const float4*>(cs + 2 * (low ? d : d - (R >> 1)));
-    const float4 a = p[0], b = p[1];
+    const float* p = cs + 2 * (low ? d : d - (R >> 1));
+    const float4 a = get(p), b = get(p + 4);
     const float f = low ? -1.f : 1.f;
     t.c[0] = a.x;
     t.c[1] = a.z;
@@ -132,7 +136,7 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
 // A lane's own four weights and its mates' (ones behind R, where nothing is added).
 __device__ __forceinline__ void load_weights(const float* w, int R, bool interleaved, int lane, float (&own)[4],
                                              float (&mate)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(w + 4 * lane);
+  const float4 a = __ldcg(reinterpret_cast<const float4*>(w + 4 * lane));
   own[0] = a.x;
   own[1] = a.y;
   own[2] = a.z;
@@ -141,7 +145,7 @@ __device__ __forceinline__ void load_weights(const float* w, int R, bool interle
   float4 b = make_float4(1.f, 1.f, 1.f, 1.f);
   if (d < R) {
     if (interleaved) b = make_float4(a.y, a.x, a.w, a.z);
-    else b = *reinterpret_cast<const float4*>(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1)));
+    else b = __ldcg(reinterpret_cast<const float4*>(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1))));
   }
   mate[0] = b.x;
   mate[1] = b.y;
@@ -296,7 +300,7 @@ __device__ __forceinline__ uint2 norm_query4(uint2 raw, const Turn& f, const flo
   float ss = sq.x + sq.y;
   float2 m0, m1;
   if constexpr (PER) {
-    const float4 w = weight ? *reinterpret_cast<const float4*>(weight + 4 * lane) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 w = weight ? __ldcg(reinterpret_cast<const float4*>(weight + 4 * lane)) : make_float4(1.f, 1.f, 1.f, 1.f);
     x0 = mul2(x0, make_float2(w.x, w.y));
     x1 = mul2(x1, make_float2(w.z, w.w));
     if (interleaved) {
@@ -744,23 +748,25 @@ cudaError_t launch_pdl(void (*kernel)(const RopeArgs), const RopeArgs& a, long l
 }
 
 // ---- queries of many rows with their norms: a warp takes 8 heads of a row, all its loads in flight.  In a kernel of its
-// own, behind that of the keys and values: short code and 64 registers (4099 rows of 32 heads: 18.5 us, 33 among the blocks
-// of the windows' kernel; 53 for the call, 60 then).
+// own: short code and 64 registers (4099 rows of 32 heads: 18.5 us, 33 among the blocks of the windows' kernel).
+// It runs beside the keys' and values' kernel, which has let it start after its own wait for what is before both on the
+// stream, so its queries are complete and are read from L2; it waits for that kernel only before it ends, so that what
+// follows on the stream follows both (as in kvq_shared.cuh; 61.7 us for the call and its read-back, 67.9 one after the other).
 template <bool PER>
-__global__ void __launch_bounds__(256, 4) norm_queries_kernel(const RopeArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__global__ void __launch_bounds__(256, 4) norm_queries_kernel(const RopeArgs a, bool beside) {
+  if (!beside) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, Hq = a.Hq, q8 = (Hq + 7) / 8;
   const uint32_t task = blockIdx.x * 8 + (threadIdx.x >> 5), r = task / q8, h0 = (task % q8) * 8;
-  const int rp = r < uint32_t(a.ap.n) ? a.rope_pos[r] : -1;
+  const int rp = r < uint32_t(a.ap.n) ? __ldcg(a.rope_pos + r) : -1;
   if (rp >= 0 && rp < a.max_pos) {
     const uint16_t* src = a.q + (long long)r * a.q_stride + h0 * kHeadDim + 4 * lane;
     uint2 raw[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      raw[k] = h0 + k < Hq ? *reinterpret_cast<const uint2*>(src + k * kHeadDim) : make_uint2(0u, 0u);
+      raw[k] = h0 + k < Hq ? __ldcg(reinterpret_cast<const uint2*>(src + k * kHeadDim)) : make_uint2(0u, 0u);
     uint16_t* dst = a.q_out + ((size_t)r * Hq + h0) * kHeadDim + 4 * lane;
-    const Turn t = load_turn(a.table + size_t(rp) * a.R, a.R, a.interleaved, lane);
+    const Turn t = load_turn<true>(a.table + size_t(rp) * a.R, a.R, a.interleaved, lane);
     const Turn f = PER ? t : fold(t, a.q_weight, a.R, a.interleaved, lane);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -771,9 +777,10 @@ __global__ void __launch_bounds__(256, 4) norm_queries_kernel(const RopeArgs a) 
   } else if (r < uint32_t(a.ap.n) && lane == 0 && h0 == 0) {
     flag(a.ap.err, KVQ_DEVERR_POSITION);
   }
+  if (beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-cudaError_t launch_norm_queries(const RopeArgs& a, cudaStream_t s) {
+cudaError_t launch_norm_queries(const RopeArgs& a, bool beside, cudaStream_t s) {
   const long long tasks = (long long)a.ap.n * ((a.Hq + 7) / 8);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned((tasks + 7) / 8));
@@ -784,7 +791,7 @@ cudaError_t launch_norm_queries(const RopeArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, a.per_head ? norm_queries_kernel<true> : norm_queries_kernel<false>, a);
+  return cudaLaunchKernelEx(&cfg, a.per_head ? norm_queries_kernel<true> : norm_queries_kernel<false>, a, beside);
 }
 
 template <bool NORM>
@@ -798,11 +805,11 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
   const long long vectors = (long long)a.ap.n * (a.Hq + (a.write ? 2 * a.ap.c.H : 0));
   if (vectors >= kRowsVectors && (!a.write || (a.ap.mode == KVQ_APPEND_QUANT && !group))) {
     if (NORM && a.Hq > 0) {
-      if (!a.write) return launch_norm_queries(a, s);
+      if (!a.write) return launch_norm_queries(a, false, s);
       RopeArgs kv = a;
       kv.Hq = 0;
       const cudaError_t e = launch_rope<NORM>(kv, s);  // by windows or one by one, as many as they are
-      return e != cudaSuccess ? e : launch_norm_queries(a, s);
+      return e != cudaSuccess ? e : launch_norm_queries(a, true, s);
     }
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

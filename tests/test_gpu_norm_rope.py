@@ -165,21 +165,22 @@ def test_window_modes(mode):
     _same(*caches)
 
 
-def test_positions_out_of_range_and_in_place():
+@pytest.mark.parametrize("n", [6, 4000])
+def test_positions_out_of_range_and_in_place(n):
     from quantized_kv_cache_07_gb300 import _lib
     from quantized_kv_cache_07_gb300.cache import HeadNorm, KVCache, RopeTable
     rng = np.random.default_rng(4)
-    n, Hq = 6, 2
+    Hq = 9
     rope, norm = RopeTable(50), HeadNorm(np.full(128, 2.0))
     q = _t(heads_of(rng, n, Hq))
-    pos, err, c = np.array([0, 49, 50, -1, 7, 8]), _i([0]), KVCache(1, 1, 8, 8)
+    pos, err, c = np.resize([0, 49, 50, -1, 7, 8], n), _i([0]), KVCache(1, 1, 8, 8)
     out = torch.full_like(q, 5)
     call = lambda o: _lib.kvq_norm_rope_append(c.desc, rope.desc, norm.desc, q, Hq, o, None, None, _i(pos), None, None,
                                                _lib.APPEND_QUANT, None, 0, 0, err_word=err)
     call(out)
-    assert err.item() == _lib.KVQ_DEVERR_POSITION and (out[2:4] == 5).all()
+    bad = (pos < 0) | (pos > 49)
+    assert err.item() == _lib.KVQ_DEVERR_POSITION and (out[bad] == 5).all() and not (out[~bad] == 5).all(-1).any()
     kept = q.clone()
     call(q)
-    ok = [0, 1, 4, 5]
-    assert torch.equal(q[ok].view(torch.int16), out[ok].view(torch.int16)) and torch.equal(q[2:4].view(torch.int16),
-                                                                                           kept[2:4].view(torch.int16))
+    bits = lambda t, rows: t[rows].view(torch.int16)
+    assert torch.equal(bits(q, ~bad), bits(out, ~bad)) and torch.equal(bits(q, bad), bits(kept, bad))

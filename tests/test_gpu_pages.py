@@ -170,6 +170,21 @@ def test_update_follows_the_rules(B, width, blocks, seed):
         refs, table, lens = (np.asarray(x) for x in want[:3])
 
 
+@pytest.mark.parametrize("B,width,blocks", [(1500, 4, 9000), (4096, 2, 20000), (9, 20, 150000)])
+def test_large_batches_and_pools(B, width, blocks):
+    """Several rows a thread, and pools whose counts do not stay in registers."""
+    rng = np.random.default_rng(B)
+    refs, table, lens = random_state(rng, B, width, blocks)
+    run = Run(blocks, B, width)
+    for parent in (rng.integers(-1, B, B), np.zeros(B, int), None):
+        lens = np.minimum(lens, 16 * width - 1)
+        want = update_rule(refs, table, lens, parent, room=1)
+        got = run(refs, table, lens, parent, room=1)
+        assert run.err.item() == 0
+        same(got, want)
+        refs, table, lens = (np.asarray(x) for x in want[:3])
+
+
 def test_too_few_pages_change_nothing():
     run = Run(6, 3, 4)
     table = np.array([[0, 1, -1, -1], [2, -1, -1, -1], [-1, -1, -1, -1]])

@@ -9,7 +9,7 @@ import pytest
 
 from harness import DeviceRun, TOL, bf16_half_ulp, oracle_state, small_workload
 from oracle import kvq_oracle as O
-from synth import make_inputs, query_rows
+from synth import f32_to_bf16_bits, make_inputs, query_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -261,6 +261,33 @@ def test_units_of_many_rows(fmt, case):
                 o, l = ref(seq[r], h, q[g], pos[r] + 1, sinks, span)
                 assert worst(out[r, g], lse[r, g], o, l) <= 1.0, (r, h, sinks, span)
                 assert worst(bf[r, g], None, o, l, True) <= 1.0
+
+
+@pytest.mark.parametrize("fmt", ["int8_g4", "asym_int8", "int4_factor_g8", "qint8_asym_k8v4"])
+def test_units_of_queries_of_any_size(fmt):
+    """Large and tiny queries, zeros, infinities and no numbers among the rows of a unit: each row its own result."""
+    w = small_workload(fmt, **dict(dict(batch=1, len_range=(400, 400)), **FORMATS[fmt]))
+    inp = make_inputs(w, 12)
+    run, ref, G = DeviceRun(inp), Oracle(inp), w.group
+    seq, pos = _rows("seq", inp.lengths, [200])
+    qbits = query_rows(len(seq), w.q_heads, 13).copy()
+    size = np.resize([1.0, 200.0, 1e-9, 0.0, 1.0, 1e-30], len(seq))
+    qbits[:] = f32_to_bf16_bits((O.bf16_to_f64(qbits) * size[:, None, None]).astype(np.float32))
+    qbits[10], qbits[33] = 0x7FC0, 0x7F80  # not a number, infinity
+    none = np.isin(np.arange(len(seq)), (10, 33))
+    out, lse = prefill(run, seq, pos, qbits, 4, 150, -2)
+    if w.q_bits != 8:  # (8-bit query codes hold a number for everything)
+        assert np.isnan(out[10]).all() and not np.isfinite(lse[none]).any()
+    for r in np.nonzero(~none)[0][::3]:
+        q = O.bf16_to_f64(qbits[r])
+        for h in range(w.kv_heads):
+            g = slice(h * G, (h + 1) * G)
+            o, l = ref(0, h, q[g], pos[r] + 1, 4, 150)
+            # scores of the large rows reach 10^3 and more: float32 holds them to 2^-24, twice rounded
+            s = 2.0 ** -22 * np.abs(l).max()
+            assert np.max(np.abs(lse[r, g] - l)) <= TOL + s, r
+            # and a weight moves by its exponent's error
+            assert np.max(np.abs(out[r, g] - o)) <= TOL + 2 * s * np.abs(ref.kv[0][h][1]).max(), r
 
 
 def test_prefill_writes_its_chunk_first():
