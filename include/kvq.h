@@ -536,7 +536,7 @@ kvq_status kvq_prefill(const kvq_cache_desc* cache, const void* q, int32_t n, in
                        uint32_t* err_word, void* stream);
 
 /* Workspace bytes kvq_prefill needs for n rows on the current device with
- * this stream_ctas (0 for KVQ_PREFILL_TILES; with 0 the split-rows size, since
+ * this stream_ctas (0 for KVQ_PREFILL_TILES and KVQ_PREFILL_UNITS; with 0 the split-rows size, since
  * the automatic choice may take that path). */
 kvq_status kvq_prefill_workspace_size(const kvq_cache_desc* cache, int32_t n, int32_t q_heads, int32_t stream_ctas,
                                       size_t* bytes);

@@ -263,6 +263,34 @@ def test_units_of_many_rows(fmt, case):
                 assert worst(bf[r, g], None, o, l, True) <= 1.0
 
 
+@pytest.mark.parametrize("fmt", ["int8_g4", "int4_factor_g8", "asym_int8", "k4v8_g3", "asym_int2_g8", "asym_int4_factor"])
+@pytest.mark.parametrize("batch", [1, 3])
+def test_units_that_clusters_share(fmt, batch):
+    """Few units on long windows: 2, 4 and 8 CTAs a unit (8, 16 and 32 tiles at least), one pass or several in a unit, the last
+    ones with fewer tiles than CTAs."""
+    w = small_workload(fmt, **dict(dict(batch=batch, len_range=(2250, 2400)), **FORMATS[fmt]))
+    inp = make_inputs(w, 14)
+    run, ref, G = DeviceRun(inp), Oracle(inp), w.group
+    ends = np.array(inp.lengths)
+    if batch == 3:   # rows of the second sequence's front: a pass of two tiles, shared all the same
+        ends[1] = 120
+    start = [int(L) - n for L, n in zip(ends, [90, 30, 41])]
+    seq, pos = _rows("seq", ends, start)
+    qbits = query_rows(len(seq), w.q_heads, 15)
+    for sinks, span in ((4, 560), (130, 1150), (0, 2200), (7, 10 ** 9)):
+        low = [max(s + 1 - span, 0) for s in start]
+        table = freed(run.table, ends, low, sinks)
+        out, lse = prefill(run, seq, pos, qbits, sinks, span, -2, table)
+        tiles, tiles_lse = prefill(run, seq, pos, qbits, sinks, span, -1, table)
+        assert np.max(np.abs(out - tiles)) <= 2 * TOL and np.max(np.abs(lse - tiles_lse)) <= 2 * TOL
+        for r in range(0, len(seq), 17):
+            q = O.bf16_to_f64(qbits[r])
+            for h in range(w.kv_heads):
+                g = slice(h * G, (h + 1) * G)
+                assert worst(out[r, g], lse[r, g], *ref(seq[r], h, q[g], pos[r] + 1, sinks, span)) <= 1.0, (r, h, sinks, span)
+    assert run.err_bits() == 0
+
+
 @pytest.mark.parametrize("fmt", ["int8_g4", "asym_int8", "int4_factor_g8", "qint8_asym_k8v4"])
 def test_units_of_queries_of_any_size(fmt):
     """Large and tiny queries, zeros, infinities and no numbers among the rows of a unit: each row its own result."""
