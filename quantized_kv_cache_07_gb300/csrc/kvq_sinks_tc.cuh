@@ -162,6 +162,36 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
 // What a code product times its key scale is multiplied by for queries scaled by 2^kFixedExp: log2(e) / sqrt(D) / 2^kFixedExp.
 constexpr float kUnitScale = kLog2e * kInvSqrtD / float(1 << kFixedExp);
 
+constexpr uint32_t kAbs2 = 0x7FFF7FFFu;     // two bf16 values without their signs: they order as their bits
+constexpr uint32_t kLeastBits = 0x3780u, kMostBits = 0x437Au;  // kFixedLeast, kFixedMost in bf16
+
+// put_query's work for a vector of ordinary size and no factor; its sum as the product sees it (ASYM).
+template <bool ASYM>
+__device__ __forceinline__ float put_plain(const uint4 (&raw)[2], uint8_t* half, int row, int sub) {
+  const int t = sub >> 1;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    uint32_t y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      y[k] = pack_half2(__uint_as_float(w[k] << 16) * float(1 << kFixedExp),
+                        __uint_as_float(w[k] & 0xFFFF0000u) * float(1 << kFixedExp));
+      if constexpr (ASYM) {
+        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&y[k]));
+        sum += h.x + h.y;
+      }
+    }
+    *reinterpret_cast<uint4*>(half + row * 128 + ((dim_chunk(t, i) ^ (row & 7)) * 16)) = make_uint4(y[0], y[1], y[2], y[3]);
+  }
+  if constexpr (ASYM) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  }
+  return sum;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -502,8 +532,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
             const int row = (v0 + lane) / G;
             sm->qlen[v0 + lane] = row < plan.nrows && plan.seq[row] == g.seq ? plan.len[row] : 0;
           }
+          // queries as they are, of ordinary size (most passes): scaled by 2^kFixedExp and rounded, eight vectors a step
+          bool plain = !TWO && a.c.q_bits == 16 && !a.c.factor;
+          if (plain) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w = 0u;
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                w = __vmaxu2(__vmaxu2(w, __vmaxu2(raw[i][x].x & kAbs2, raw[i][x].y & kAbs2)),
+                             __vmaxu2(raw[i][x].z & kAbs2, raw[i][x].w & kAbs2));
+              w = max(w & 0xFFFFu, w >> 16);  // a lane's 16 values; a lane of zeros (its vector's other lanes decide) is plain
+              plain = plain && (w == 0u || w - kLeastBits <= kMostBits - kLeastBits);
+            }
+            plain = __all_sync(kFull, plain);
+          }
+          if (plain) {
 #pragma unroll 1
-          for (int b = 0; b < per; b += 4) {
+            for (int b = 0; b < per; b += 8) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int at = v0 + b + 4 * e + (lane >> 3);
+                const float sum = put_plain<ASYM>(raw[e], half, at & (kQ - 1), sub);
+                if (sub == 0) {
+                  sm->qs[at] = 1.f;
+                  sm->qz[at] = sum;
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 6; ++e) {
+                raw[e][0] = raw[e + 2][0];
+                raw[e][1] = raw[e + 2][1];
+              }
+            }
+          }
+#pragma unroll 1
+          for (int b = plain ? per : 0; b < per; b += 4) {
             const uint4 cur[2] = {raw[0][0], raw[0][1]};
 #pragma unroll
             for (int e = 0; e < 7; ++e) {  // rotate: the loop stays short and every index is known

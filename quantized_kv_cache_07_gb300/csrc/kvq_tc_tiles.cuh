@@ -163,9 +163,10 @@ __device__ __forceinline__ void put_values(const Raw<VB>& raw, uint8_t* const ti
 // Four vectors a step in a loop, not unrolled: code that runs once is fetched at memory speed (unrolled over the
 // 32 vectors of a warp the staging took 13 us).
 // TWO: what the fp16 rounding leaves goes to a second tile `lo` bytes behind.
-// FIXED: vectors of ordinary size (up to 250) are all scaled by 2^kFixedExp, exact in fp16 for bf16 values from 2^-22 on; the
-// scale that comes back is relative to that one's, 1 for them.
+// FIXED: vectors of ordinary size (their largest value 2^-16 to 250, or zeros) are all scaled by 2^kFixedExp, exact in fp16
+// for bf16 values from 2^-22 on; the scale that comes back is relative to that one's, 1 for them.
 constexpr int kFixedExp = 8;
+constexpr float kFixedLeast = 1.52587890625e-05f, kFixedMost = 250.f;
 template <bool ASYM, bool TWO, bool FIXED = false>
 __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw)[2], const float (&f)[16], uint8_t* half,
                                           int lo, int row, int sub, float& scale, float& sum) {
@@ -205,7 +206,7 @@ __device__ __forceinline__ void put_query(const DecodeArgs& a, const uint4 (&raw
   } else {
     // exact powers of two: am * 2^(14 - e) in [2^14, 2^15); below 2^-112 the scores are zero to any precision
     const uint32_t e = max(__float_as_uint(am) >> 23, 15u);
-    const bool fixed = FIXED && am <= 250.f;
+    const bool fixed = FIXED && am <= kFixedMost && (am >= kFixedLeast || am == 0.f);
     const float f2 = fixed ? float(1 << kFixedExp) : __uint_as_float((268u - e) << 23);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] *= f2;

@@ -318,6 +318,22 @@ def test_units_of_queries_of_any_size(fmt):
             assert np.max(np.abs(out[r, g] - o)) <= TOL + 2 * s * np.abs(ref.kv[0][h][1]).max(), r
 
 
+@pytest.mark.parametrize("ctas", [-1, -2])
+@pytest.mark.parametrize("power", [-40, -26, -17, 6, 30])
+@pytest.mark.parametrize("fmt", ["int8_g4", "asym_int8", "int4_factor_g8"])
+def test_queries_and_keys_that_trade_a_power_of_two(fmt, power, ctas):
+    """Queries times 2^p on keys times 2^-p: every code, product and sum of the definition stays as it was."""
+    w = small_workload(fmt, **dict(dict(batch=1, len_range=(300, 300)), **FORMATS[fmt]))
+    inp = make_inputs(w, 17)
+    seq, pos = _rows("seq", inp.lengths, [150])
+    qbits = query_rows(len(seq), w.q_heads, 18)
+    want, want_lse = prefill(DeviceRun(inp), seq, pos, qbits, 4, 150, ctas)
+    times = lambda bits, p: f32_to_bf16_bits((O.bf16_to_f64(bits) * 2.0 ** p).astype(np.float32))
+    inp.k = times(inp.k, -power)
+    out, lse = prefill(DeviceRun(inp), seq, pos, times(qbits, power), 4, 150, ctas)
+    assert np.max(np.abs(out - want)) <= 2 * TOL and np.max(np.abs(lse - want_lse)) <= 2 * TOL
+
+
 def test_prefill_writes_its_chunk_first():
     w = small_workload("w", batch=2, len_range=(90, 120))
     inp = make_inputs(w, 5)
