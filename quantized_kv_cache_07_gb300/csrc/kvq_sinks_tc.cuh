@@ -55,7 +55,7 @@ struct UnitSmem {
   float svmax[kRing][4];
   float qs[2 * kQ], qz[2 * kQ];  // after a pass of one half: the second warpgroup's m and l
   int qlen[2 * kQ];
-  float rm[2 * kQ], rl[2 * kQ];  // a share's m and l, for the cluster
+  float rm[2 * kQ], rl[2 * kQ];  // each row's m and sigma, which few tiles move; then a share's m and l, for the cluster
   // full: a stage's 128 converting threads; empty: its products are done, of both warpgroups; q_full: the softmax threads have staged a
   // pass's queries; s_full, p_full, o_done [warpgroup][S buffer]: scores, weights, P . V done; plan_full, plan_empty
   // [plan buffer]; meet: both softmax warpgroups; gather, release: the cluster's softmax threads have left their states, and
@@ -198,6 +198,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// 2^n, 0 below float32's normal numbers, infinity at 128.
+__device__ __forceinline__ float pow2(int n) { return n < -126 ? 0.f : __uint_as_float(uint32_t(n + 127) << 23); }
+
+// 64 columns of 16 of this warp's lanes as fragments: thread (g, t) = (lane / 4, lane % 4) holds columns 8 n + 2 t and the
+// next of lanes g and g + 8; and 32 columns of packed pairs, 4 n + t, back.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16x128(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 // Four outputs of a row.
 __device__ __forceinline__ void put_out(const DecodeArgs& a, size_t at, float4 o) {
   if (a.out_fp32) {
@@ -305,7 +330,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
   auto pair_wait = [&](uint64_t* bars, int c) { return mbar_wait(&bars[c & 1], uint32_t(c >> 1) & 1u); };
 
   if (warp >= 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 13) {
       // -------------------------------------------------------------- plans
       for (int u = ci, k = 0; u < units; u += P, ++k) {
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- conversion
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     const int w = warp - 8;
     const uint32_t km = magic_f16x2(a.B);
     const uint32_t c64 = 0x64646464u | (uint32_t(a.B) >> 16);  // a.B <= 4096: the constant itself
@@ -478,7 +503,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int j = warp >> 2, v = tid & (kQ - 1);  // warpgroup, its vector
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t o_cols = lanes + 128 * j, s_cols = lanes + 256 + 128 * j;
@@ -587,122 +612,197 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         mbar_arrive(&sm->q_full);
         ok = __all_sync(kFull, mbar_wait(&sm->q_full, uint32_t(seg) & 1u));
         if (!ok) break;
-        const int at = g.both ? tid : v;
-        const float qs = sm->qs[at], qz = ASYM ? sm->qz[at] * qs : 0.f;
-        const int len = sm->qlen[at], lo = len - a.span;
-        const int hidden = lo > a.sinks ? lo - a.sinks : 0;  // tokens from the sinks on that the row does not see
+        // Of its warp's 32 rows a thread holds four, lane / 4 + 8 b, and of their scores two columns of every eight,
+        // 8 n + 2 (lane % 4) and the next (the fragments of 16-lane tensor-memory accesses): a scale that is read serves four rows.
+        const int base_v = g.both ? warp * 32 : (warp & 3) * 32, t = lane & 3;
+        float l[4][2], z[4], qz[4];  // l: two partial sums of the weights
+        float nb[4], thr[4];  // sigma - m; the exponent from which on the maximum has to move
+        float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);  // the largest value scale that all four rows allow
+        uint32_t nan_rows = 0;  // rows whose outputs are no numbers
+        bool scaled = false;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int at = base_v + (lane >> 2) + 8 * b;
+          scaled |= sm->qs[at] != 1.f;
+          qz[b] = ASYM ? sm->qz[at] * sm->qs[at] : 0.f;
+          thr[b] = kNegInf;
+          l[b][0] = l[b][1] = z[b] = nb[b] = 0.f;
+          sm->rm[warp * 32 + (lane >> 2) + 8 * b] = kNegInf;
+          sm->rl[warp * 32 + (lane >> 2) + 8 * b] = float(kSigma0);
+        }
+        scaled = __any_sync(kFull, scaled);
+        const int len = sm->qlen[base_v + lane];  // of the row that this thread writes
         // the warp's shortest row and latest window decide whether a tile needs the mask at all (vectors that are not of
         // this pass do not count)
         const int minlen = __reduce_min_sync(kFull, len > 0 ? len : 0x7fffffff);
-        const int maxlo = __reduce_max_sync(kFull, len > 0 ? lo : -0x7fffffff);
-        const bool scaled = __any_sync(kFull, qs != 1.f);
-        float m = kNegInf, l = 0.f, z = 0.f, sg = float(kSigma0);
-        float nb = 0.f, thr = kNegInf;  // sigma - m; the exponent from which on the maximum has to move
-        float svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - kSigma0);
+        const int maxlo = __reduce_max_sync(kFull, len > 0 ? len - a.span : -0x7fffffff);
         const int jobs = jobs_of(g, j);
 #pragma unroll 1
         for (int i = 0; i < jobs; ++i, ++c) {
           const int tile = g.both ? i : 2 * i + j, sc = (n0 + tile) & (kRing - 1);
-          ok = __all_sync(kFull, ring_wait(sm->full, n0 + tile) && pair_wait(sm->s_full[j], c));  // scales, scores
+          // the tile's scales are asked for before its scores: an answer of shared memory takes some 300 cycles beside the products' reads
+          ok = __all_sync(kFull, ring_wait(sm->full, n0 + tile));
+          if (!ok) break;
+          const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
+          float2 ks[8], ko[8], vs[8], vo[8];
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+            ks[n] = *reinterpret_cast<const float2*>(&sm->sk[sc][8 * n + 2 * t]);
+            if constexpr (ASYM) ko[n] = *reinterpret_cast<const float2*>(&sm->mk[sc][8 * n + 2 * t]);
+            else vs[n] = *reinterpret_cast<const float2*>(&sm->sv[sc][8 * n + 2 * t]);
+          }
+          ok = __all_sync(kFull, pair_wait(sm->s_full[j], c));
           if (!ok) break;
           tc_fence_after();
           const uint32_t st = s_cols + 64 * (c & 1);
-          uint32_t r[kTok];
-          tmem_ld32(st, r);
-          tmem_ld32(st + 32, r + 32);
+          uint32_t r[2][32];  // rows 16 h ..: score (n, e, x) of row 16 h + lane / 4 + 8 e, column 8 n + 2 t + x at 4 n + 2 e + x
+          tmem_ld16(st, r[0]);
+          tmem_ld16(st + (16u << 16), r[1]);
           tc_wait_ld();
           const int tok0 = g.tile(tile) * kTok;
           if (scaled) {
 #pragma unroll
-            for (int e = 0; e < kTok; e += 2) mul2(r[e], r[e + 1], qs, qs);
-          }
+            for (int b = 0; b < 4; ++b) {
+              const float qs = sm->qs[base_v + (lane >> 2) + 8 * b];
 #pragma unroll
-          for (int e = 0; e < kTok; e += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&sm->sk[sc][e]);
-            if constexpr (ASYM) {
-              const float4 ko = *reinterpret_cast<const float4*>(&sm->mk[sc][e]);
-              fma2(r[e], r[e + 1], ks.x, ks.y, fmaf(ko.x, qz, nb), fmaf(ko.y, qz, nb));
-              fma2(r[e + 2], r[e + 3], ks.z, ks.w, fmaf(ko.z, qz, nb), fmaf(ko.w, qz, nb));
-            } else {
-              fma2(r[e], r[e + 1], ks.x, ks.y, nb, nb);
-              fma2(r[e + 2], r[e + 3], ks.z, ks.w, nb, nb);
+              for (int n = 0; n < 8; ++n) mul2(r[b >> 1][4 * n + 2 * (b & 1)], r[b >> 1][4 * n + 2 * (b & 1) + 1], qs, qs);
             }
           }
-          // a row of the warp that ends inside this tile or before it, or hides tokens of it
+#pragma unroll
+          for (int n = 0; n < 8; ++n) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              uint32_t &x = r[b >> 1][4 * n + 2 * (b & 1)], &y = r[b >> 1][4 * n + 2 * (b & 1) + 1];
+              if constexpr (ASYM) {
+                uint32_t bx = __float_as_uint(ko[n].x), by = __float_as_uint(ko[n].y);
+                fma2(bx, by, qz[b], qz[b], nb[b], nb[b]);
+                fma2(x, y, ks[n].x, ks[n].y, __uint_as_float(bx), __uint_as_float(by));
+              } else {
+                fma2(x, y, ks[n].x, ks[n].y, nb[b], nb[b]);
+              }
+            }
+          }
+          auto value_scales = [&]() {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              vs[n] = *reinterpret_cast<const float2*>(&sm->sv[sc][8 * n + 2 * t]);
+              if constexpr (ASYM) vo[n] = *reinterpret_cast<const float2*>(&sm->mv[sc][8 * n + 2 * t]);
+            }
+          };
+          if constexpr (ASYM) value_scales();
+          // a row of the warp that ends inside this tile or before it, or hides tokens of it.  Column (n, x) of this
+          // thread is token 16 (n % 4) + 4 (n / 4) + t + 8 x of the tile
           if (tok0 + kTok > minlen || (tok0 < maxlo && tok0 + kTok > a.sinks)) {
-            const int left = len - tok0, first = a.sinks - tok0;
+            const int first = a.sinks - tok0 - t;
 #pragma unroll
-            for (int e = 0; e < kTok; ++e)
-              if (tile_token(e) >= left || unsigned(tile_token(e) - first) < unsigned(hidden)) r[e] = __float_as_uint(kNegInf);
-          }
-          float x4[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            for (int b = 0; b < 4; ++b) {
+              const int own = sm->qlen[base_v + (lane >> 2) + 8 * b], left = own - tok0 - t, hidden = max(own - a.span - a.sinks, 0);
 #pragma unroll
-          for (int e = 0; e < kTok; e += 8)
+              for (int n = 0; n < 8; ++n)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) x4[b] = max3(x4[b], __uint_as_float(r[e + 2 * b]), __uint_as_float(r[e + 2 * b + 1]));
-          const float mx = fmaxf(fmaxf(x4[0], x4[1]), fmaxf(x4[2], x4[3]));
-          const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
-          const float svm = max_nan(max_nan(sm4.x, sm4.y), max_nan(sm4.z, sm4.w));  // the same in every thread
-          if (__any_sync(kFull, mx > thr || !(svm <= svlim))) {
-            float f = 1.f;
-            if (__any_sync(kFull, mx > thr)) {
-              const float mn = fmaxf(m, mx - nb);
-              f = mn == kNegInf ? 1.f : ex2(m - mn);
-              m = mn;
-            }
-            float sv = svm;
-            if (!(svm <= kFloatMax)) {
-              // A value scale that is not finite: -1 stands for it, as in rows that do not see its token 0 x inf would be
-              // no number.  Every warp that goes on to use the scales writes the same.
-              for (int e = lane; e < kTok; e += 32)
-                if (!(fabsf(sm->sv[sc][e]) <= kFloatMax)) {
-                  sm->sv[sc][e] = -1.f;
-                  if constexpr (ASYM) sm->mv[sc][e] = 0.f;
+                for (int x = 0; x < 2; ++x) {
+                  const int off = 16 * (n & 3) + 4 * (n >> 2) + 8 * x;
+                  if (off >= left || unsigned(off - first) < unsigned(hidden))
+                    r[b >> 1][4 * n + 2 * (b & 1) + x] = __float_as_uint(kNegInf);
                 }
-              __syncwarp();
             }
-            // by the scales that this row sees
-            const bool none = tok0 >= len || (tok0 >= a.sinks && tok0 + kTok <= lo);
-            const bool all = tok0 + kTok <= len && (tok0 >= lo || tok0 + kTok <= a.sinks);
-            if (none) {
-              sv = 0.f;
-              if (tok0 >= len) svlim = fmaxf(svlim, kFloatMax);  // the row has ended, or is not of this pass
-            } else if (!(svm <= svlim) && (!all || !(svm <= kFloatMax))) {
-              float least = 0.f;
-              sv = 0.f;
-              // 8 columns a step, their tokens at fixed distances (one column a step: 16,000 cycles for a tile)
-#pragma unroll 1
-              for (int e = 0; e < kTok; e += 8) {
-                const float4 s0 = *reinterpret_cast<const float4*>(&sm->sv[sc][e]);
-                const float4 s1 = *reinterpret_cast<const float4*>(&sm->sv[sc][e + 4]);
-                const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                const int t0 = 16 * ((e >> 3) & 3) + 4 * (e >> 5), left = len - tok0 - t0, first = a.sinks - tok0 - t0;
+          }
+          float mx[4];
+          bool over = false;
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                  const bool hide = tile_token(b) >= left || unsigned(tile_token(b) - first) < unsigned(hidden);
-                  const float own = hide ? 0.f : s[b];
-                  sv = fmaxf(sv, own);
-                  least = fminf(least, own);
+          for (int b = 0; b < 4; ++b) {
+            float x2[2] = {kNegInf, kNegInf};
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              x2[n & 1] = max3(x2[n & 1], __uint_as_float(r[b >> 1][4 * n + 2 * (b & 1)]),
+                               __uint_as_float(r[b >> 1][4 * n + 2 * (b & 1) + 1]));
+            mx[b] = fmaxf(x2[0], x2[1]);
+            over |= mx[b] > thr[b];
+          }
+          const float svm = max_nan(max_nan(sm4.x, sm4.y), max_nan(sm4.z, sm4.w));  // the same in every thread
+          if (__any_sync(kFull, over || !(svm <= svlim))) {
+            float f[4] = {1.f, 1.f, 1.f, 1.f}, m[4], sg[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              m[b] = sm->rm[warp * 32 + (lane >> 2) + 8 * b];
+              sg[b] = sm->rl[warp * 32 + (lane >> 2) + 8 * b];
+            }
+            __syncwarp();
+            if (__any_sync(kFull, over)) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                mx[b] = fmaxf(mx[b], __shfl_xor_sync(kFull, mx[b], 1));
+                mx[b] = fmaxf(mx[b], __shfl_xor_sync(kFull, mx[b], 2));
+                const float mn = fmaxf(m[b], mx[b] - nb[b]);
+                f[b] = mn == kNegInf ? 1.f : ex2(m[b] - mn);
+                m[b] = mn;
+              }
+            }
+            if (__any_sync(kFull, !(svm <= svlim))) {
+              if (!(svm <= kFloatMax)) {
+                // A value scale that is not finite: -1 stands for it, as in rows that do not see its token 0 x inf would be
+                // no number.  Every warp that goes on to use the scales writes the same.
+                for (int e = lane; e < kTok; e += 32)
+                  if (!(fabsf(sm->sv[sc][e]) <= kFloatMax)) {
+                    sm->sv[sc][e] = -1.f;
+                    if constexpr (ASYM) sm->mv[sc][e] = 0.f;
+                  }
+                __syncwarp();
+                value_scales();
+              }
+              // by the scales that each row sees: of this thread's columns, then of the row's four threads
+              float sv[4] = {0.f, 0.f, 0.f, 0.f}, least[4] = {0.f, 0.f, 0.f, 0.f};
+              int own[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b) own[b] = sm->qlen[base_v + (lane >> 2) + 8 * b];
+              const int first = a.sinks - tok0 - t;
+#pragma unroll 1
+              for (int n = 0; n < 8; ++n) {
+                const float2 s2 = *reinterpret_cast<const float2*>(&sm->sv[sc][8 * n + 2 * t]);
+                const int off = 16 * (n & 3) + 4 * (n >> 2);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  const int left = own[b] - tok0 - t, hidden = max(own[b] - a.span - a.sinks, 0);
+                  const float s0 = off >= left || unsigned(off - first) < unsigned(hidden) ? 0.f : s2.x;
+                  const float s1 = off + 8 >= left || unsigned(off + 8 - first) < unsigned(hidden) ? 0.f : s2.y;
+                  sv[b] = fmaxf(sv[b], fmaxf(s0, s1));
+                  least[b] = fminf(least[b], fminf(s0, s1));
                 }
               }
-              if (least < 0.f) svlim = -kNegInf;  // the row's outputs are no numbers
-            }
-            if (sv > svlim) {
-              int e;
-              frexpf(sv, &e);
-              const int sn = min(int(sg), kWeightExp - int(kMaxSlack) - e);
-              f *= ldexpf(1.f, sn - int(sg));
-              sg = float(sn);
-              svlim = ldexpf(1.f, kWeightExp - int(kMaxSlack) - sn);
-            }
-            const float nb_was = nb;
-            nb = m == kNegInf ? 0.f : sg - m;
-            thr = m == kNegInf ? kNegInf : kMaxSlack + sg;
+              svlim = kFloatMax;
 #pragma unroll
-            for (int e = 0; e < kTok; e += 2)
-              add2(r[e], r[e + 1], __float_as_uint(nb - nb_was), __float_as_uint(nb - nb_was));
-            l *= f;
-            z *= f;
+              for (int b = 0; b < 4; ++b) {
+                sv[b] = fmaxf(sv[b], __shfl_xor_sync(kFull, sv[b], 1));
+                sv[b] = fmaxf(sv[b], __shfl_xor_sync(kFull, sv[b], 2));
+                least[b] = fminf(least[b], __shfl_xor_sync(kFull, least[b], 1));
+                least[b] = fminf(least[b], __shfl_xor_sync(kFull, least[b], 2));
+                if (least[b] < 0.f) nan_rows |= 1u << b;
+                // sigma down to what the row's largest scale asks for (below 2^e, normal wherever it asks)
+                const int e = int(__float_as_uint(sv[b]) >> 23) - 126, s0 = int(sg[b]);
+                const int sn = min(s0, kWeightExp - int(kMaxSlack) - e);
+                f[b] *= pow2(sn - s0);
+                sg[b] = float(sn);
+                // a row that has ended, is not of this pass, or is no number has no more say
+                if (own[b] > tok0 && !(nan_rows >> b & 1u)) svlim = fminf(svlim, pow2(kWeightExp - int(kMaxSlack) - sn));
+              }
+            }
+            float fo = 1.f;  // of the row whose O this thread holds: lane
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              sm->rm[warp * 32 + (lane >> 2) + 8 * b] = m[b];  // all four threads of the row
+              sm->rl[warp * 32 + (lane >> 2) + 8 * b] = sg[b];
+              const float was = nb[b];
+              nb[b] = m[b] == kNegInf ? 0.f : sg[b] - m[b];
+              thr[b] = m[b] == kNegInf ? kNegInf : kMaxSlack + sg[b];
+              const uint32_t by = __float_as_uint(nb[b] - was);
+#pragma unroll
+              for (int n = 0; n < 8; ++n) add2(r[b >> 1][4 * n + 2 * (b & 1)], r[b >> 1][4 * n + 2 * (b & 1) + 1], by, by);
+              l[b][0] *= f[b];
+              l[b][1] *= f[b];
+              z[b] *= f[b];
+              const float fb = __shfl_sync(kFull, f[b], 4 * (lane & 7));
+              fo = (lane >> 3) == b ? fb : fo;
+            }
             if (i > 0) {  // O too, once the products so far are complete
               ok = __all_sync(kFull, pair_wait(sm->o_done[j], c - 1));
               if (!ok) break;
@@ -713,36 +813,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
                 tmem_ld32(o_cols + e, o);
                 tc_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 32; ++b) o[b] = __float_as_uint(__uint_as_float(o[b]) * f);
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
                 tmem_st32(o_cols + e, o);
               }
               tc_wait_st();
             }
           }
-          uint32_t la[4] = {0u, 0u, 0u, 0u};  // four partial sums of the weights
+          uint32_t p[2][16];
 #pragma unroll
-          for (int half = 0; half < kTok; half += 32) {
-            uint32_t p[16];
+          for (int n = 0; n < 8; ++n) {
 #pragma unroll
-            for (int e = half; e < half + 32; e += 4) {
-              const float4 vs = *reinterpret_cast<const float4*>(&sm->sv[sc][e]);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) r[e + b] = __float_as_uint(ex2(__uint_as_float(r[e + b])));
-              add2(la[0], la[1], r[e], r[e + 1]);
-              add2(la[2], la[3], r[e + 2], r[e + 3]);
-              if constexpr (ASYM) {
-                const float4 vo = *reinterpret_cast<const float4*>(&sm->mv[sc][e]);
-                z = fmaf(__uint_as_float(r[e]), vo.x, fmaf(__uint_as_float(r[e + 1]), vo.y, z));
-                z = fmaf(__uint_as_float(r[e + 2]), vo.z, fmaf(__uint_as_float(r[e + 3]), vo.w, z));
-              }
-              mul2(r[e], r[e + 1], vs.x, vs.y);
-              mul2(r[e + 2], r[e + 3], vs.z, vs.w);
-              p[(e - half) / 2] = pack_half2(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-              p[(e - half) / 2 + 1] = pack_half2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+            for (int b = 0; b < 4; ++b) {
+              uint32_t x = r[b >> 1][4 * n + 2 * (b & 1)], y = r[b >> 1][4 * n + 2 * (b & 1) + 1];
+              x = __float_as_uint(ex2(__uint_as_float(x)));
+              y = __float_as_uint(ex2(__uint_as_float(y)));
+              uint32_t &l0 = reinterpret_cast<uint32_t&>(l[b][0]), &l1 = reinterpret_cast<uint32_t&>(l[b][1]);
+              add2(l0, l1, x, y);
+              if constexpr (ASYM) z[b] = fmaf(__uint_as_float(x), vo[n].x, fmaf(__uint_as_float(y), vo[n].y, z[b]));
+              mul2(x, y, vs[n].x, vs[n].y);
+              p[b >> 1][2 * n + (b & 1)] = pack_half2(__uint_as_float(x), __uint_as_float(y));
             }
-            tmem_st16(st + half / 2, p);  // over S, which has been read
           }
-          l += (__uint_as_float(la[0]) + __uint_as_float(la[1])) + (__uint_as_float(la[2]) + __uint_as_float(la[3]));
+          tmem_st16x128(st, p[0]);  // over S, which has been read
+          tmem_st16x128(st + (16u << 16), p[1]);
           tc_wait_st();
           tc_fence_before();
           mbar_arrive(&sm->p_full[j][c & 1]);
@@ -754,7 +847,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           if (!ok) break;
           tc_fence_after();
         }
-        const float add = svlim == -kNegInf ? __int_as_float(0x7fffffff) : z;
+        // the state of row `lane`, from its four threads: exponent base, sum, what is added to each output
+        __syncwarp();
+        float row_m = sm->rm[warp * 32 + lane], row_l = 0.f, add = 0.f;
+        if (row_m != kNegInf) row_m -= sm->rl[warp * 32 + lane];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float lb = l[b][0] + l[b][1], zb = z[b];
+          lb += __shfl_xor_sync(kFull, lb, 1);
+          lb += __shfl_xor_sync(kFull, lb, 2);
+          if constexpr (ASYM) {
+            zb += __shfl_xor_sync(kFull, zb, 1);
+            zb += __shfl_xor_sync(kFull, zb, 2);
+          }
+          if (nan_rows >> b & 1u) zb = __int_as_float(0x7fffffff);
+          lb = __shfl_sync(kFull, lb, 4 * (lane & 7));
+          zb = __shfl_sync(kFull, zb, 4 * (lane & 7));
+          if ((lane >> 3) == b) {
+            row_l = lb;
+            add = zb;
+          }
+        }
         // row i of the warp: its place, or -1 (its own thread's length)
         const size_t out0 = size_t(plan.r0) * a.Hq + g.h * G;
         auto place = [&](int vec) { return (out0 + size_t(vec / G) * a.Hq + vec % G) * kHeadDim; };
@@ -764,8 +877,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         if (SHARED && g.both) {
           ok = meet();  // the ring is drained once both have seen their last products
           if (!ok) break;
-          sm->rm[tid] = m == kNegInf ? kNegInf : m - sg;
-          sm->rl[tid] = l;
+          sm->rm[tid] = row_m;
+          sm->rl[tid] = row_l;
           if (jobs > 0) {
 #pragma unroll 1
             for (int e = 0; e < kHeadDim; e += 32) {
@@ -782,8 +895,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         } else if (g.both) {
           // by way of 4 KB of this warp's in its own Q, which no product reads any more
           buf = reinterpret_cast<float4*>(sm->q[j][0]) + (warp & 3) * 256;
-          const float inv = 1.f / l;
-          if (len > 0 && a.lse) a.lse[place(tid) / kHeadDim] = (m - sg + log2f(l)) * kLn2;
+          const float inv = 1.f / row_l;
+          if (len > 0 && a.lse) a.lse[place(tid) / kHeadDim] = (row_m + log2f(row_l)) * kLn2;
           size_t to[8];  // of the rows that this lane writes
 #pragma unroll
           for (int b = 0; b < 8; ++b) to[b] = place(warp * 32 + 4 * b + (lane >> 3)) + 4 * (lane & 7);
@@ -812,8 +925,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           if (!ok) break;
           buf = reinterpret_cast<float4*>(sm->q[0][0]) + v * 32;  // this vector's 128 values, chunks by its lane
           if (j == 1) {
-            sm->qs[v] = jobs > 0 && m != kNegInf ? m - sg : kNegInf;
-            sm->qz[v] = l;
+            sm->qs[v] = row_m;
+            sm->qz[v] = row_l;
             if (jobs > 0) {
 #pragma unroll 1
               for (int e = 0; e < kHeadDim; e += 32) {
@@ -831,10 +944,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           ok = meet();
           if (!ok) break;
           if (j == 0) {
-            const float m0 = m == kNegInf ? kNegInf : m - sg, m1 = sm->qs[v];
+            const float m0 = row_m, m1 = sm->qs[v];
             const float M = fmaxf(m0, m1);
             const float w0 = m0 == kNegInf ? 0.f : exp2f(m0 - M), w1 = m1 == kNegInf ? 0.f : exp2f(m1 - M);
-            const float L = w0 * l + w1 * sm->qz[v], inv = 1.f / L;
+            const float L = w0 * row_l + w1 * sm->qz[v], inv = 1.f / L;
             // a warpgroup without a tile has left no values; one that is no number stays none
             const bool other = jobs_of(g, 1) > 0, here = jobs > 0;
             const float scale = SHARED ? 1.f : inv;
