@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           if constexpr (ASYM) value_scales();
           // a row of the warp that ends inside this tile or before it, or hides tokens of it.  Column (n, x) of this
           // thread is token 16 (n % 4) + 4 (n / 4) + t + 8 x of the tile
-          if (tok0 + kTok > minlen || (tok0 < maxlo && tok0 + kTok > a.sinks)) {
+          const bool masked = tok0 + kTok > minlen || (tok0 < maxlo && tok0 + kTok > a.sinks);
+          if (masked) {
             const int first = a.sinks - tok0 - t;
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
@@ -756,8 +757,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
 #pragma unroll
               for (int b = 0; b < 4; ++b) own[b] = sm->qlen[base_v + (lane >> 2) + 8 * b];
               const int first = a.sinks - tok0 - t;
+#pragma unroll
+              for (int b = 0; b < 4; ++b) sv[b] = own[b] > 0 && !masked && svm <= kFloatMax ? svm : 0.f;
 #pragma unroll 1
-              for (int n = 0; n < 8; ++n) {
+              for (int n = masked || !(svm <= kFloatMax) ? 0 : 8; n < 8; ++n) {
                 const float2 s2 = *reinterpret_cast<const float2*>(&sm->sv[sc][8 * n + 2 * t]);
                 const int off = 16 * (n & 3) + 4 * (n >> 2);
 #pragma unroll
