@@ -822,23 +822,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
               tc_wait_st();
             }
           }
-          uint32_t p[2][16];
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
+          for (int h = 0; h < 2; ++h) {  // 16 rows, stored while the next are at work
+            uint32_t p[16];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              uint32_t x = r[b >> 1][4 * n + 2 * (b & 1)], y = r[b >> 1][4 * n + 2 * (b & 1) + 1];
-              x = __float_as_uint(ex2(__uint_as_float(x)));
-              y = __float_as_uint(ex2(__uint_as_float(y)));
-              uint32_t &l0 = reinterpret_cast<uint32_t&>(l[b][0]), &l1 = reinterpret_cast<uint32_t&>(l[b][1]);
-              add2(l0, l1, x, y);
-              if constexpr (ASYM) z[b] = fmaf(__uint_as_float(x), vo[n].x, fmaf(__uint_as_float(y), vo[n].y, z[b]));
-              mul2(x, y, vs[n].x, vs[n].y);
-              p[b >> 1][2 * n + (b & 1)] = pack_half2(__uint_as_float(x), __uint_as_float(y));
-            }
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int b = 2 * h + e;
+                uint32_t x = __float_as_uint(ex2(__uint_as_float(r[h][4 * n + 2 * e])));
+                uint32_t y = __float_as_uint(ex2(__uint_as_float(r[h][4 * n + 2 * e + 1])));
+                uint32_t &l0 = reinterpret_cast<uint32_t&>(l[b][0]), &l1 = reinterpret_cast<uint32_t&>(l[b][1]);
+                add2(l0, l1, x, y);
+                if constexpr (ASYM) z[b] = fmaf(__uint_as_float(x), vo[n].x, fmaf(__uint_as_float(y), vo[n].y, z[b]));
+                mul2(x, y, vs[n].x, vs[n].y);
+                p[2 * n + e] = pack_half2(__uint_as_float(x), __uint_as_float(y));
+              }
+            tmem_st16x128(st + (uint32_t(16 * h) << 16), p);  // over S, which has been read
           }
-          tmem_st16x128(st, p[0]);  // over S, which has been read
-          tmem_st16x128(st + (16u << 16), p[1]);
           tc_wait_st();
           tc_fence_before();
           mbar_arrive(&sm->p_full[j][c & 1]);
