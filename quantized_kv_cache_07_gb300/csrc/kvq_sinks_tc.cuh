@@ -4,9 +4,8 @@
 // CTA takes units in turn and, for every sequence among a unit's rows (a "pass", mostly one), streams the tiles of
 // 64 tokens that one row at least sees: those of the sinks, then from the shortest row's window on.  The products, the
 // softmax and the conversion of codes are those of kvq_shared_tc.cu, which has the layouts and the roles:
-//   warpgroups 0 and 1 softmax (thread v = vector v), warpgroup 2 converts, warps 12 and 14 issue the products of one
-// softmax warpgroup each, and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while
-// this one runs.
+//   warpgroups 0 and 1 softmax, warpgroup 2 converts, warps 12 and 14 issue the products of one softmax warpgroup each,
+// and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while this one runs.
 //
 // Few units: a cluster of 2, 4 or 8 CTAs takes each, every one an equal share of a pass's tiles, and they join their
 // states through the cluster's shared memory (the ring's place, once the pass has drained it), each writing its share of the
@@ -16,14 +15,19 @@
 // the token's alone: the converting warps store its key scale times log2(e) / sqrt(D) times that power, and an exponent
 // is one fused product and sum, S s_k - (m - sigma); rows of other sizes are brought to it first.
 //
-// Measured: 2048 rows of 32 / 8 heads on windows of 4096 (256 units of 66 tiles, int8): 187 us, where the products alone
-// would take 72 on all SMs; 752 on 16-vector tiles.  A tile of 256 vectors takes 2500 cycles: 1024 of the tensor
-// core's, and a softmax thread's 64 columns cost about 260 instructions that two warps a scheduler do not overlap better.
-// One warp that issued both warpgroups' products was itself what they waited for (195 us).  A unit's start and
-// end take 25,000 cycles (queries 9,500, the first tiles with their maximum and scales 5,000, outputs 11,000), and 256 units are
-// two rounds of 152 SMs.  Reading the scales in fragments (a thread four rows, two columns of eight) took the shared-memory
-// wavefronts of a tile from 2640 to 1870 and no time; leaving out the maximum of a tile until a sum passes
-// its bound takes too many tiles twice (255 us).
+// A softmax thread holds four rows of its warp's 32 and two columns of every eight, so that a scale it reads serves four
+// scores: with a row a thread, each warp read all of a tile's scales for every lane, and shared memory answered 2660 requests
+// of 128 bytes a tile (1024 of them operands of the products) in 2300 cycles; now 1830 in 2130.  The scales are asked for
+// before the scores are waited for.
+//
+// Measured: 2048 rows of 32 / 8 heads on windows of 4096 (256 units of 66 tiles, int8): 167 us (184 with a row a thread),
+// where the products alone would take 72 on all SMs; 752 on 16-vector tiles.  A tile of 256 vectors takes 2130 cycles: 1024
+// of the tensor core's, whose operands also fill shared memory's port for as long, and about 1350 issued instructions a
+// scheduler, which two softmax warps and a converting one do not overlap better.  A unit's start and end take 25,000 cycles,
+// and 256 units are two rounds of 152 SMs.  Tried and slower: scores of the next tile while one S buffer's are at work and
+// weights apart from them (198 us); queries in tensor memory, which halves the operands read, with the weights in S's only place
+// (197: the products then wait for the softmax and it for them); no maximum until a sum passes its bound (255, too many
+// tiles twice).  One warp that issued both warpgroups' products was itself what they waited for (195 before 187).
 //
 // Masks.  Row of length L sees token i < L if i < sinks or i >= L - span.  Tiles are aligned to 64 tokens; a
 // tile that every row of a warp sees whole skips the mask, so it costs the tiles at the window's start and at the chunk itself.
@@ -503,7 +507,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");  // 256 x 176 + 128 x (96 + 64): the launch's 512 x 128
     const int j = warp >> 2, v = tid & (kQ - 1);  // warpgroup, its vector
     const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t o_cols = lanes + 128 * j, s_cols = lanes + 256 + 128 * j;
@@ -640,7 +644,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
 #pragma unroll 1
         for (int i = 0; i < jobs; ++i, ++c) {
           const int tile = g.both ? i : 2 * i + j, sc = (n0 + tile) & (kRing - 1);
-          // the tile's scales are asked for before its scores: an answer of shared memory takes some 300 cycles beside the products' reads
+          // the tile's scales are asked for before its scores: shared memory takes some 300 cycles to answer beside the
+          // products' reads
           ok = __all_sync(kFull, ring_wait(sm->full, n0 + tile));
           if (!ok) break;
           const float4 sm4 = *reinterpret_cast<const float4*>(sm->svmax[sc]);
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
               for (int b = 0; b < 4; ++b) {
                 mx[b] = fmaxf(mx[b], __shfl_xor_sync(kFull, mx[b], 1));
                 mx[b] = fmaxf(mx[b], __shfl_xor_sync(kFull, mx[b], 2));
-                const float mn = fmaxf(m[b], mx[b] - nb[b]);
+                const float mn = fmaxf(m[b], mx[b] - nb[b]);  // every row's: one at a time, they would come back often (195 us)
                 f[b] = mn == kNegInf ? 1.f : ex2(m[b] - mn);
                 m[b] = mn;
               }
