@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1
 
   // ---- every row takes its parent's pages: those that hold tokens, but for those between the sinks and the window,
   // and its own that were kept for coming ones
-  const int chunks = (width + 32 * kCols - 1) / (32 * kCols), front = (a.sinks + kBlock - 1) / kBlock;
+  // (no sum passes 32 bits: width may be 2^31 - 1, and so may the sinks, which are cut to what a row can hold)
+  const int chunks = (width - 1) / (32 * kCols) + 1;
+  const int front = (min(a.sinks, table_tokens(width, a.window)) + kBlock - 1) / kBlock;
   for (int w = gwarp; w < B * chunks; w += kPageWarps) {
     const int r = w / chunks, j0 = (w % chunks) * 32 * kCols + lane;
     const Row x = rows[r];
