@@ -132,6 +132,14 @@ __host__ __device__ inline int update_smem(int B) {
   return B * int(sizeof(Row)) + (2 * B + 4) * 4 + 3 * writer_slots(B) * 4;
 }
 
+// Shared memory of fork_windows_kernel, whose slices are as wide as 52 KB each hold for every row.
+__host__ inline int ring_slice(int B) {
+  int bytes = 4096;
+  while (bytes > 16 && bytes * B > 53248) bytes /= 2;
+  return bytes;
+}
+__host__ inline int ring_smem(int B) { return (B * 4 + 15) / 16 * 16 + 2 * B * ring_slice(B); }
+
 __global__ void __launch_bounds__(kPageThreads) __cluster_dims__(kPageCtas, 1, 1) pages_update_kernel(const PagesArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int warp_sum[32];
@@ -647,11 +655,11 @@ size_t pages_workspace_bytes(int num_blocks) { return (size_t(kWsMap) + num_bloc
 
 cudaError_t launch_pages_update(PagesArgs a, cudaStream_t s) {
   const void* k = reinterpret_cast<const void*>(pages_update_kernel);
-  const int smem = update_smem(a.B);
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the most that any call takes: another thread's call sets the same between this and the launch
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, update_smem(kMaxBatch));
   if (e != cudaSuccess) return e;
   void* args[] = {&a};
-  return launch(k, dim3(kPageCtas), kPageThreads, smem, s, args);
+  return launch(k, dim3(kPageCtas), kPageThreads, update_smem(a.B), s, args);
 }
 
 cudaError_t launch_pages_compact(PagesArgs a, cudaStream_t s) {
@@ -684,8 +692,9 @@ cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s) {
   a.slice_bytes = 4096;
   while (a.slice_bytes > 16 && a.slice_bytes * a.B > 53248) a.slice_bytes /= 2;
   const void* k = reinterpret_cast<const void*>(fork_windows_kernel);
-  const int smem = (a.B * 4 + 15) / 16 * 16 + 2 * a.B * a.slice_bytes;
-  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  const int smem = ring_smem(a.B);
+  // the most that any call takes, as above: no smaller number of rows takes more than kMaxBatch of them
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, ring_smem(kMaxBatch))) != cudaSuccess) return e;
   const long long units = 2ll * a.layers * (a.row_bytes / a.slice_bytes);
   void* args[] = {&a};
   const int room = 224 * 1024 / (smem + 1024), most = sms * (room < 1 ? 1 : room > 4 ? 4 : room);

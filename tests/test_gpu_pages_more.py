@@ -28,3 +28,56 @@ def test_sinks_beyond_every_length_free_nothing(sinks, window):
     same(got, update_rule(refs, table, lens, None, **kw))
     if sinks >= 128:
         assert np.array_equal(got[1][table >= 0], table[table >= 0])
+
+
+def both(calls, times=20000):
+    """Each call over and over in a thread and on a stream of its own; the errors."""
+    import threading
+    failed, start = [], threading.Barrier(len(calls))
+
+    def go(call):
+        stream = torch.cuda.Stream()
+        start.wait()
+        try:
+            for _ in range(times):
+                call(stream)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=go, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return failed
+
+
+def test_two_threads_update_batches_of_different_sizes():
+    """The launch of a large batch beside that of a small one: both go through."""
+    from quantized_kv_cache_07_gb300 import _lib
+    calls = []
+    for B in (4096, 1, 1, 1):
+        run = Run(4, B, 1)
+        i = lambda n, v: torch.full((n,), v, dtype=torch.int32, device="cuda")
+        refs, table, lens = i(4, 0), i(B, -1).view(B, 1), i(B, 0)
+
+        def call(stream, run=run, args=(refs, table, lens)):
+            _lib.kvq_pages_update(*args, *run.out, workspace=run.ws, stream=stream)
+        calls.append(call)
+    torch.cuda.synchronize()
+    assert both(calls) == []
+
+
+def test_two_threads_fork_windows_of_different_batches():
+    from quantized_kv_cache_07_gb300 import _lib
+    from quantized_kv_cache_07_gb300.cache import KVCache
+    calls = []
+    for B in (4096, 1, 1, 1):
+        cache = KVCache(1, 1, 8, 8, window=16, window_batch=B)
+        parent = torch.arange(B, dtype=torch.int32, device="cuda")
+
+        def call(stream, caches=_lib.CacheList([cache.desc]), parent=parent, B=B, cache=cache):
+            _lib.kvq_fork_windows(caches, parent, B, stream=stream)
+        calls.append(call)
+    torch.cuda.synchronize()
+    assert both(calls) == []
