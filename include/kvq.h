@@ -655,7 +655,8 @@ kvq_status kvq_evict(const kvq_cache_desc* cache, const float* mass, float* mass
  *   table_out[r] = the parent's blocks that hold tokens (of length - window, where the last `window`
  *                  tokens are in a bf16 ring), but those that no coming query of kvq_decode_sinks sees (span > 0:
  *                  blocks behind the sinks whose last token is below length - span): -1;
- *                  a row that is its own parent keeps the blocks handed out to it that are still empty
+ *                  a row that is its own parent keeps, of the empty blocks handed out to it, those for
+ *                  this call's room; what an earlier call with a larger room gave beyond them is given back
  * and then, for every row that goes on,
  *   - its last block, if there is room left in it, is its own: of the rows that share it the lowest keeps it
  *     unless other entries or claims hold it too, the others get a new block and a pair (source,

@@ -156,7 +156,7 @@ class Pages:
 
     def update(self, parent=None, room=1, err_word=None, stream=None):
         """kvq_pages_update: rows become their parents' sequences (-1 ends one), with room for the next ``room`` tokens (a
-        number, or an int32 tensor [batch])."""
+        number, or an int32 tensor [batch]); empty blocks of an earlier, larger room are given back."""
         _lib.kvq_pages_update(self.refs, self.table, self.lens, self.refs, self._table, self._lens, self.copies, self.counts,
                               parent=parent, room=room, window=self.window, sinks=self.sinks, span=self.span,
                               parent_out=self.parents, workspace=self.workspace, err_word=err_word, stream=stream)

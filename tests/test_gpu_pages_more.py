@@ -81,3 +81,19 @@ def test_two_threads_fork_windows_of_different_batches():
         calls.append(call)
     torch.cuda.synchronize()
     assert both(calls) == []
+
+
+def test_empty_blocks_of_a_larger_room_are_given_back():
+    """Room for 64 tokens, then for one: a row keeps the blocks of its tokens and of this call's room; the others are
+    free at once, for another row of the same call too.  The same room again changes nothing."""
+    blocks, width = 16, 8
+    run, none = Run(blocks, 2, width), [-1] * 8
+    refs, table, lens = np.zeros(blocks, int), np.array([[9, 3] + [-1] * 6, none]), np.array([20, 0])
+    refs[[9, 3]] = 1
+    for _ in range(2):
+        refs, table, lens, copies = (x.copy() for x in run(refs, table, lens, None, room=np.array([64, 0])))
+        assert table.tolist() == [[9, 3, 0, 1, 2, 4, -1, -1], none] and len(copies) == 0
+        assert np.nonzero(refs)[0].tolist() == [0, 1, 2, 3, 4, 9]
+    refs, table, lens, copies = (x.copy() for x in run(refs, table, lens, None, room=np.array([1, 16])))
+    assert table.tolist() == [[9, 3] + [-1] * 6, [0] + [-1] * 7] and np.nonzero(refs)[0].tolist() == [0, 3, 9]
+    assert lens.tolist() == [20, 0] and run.err.item() == 0
