@@ -688,9 +688,7 @@ cudaError_t launch_fork_windows(RingArgs a, cudaStream_t s) {
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // two slices as wide as 52 KB each hold for every row, from 16 bytes (above 1664 rows: 64 KB at 4096) to 4 KB
-  a.slice_bytes = 4096;
-  while (a.slice_bytes > 16 && a.slice_bytes * a.B > 53248) a.slice_bytes /= 2;
+  a.slice_bytes = ring_slice(a.B);  // 16 bytes (above 1664 rows: 64 KB at 4096) to 4 KB
   const void* k = reinterpret_cast<const void*>(fork_windows_kernel);
   const int smem = ring_smem(a.B);
   // the most that any call takes, as above: no smaller number of rows takes more than kMaxBatch of them
