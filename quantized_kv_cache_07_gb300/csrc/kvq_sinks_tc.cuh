@@ -124,11 +124,11 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
         if (h == 0 && report) flag(a.err, KVQ_DEVERR_POSITION);
         seq = -1;
       } else {
-        const int most = table_tokens(a.mbps, 0), pos = a.pos[r0 + i];
-        len = pos < 0x7fffffff ? pos + 1 : -1;
+        const int most = table_tokens(a.mbps, 0);
+        len = row_tokens(a.pos[r0 + i]);
         if (len < 0 || len > most) {
           if (h == 0 && report) flag(a.err, KVQ_DEVERR_SEQ_LEN);
-          len = len < 0 && pos < 0 ? 0 : most;
+          len = len < 0 ? 0 : most;
         }
         if (len == 0) seq = -1;
       }
@@ -447,7 +447,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         auto load_ids = [&](int i) {
           const int blk = g.tile(i + lane) * kStep + w;
           int id = -1;
-          if (i + lane < g.nt && blk * kBlock < g.most && (blk * kBlock < a.sinks || (blk + 1) * kBlock > g.from)) {
+          bool seen = i + lane < g.nt && blk * kBlock < g.most && (blk * kBlock < a.sinks || (blk + 1) * kBlock > g.from);
+          if (g.apart && seen) {
+            show_next = seen_tokens(plan, g.seq, blk, a.sinks, a.span);
+            seen = show_next != 0;
+          }
+          if (seen) {
             id = __ldcg(table + blk);
             if (id < 0 || id >= a.c.num_blocks) {
               flag(a.err, KVQ_DEVERR_BLOCK_ID);
@@ -464,12 +469,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         auto block_of = [&](int i) {  // called once per tile, in order
           if ((i & 31) == 0) {
             ids = ids_next;
+            show = show_next;
             ids_next = load_ids(i + 32);
           }
           return i < g.nt ? __shfl_sync(kFull, ids, i & 31) : -1;
         };
         auto fetch_keys = [&](int phys) {
-            show = show_next;
           ks = vs = ko = vo = 0.f;
           rk.clear();
           if (phys < 0) return;
