@@ -134,9 +134,13 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
 }
 
 // A lane's own four weights and its mates' (ones behind R, where nothing is added).
+template <bool L2 = true>
 __device__ __forceinline__ void load_weights(const float* w, int R, bool interleaved, int lane, float (&own)[4],
                                              float (&mate)[4]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(w + 4 * lane));
+  auto get = [](const float* p) {
+    return L2 ? __ldcg(reinterpret_cast<const float4*>(p)) : *reinterpret_cast<const float4*>(p);
+  };
+  const float4 a = get(w + 4 * lane);
   own[0] = a.x;
   own[1] = a.y;
   own[2] = a.z;
@@ -145,7 +149,7 @@ __device__ __forceinline__ void load_weights(const float* w, int R, bool interle
   float4 b = make_float4(1.f, 1.f, 1.f, 1.f);
   if (d < R) {
     if (interleaved) b = make_float4(a.y, a.x, a.w, a.z);
-    else b = __ldcg(reinterpret_cast<const float4*>(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1))));
+    else b = get(w + (d < (R >> 1) ? d + (R >> 1) : d - (R >> 1)));
   }
   mate[0] = b.x;
   mate[1] = b.y;
@@ -154,10 +158,11 @@ __device__ __forceinline__ void load_weights(const float* w, int R, bool interle
 }
 
 // The turn with a head's weights in it (null: ones).
+template <bool L2 = true>
 __device__ __forceinline__ Turn fold(const Turn& t, const float* w, int R, bool interleaved, int lane) {
   if (!w) return t;
   float own[4], mate[4];
-  load_weights(w, R, interleaved, lane, own, mate);
+  load_weights<L2>(w, R, interleaved, lane, own, mate);
   Turn f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -345,8 +350,11 @@ __device__ __forceinline__ uint2 turn_head(const RopeArgs& a, uint2 raw, const T
     const float* w = weight_of(weights, a.per_head, h);
     if constexpr (KEY)
       return norm_key4(raw, t, fold(t, w, a.R, a.interleaved, lane), w, a.eps, a.R, a.interleaved, lane);
-    else
+    // as norm_queries_kernel takes it: a query's bits do not depend on how many rows the call has
+    else if (a.per_head)
       return norm_query4<true>(raw, t, w, a.eps, a.R, a.interleaved, lane);
+    else
+      return norm_query4<false>(raw, fold<false>(t, w, a.R, a.interleaved, lane), nullptr, a.eps, a.R, a.interleaved, lane);
   } else {
     return rotate4(raw, t, a.R, a.interleaved, lane);
   }
