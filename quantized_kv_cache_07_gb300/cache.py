@@ -68,6 +68,9 @@ class KVCache:
             k_window=self.k_window.data_ptr() if self.k_window is not None else None,
             v_window=self.v_window.data_ptr() if self.v_window is not None else None,
             q_bits=int(q_bits), k_per_channel=int(self.k_per_channel))
+        # a descriptor kept without its KVCache (in a CacheList) still points at live memory
+        self.desc.held = [t for t in (self.k_codes, self.v_codes, self.meta, self.channel_factor, self.k_window,
+                                      self.v_window) if t is not None]
 
     # bytes the decode reads per cached token per KV head (codes + scales + zero
     # points); 2-bit blocks share one 16-byte record per 16 tokens

@@ -1,0 +1,32 @@
+"""Classes of sliding-window serving without a GPU: what they hold and what they refuse."""
+import gc
+import weakref
+
+import pytest
+
+from test_ops_host import lib as built  # noqa: F401  (a fixture)
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture
+def cache_py(built, monkeypatch):  # noqa: F811
+    from quantized_kv_cache_07_gb300 import cache
+    monkeypatch.setattr(cache, "_require_cuda", lambda: None)
+    return cache
+
+
+def test_a_descriptor_holds_its_buffers(cache_py):
+    """What a list of caches points at lives as long as the list, as a rotary table's descriptor holds its table."""
+    lib = cache_py._lib
+    c = cache_py.KVCache(3, 2, 4, 4, window=16, window_batch=2, channel_factor=[[1.0] * 128] * 2, device="cpu")
+    tensors = (c.k_codes, c.v_codes, c.meta, c.k_window, c.v_window, c.channel_factor)
+    storages = [weakref.ref(t) for t in tensors]
+    layers = lib.CacheList([c.desc])
+    del c, tensors
+    gc.collect()
+    assert all(s() is not None for s in storages)
+    assert layers.array[0].k_codes == storages[0]().data_ptr()
+    del layers
+    gc.collect()
+    assert all(s() is None for s in storages)
