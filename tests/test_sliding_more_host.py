@@ -30,3 +30,13 @@ def test_a_descriptor_holds_its_buffers(cache_py):
     del layers
     gc.collect()
     assert all(s() is None for s in storages)
+
+
+def test_pages_refuse_rings_of_fewer_rows(cache_py):
+    """An update that forks rows would leave its tables changed and its rings not: refused when the pages are made."""
+    make = lambda rows: cache_py.KVCache(8, 1, 8, 8, window=16, window_batch=rows, device="cpu")
+    with pytest.raises(ValueError):
+        cache_py.Pages([make(4), make(3)], 4, 8)
+    pages = cache_py.Pages([make(4), make(7)], 4, 8)
+    assert pages.table.shape == (4, 8)
+    cache_py.Pages([cache_py.KVCache(8, 1, 8, 8, device="cpu")], 4, 8)  # no rings: any batch
