@@ -146,6 +146,8 @@ class Pages:
         first = caches[0]
         if any((c.num_blocks, c.window) != (first.num_blocks, first.window) for c in caches):
             raise ValueError("the caches of one model hold the same blocks and the same window")
+        if any(c.k_codes.device != first.k_codes.device for c in caches):
+            raise ValueError("the caches of one model are on one device")
         if first.window and any(c.desc.window_batch < batch for c in caches):  # found here: an update would be half done
             raise ValueError("the caches hold rings of fewer rows than the batch")
         self.window, self.sinks, self.span = first.window, sinks, span

@@ -40,3 +40,11 @@ def test_pages_refuse_rings_of_fewer_rows(cache_py):
     pages = cache_py.Pages([make(4), make(7)], 4, 8)
     assert pages.table.shape == (4, 8)
     cache_py.Pages([cache_py.KVCache(8, 1, 8, 8, device="cpu")], 4, 8)  # no rings: any batch
+
+
+def test_pages_refuse_caches_of_two_devices(cache_py):
+    one, other = (cache_py.KVCache(8, 1, 8, 8, device="cpu") for _ in range(2))
+    cache_py.Pages([one, other], 2, 4)
+    other.k_codes = other.k_codes.to("meta")
+    with pytest.raises(ValueError):
+        cache_py.Pages([one, other], 2, 4)
