@@ -41,7 +41,8 @@ namespace {
 
 // A sub-pass: the rows of the tile that belong to sequence seq; nblk blocks
 // cover the longest of them (maxlen tokens).  With sinks and a sliding window (SPAN) they are the blocks that one row
-// at least sees: those of the sinks and from the shortest row's window on (token `from`).
+// at least sees: those of the sinks and from the shortest row's window on (token `from`).  `seq` is a sequence, or with
+// SPAN a group of rows (group_rows), by its first row.
 struct SubPass {
   int seq, maxlen, nblk;
   int from;
@@ -73,6 +74,35 @@ __device__ __forceinline__ SubPass sub_pass_at(const DecodeArgs& a, const int* r
     sp.nblk = sp.sb.count;
   }
   return sp;
+}
+
+// With a sliding window: the group that row `lane` of the tile (sequence sb, -1: none, and its length) belongs to, named by
+// its first row.  Rows of a sequence are a group, unless they are so far apart that tokens between their windows are
+// nobody's: then each group's windows join, and no block is read that none of its rows sees.  One warp, all lanes.
+__device__ __forceinline__ int group_rows(int sb, int len, int span, int lane) {
+  int first = __ffs(__match_any_sync(kFull, sb)) - 1;
+  // most tiles: every row but a sequence's first is within a window of the row before it
+  const int sb_up = __shfl_up_sync(kFull, sb, 1), len_up = __shfl_up_sync(kFull, len, 1);
+  const bool far = lane == 0 || sb_up != sb || abs(len - len_up) > span;
+  if (__any_sync(kFull, sb >= 0 && far && first != lane)) {
+    int lo = len, hi = len;  // of the rows that windows join to this one
+    for (bool more = true; more;) {
+      more = false;
+      for (int k = 0; k < kTileQ; ++k) {
+        const int s = __shfl_sync(kFull, sb, k), l = __shfl_sync(kFull, len, k);
+        if (s != sb || (l >= lo && l <= hi) || l < lo - span || l - hi > span) continue;
+        lo = min(lo, l);
+        hi = max(hi, l);
+        more = true;
+      }
+      more = __any_sync(kFull, more);
+    }
+    for (int k = kTileQ - 1; k >= 0; --k) {
+      const int s = __shfl_sync(kFull, sb, k), l = __shfl_sync(kFull, lo, k);
+      if (s == sb && l == lo) first = k;
+    }
+  }
+  return sb < 0 ? -1 : first;
 }
 
 template <int KB, int VB, bool ASYM, bool LOQ, bool SPAN>
@@ -131,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 3) prefill_tile_kernel(const DecodeA
   // the tile's rows: sequence and causal length (positions 0..pos), clamped to
   // the block table's capacity as kvq_decode clamps lengths; a row with an
   // invalid sequence or no position to attend to is empty (sequence -1)
-  if (warp == 0 && lane < kTileQ) {
+  __shared__ int group_seq[SPAN ? kTileQ : 1];  // each group's sequence, by its first row
+  if (warp == 0 && (SPAN || lane < kTileQ)) {
     int sb = -1, len = 0;
     if (lane < nrows) {
       sb = a.seq_of[r0 + lane];
@@ -147,8 +178,14 @@ __global__ void __launch_bounds__(kThreads, 3) prefill_tile_kernel(const DecodeA
         if (len == 0) sb = -1;
       }
     }
-    rowseq[lane] = sb;
-    rowlen[lane] = len;
+    if constexpr (SPAN) {
+      if (lane < kTileQ) group_seq[lane] = sb;
+      sb = group_rows(sb, len, a.span, lane);
+    }
+    if (lane < kTileQ) {
+      rowseq[lane] = sb;
+      rowlen[lane] = len;
+    }
   }
   __syncthreads();
   // empty rows: out = 0, lse = -inf (as kvq_decode for a sequence of length 0)
@@ -196,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 3) prefill_tile_kernel(const DecodeA
         }
         int phys = 0;
         if (lane < nb) {
-          phys = a.table[size_t(sp.seq) * a.mbps + (SPAN ? sp.sb.logical(b0 + lane) : b0 + lane)];
+          phys = a.table[size_t(SPAN ? group_seq[sp.seq] : sp.seq) * a.mbps +
+                         (SPAN ? sp.sb.logical(b0 + lane) : b0 + lane)];
           if (phys < 0 || phys >= a.c.num_blocks) {
             flag(a.err, KVQ_DEVERR_BLOCK_ID);
             phys = 0;

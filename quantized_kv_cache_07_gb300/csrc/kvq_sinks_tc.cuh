@@ -2,7 +2,7 @@
 //
 // A unit is up to 256 query vectors: 256 / G consecutive rows of the call x the G query heads of one KV head.  A
 // CTA takes units in turn and, for every sequence among a unit's rows (a "pass", mostly one), streams the tiles of
-// 64 tokens that one row at least sees: those of the sinks, then from the shortest row's window on.  The products, the
+// 64 tokens of the sinks, then from the shortest row's window to the longest row's end.  The products, the
 // softmax and the conversion of codes are those of kvq_shared_tc.cu, which has the layouts and the roles:
 //   warpgroups 0 and 1 softmax, warpgroup 2 converts, warps 12 and 14 issue the products of one softmax warpgroup each,
 // and warp 13 plans: it reads the rows of the next unit (their sequences and lengths) while this one runs.
@@ -31,8 +31,9 @@
 //
 // Masks.  Row of length L sees token i < L if i < sinks or i >= L - span.  Tiles are aligned to 64 tokens; a
 // tile that every row of a warp sees whole skips the mask, so it costs the tiles at the window's start and at the chunk itself.
-// Blocks that no row sees are not read (their table entries may be gone); of blocks that are read, hidden tokens have no
-// say: scores -inf, value scales by row (as sequences stand apart in kvq_shared_tc.cu).
+// Blocks that no row sees are not read (their table entries may be gone): those before the shortest row's window, and
+// those between the windows of rows that are further apart than a window, which are found row by row.  Of blocks that are
+// read, hidden tokens have no say: scores -inf, value scales by row (as sequences stand apart in kvq_shared_tc.cu).
 #pragma once
 
 #include "kvq_tc_tiles.cuh"
@@ -44,6 +45,7 @@ constexpr int kPlanRows = 2 * kQ;  // G = 1
 
 struct Pass {
   int seq, least, most;  // shortest and longest row
+  int far;  // rows that are not within a window of the row before: with the first alone, no token between the rows is unseen
 };
 
 struct Plan {
@@ -75,6 +77,7 @@ struct UnitSmem {
 struct Walk {
   int seq, h, nt, first, front, skip;
   int from, most;  // no row sees the tokens between the sinks and `from`, nor those from `most` on
+  bool apart;  // nor, perhaps, tokens between these: rows further apart than a window
   int nv;
   bool both;  // more than 128 vectors: both warpgroups meet every tile
   __device__ __forceinline__ int tile(int i) const { return first + i + (first + i < front ? 0 : skip); }
@@ -87,6 +90,7 @@ __device__ __forceinline__ Walk walk_of(const DecodeArgs& a, const Plan& p, int 
   w.h = p.h;
   w.most = ps.most;
   w.from = max(ps.least - a.span, 0);
+  w.apart = ps.far > 1;
   w.front = (min(a.sinks, ps.most) + kTok - 1) / kTok;
   w.skip = max(w.from / kTok - w.front, 0);
   const long long tiles = all - w.skip;
@@ -95,6 +99,14 @@ __device__ __forceinline__ Walk walk_of(const DecodeArgs& a, const Plan& p, int 
   w.nv = p.nrows * a.G;
   w.both = w.nv > kQ;
   return w;
+}
+// Which tokens of block blk one row at least of the pass sees, as bits.
+__device__ __forceinline__ uint32_t seen_tokens(const Plan& p, int seq, int blk, int sinks, int span) {
+  auto below = [&](int n) { return (1u << min(max(n - blk * kBlock, 0), kBlock)) - 1u; };  // those before position n
+  uint32_t m = 0;
+  for (int i = 0; i < p.nrows && m != 0xFFFFu; ++i)
+    if (p.seq[i] == seq) m |= below(p.len[i]) & (below(sinks) | ~below(max(p.len[i] - span, 0)));
+  return m;
 }
 // Tiles of a pass that warpgroup j takes.
 __device__ __forceinline__ int jobs_of(const Walk& g, int j) { return g.both ? g.nt : (g.nt + 1 - j) / 2; }
@@ -123,6 +135,9 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
       p->seq[i] = seq;
       p->len[i] = len;
     }
+    __syncwarp();
+    const bool near = i > 0 && i < nrows && p->seq[i - 1] == seq && abs(len - p->len[i - 1]) <= a.span;
+    const uint32_t far = __ballot_sync(kFull, !near);
     uint32_t left = __ballot_sync(kFull, seq >= 0);
     while (left) {  // the sequences among these 32 rows
       const int s = __shfl_sync(kFull, seq, __ffs(left) - 1);
@@ -139,7 +154,8 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
       }
       if (lane == 0) {
         Pass& ps = p->pass[at < 0 ? passes : at];
-        ps = at < 0 ? Pass{s, least, most} : Pass{s, min(ps.least, least), max(ps.most, most)};
+        const int n = __popc(who & far);
+        ps = at < 0 ? Pass{s, least, most, n} : Pass{s, min(ps.least, least), max(ps.most, most), ps.far + n};
       }
       passes += at < 0;
       left &= ~who;
@@ -427,10 +443,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         }
         const int* table = a.table + size_t(g.seq) * a.mbps;
         int ids = -1, ids_next = -1;  // this warp's table entries of 32 tiles, and of the next 32
+        uint32_t show = 0xFFFFu, show_next = 0xFFFFu;  // which of their tokens are seen, where rows are apart
         auto load_ids = [&](int i) {
           const int blk = g.tile(i + lane) * kStep + w;
           int id = -1;
-          if (i + lane < g.nt && blk * kBlock < g.most && (blk * kBlock < a.sinks || (blk + 1) * kBlock > g.from)) {
+          bool seen = i + lane < g.nt && blk * kBlock < g.most && (blk * kBlock < a.sinks || (blk + 1) * kBlock > g.from);
+          if (g.apart && seen) {
+            show_next = seen_tokens(plan, g.seq, blk, a.sinks, a.span);
+            seen = show_next != 0;
+          }
+          if (seen) {
             id = __ldcg(table + blk);
             if (id < 0 || id >= a.c.num_blocks) {
               flag(a.err, KVQ_DEVERR_BLOCK_ID);
@@ -447,6 +469,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
         auto block_of = [&](int i) {  // called once per tile, in order
           if ((i & 31) == 0) {
             ids = ids_next;
+            show = show_next;
             ids_next = load_ids(i + 32);
           }
           return i < g.nt ? __shfl_sync(kFull, ids, i & 31) : -1;
@@ -481,7 +504,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) sinks_tc_kernel(const DecodeArg
           if (!ok) break;
           put_keys<KB>(rk, sm->st[s].k[0], sm->st[s].k[1], w, lane, km, c64);
           const int pos = (g.tile(i) * kStep + w) * kBlock + lane;
-          const bool data = pos < g.most && (pos < a.sinks || pos >= g.from);
+          bool data = pos < g.most && (pos < a.sinks || pos >= g.from);
+          if (g.apart) {
+            const uint32_t tokens = __shfl_sync(kFull, show, i & 31);
+            data = data && (tokens >> (lane & 15) & 1u);
+          }
           if (!data) vs = 0.f;
           if (lane < kBlock) {
             const int col = tile_col(w, lane);
