@@ -1215,7 +1215,7 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Params prm) {
       return 0;
     }
     rows_s[b] = sb;
-    return a.pos[b] + 1;
+    return row_tokens(a.pos[b]);
   };
   const Geo geo{pre_s, vpre_s, B, H, X};
   // Decode whose lengths and block table the caller declares final before the

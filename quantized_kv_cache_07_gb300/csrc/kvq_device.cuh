@@ -28,6 +28,10 @@ __host__ __device__ __forceinline__ int table_tokens(int entries, int window) {
   return int(n < most ? n : most);
 }
 
+// Tokens that a row of a chunk attends to, not yet cut to its table: those up to its position (there is no token behind
+// 2^31 - 1; every table cuts it).
+__host__ __device__ __forceinline__ int row_tokens(int pos) { return pos < 0x7fffffff ? pos + 1 : pos; }
+
 // ------------------------------------------------------------------ layout
 // Byte offset (and nibble shift for 4-bit codes) of key element (token i, dim d)
 // inside one 16-token block of one head.

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 3) prefill_tile_kernel(const DecodeA
         if (h == 0) flag(a.err, KVQ_DEVERR_POSITION);
         sb = -1;
       } else {
-        len = a.pos[r0 + lane] + 1;
+        len = row_tokens(a.pos[r0 + lane]);
         if (len < 0 || len > table_tokens(a.mbps, 0)) {
           if (h == 0) flag(a.err, KVQ_DEVERR_SEQ_LEN);
           len = len < 0 ? 0 : table_tokens(a.mbps, 0);

@@ -124,11 +124,11 @@ __device__ __forceinline__ void plan_unit(const DecodeArgs& a, Plan* p, int u, i
         if (h == 0 && report) flag(a.err, KVQ_DEVERR_POSITION);
         seq = -1;
       } else {
-        const int most = table_tokens(a.mbps, 0), pos = a.pos[r0 + i];
-        len = pos < 0x7fffffff ? pos + 1 : -1;
+        const int most = table_tokens(a.mbps, 0);
+        len = row_tokens(a.pos[r0 + i]);
         if (len < 0 || len > most) {
           if (h == 0 && report) flag(a.err, KVQ_DEVERR_SEQ_LEN);
-          len = len < 0 && pos < 0 ? 0 : most;
+          len = len < 0 ? 0 : most;
         }
         if (len == 0) seq = -1;
       }

@@ -96,3 +96,36 @@ def test_a_missing_block_between_the_windows_that_a_row_sees(fmt):
         prefill(run, pos * 0, pos, query_rows(len(pos), w.q_heads, 26), 4, 20, ctas, table)
         assert run.err_bits() == run.lib.KVQ_DEVERR_BLOCK_ID, ctas
         run.err.zero_()
+
+
+@pytest.mark.parametrize("windowed", [True, False])
+@pytest.mark.parametrize("fmt", ["int8_g4", "asym_int2_g8", "bf16_g7"])
+def test_the_last_position_is_cut_to_the_table_on_every_path(fmt, windowed):
+    """A row at 2^31 - 1 is reported and attends as the table's last position does, as any position behind the table."""
+    w = small_workload(fmt, **dict(dict(batch=1, len_range=(300, 300)), **FORMATS[fmt]))
+    run = DeviceRun(make_inputs(w, 27))
+    lib, table, q_heads = run.lib, run.table, w.q_heads
+    pos, qbits, end = np.arange(250, 290), query_rows(40, q_heads, 28), 16 * run.inp.max_blocks - 1
+    i = lambda x: torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
+
+    def whole(pos, ctas):
+        q = torch.from_numpy(qbits.view(np.int16)).cuda().view(torch.bfloat16)
+        out, lse = torch.empty(40, q_heads, 128, device="cuda"), torch.empty(40, q_heads, device="cuda")
+        ws = torch.zeros(lib.kvq_prefill_workspace_size(run.cache.desc, 40, q_heads, max(ctas, 0)) + 16, dtype=torch.uint8,
+                         device="cuda")
+        lib.kvq_prefill(run.cache.desc, q, q_heads, i(pos * 0), i(pos), table, 1, run.inp.max_blocks, out, lse=lse,
+                        workspace=ws, workspace_bytes=ws.numel(), stream_ctas=ctas, err_word=run.err)
+        return out.cpu().numpy(), lse.cpu().numpy()
+    for ctas in paths(w):
+        if ctas == -2 and not windowed:
+            continue
+        got = []
+        for p, bits in ((end, 0), (end + 1, lib.KVQ_DEVERR_SEQ_LEN), (2 ** 31 - 2, lib.KVQ_DEVERR_SEQ_LEN),
+                        (2 ** 31 - 1, lib.KVQ_DEVERR_SEQ_LEN)):
+            at = pos.copy()
+            at[13] = p
+            got.append(prefill(run, pos * 0, at, qbits, 4, 64, ctas) if windowed else whole(at, ctas))
+            assert run.err_bits() == bits, (ctas, p)
+            run.err.zero_()
+            np.testing.assert_array_equal(got[0][0], got[-1][0], err_msg=str((ctas, p)))
+            np.testing.assert_array_equal(got[0][1], got[-1][1], err_msg=str((ctas, p)))
