@@ -315,8 +315,9 @@ typedef struct {
  *   z_j = x_j / sqrt(mean(x^2) + eps) * weight_j over the head's 128 dimensions,
  * then turned (dimensions behind rotary_dim are normed too).  Keys are computed as the exact value rounded to
  * float32 and then to bf16, up to one case in about 2^30, and written as kvq_append writes them; queries in float32
- * (within 2^-20 of the two terms of a turn), rounded to bf16 once.  Weights are float32: 1 + w of a model that
- * stores w is added by the caller.  Values are stored as they come.  Everything else as kvq_rope_append.
+ * (within 2^-20 of the two terms of a turn), rounded to bf16 once, the same bits whatever else the call holds.
+ * Weights are float32: 1 + w of a model that stores w is added by the caller.  Values are stored as they come.
+ * Everything else as kvq_rope_append.
  */
 kvq_status kvq_norm_rope_append(const kvq_cache_desc* cache, const kvq_rope_desc* rope, const kvq_norm_desc* norm,
                                 const void* q, int32_t q_heads, int64_t q_stride, void* q_out, const void* k_new,
@@ -517,7 +518,8 @@ kvq_status kvq_decode_static_scratch(const kvq_cache_desc* cache, const void* q,
  * differ in rounding order only).
  *   q          : device bf16 [n][q_heads][128]
  *   seq_idx,pos: device int32 [n] (as kvq_append); a row with a sequence outside
- *                [0, batch) sets KVQ_DEVERR_POSITION and gets out = 0, lse = -inf
+ *                [0, batch) sets KVQ_DEVERR_POSITION and gets out = 0, lse = -inf; a position
+ *                beyond the table's capacity sets KVQ_DEVERR_SEQ_LEN and is cut to it
  *   k_new,v_new: device bf16 [n][num_kv_heads][128] to write first, or both NULL
  *                when the chunk is already in the cache; for 2-bit caches the
  *                chunk's positions must start at a block boundary (blocks are
@@ -569,8 +571,12 @@ kvq_status kvq_decode_sinks(const kvq_cache_desc* cache, const void* q, int32_t 
  * paths, kvq_prefill_workspace_size, the chunk's own write), block table and key factor as kvq_decode_sinks.
  * One more path, stream_ctas = KVQ_PREFILL_UNITS (-2), on tcgen05: 256 / G consecutive rows x the G query heads of
  * a KV head meet every tile of 64 tokens, once for each sequence among the rows.  Quantized caches, not q_bits 32
- * (KVQ_ERR_UNSUPPORTED); no workspace.  0 takes it where the rows are 128 query vectors (of a KV head) for
- * every sequence of the batch on average, 64 for a batch of one.
+ * (KVQ_ERR_UNSUPPORTED); no workspace.  It carries the value weights in one fp16 part, under a key factor too (the other
+ * paths in two there).  0 takes it where the rows are 128 query vectors (of a KV head) for
+ * every row of the block table on average, 64 for a batch of one: the call counts `batch` sequences, as which of
+ * them the chunk names is known on the device alone.  A chunk of few sequences with a larger table is faster
+ * with -2, or with a table of its own rows (1024 rows of one sequence, windows of 4096, 32 / 8 heads, a table of 64 rows:
+ * 97 us with -2, 409 with 0).
  */
 kvq_status kvq_prefill_sinks(const kvq_cache_desc* cache, const void* q, int32_t n, int32_t q_heads,
                              const int32_t* seq_idx, const int32_t* pos, const void* k_new, const void* v_new,

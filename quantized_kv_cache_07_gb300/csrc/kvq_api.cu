@@ -122,7 +122,9 @@ long long prefill_tiles(int n, int q_heads, int kv_heads) {
 
 // Units of 256 query vectors for a chunk with sinks: where a sequence of the batch has 128 of them on average, as each
 // sequence in a unit is a pass over its own tokens (one sequence: 64).  Units / the other paths' best, us, 32 / 8 heads on
-// windows of 4096: 4 sequences of 16 / 32 / 64 rows 123 / 84, 76 / 88, 44 / 140; one of 16 / 64 / 2048 rows 27 / 32, 36 / 83, 167 / 752.
+// windows of 4096: 4 sequences of 16 / 32 / 64 rows 123 / 84, 76 / 88, 44 / 140; one of 16 / 64 / 2048 rows 27 / 32, 36 / 83, 171 / 752.
+// `batch` is the table's rows: which of them are in the chunk is known on the device alone.  Measured with all of them in it;
+// one sequence beside 63 idle rows goes to tiles (256 / 512 / 1024 rows 147 / 226 / 409 us, on units 52 / 71 / 97), as the header says.
 bool prefill_units(int n, int group, int batch) { return (long long)n * group >= (batch == 1 ? 64ll : 128ll * batch); }
 
 // The cache as the kernels of kvq_decode_shared see it: under a key factor the query times the factor

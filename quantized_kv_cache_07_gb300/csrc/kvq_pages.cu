@@ -8,8 +8,8 @@
 // 8 CTAs: the steps need the whole batch's counts in between, and a cluster barrier costs less than a
 // launch.  Both are bound by latency, a chain of reads from L2 between barriers.
 //
-// Moving pages is copying: a warp takes one page of one head and layer, keys, values and metadata, all its
-// loads in flight before its first store.
+// Moving pages is copying: a warp takes pages of one head and layer in turn, and its lane 0 moves keys, values and
+// metadata by bulk copies through a ring of places in shared memory, a page out as soon as it has landed.
 #include "kvq_decode_impl.cuh"
 
 namespace kvq {

@@ -122,9 +122,10 @@ __device__ __forceinline__ uint2 rotate4(uint2 raw, const Turn& t, int R, bool i
 // z_j = x_j w_j r, r = (mean(x^2) + eps)^-1/2, then turned: y_j = r (x_j (w_j c_j) + m_j (w'_j s_j)) with w' the mate's
 // weights, so the weights are folded into the turn, once for all heads that share them.  Queries are what float32 gives,
 // rounded to bf16 (off by 2^-20 of the terms before that).  Keys are the rotation's: the exact value rounded to
-// float32 and then to bf16, so that 4-bit codes do not depend on how the norm was summed.  In float32 r is off by 5 x 2^-24 at most (the sum of squares, which are exact, by 8 roundings of which the
-// root leaves half, eps, the root), the folded factors and the products by one each, y r and the bounds
-// themselves by one: 12 x 2^-24 of the terms covers it.  Where both ends round to the same bf16 values that is the exact
+// float32 and then to bf16, so that 4-bit codes do not depend on how the norm was summed.  In float32, in units of 2^-24, r is
+// off by 5.5 at most: the sum of squares, which are exact, by 8 roundings of which the root leaves half, eps by half of one,
+// the root by its own.  Of the terms |y| + |w| the folded factors, w's product and the fused sum y are 3, y r and the
+// bounds themselves 2: 10.5, and 12 covers it.  Where both ends round to the same bf16 values that is the exact
 // one; otherwise (one vector in 20) the warp takes it again in pairs of floats (about 2^-44).
 
 // The sum of two floats and its rounding error.

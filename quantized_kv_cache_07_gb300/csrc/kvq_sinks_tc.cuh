@@ -20,8 +20,8 @@
 // of 128 bytes a tile (1024 of them operands of the products) in 2300 cycles; now 1830 in 2130.  The scales are asked for
 // before the scores are waited for.
 //
-// Measured: 2048 rows of 32 / 8 heads on windows of 4096 (256 units of 66 tiles, int8): 167 us (184 with a row a thread),
-// where the products alone would take 72 on all SMs; 752 on 16-vector tiles.  A tile of 256 vectors takes 2130 cycles: 1024
+// Measured: 2048 rows of 32 / 8 heads on windows of 4096 (256 units of 66 tiles, int8): 171 us a call (184 with a row a
+// thread), where the products alone would take 72 on all SMs; 752 on 16-vector tiles.  A tile of 256 vectors takes 2130 cycles: 1024
 // of the tensor core's, whose operands also fill shared memory's port for as long, and about 1350 issued instructions a
 // scheduler, which two softmax warps and a converting one do not overlap better.  A unit's start and end take 25,000 cycles,
 // and 256 units are two rounds of 152 SMs.  Tried and slower: scores of the next tile while one S buffer's are at work and
